@@ -16,6 +16,8 @@ from . import build as _build
 HLA_OK = 0
 HLA_F32 = 0
 HLA_BF16 = 1
+HLA_E4M3 = 2  # cached keys and values only
+HLA_ERR_INVALID_ARG = 1
 HLA_SPEC_VERIFY = 1
 HLA_SPEC_REPLAY = 2
 HLA_SPEC_BOTH = 3  # named by the ABI, answered with HLA_ERR_UNSUPPORTED (see include/hla.h)
@@ -28,8 +30,8 @@ P = c_void_p  # every tensor / stream argument is an address
 
 
 class HlaError(RuntimeError):
-    def __init__(self, fn, status):
-        super().__init__(f"{fn}: status {status} ({status_string(status)})")
+    def __init__(self, fn, status, detail=""):
+        super().__init__(f"{fn}: status {status} ({status_string(status)})" + (f": {detail}" if detail else ""))
         self.status = status
 
 
@@ -41,6 +43,14 @@ class hla_layer(ctypes.Structure):
                 ("W_router", P), ("W_gate", P), ("W_up", P), ("W_down", P),
                 ("Ws_gate", P), ("Ws_up", P), ("Ws_down", P)]
 
+
+class hla_kv_cache(ctypes.Structure):
+    _fields_ = [("dtype", c_int), ("n_pages", c_int), ("page_size", c_int), ("kv_heads", c_int),
+                ("head_dim", c_int), ("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("k_min", P),
+                ("k_max", P)]
+
+
+CACHE = ctypes.POINTER(hla_kv_cache)
 
 SIGNATURES = {
     "hla_status_string": (c_char_p, [c_int]),
@@ -70,6 +80,16 @@ SIGNATURES = {
     "hla_decode_layer": (c_int, [ctypes.POINTER(hla_layer), c_int] + [P] * 4 + [P, c_size_t, P, P]),
     "hla_decode_layer_routing": (c_int, [ctypes.POINTER(hla_layer), c_int, P,
                                          ctypes.POINTER(c_void_p), ctypes.POINTER(c_void_p)]),
+    "kv_cache_append": (c_int, [CACHE, c_int, c_int, P, P, c_int, P, c_int, P, P, P, c_int, c_int, P,
+                                P, P]),
+    "attn_paged_decode_workspace_size": (c_size_t, [CACHE] + [c_int] * 3),
+    "attn_paged_decode": (c_int, [CACHE] + [c_int] * 4 + [P, P, c_float, P, P, c_int, P, c_size_t, P]),
+    "attn_select_blocks_workspace_size": (c_size_t, [CACHE] + [c_int] * 4),
+    "attn_select_blocks": (c_int, [CACHE] + [c_int] * 4 + [P, P, c_int, c_int, c_int, P, P, P, c_size_t,
+                                                           P]),
+    "attn_paged_sparse_workspace_size": (c_size_t, [CACHE] + [c_int] * 3),
+    "attn_paged_sparse": (c_int, [CACHE] + [c_int] * 4 + [P, P, c_int, P, c_float, P, P, c_int, P,
+                                                          c_size_t, P]),
     "skinny_proj_splitk_noalloc": (c_int, [c_int] * 3 + [P] * 4 + [c_int, c_int, P]),
     "hla_launch_count": (ctypes.c_ulonglong, []),
     "hla_device_status": (c_int, []),
@@ -273,6 +293,99 @@ def hla_decode_layer_routing(L, M, ws):
     _check("hla_decode_layer_routing", load().hla_decode_layer_routing(ctypes.byref(L), M, _p(ws),
                                                                       ctypes.byref(a), ctypes.byref(b)))
     return a.value, b.value
+
+
+def _tensors(fn, args):
+    """Refuse torch tensors that a kernel would misread: (name, tensor, dtype, least number of elements)."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for name, t, dtype, n in args:
+        if t is None or isinstance(t, int):
+            continue
+        if t.dtype is not dtype or t.numel() < n or t.get_device() != dev or not t.is_contiguous():
+            raise HlaError(fn, HLA_ERR_INVALID_ARG,
+                           f"{name} must be a contiguous {dtype} tensor of at least {n} elements on the current "
+                           f"device (cuda:{dev}); got {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}, {t.device}")
+
+
+def make_kv_cache(dtype, n_pages, page_size, kv_heads, head_dim, k, v, k_scale=None, v_scale=None, k_min=None,
+                  k_max=None):
+    """Build an hla_kv_cache descriptor; it keeps the tensors it was given alive."""
+    import torch
+    C = hla_kv_cache(dtype, n_pages, page_size, kv_heads, head_dim)
+    if min(n_pages, page_size, kv_heads, head_dim) >= 1:
+        kv = torch.float8_e4m3fn if dtype == HLA_E4M3 else torch.bfloat16
+        n, m = n_pages * kv_heads * page_size * head_dim, n_pages * kv_heads * head_dim
+        _tensors("make_kv_cache", [("k", k, kv, n), ("v", v, kv, n), ("k_scale", k_scale, torch.float32, kv_heads),
+                                   ("v_scale", v_scale, torch.float32, kv_heads), ("k_min", k_min, torch.bfloat16, m),
+                                   ("k_max", k_max, torch.bfloat16, m)])
+    C.tensors = dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale, k_min=k_min, k_max=k_max)
+    for name, t in C.tensors.items():
+        setattr(C, name, _p(t))
+    return C
+
+
+def kv_cache_append(C, N, B, cu_seqlens, past_len, max_blocks, block_table, H, q, k, v, rope_dim,
+                    rope_interleaved, inv_freq, q_out, stream=None):
+    import torch
+    bf, i32, d, hk = torch.bfloat16, torch.int32, C.head_dim, C.kv_heads
+    _tensors("kv_cache_append", [
+        ("cu_seqlens", cu_seqlens, i32, B + 1), ("past_len", past_len, i32, B),
+        ("block_table", block_table, i32, B * max_blocks), ("q", q, bf, N * H * d), ("k", k, bf, N * hk * d),
+        ("v", v, bf, N * hk * d), ("inv_freq", inv_freq, torch.float64, rope_dim // 2), ("q_out", q_out, bf, N * H * d)])
+    return _check("kv_cache_append", load().kv_cache_append(
+        ctypes.byref(C), N, B, _p(cu_seqlens), _p(past_len), max_blocks, _p(block_table), H, _p(q), _p(k), _p(v),
+        rope_dim, rope_interleaved, _p(inv_freq), _p(q_out), _stream(stream)))
+
+
+def attn_paged_decode_workspace_size(C, B, T, H):
+    return load().attn_paged_decode_workspace_size(ctypes.byref(C), B, T, H)
+
+
+def attn_paged_decode(C, B, T, H, max_blocks, block_table, past_len, scale, q, o, o_dtype, ws, ws_bytes,
+                      stream=None):
+    import torch
+    n = B * T * H * C.head_dim
+    _tensors("attn_paged_decode", [
+        ("block_table", block_table, torch.int32, B * max_blocks), ("past_len", past_len, torch.int32, B),
+        ("q", q, torch.bfloat16, n), ("o", o, torch.bfloat16 if o_dtype == HLA_BF16 else torch.float32, n),
+        ("ws", ws, torch.uint8, ws_bytes)])
+    return _check("attn_paged_decode", load().attn_paged_decode(
+        ctypes.byref(C), B, T, H, max_blocks, _p(block_table), _p(past_len), scale, _p(q), _p(o), o_dtype, _p(ws),
+        ws_bytes, _stream(stream)))
+
+
+def attn_select_blocks_workspace_size(C, B, T, H, max_blocks):
+    return load().attn_select_blocks_workspace_size(ctypes.byref(C), B, T, H, max_blocks)
+
+
+def attn_select_blocks(C, B, T, H, max_blocks, block_table, past_len, n_select, n_first, n_last, q, sel, ws,
+                       ws_bytes, stream=None):
+    import torch
+    _tensors("attn_select_blocks", [
+        ("block_table", block_table, torch.int32, B * max_blocks), ("past_len", past_len, torch.int32, B),
+        ("q", q, torch.bfloat16, B * T * H * C.head_dim), ("sel", sel, torch.int32, B * T * C.kv_heads * n_select),
+        ("ws", ws, torch.uint8, ws_bytes)])
+    return _check("attn_select_blocks", load().attn_select_blocks(
+        ctypes.byref(C), B, T, H, max_blocks, _p(block_table), _p(past_len), n_select, n_first, n_last, _p(q), _p(sel),
+        _p(ws), ws_bytes, _stream(stream)))
+
+
+def attn_paged_sparse_workspace_size(C, B, T, H):
+    return load().attn_paged_sparse_workspace_size(ctypes.byref(C), B, T, H)
+
+
+def attn_paged_sparse(C, B, T, H, max_blocks, block_table, past_len, n_select, sel, scale, q, o, o_dtype, ws,
+                      ws_bytes, stream=None):
+    import torch
+    n = B * T * H * C.head_dim
+    _tensors("attn_paged_sparse", [
+        ("block_table", block_table, torch.int32, B * max_blocks), ("past_len", past_len, torch.int32, B),
+        ("sel", sel, torch.int32, B * T * C.kv_heads * n_select), ("q", q, torch.bfloat16, n),
+        ("o", o, torch.bfloat16 if o_dtype == HLA_BF16 else torch.float32, n), ("ws", ws, torch.uint8, ws_bytes)])
+    return _check("attn_paged_sparse", load().attn_paged_sparse(
+        ctypes.byref(C), B, T, H, max_blocks, _p(block_table), _p(past_len), n_select, _p(sel), scale, _p(q), _p(o),
+        o_dtype, _p(ws), ws_bytes, _stream(stream)))
 
 
 def hla_launch_count():

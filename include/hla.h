@@ -78,7 +78,7 @@ enum hla_status {
     HLA_ERR_DEVICE_TIMEOUT = 6   /* a bounded device-side wait gave up */
 };
 
-enum hla_dtype { HLA_F32 = 0, HLA_BF16 = 1 };
+enum hla_dtype { HLA_F32 = 0, HLA_BF16 = 1, HLA_E4M3 = 2 /* cached keys and values only */ };
 
 enum hla_spec_phase { HLA_SPEC_VERIFY = 1, HLA_SPEC_REPLAY = 2, HLA_SPEC_BOTH = 3 };
 
@@ -373,6 +373,98 @@ int hla_decode_layer(const hla_layer *L, int M, const hla_bf16 *x, float *S,
  * Valid until the workspace is reused.  Returns HLA_ERR_INVALID_ARG on bad arguments. */
 int hla_decode_layer_routing(const hla_layer *L, int M, const void *ws, const int32_t **topk_idx,
                              const float **topk_w);
+
+/* ---------------------------------------------------------------------------
+ * Paged key-value cache of the softmax-attention layers that a hybrid model interleaves with its KDA
+ * layers.  [KIMI-WEBINAR] names the pair: a fixed-size recurrent state next to an attention cache that
+ * grows with the sequence; [VLLM-K3] Part 1 sec. 1 (split of a long cache and join of the parts).  The
+ * pages give no layout or kernel for it.
+ *
+ * The cache is a pool of pages of page_size tokens; a block table int32 [B, max_blocks] names the page
+ * of each block of page_size consecutive positions of a sequence.  A table entry outside [0, n_pages)
+ * holds no page: nothing is read or written there, and its positions hold no keys.  Pages may be shared
+ * by sequences for reading; a page that a call appends to belongs to one sequence of that call.
+ * past_len int32 [B] counts the tokens cached before a step's new ones (committed_len of
+ * spec_accept_prefix, say), so one array serves the append and the attention of a step; a negative
+ * entry marks an idle slot.  Positions at or behind max_blocks * page_size are dropped.
+ * All pointers are device pointers; the descriptor itself is read during the call only.
+ * -------------------------------------------------------------------------*/
+typedef struct hla_kv_cache {
+    int dtype;                 /* HLA_BF16, or HLA_E4M3 (8 bits, one scale per kv head) */
+    int n_pages, page_size;    /* page_size 16, 32, 64 or 128 */
+    int kv_heads, head_dim;    /* head_dim 64 or 128 */
+    void *k, *v;               /* [n_pages, kv_heads, page_size, head_dim] */
+    const float *k_scale;      /* [kv_heads], HLA_E4M3 only: key = k_scale * stored */
+    const float *v_scale;      /* [kv_heads], HLA_E4M3 only */
+    hla_bf16 *k_min, *k_max;   /* [n_pages, kv_heads, head_dim] bounds of each page's stored keys (unscaled), or both NULL */
+} hla_kv_cache;
+
+/* ---------------------------------------------------------------------------
+ * Append: rotate q and k by position, write k and v into the cache, bound the touched pages' keys.
+ *  Sequence b owns the packed token rows cu_seqlens[b] .. cu_seqlens[b+1]-1 (any number, none too; as
+ *  kda_extend), at positions past_len[b], past_len[b] + 1, ...
+ *  Rotation of the first rope_dim channels of every head (0: none, inv_freq NULL): pair i of position p
+ *  turns by p * inv_freq[i], (x, y) -> (x cos - y sin, x sin + y cos).  Pair i is channels (i, i + rope_dim/2),
+ *  or (2i, 2i + 1) with rope_interleaved = 1.  rope_dim % 16 == 0.  Angles are exact to 2^-32 of a turn at
+ *  any position.  q_out = the rotated q; k and v are rounded once, to bf16 or to e4m3 of value / scale
+ *  (saturating at +-448, infinities too).
+ *  Bounds (when k_min and k_max are set): of every page that got a token, over its stored keys at positions
+ *  below past_len[b] + new tokens, whatever the page held before; a NaN key makes its channel's bounds NaN.
+ *  N: rows of q [N, H, d], k, v [N, kv_heads, d], q_out [N, H, d] (may be q itself), all bf16.  Rows at or
+ *  behind cu_seqlens[B], and the rows of idle sequences, are left as they were.
+ *  cu_seqlens int32 [B + 1] (device, non-decreasing); inv_freq fp64 [rope_dim / 2].
+ *  1 <= B <= 1024, max_blocks * page_size < 2^30, H a multiple of kv_heads, H <= 1024.
+ * -------------------------------------------------------------------------*/
+int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_t *cu_seqlens, const int32_t *past_len,
+                    int max_blocks, const int32_t *block_table, int H, const hla_bf16 *q, const hla_bf16 *k,
+                    const hla_bf16 *v, int rope_dim, int rope_interleaved, const double *inv_freq,
+                    hla_bf16 *q_out, hla_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of the T newest tokens of each sequence (1: decode; up to 8: a speculative window) over its
+ * cache, the T tokens' own keys appended before.
+ *  Token t of sequence b sees positions 0 .. past_len[b] + t:
+ *    o[b, t, h] = sum_c softmax_c(scale q[b, t, h] . k_c) v_c,   k_c, v_c of kv head h / (H / kv_heads).
+ *  A row that sees no key (an idle slot, no pages) is 0.  A position that a row does not see has no effect on
+ *  it, whatever it holds.
+ *  q bf16 [B, T, H, d]; o [B, T, H, d] (o_dtype: HLA_F32 or HLA_BF16).  Products on tensor cores with fp32
+ *  sums; softmax statistics in fp32; the weights meet the values in 16 bits for a bf16 output and as two
+ *  16-bit parts for an fp32 one.  The work is split over sequences and positions by the lengths on the
+ *  device, so one captured graph serves any lengths.  B <= 1024, T <= 8, H <= 1024.
+ * -------------------------------------------------------------------------*/
+size_t attn_paged_decode_workspace_size(const hla_kv_cache *C, int B, int T, int H);
+int attn_paged_decode(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const int32_t *block_table,
+                      const int32_t *past_len, float scale, const hla_bf16 *q, void *o, int o_dtype,
+                      void *ws, size_t ws_bytes, hla_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Block choice for attn_paged_sparse: for each (sequence, token, kv head) the blocks of the cache whose
+ * key bounds promise the largest scores.
+ *  Of the visible blocks j = 0 .. (past_len[b] + t) / page_size the first n_first and the last n_last are
+ *  taken, and of the others those with the highest
+ *    max over the kv head's query heads h of  sum_d max(q[b,t,h,d], 0) k_max[j,d] + min(q[b,t,h,d], 0) k_min[j,d],
+ *  n_select in all (every visible one when there are no more).  The order is that of exact arithmetic up to
+ *  fp64 rounding; equal scores go to the lower block, a NaN score is above all others, a block without a page
+ *  scores -infinity.
+ *  sel int32 [B, T, kv_heads, n_select]: the chosen blocks, ascending, then -1.  The cache's k and v are not
+ *  used.  max_blocks <= 65536; n_first + n_last <= n_select; B * kv_heads <= 65535.
+ * -------------------------------------------------------------------------*/
+size_t attn_select_blocks_workspace_size(const hla_kv_cache *C, int B, int T, int H, int max_blocks);
+int attn_select_blocks(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const int32_t *block_table,
+                       const int32_t *past_len, int n_select, int n_first, int n_last, const hla_bf16 *q,
+                       int32_t *sel, void *ws, size_t ws_bytes, hla_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * attn_paged_decode over listed blocks: token t of sequence b, for the query heads of kv head h, sees the
+ * positions of the blocks sel[b, t, h, 0 .. n_select-1], up to past_len[b] + t.  Entries outside
+ * [0, max_blocks) are skipped, blocks behind the token hold nothing for it, and a block listed twice counts
+ * twice.  Other arguments as attn_paged_decode.  Listing every visible block once gives attn_paged_decode's
+ * sum, in another order.
+ * -------------------------------------------------------------------------*/
+size_t attn_paged_sparse_workspace_size(const hla_kv_cache *C, int B, int T, int H);
+int attn_paged_sparse(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const int32_t *block_table,
+                      const int32_t *past_len, int n_select, const int32_t *sel, float scale,
+                      const hla_bf16 *q, void *o, int o_dtype, void *ws, size_t ws_bytes, hla_stream stream);
 
 /* ---------------------------------------------------------------------------
  * skinny_proj_splitk without a workspace.  No counterpart on the source pages: this is

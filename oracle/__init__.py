@@ -16,10 +16,12 @@ defining equations by eye; speed is not a goal.  Modules:
   the SwiGLU routed + shared experts.
 * ``layer``    -- the q/k/v/gate/beta projection epilogue and the composed
   hybrid decode layer.
+* ``attention`` -- softmax attention over a paged key-value cache, the append
+  with position rotation, and block choice by key bounds.
 
 Parity status: every function is pinned by the ``-m "not gpu"`` tests in
 ``tests/test_oracle_*.py`` (closed forms, hand-worked examples under
 ``tests/golden/``, brute force and invariants).  No function is unpinned.
 """
 
-from . import numerics, kda, moe, layer  # noqa: F401
+from . import numerics, kda, moe, layer, attention  # noqa: F401

@@ -1,0 +1,279 @@
+"""Paged attention of the newest tokens, dense and over listed blocks, against the fp64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from hybrid_linear_attention_gated_gb300 import hla
+from tests.attn_common import BF16, I32, Problem, attention_tolerance, bits
+from tests.gpu_common import f64, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+def check(p, o, o_dtype, sel=None):
+    k, v = p.values()
+    q = p.q.double().numpy()
+    table = p.table.numpy()
+    ref, mag = oracle.attention.attend(q, k, v, table, p.past, p.scale, sel)
+    n = max([x + p.T for x in p.past] + [1]) if sel is None else sel.shape[-1] * p.page
+    size = p.scale * np.abs(q).sum(-1).max() * np.nanmax(np.abs(np.where(np.isfinite(k), k, 0.0)))
+    tol = attention_tolerance(ref, mag, n, p.d, size, o_dtype, p.dtype)
+    got = f64(o)
+    assert np.all(np.isfinite(got))
+    worst = np.max(np.abs(got - ref) - tol)
+    assert worst <= 0, worst
+    # and far closer on average than the elementwise bound: rounding of the output, or fp32
+    rel = np.linalg.norm(got - ref) / max(np.linalg.norm(ref), 1e-30)
+    assert rel < (2.0 ** -8 if o_dtype == hla.HLA_BF16 else 2e-5), rel
+    return ref
+
+
+# (past per sequence, T, H, Hkv, d, page): 16-, 32- and 64-row tiles, one key, page and tile borders, idle slots
+CASES = [
+    ([0], 1, 1, 1, 64, 16),
+    ([0, 1, 15, 16, 17, -1], 1, 8, 2, 128, 16),
+    ([62, 63, 64, 65, 127, 128], 1, 32, 8, 128, 64),
+    ([300, -1, 5, 1021], 4, 16, 4, 128, 32),        # 16 rows
+    ([97, 2000], 5, 10, 2, 128, 128),               # 25 rows
+    ([31, 500, 0], 8, 16, 4, 64, 64),               # 32 rows
+    ([700, 12], 8, 16, 1, 128, 16),                 # 128 rows: two tiles of 64
+    ([130, 64, -1], 3, 24, 1, 64, 32),              # 72 rows: a full tile and a ragged one
+    ([4093], 2, 6, 2, 128, 64),
+    ([-1, -1], 2, 4, 2, 64, 16),
+]
+
+
+@pytest.mark.parametrize("o_dtype", [hla.HLA_BF16, hla.HLA_F32])
+@pytest.mark.parametrize("dtype", [hla.HLA_BF16, hla.HLA_E4M3])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_decode_matches_oracle(case, dtype, o_dtype):
+    past, T, H, Hkv, d, page = CASES[case]
+    p = Problem(require_gpu(), past, T, H, Hkv, d, page, dtype, seed=case).upload()
+    o = p.decode(o_dtype)
+    rows = T * H // Hkv
+    m = 16 if rows <= 16 else 32 if rows <= 32 else 64
+    assert hla.hla_last_variant() == f"attn_paged<d{d},{'e4m3' if dtype == hla.HLA_E4M3 else 'bf16'},m{m}>"
+    torch.cuda.synchronize()
+    check(p, o, o_dtype)
+    again = p.decode(o_dtype)
+    assert torch.equal(bits(again), bits(o))  # fixed order of all sums
+
+
+@pytest.mark.parametrize("T,H,Hkv", [(1, 8, 2), (4, 16, 2), (8, 8, 1)])
+def test_many_ragged_sequences(T, H, Hkv):
+    """More units than CTAs and fewer, with pieces joined across CTAs: every sequence against the oracle."""
+    g = np.random.default_rng(5)
+    past = [int(x) for x in g.integers(-1, 700, size=70)]
+    p = Problem(require_gpu(), past, T, H, Hkv, 64, 32, seed=9).upload()
+    check(p, p.decode(hla.HLA_F32), hla.HLA_F32)
+
+
+@pytest.mark.parametrize("dtype", [hla.HLA_BF16, hla.HLA_E4M3])
+def test_large_scores_and_flat_scores(dtype):
+    """Scores of hundreds (one key takes all) and of zero (all keys alike)."""
+    dev = require_gpu()
+    for scale in (8.0, 0.0, -1.0):
+        p = Problem(dev, [513, 64], 2, 8, 2, 128, 64, dtype, seed=3).upload()
+        p.scale = scale
+        k, v = p.values()
+        ref, mag = oracle.attention.attend(p.q.double().numpy(), k, v, p.table.numpy(), p.past, scale)
+        got = f64(p.decode(hla.HLA_F32))
+        # a score's error is d 2^-23 of its terms' magnitudes: about 128 x 2^-23 x 8 x 128 x 3 at scale 8
+        assert np.all(np.abs(got - ref) <= (1e-5 + abs(scale) * 0.012) * mag + 1e-6)
+
+
+def test_small_and_large_queries_with_an_8_bit_cache():
+    """Query rows go to fp16 by a power of two of their own: tiny, huge, zero and one-element rows keep their precision."""
+    dev = require_gpu()
+    p = Problem(dev, [200], 1, 8, 1, 128, 64, hla.HLA_E4M3, seed=4)
+    q = p.q.float()
+    q[0, 0, 0] *= 2.0 ** -60
+    q[0, 0, 1] *= 1e-30
+    q[0, 0, 2] = 0
+    q[0, 0, 3, 1:] = 0
+    q[0, 0, 4] *= 2.0 ** 3
+    q[0, 0, 5, 7] = 2.0 ** 17      # beyond fp16
+    q[0, 0, 5, :7] = 0
+    p.q = q.to(BF16)
+    p.scale = 1.0 / 128
+    p.upload()
+    k, v = p.values()
+    ref, mag = oracle.attention.attend(p.q.double().numpy(), k, v, p.table.numpy(), p.past, p.scale)
+    got = f64(p.decode(hla.HLA_F32))
+    qs = np.abs(p.q.double().numpy()).sum(-1)
+    size = p.scale * qs * np.nanmax(np.abs(k))
+    # elements below 2^-38 of a row's largest may vanish in fp16: within d 2^-23 of the score's size as well
+    tol = (2 * (128 * 2.0 ** -23 * size + 2.0 ** -21) + 2.0 ** -21 + 400 * 2.0 ** -23)[..., None] * mag + 1e-7
+    assert np.all(np.abs(got - ref) <= tol)
+
+
+def test_masked_places_may_hold_anything():
+    """Infinities and NaN at keys and values a row does not see: the window's later tokens, rows behind the last token (the
+    problem's poison), whole foreign pages; a row sees its own infinities."""
+    dev = require_gpu()
+    for dtype in (hla.HLA_BF16, hla.HLA_E4M3):
+        for H, Hkv in ((4, 2), (16, 2), (16, 1)):  # 16-, 32- and 64-row tiles at T = 4
+            for past in (62, 64, 13):              # the window across a page and tile border, at its start, inside
+                p = Problem(dev, [past, 100], 4, H, Hkv, 64, 16, dtype, seed=past)
+                clean = Problem(dev, [past, 100], 4, H, Hkv, 64, 16, dtype, seed=past).upload().decode(hla.HLA_F32)
+                for t, what in ((2, float("nan")), (3, float("inf") if dtype == hla.HLA_BF16 else float("nan"))):
+                    c = past + t
+                    p.v[p.table[0, c // 16], :, c % 16] = torch.tensor(what).to(p.v.dtype)
+                    p.k[p.table[0, c // 16], :, c % 16] = torch.tensor(what).to(p.k.dtype)
+                o = p.upload().decode(hla.HLA_F32)
+                torch.cuda.synchronize()
+                # rows 0 and 1 of sequence 0 and all of sequence 1 see none of it; sums may run in another order
+                assert torch.isfinite(o[0, :2]).all() and torch.isfinite(o[1]).all()
+                assert torch.allclose(o[0, :2], clean[0, :2], rtol=1e-4, atol=1e-5)
+                assert torch.equal(o[1], clean[1])
+                assert torch.isnan(o[0, 2:]).all()
+
+
+def test_blocks_without_a_page_hold_no_keys():
+    dev = require_gpu()
+    for sel in (False, True):
+        p = Problem(dev, [500, 90, 40], 2, 8, 2, 128, 32, seed=6)
+        p.table[0, 0], p.table[0, 3], p.table[0, 15] = -1, p.n_pages, 2 ** 31 - 1
+        p.table[1] = -(2 ** 31)
+        p.upload()
+        lists = None
+        if sel:
+            lists = torch.arange(16, dtype=I32).repeat(3, 2, 2, 1)
+        o = p.decode(hla.HLA_F32, None if lists is None else lists.to(dev))
+        torch.cuda.synchronize()
+        check(p, o, hla.HLA_F32, None if lists is None else lists.numpy())
+        assert torch.all(o[1] == 0)
+
+
+def test_positions_behind_the_table_are_dropped():
+    dev = require_gpu()
+    p = Problem(dev, [200, 100], 2, 4, 2, 64, 16, seed=7, max_blocks=5)
+    p.upload()
+    o = p.decode(hla.HLA_F32)
+    check(p, o, hla.HLA_F32)
+    # lengths far behind the table: every row sees the whole table
+    far = p.D["past"]
+    far.copy_(torch.tensor([2 ** 31 - 1, 2 ** 30], dtype=I32))
+    o = p.decode(hla.HLA_F32)
+    p.past = [10 ** 6, 10 ** 6]
+    k, v = p.values()
+    ref, _ = oracle.attention.attend(p.q.double().numpy(), k, v, p.table.numpy(), p.past, p.scale)
+    assert np.allclose(f64(o), ref, rtol=1e-4, atol=1e-5)
+
+
+@pytest.mark.parametrize("dtype", [hla.HLA_BF16, hla.HLA_E4M3])
+@pytest.mark.parametrize("T,H,Hkv,d,page,n_sel", [(1, 8, 2, 128, 64, 5), (3, 12, 4, 64, 16, 9), (2, 40, 2, 128, 32, 3),
+                                                  (1, 48, 1, 64, 128, 2)])
+def test_sparse_matches_oracle(T, H, Hkv, d, page, n_sel, dtype):
+    """Arbitrary lists: unsorted, repeated, behind the token, outside the table, empty."""
+    dev = require_gpu()
+    p = Problem(dev, [40 * page // 8, 11 * page + 3, -1, 0], T, H, Hkv, d, page, dtype, seed=n_sel, max_blocks=13).upload()
+    g = np.random.default_rng(n_sel)
+    sel = g.integers(-2, 15, size=(4, T, Hkv, n_sel))
+    sel[1, 0, 0] = -1                       # nothing listed
+    sel[0, -1, -1] = 2                      # one block, n_sel times
+    o = p.decode(hla.HLA_F32, torch.from_numpy(sel).to(I32).to(dev))
+    assert hla.hla_last_variant().startswith("attn_sparse<")
+    check(p, o, hla.HLA_F32, sel)
+    assert torch.all(o[2] == 0) and torch.all(o[1, 0, :H // Hkv] == 0)
+
+
+def test_listing_every_block_is_the_dense_form():
+    dev = require_gpu()
+    p = Problem(dev, [333, 64, 5], 2, 8, 2, 128, 32, seed=8).upload()
+    sel = torch.arange(p.max_blocks, dtype=I32, device=dev).repeat(3, 2, 2, 1)
+    dense, sparse = p.decode(hla.HLA_F32), p.decode(hla.HLA_F32, sel)
+    assert torch.allclose(dense, sparse, rtol=1e-5, atol=1e-6)
+
+
+def test_cache_beyond_32_bit_offsets():
+    """Pages whose element offsets pass 2^31 and 2^32, in a pool that is written only where it is used."""
+    dev = require_gpu()
+    p = Problem(dev, [150, 70], 1, 8, 8, 128, 64, seed=10)
+    page_elems = 8 * 64 * 128
+    n_pages = 2 ** 32 // page_elems + 64
+    k, v = (torch.empty(n_pages, 8, 64, 128, dtype=BF16, device=dev) for _ in range(2))
+    moved = p.table.clone()
+    places = [n_pages - 1, 2 ** 31 // page_elems, 2 ** 32 // page_elems + 1, 2 ** 31 // page_elems - 1, 3]
+    for n, (b, j) in enumerate([(0, 0), (0, 1), (0, 2), (1, 0), (1, 1)]):
+        moved[b, j] = places[n]
+        k[places[n]], v[places[n]] = p.k[p.table[b, j]].to(dev), p.v[p.table[b, j]].to(dev)
+    small = p.upload().decode(hla.HLA_F32)
+    C = hla.make_kv_cache(hla.HLA_BF16, n_pages, 64, 8, 128, k, v)
+    o = torch.empty_like(small)
+    ws = torch.empty(hla.attn_paged_decode_workspace_size(C, 2, 1, 8), dtype=torch.uint8, device=dev)
+    hla.attn_paged_decode(C, 2, 1, 8, p.max_blocks, moved.to(dev), p.D["past"], p.scale, p.D["q"], o, hla.HLA_F32, ws, ws.numel())
+    assert torch.equal(o, small)
+    check(p, o, hla.HLA_F32)
+
+
+def test_one_captured_graph_serves_any_lengths_and_pages():
+    dev = require_gpu()
+    p = Problem(dev, [700, 300, 20], 2, 8, 2, 64, 32, seed=11, poison=False).upload()
+    o = torch.empty(3, 2, 8, 64, device=dev)
+    ws = torch.empty(hla.attn_paged_decode_workspace_size(p.C, 3, 2, 8), dtype=torch.uint8, device=dev)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        p.decode(hla.HLA_F32, ws=ws, o=o)
+    side.synchronize()
+    graphs = []
+    for _ in range(2):  # two graphs that share the workspace, replayed one after the other
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            p.decode(hla.HLA_F32, ws=ws, o=o)
+        graphs.append(g)
+    for past in ([700, 300, 20], [1, 640, -1], [0, 0, 0], [650, 2, 33]):
+        p.D["past"].copy_(torch.tensor(past, dtype=I32))
+        eager = p.decode(hla.HLA_F32)
+        for g in graphs:
+            ws.fill_(255)
+            o.fill_(3.0)
+            g.replay()
+            assert torch.equal(o, eager)
+
+
+def test_two_streams_at_once_with_their_own_workspaces():
+    dev = require_gpu()
+    ps = [Problem(dev, [900 + 40 * n, 100], 4, 16, 4, 128, 64, seed=12 + n).upload() for n in range(2)]
+    want = [p.decode(hla.HLA_F32) for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for p, s in zip(ps, streams):
+            with torch.cuda.stream(s):
+                got.append(p.decode(hla.HLA_F32))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_output_and_workspace_stay_inside_their_bounds():
+    dev = require_gpu()
+    for T, H, Hkv, d in ((1, 8, 2, 128), (5, 8, 2, 64), (8, 16, 1, 128)):
+        p = Problem(dev, [500, 33], T, H, Hkv, d, 16, seed=13).upload()
+        n = hla.attn_paged_decode_workspace_size(p.C, 2, T, H)
+        ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device=dev)
+        elems = 2 * T * H * d
+        o = torch.full((elems + 1024,), 5.0, device=dev)
+        hla.attn_paged_decode(p.C, 2, T, H, p.max_blocks, p.D["table"], p.D["past"], p.scale, p.D["q"], o, hla.HLA_F32, ws, n)
+        torch.cuda.synchronize()
+        assert torch.all(ws[n:] == 0x5A) and torch.all(o[elems:] == 5.0) and not torch.any(o[:elems] == 5.0)
+
+
+def test_inside_a_launch_chain():
+    dev = require_gpu()
+    p = Problem(dev, [400, 60], 1, 8, 2, 128, 64, seed=14).upload()
+    want = p.decode(hla.HLA_F32)
+    o = torch.zeros_like(want)
+    ws = torch.empty(hla.attn_paged_decode_workspace_size(p.C, 2, 1, 8), dtype=torch.uint8, device=dev)
+    torch.cuda.synchronize()
+    hla.hla_chain_begin()
+    try:
+        for _ in range(4):
+            p.decode(hla.HLA_F32, ws=ws, o=o)
+    finally:
+        hla.hla_chain_end()
+    assert torch.equal(o, want)
