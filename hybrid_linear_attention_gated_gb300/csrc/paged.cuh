@@ -79,8 +79,10 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
                  : "memory");
 }
 
-__device__ __forceinline__ void ldmatrix_x2_trans(uint32_t &a, uint32_t &b, uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
+// A 16x16 matrix of bytes, transposed: lane l (0-15) gives the address of row l; lane (i, j) = (l / 4, l % 4) gets rows
+// 4 j .. 4 j + 3 of column i in a and of column i + 8 in b.
+__device__ __forceinline__ void ldmatrix_trans8(uint32_t &a, uint32_t &b, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x1.trans.shared.b8 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
 }
 
 // D(16x8 fp32) += A(16x16 fp16, row) * B(16x8 fp16, col)
@@ -98,12 +100,19 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
+// 16 bytes from global into shared memory through L2
+__device__ __forceinline__ void cp_async16_s(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Byte offset of 16-byte chunk c of row r in rows of RB bytes (64, 128 or 256), the chunks of a row permuted so
-// that the eight rows an ldmatrix reads at one chunk index fall into different banks.
+// that eight rows read at one chunk index fall into different banks, both rows 0-7 (or 8-15) of a group and the
+// rows 0, 1, 8, 9, 2, 3, 10, 11 (4, 5, 12, 13, ...) that an 8-bit transposed read takes together.
 template <int RB>
 __device__ __forceinline__ uint32_t swizzled(int r, int c) {
     constexpr int CPR = RB / 16;
-    const int x = CPR >= 8 ? (r & 7) : ((r >> 1) & (CPR - 1));
+    const int y = r ^ ((r >> 1) & 4);
+    const int x = CPR >= 8 ? (y & 7) : ((y >> 1) & (CPR - 1));
     return (uint32_t)(r * RB + ((c ^ x) << 4));
 }
 
