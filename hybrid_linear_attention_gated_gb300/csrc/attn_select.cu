@@ -6,20 +6,26 @@
 // exactly: two blocks at the border may differ by less than fp32 sums hold.
 //
 // attn_score_kernel computes all scores on mma.sync (bf16 products are exact in fp32; the sums are not) and is
-// bound by reading the bounds, 4 d bytes per block.  attn_choose_kernel then needs only fp32's word on most
-// blocks: with e a bound on the error of any score and t the n-th highest fp32 score, blocks above t + 2 e are
-// in and blocks below t - 2 e are out; the few between are scored again in fp64 and ranked.
+// bound by reading the bounds, 4 d bytes per block: every warp streams an equal, contiguous share of all groups
+// of 16 blocks through its own ring of cp.async stages, whatever the lengths are.  attn_choose_kernel then needs
+// only fp32's word on most blocks: with e a bound on the error of any score and t the n-th highest fp32 score,
+// blocks above t + 2 e are in and blocks below t - 2 e are out; the few between are scored again exactly and
+// ranked.
 #include "paged.cuh"
 
 namespace hla {
 namespace {
 
-constexpr int kScoreBlocks = 64;      // blocks scored per CTA
+constexpr int kGroupBlocks = 16;      // blocks scored together by a warp
 constexpr int kScoreThreads = 128;
+constexpr int kScoreStages = 3;       // groups in flight or in use per warp
+constexpr int kScoreCtas = 2;         // CTAs per SM
 constexpr int kChooseThreads = 256;
 constexpr int kMaxBlocks = 65536;     // blocks per sequence (a bit each in shared memory)
 constexpr int kStaged = 6144;         // scores of a row kept in shared memory; longer rows are read through L2
 constexpr int kListed = 1024;         // blocks near the border kept in shared memory
+constexpr int kBins = 1024;           // of a row's scores, to find the n-th highest
+constexpr int kFewInBin = 64;         // a bin with no more scores is not split again
 
 struct SelectParams {
     const uint16_t *q, *k_min, *k_max;
@@ -27,11 +33,11 @@ struct SelectParams {
     int32_t *sel;
     float *score;                 // [B, T, Hkv, stride]
     unsigned long long *exact;    // [B, T, Hkv, stride]: fp64 scores of the blocks near the border, when too many to list
-    float *absmax;                // [B, Hkv, chunks]
+    float *absmax;                // [B, Hkv, groups]: largest magnitude among the bounds of each group of 16 blocks
     int B, T, H, Hkv, G, d;
     int max_blocks, n_pages, pshift;
     int n_select, n_first, n_last;
-    int stride, chunks;
+    int stride, groups;
 };
 
 // Blocks that token t of a sequence sees.
@@ -53,294 +59,432 @@ __device__ __forceinline__ uint32_t neg2(uint32_t x) {  // min(x, 0) of two bf16
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// Scores of 64 blocks of one (sequence, kv head) for all T x G queries.  Warp w scores blocks 16 w .. 16 w + 15;
-// the rows go in tiles of 16 that hold whole groups of G heads (or a part of one group, for G > 16).
+// Prefix sums of the sequences' groups per kv head into pre[0..B]; ends with a block barrier.
+__device__ __forceinline__ void group_prefix(const SelectParams &p, int *pre) {
+    const int lane = threadIdx.x;
+    if (lane < 32) {
+        int base = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            int x = b < p.B ? (visible_blocks(p, b, p.T - 1) + kGroupBlocks - 1) / kGroupBlocks : 0;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, m);
+                if (lane >= m) x += y;
+            }
+            if (b < p.B) pre[b + 1] = base + x;
+            base += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) pre[0] = 0;
+    }
+    __syncthreads();
+}
+
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads) attn_score_kernel(const SelectParams p) {
-    constexpr int RB = 2 * D, CPR = RB / 16, KS = D / 16;
-    __shared__ __align__(128) uint8_t s_max[kScoreBlocks * RB], s_min[kScoreBlocks * RB];
+__host__ __device__ constexpr int score_ring() {  // shared memory of one warp's stages
+    return kScoreStages * 2 * kGroupBlocks * 2 * D;
+}
+
+// Scores of groups of 16 blocks of one (sequence, kv head) for all T x G queries.  The rows go in tiles of 16
+// that hold whole groups of G heads (or a part of one, for G > 16).
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(const SelectParams p) {
+    constexpr int RB = 2 * D, CPR = RB / 16, KS = D / 16, GB = kGroupBlocks * RB, NS = kScoreStages;
+    constexpr unsigned ALL = 0xffffffffu;
+    extern __shared__ __align__(128) uint8_t smem[];
+    int *const s_pre = reinterpret_cast<int *>(smem + 4 * score_ring<D>());  // [B + 1]
     __shared__ float s_tile[4][16][17];
-    __shared__ uint32_t s_abs[4];
+    __shared__ unsigned s_has[4][NS];  // blocks of each staged group that have a page
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = lane >> 2, j = lane & 3;
     pdl_wait_trigger();
-    const int chunk = blockIdx.x, b = blockIdx.y / p.Hkv, hk = blockIdx.y % p.Hkv;
-    const int nb = visible_blocks(p, b, p.T - 1), j0 = chunk * kScoreBlocks + warp * 16;
-    if (chunk * kScoreBlocks >= nb) return;
+    group_prefix(p, s_pre);
+    const int total = s_pre[p.B] * p.Hkv, warps = gridDim.x * 4;
+    const int share = (total + warps - 1) / warps, w = blockIdx.x * 4 + warp;
+    const int begin = (long)share * w < total ? share * w : total, n = share < total - begin ? share : total - begin;
+    const uint32_t ring = smem_u32(smem) + warp * score_ring<D>();
 
-    // bounds of this warp's 16 blocks: lane l looks up block l, then rows are copied chunk by chunk
-    const int blk = j0 + (lane & 15);
-    int pg = blk < nb ? p.table[(size_t)b * p.max_blocks + blk] : -1;
-    if (pg >= p.n_pages) pg = -1;
-    const uint32_t bmax = smem_u32(s_max) + warp * 16 * RB, bmin = smem_u32(s_min) + warp * 16 * RB;
+    // place of group x of all: sequence, kv head, group of the sequence.  cur: where the copies are; use: the products
+    struct Place {
+        int b, hk, g, groups, nb;
+    };
+    auto place = [&](int x) {
+        int lo = 0, hi = p.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_pre[mid] * p.Hkv <= x) lo = mid;
+            else hi = mid;
+        }
+        Place a;
+        a.b = lo;
+        a.groups = s_pre[lo + 1] - s_pre[lo];
+        const int rem = x - s_pre[lo] * p.Hkv;
+        a.hk = rem / a.groups;
+        a.g = rem - a.hk * a.groups;
+        a.nb = visible_blocks(p, lo, p.T - 1);
+        return a;
+    };
+    auto page_of = [&](const Place &a) -> int {  // lane l: page of the group's block l (16 lanes)
+        const int blk = a.g * kGroupBlocks + (lane & 15);
+        const int pg = blk < a.nb ? p.table[(size_t)a.b * p.max_blocks + blk] : -1;
+        return pg < p.n_pages ? pg : -1;
+    };
+    // The place and pages of the group that is copied next are looked up one step ahead.
+    Place ahead = n > 0 ? place(begin) : Place{};
+    int pg = n > 0 ? page_of(ahead) : -1;
+    auto issue = [&](int x, int stage) {
+        const uint32_t bmax = ring + stage * 2 * GB, bmin = bmax + GB;
 #pragma unroll
-    for (int x = 0; x < 16 * CPR / 32; ++x) {
-        const int r = (x * 32 + lane) / CPR, c = (x * 32 + lane) % CPR;
-        const int rp = __shfl_sync(0xffffffffu, pg, r);
-        const size_t o = rp >= 0 ? ((size_t)rp * p.Hkv + hk) * D + c * 8 : 0;
-        cp_async16_or_zero(bmax + swizzled<RB>(r, c), p.k_max + o, rp >= 0);
-        cp_async16_or_zero(bmin + swizzled<RB>(r, c), p.k_min + o, rp >= 0);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncwarp();
-
-    // largest magnitude among the bounds, as the bits of a bf16 (a NaN's are the largest)
-    uint32_t big = 0;
+        for (int y = 0; y < GB / 512; ++y) {
+            const int r = (y * 32 + lane) / CPR, c = lane % CPR;
+            const int rp = __shfl_sync(ALL, pg, r);
+            const size_t o = rp >= 0 ? ((size_t)rp * p.Hkv + ahead.hk) * D + c * 8 : 0;
+            const uint32_t at = swizzled<RB>(r, c);
+            cp_async16_or_zero(bmax + at, p.k_max + o, rp >= 0);
+            cp_async16_or_zero(bmin + at, p.k_min + o, rp >= 0);
+        }
+        const unsigned has = __ballot_sync(ALL, pg >= 0);
+        if (lane == 0) s_has[warp][stage] = has;
+        if (x + 1 < n) {
+            if (ahead.g + 1 < ahead.groups) ++ahead.g;
+            else ahead = place(begin + x + 1);
+            pg = page_of(ahead);
+        }
+    };
 #pragma unroll
-    for (int x = 0; x < 16 * CPR / 32; ++x) {
-        const uint4 u = reinterpret_cast<const uint4 *>(s_max + warp * 16 * RB)[x * 32 + lane],
-                    w = reinterpret_cast<const uint4 *>(s_min + warp * 16 * RB)[x * 32 + lane];
-        big = __vmaxu2(big, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
-        big = __vmaxu2(big, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-    }
-    big = big >> 16 > (big & 0xffffu) ? big >> 16 : big & 0xffffu;
-    big = __reduce_max_sync(0xffffffffu, big);
-    if (lane == 0) s_abs[warp] = big;
-    __syncthreads();
-    if (tid == 0) {
-        uint32_t m = s_abs[0];
-        for (int w = 1; w < 4; ++w) m = s_abs[w] > m ? s_abs[w] : m;
-        p.absmax[((size_t)b * p.Hkv + hk) * p.chunks + chunk] = bf16_bits_to_float((uint16_t)m);
+    for (int x = 0; x < NS - 1; ++x) {
+        if (x < n) issue(x, x);
+        cp_async_commit();
     }
 
     const int per = p.G <= 16 ? 16 / p.G : 1;     // tokens per row tile
     const int parts = (p.G + 15) / 16;            // row tiles per token
-    for (int t0 = 0; t0 < p.T; t0 += per) {
-        float best = 0.f;                         // of (token t0 + y / 16, block y % 16) for outputs y of this lane
-        float keep[8];
+    const bool one_tile = parts == 1 && per >= p.T;
+    Place use = n > 0 ? place(begin) : Place{};
+    bool fresh = true;                            // the query fragments are not this unit's
+    uint32_t qf[KS][4];
+    // fragments of the row tile of tokens t0.. and part `part` of the heads
+    auto load_q = [&](int t0, int part) {
 #pragma unroll
-        for (int y = 0; y < 8; ++y) keep[y] = -INFINITY;
-        for (int part = 0; part < parts; ++part) {
-            float s[2][4] = {};
-            const uint16_t *src[2];
-            bool on[2];
-#pragma unroll
-            for (int hrow = 0; hrow < 2; ++hrow) {
-                const int r = i + 8 * hrow;
-                const int t = t0 + (parts == 1 ? r / p.G : 0), g = parts == 1 ? r % p.G : part * 16 + r;
-                on[hrow] = t < p.T && g < p.G && (parts > 1 || r < per * p.G);
-                src[hrow] = p.q + (on[hrow] ? ((size_t)(b * p.T + t) * p.H + hk * p.G + g) * D : 0);
-            }
+        for (int hrow = 0; hrow < 2; ++hrow) {
+            const int r = i + 8 * hrow;
+            const int t = t0 + (parts == 1 ? r / p.G : 0), g = parts == 1 ? r % p.G : part * 16 + r;
+            const bool on = t < p.T && g < p.G && (parts > 1 || r < per * p.G);
+            const uint16_t *src = p.q + (on ? ((size_t)(use.b * p.T + t) * p.H + use.hk * p.G + g) * D : 0);
 #pragma unroll
             for (int c = 0; c < KS; ++c) {
-                uint32_t a[4], f[4], g[4];
+                qf[c][hrow] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * c + 2 * j) : 0u;
+                qf[c][2 + hrow] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * c + 8 + 2 * j) : 0u;
+            }
+        }
+    };
+    for (int x = 0, stage = 0, next = NS - 1; x < n; ++x) {
+        cp_async_wait<NS - 2>();
+        __syncwarp();
+        if (x + NS - 1 < n) issue(x + NS - 1, next);
+        cp_async_commit();
+        const uint32_t bmax = ring + stage * 2 * GB, bmin = bmax + GB;
+        const int j0 = use.g * kGroupBlocks;
+        const unsigned has = s_has[warp][stage];
+
+        // largest magnitude among the bounds, as the bits of a bf16 (a NaN's are the largest)
+        uint32_t big = 0;
 #pragma unroll
-                for (int hrow = 0; hrow < 2; ++hrow) {
-                    a[hrow] = on[hrow] ? *reinterpret_cast<const uint32_t *>(src[hrow] + 16 * c + 2 * j) : 0u;
-                    a[2 + hrow] = on[hrow] ? *reinterpret_cast<const uint32_t *>(src[hrow] + 16 * c + 8 + 2 * j) : 0u;
+        for (int y = 0; y < 2 * GB / 512; ++y) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(smem + (bmax - smem_u32(smem)) + (y * 32 + lane) * 16);
+            big = __vmaxu2(big, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+        }
+        big = __reduce_max_sync(ALL, big >> 16 > (big & 0xffffu) ? big >> 16 : big & 0xffffu);
+        if (lane == 0) p.absmax[((size_t)use.b * p.Hkv + use.hk) * p.groups + use.g] = bf16_bits_to_float((uint16_t)big);
+
+        for (int t0 = 0; t0 < p.T; t0 += per) {
+            float keep[8];                        // of (token t0 + y / 16, block y % 16) for outputs y of this lane
+#pragma unroll
+            for (int y = 0; y < 8; ++y) keep[y] = -INFINITY;
+            for (int part = 0; part < parts; ++part) {
+                if (fresh || !one_tile) load_q(t0, part);
+                fresh = false;
+                float s[2][4] = {};
+#pragma unroll
+                for (int c = 0; c < KS; ++c) {
+                    uint32_t f[4], g[4];
+                    const uint32_t at = swizzled<RB>((lane & 7) + ((lane >> 4) << 3), 2 * c + ((lane >> 3) & 1));
+                    ldmatrix_x4(f, bmax + at);
+                    ldmatrix_x4(g, bmin + at);
+                    const uint32_t up[4] = {relu2(qf[c][0]), relu2(qf[c][1]), relu2(qf[c][2]), relu2(qf[c][3])};
+                    const uint32_t dn[4] = {neg2(qf[c][0]), neg2(qf[c][1]), neg2(qf[c][2]), neg2(qf[c][3])};
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        mma_bf16_16816(s[y], up[0], up[1], up[2], up[3], f[2 * y], f[2 * y + 1]);
+                        mma_bf16_16816(s[y], dn[0], dn[1], dn[2], dn[3], g[2 * y], g[2 * y + 1]);
+                    }
                 }
-                const uint32_t at = swizzled<RB>((lane & 7) + ((lane >> 4) << 3), 2 * c + ((lane >> 3) & 1));
-                ldmatrix_x4(f, bmax + at);
-                ldmatrix_x4(g, bmin + at);
+                __syncwarp();
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    mma_bf16_16816(s[x], relu2(a[0]), relu2(a[1]), relu2(a[2]), relu2(a[3]), f[2 * x], f[2 * x + 1]);
-                    mma_bf16_16816(s[x], neg2(a[0]), neg2(a[1]), neg2(a[2]), neg2(a[3]), g[2 * x], g[2 * x + 1]);
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s_tile[warp][i + 8 * (e >> 1)][8 * y + 2 * j + (e & 1)] = s[y][e];
+                __syncwarp();
+                // maximum over the heads (a NaN stays)
+                const int rows = parts == 1 ? p.G : (p.G - part * 16 < 16 ? p.G - part * 16 : 16);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const int o = y * 32 + lane, tl = o >> 4, bl = o & 15;
+                    if (tl >= per || t0 + tl >= p.T) break;
+                    for (int g = 0; g < rows; ++g) {
+                        const float v = s_tile[warp][(parts == 1 ? tl * p.G : 0) + g][bl];
+                        keep[y] = v > keep[y] || v != v ? v : keep[y];
+                    }
                 }
             }
-            __syncwarp();
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s_tile[warp][i + 8 * (e >> 1)][8 * x + 2 * j + (e & 1)] = s[x][e];
-            __syncwarp();
-            // maximum over the heads (a NaN stays)
-            const int rows = parts == 1 ? p.G : (p.G - part * 16 < 16 ? p.G - part * 16 : 16);
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
-                const int o = y * 32 + lane, tl = o >> 4, bl = o & 15;
-                if (tl >= per) break;
-                best = keep[y];
-                for (int g = 0; g < rows; ++g) {
-                    const float v = s_tile[warp][(parts == 1 ? tl * p.G : 0) + g][bl];
-                    best = v > best || v != v ? v : best;
-                }
-                keep[y] = best;
+                const int o = y * 32 + lane, tl = o >> 4, bl = o & 15, t = t0 + tl;
+                if (tl < per && t < p.T && j0 + bl < use.nb)
+                    p.score[((size_t)(use.b * p.T + t) * p.Hkv + use.hk) * p.stride + j0 + bl] = has >> bl & 1 ? keep[y] : -INFINITY;
             }
         }
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-            const int o = y * 32 + lane, tl = o >> 4, bl = o & 15, t = t0 + tl;
-            const bool has = __shfl_sync(0xffffffffu, pg, bl) >= 0;
-            if (tl < per && t < p.T && j0 + bl < nb)
-                p.score[((size_t)(b * p.T + t) * p.Hkv + hk) * p.stride + j0 + bl] = has ? keep[y] : -INFINITY;
+        if (use.g + 1 < use.groups) {
+            ++use.g;
+        } else if (x + 1 < n) {
+            use = place(begin + x + 1);
+            fresh = true;
         }
+        stage = stage + 1 == NS ? 0 : stage + 1;
+        next = next + 1 == NS ? 0 : next + 1;
     }
 }
 
 // Unsigned integers in the order of the values (-0 and +0 alike, NaN above all; never 0).
-__device__ __forceinline__ uint32_t ordered(float x) {
-    if (x != x) return 0xffffffffu;
-    const uint32_t u = __float_as_uint(x + 0.f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ float unordered(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-}
 __device__ __forceinline__ unsigned long long ordered(double x) {
     if (x != x) return ~0ull;
     const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
     return u >> 63 ? ~u : u | 1ull << 63;
 }
+__device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }  // a NaN stays
+
+constexpr int kWarps = kChooseThreads / 32;
 
 __device__ __forceinline__ int block_sum(int x, int *s_red) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     x = __reduce_add_sync(0xffffffffu, x);
     __syncthreads();
-    if (lane == 0) s_red[warp] = x;
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = x;
     __syncthreads();
     int all = 0;
 #pragma unroll
-    for (int w = 0; w < kChooseThreads / 32; ++w) all += s_red[w];
+    for (int w = 0; w < kWarps; ++w) all += s_red[w];
     return all;
 }
-
-// One CTA per (sequence, token, kv head).
+// One CTA per (sequence, token, kv head).  The steps are short and latency-bound (about 3 us for 2048 blocks): few
+// barriers, and loops kept rolled, since code that runs once is fetched once.
+template <int D>
 __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const SelectParams p) {
     __shared__ float s_score[kStaged];
     __shared__ uint32_t s_bits[kMaxBlocks / 32];       // the choice
     __shared__ unsigned long long s_key[kListed];
     __shared__ int s_blk[kListed];
-    __shared__ int s_red[kChooseThreads / 32];
-    __shared__ uint32_t s_lo, s_hi;
-    __shared__ float s_f[2][kChooseThreads / 32];
-    __shared__ int s_n;
+    __shared__ int s_red[kWarps];
+    __shared__ float s_f[4][kWarps];
+    __shared__ int s_near, s_sure, s_bin, s_count;
+    int *const s_hist = reinterpret_cast<int *>(s_key);  // [kBins], before the keys
+    static_assert(kBins * sizeof(int) <= sizeof(s_key) && kBins == 4 * kChooseThreads, "four bins per thread");
+    constexpr int CPL = D / 32;                          // channels per lane
+    constexpr unsigned ALL = 0xffffffffu;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int NW = kChooseThreads / 32;
-    pdl_wait_trigger();
     const int row = blockIdx.x, hk = row % p.Hkv, t = row / p.Hkv % p.T, b = row / p.Hkv / p.T;
     int32_t *sel = p.sel + (size_t)row * p.n_select;
+
+    // what the score kernel does not write, before waiting for it: lengths and the query's size
     const int nb = visible_blocks(p, b, t);
-    if (nb <= p.n_select) {
+    const int words = (nb + 31) >> 5;
+    const bool choose = nb > p.n_select;
+    // the first and last blocks are in; k of those between, [e0, e1), are to be chosen
+    const int e0 = p.n_first, e1 = nb - p.n_last, k = p.n_select - p.n_first - p.n_last;
+    const uint16_t *qrow = p.q + ((size_t)(b * p.T + t) * p.H + hk * p.G) * D + lane * CPL;
+    const int32_t *table = p.table + (size_t)b * p.max_blocks;
+    // this lane's channels of a row of D bf16
+    auto channels = [](const uint16_t *at, float (&f)[CPL]) {
+#pragma unroll
+        for (int c = 0; c < CPL; c += 2) {
+            const uint32_t u = *reinterpret_cast<const uint32_t *>(at + c);
+            f[c] = bf16_lo(u);
+            f[c + 1] = bf16_hi(u);
+        }
+    };
+    float absq = 0.f, absb = 0.f;
+    if (choose) {
+#pragma unroll 1
+        for (int g = warp; g < p.G; g += kWarps) {
+            float f[CPL], a = 0.f;
+            channels(qrow + (size_t)g * D, f);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) a += fabsf(f[c]);
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) a += __shfl_xor_sync(ALL, a, m);
+            absq = max_nan(a, absq);
+        }
+        for (int x = tid; x < words; x += kChooseThreads) {  // bits e0.. e1 - 1 open, the others in
+            const int f = e0 - 32 * x, l = e1 - 32 * x, last = nb - 32 * x;
+            auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ALL : (1u << n) - 1u; };
+            s_bits[x] = below(f) | (below(last) & ~below(l));
+        }
+        for (int x = tid; x < kBins; x += kChooseThreads) s_hist[x] = 0;
+        if (tid == 0) s_near = s_sure = 0;
+    }
+    pdl_wait_trigger();
+    if (!choose) {
         for (int x = tid; x < p.n_select; x += kChooseThreads) sel[x] = x < nb ? x : -1;
         return;
     }
-    // the first and last blocks are in; k of those between, [e0, e1), are to be chosen
-    const int e0 = p.n_first, e1 = nb - p.n_last, k = p.n_select - p.n_first - p.n_last;
-    const int words = (nb + 31) >> 5;
+
+    // the scores; a block without a page below every other, but finite
     const float *row_score = p.score + (size_t)row * p.stride;
     const bool staged = nb <= kStaged;
-    uint32_t lo = ~0u, hi = 0;
+    float lo = INFINITY, hi = -INFINITY;
     for (int x = tid; x < nb; x += kChooseThreads) {
-        const float v = row_score[x];
+        const float v = fmaxf(row_score[x], -3e38f);
         if (staged) s_score[x] = v;
         if (x >= e0 && x < e1) {
-            const uint32_t o = ordered(v);
-            lo = o < lo ? o : lo;
-            hi = o > hi ? o : hi;
+            lo = fminf(lo, v);
+            hi = fmaxf(hi, v);
         }
     }
-    for (int x = tid; x < words; x += kChooseThreads) {
-        uint32_t m = 0;
-        for (int y = 0; y < 32; ++y)
-            if (32 * x + y < e0 || (32 * x + y >= e1 && 32 * x + y < nb)) m |= 1u << y;
-        s_bits[x] = m;
-    }
-    const float *src = staged ? s_score : row_score;
-
-    // bound on any score's error: 2^-14 sum |q| max |bound|.  A score is a chain of 2 d / 16 products of 16 terms; a
-    // sum of 17 values that keeps 23 bits of the largest errs by at most 17 2^-23 of it, 2 d / 16 <= 16 times over.
-    float absq = 0.f, absb = 0.f;
-    const uint16_t *qrow = p.q + ((size_t)(b * p.T + t) * p.H + hk * p.G) * p.d;
-    for (int g = warp; g < p.G; g += NW) {
-        float a = 0.f;
-        for (int c = lane; c < p.d; c += 32) a += fabsf(bf16_bits_to_float(qrow[g * p.d + c]));
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
-        absq = a > absq || a != a ? a : absq;
-    }
-    const int chunks = (visible_blocks(p, b, p.T - 1) + kScoreBlocks - 1) / kScoreBlocks;
-    for (int c = tid; c < chunks; c += kChooseThreads) {
-        const float a = p.absmax[((size_t)b * p.Hkv + hk) * p.chunks + c];
-        absb = a > absb || a != a ? a : absb;
-    }
+    const int groups = (visible_blocks(p, b, p.T - 1) + kGroupBlocks - 1) / kGroupBlocks;
+    for (int c = tid; c < groups; c += kChooseThreads) absb = max_nan(p.absmax[((size_t)b * p.Hkv + hk) * p.groups + c], absb);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
-        const float a = __shfl_xor_sync(0xffffffffu, absb, m);
-        absb = a > absb || a != a ? a : absb;
+        absb = max_nan(__shfl_xor_sync(ALL, absb, m), absb);
+        lo = fminf(lo, __shfl_xor_sync(ALL, lo, m));
+        hi = fmaxf(hi, __shfl_xor_sync(ALL, hi, m));
     }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (tid == 0) {
-        s_lo = ~0u;
-        s_hi = 0;
-        s_n = 0;
-    }
-    __syncthreads();
     if (lane == 0) {
         s_f[0][warp] = absq;
         s_f[1][warp] = absb;
-        atomicMin(&s_lo, lo);
-        atomicMax(&s_hi, hi);
+        s_f[2][warp] = lo;
+        s_f[3][warp] = hi;
     }
     __syncthreads();
-    for (int w = 0; w < NW; ++w) {
-        absq = s_f[0][w] > absq || s_f[0][w] != s_f[0][w] ? s_f[0][w] : absq;
-        absb = s_f[1][w] > absb || s_f[1][w] != s_f[1][w] ? s_f[1][w] : absb;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        absq = max_nan(s_f[0][w], absq);
+        absb = max_nan(s_f[1][w], absb);
+        lo = fminf(lo, s_f[2][w]);
+        hi = fmaxf(hi, s_f[3][w]);
     }
-    const float size = absq * absb, err = size * 6.103515625e-05f;
-    lo = s_lo;
-    hi = s_hi;
+    auto score = [&](int x) -> float { return staged ? s_score[x] : fmaxf(row_score[x], -3e38f); };
 
-    // [low, high]: the band in which fp32 does not decide.  Infinities, NaN and sums near fp32's range decide nothing.
+    // Bound on any score's error: 2^-14 sum |q| max |bound|.  A score is a chain of 2 d / 16 products of 16 terms; a
+    // sum of 17 values that keeps 23 bits of the largest errs by at most 17 2^-23 of it, 2 d / 16 <= 16 times over.
+    const float size = absq * absb, err = size * 6.103515625e-05f;
+
+    // [low, high]: the band in which fp32 does not decide.  The k-th highest score is in the bin of scores in which the
+    // count from above reaches k; a bin with many scores is split again until it is as narrow as the error.
+    // Infinities, NaN and sums near the ends of fp32's range decide nothing.
     float low = -INFINITY, high = INFINITY;
-    const bool usable = size < 1e37f;
+    const bool usable = size > 1e-20f && size < 1e37f;
     if (k > 0 && usable) {
-        // lo <= t < hi: halve until the ends are equal or closer than the error
-        if (hi != ~0u) ++hi;
-        while (hi - lo > 1 && unordered(hi) - unordered(lo) > err) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            int n = 0;
-            for (int x = e0 + tid; x < e1; x += kChooseThreads) n += ordered(src[x]) >= mid;
-            if (block_sum(n, s_red) >= k) lo = mid;
-            else hi = mid;
+        int need = k;  // rank wanted among the scores in [lo, hi]
+        while (hi - lo > err) {
+            // (infinite for a range of zero to fp32: then NaN and infinity all go to the last bin)
+            const float inv = (kBins - 1) / (hi - lo);
+            for (int x = e0 + tid; x < e1; x += kChooseThreads) {
+                const float v = score(x);
+                if (v >= lo && v <= hi) atomicAdd(&s_hist[(int)fminf((v - lo) * inv, kBins - 1)], 1);
+            }
+            __syncthreads();
+            // counts from the highest bin down: thread tid has bins kBins - 4 - 4 tid .. kBins - 1 - 4 tid
+            const int4 c = reinterpret_cast<const int4 *>(s_hist)[kBins / 4 - 1 - tid];
+            const int sum = c.x + c.y + c.z + c.w;
+            int before = sum;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int y = __shfl_up_sync(ALL, before, m);
+                if (lane >= m) before += y;
+            }
+            if (lane == 31) s_red[warp] = before;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) before += w < warp ? s_red[w] : 0;
+            before -= sum;
+            if (before < need && need <= before + sum) {  // one thread's
+                int at = kBins - 1 - 4 * tid, n = c.w;
+                if (need > before + n) { before += n; --at; n = c.z; }
+                if (need > before + n) { before += n; --at; n = c.y; }
+                if (need > before + n) { before += n; --at; n = c.x; }
+                s_bin = at;
+                s_count = n;
+            }
+            reinterpret_cast<int4 *>(s_hist)[kBins / 4 - 1 - tid] = make_int4(0, 0, 0, 0);
+            __syncthreads();
+            // The bin's ends, wider by more than the rounding of a bin number, 1024 2^-22.  (That of lo itself, 2^-23 of
+            // a score, is far below the error.)
+            const float l = fmaxf(lo, lo + (s_bin - 0.01f) / inv), h = fminf(hi, lo + (s_bin + 1.01f) / inv);
+            if (!(l > lo || h < hi)) break;
+            lo = l;
+            hi = h;
+            if (s_count <= kFewInBin) break;
+            int above = 0;  // (the widened end may take in scores of the bin above)
+            for (int x = e0 + tid; x < e1; x += kChooseThreads) above += score(x) > hi;
+            need = k - block_sum(above, s_red);
         }
-        low = unordered(lo) - 2.f * err;
-        high = unordered(hi) + 2.f * err;
+        low = lo - 2.f * err;
+        high = hi + 2.f * err;
     }
-    __syncthreads();
-    int sure = 0, near = 0;
+    auto in_band = [&](float v) -> bool { return !usable || (v >= low && v <= high); };
     if (k > 0) {
+        int sure = 0;
         for (int x = e0 + tid; x < e1; x += kChooseThreads) {
-            const float v = src[x];
-            if (usable && v > high) {
+            const float v = score(x);
+            if (in_band(v)) {
+                const int at = atomicAdd(&s_near, 1);  // any order: they are ranked by score and index below
+                if (at < kListed) s_blk[at] = x;
+            } else if (v > high) {
                 ++sure;
                 atomicOr(&s_bits[x >> 5], 1u << (x & 31));
-            } else if (!usable || v >= low) {
-                ++near;
-                const int at = atomicAdd(&s_n, 1);  // any order: they are ranked by score and index below
-                if (at < kListed) s_blk[at] = x;
             }
         }
+        sure = __reduce_add_sync(ALL, sure);
+        if (lane == 0 && sure) atomicAdd(&s_sure, sure);
     }
-    sure = block_sum(sure, s_red);
-    near = block_sum(near, s_red);
-    const int want = k - sure;
+    __syncthreads();
+    const int near = s_near, want = k - s_sure;
     if (want > 0 && near > want) {
-        // fp64 scores of the blocks in the band, a warp each
-        auto score64 = [&](int x) -> unsigned long long {
-            int pg = p.table[(size_t)b * p.max_blocks + x];
-            if (pg < 0 || pg >= p.n_pages) return ordered(-INFINITY + 0.0);
-            const uint16_t *bx = p.k_max + ((size_t)pg * p.Hkv + hk) * p.d, *bn = p.k_min + ((size_t)pg * p.Hkv + hk) * p.d;
-            unsigned long long best = 0;
-            for (int g = 0; g < p.G; ++g) {
-                double s = 0.0;
-                for (int ch = lane; ch < p.d; ch += 32) {
-                    const float qv = bf16_bits_to_float(qrow[g * p.d + ch]);
-                    const float up = qv > 0.f || qv != qv ? qv : 0.f, dn = qv < 0.f || qv != qv ? qv : 0.f;
-                    s += (double)up * (double)bf16_bits_to_float(bx[ch]) + (double)dn * (double)bf16_bits_to_float(bn[ch]);
-                }
+        // Exact scores of the blocks in the band as integers in their order, a warp to a (block, head).  A product of two
+        // bf16 is exact in fp32 and, times a power of two that holds the sum below 2^62, in 64-bit fixed point down to
+        // 2^-37 of the largest: integer sums, so equal scores are equal whatever the order.  Where the size is out of
+        // fp32's comfort (infinities and NaN too) the sum is fp64's.
+        const int shift = usable ? 61 - ilogbf(size) : 0;  // 2^shift size < 2^62
+        const float s1 = exp2f((float)(shift / 2)), s2 = exp2f((float)(shift - shift / 2));
+        auto exact = [&](int x, int g) -> unsigned long long {
+            const int pg = table[x];
+            if (pg < 0 || pg >= p.n_pages) return 1;
+            float q[CPL], up[CPL], dn[CPL];
+            channels(qrow + (size_t)g * D, q);
+            channels(p.k_max + ((size_t)pg * p.Hkv + hk) * D + lane * CPL, up);
+            channels(p.k_min + ((size_t)pg * p.Hkv + hk) * D + lane * CPL, dn);
+            if (usable) {
+                long long s = 0;
 #pragma unroll
-                for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-                const unsigned long long o = ordered(s);
-                best = o > best ? o : best;
+                for (int c = 0; c < CPL; ++c)
+                    s += __float2ll_rn(__fmul_rn(__fmul_rn(__fmul_rn(q[c], q[c] > 0.f ? up[c] : dn[c]), s1), s2));
+#pragma unroll
+                for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(ALL, s, m);
+                return (unsigned long long)s ^ 1ull << 63;
             }
-            return best;
+            double s = 0.0;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c)
+                s += (double)(q[c] < 0.f ? 0.f : q[c]) * (double)up[c] + (double)(q[c] > 0.f ? 0.f : q[c]) * (double)dn[c];
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(ALL, s, m);
+            return ordered(s);
         };
         if (near <= kListed) {  // ranked one against another
-            for (int c = warp; c < near; c += NW) {
-                const unsigned long long o = score64(s_blk[c]);
-                if (lane == 0) s_key[c] = o;
+            for (int c = tid; c < near; c += kChooseThreads) s_key[c] = 0;
+            __syncthreads();
+#pragma unroll 1
+            for (int c = warp; c < near * p.G; c += kWarps) {
+                const unsigned long long o = exact(s_blk[c / p.G], c % p.G);
+                if (lane == 0) atomicMax(&s_key[c / p.G], o);
             }
             __syncthreads();
             for (int c = tid; c < near; c += kChooseThreads) {
@@ -352,10 +496,16 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
             }
         } else {  // many equals (keys never written, say): by block in the workspace, 0 for those outside the band
             unsigned long long *key = p.exact + (size_t)row * p.stride;
-            for (int x = e0 + warp; x < e1; x += NW) {
-                const bool in = !usable || (src[x] >= low && !(src[x] > high));
-                const unsigned long long o = in ? score64(x) : 0;
-                if (lane == 0) key[x] = o;
+#pragma unroll 1
+            for (int x = e0 + warp; x < e1; x += kWarps) {
+                unsigned long long best = 0;
+                if (in_band(score(x)))
+#pragma unroll 1
+                    for (int g = 0; g < p.G; ++g) {
+                        const unsigned long long o = exact(x, g);
+                        best = o > best ? o : best;
+                    }
+                if (lane == 0) key[x] = best;
             }
             __syncthreads();
             // the want-th highest key: the largest klo with count(key >= klo) >= want
@@ -389,27 +539,29 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
         }
     } else if (want > 0) {  // the whole band
         for (int x = e0 + tid; x < e1; x += kChooseThreads)
-            if (!usable || (src[x] >= low && !(src[x] > high))) atomicOr(&s_bits[x >> 5], 1u << (x & 31));
+            if (in_band(score(x))) atomicOr(&s_bits[x >> 5], 1u << (x & 31));
     }
     __syncthreads();
 
     // the chosen indexes in ascending order
     int base = 0;
+#pragma unroll 1
     for (int w0 = 0; w0 < words; w0 += kChooseThreads) {
         const uint32_t m = w0 + tid < words ? s_bits[w0 + tid] : 0u;
         int n = __popc(m);
         const int mine = n;
 #pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, n, s);
-            if (lane >= s) n += y;
+        for (int y = 1; y < 32; y <<= 1) {
+            const int z = __shfl_up_sync(ALL, n, y);
+            if (lane >= y) n += z;
         }
-        __syncthreads();
+        if (w0) __syncthreads();
         if (lane == 31) s_red[warp] = n;
         __syncthreads();
         int at = base + n - mine;
-        for (int w = 0; w < NW; ++w) {
-            if (w < warp) at += s_red[w];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            at += w < warp ? s_red[w] : 0;
             base += s_red[w];
         }
         for (uint32_t x = m; x; x &= x - 1) {
@@ -419,13 +571,32 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
     }
 }
 
+template <int D>
+cudaError_t launch_score(const SelectParams &p, cudaStream_t st) {
+    constexpr size_t ring = 4 * (size_t)score_ring<D>();
+    // the shared-memory limit is a per-device attribute: raise it once on every device used
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !done[dev]) {
+        e = cudaFuncSetAttribute(attn_score_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(ring + (kMaxBatch + 1) * sizeof(int)));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) done[dev] = true;
+    }
+    const long most = ((long)p.B * p.Hkv * p.groups + 3) / 4;  // a group per warp
+    const int slots = kScoreCtas * sm_count();
+    return launch_kernel(attn_score_kernel<D>, dim3((unsigned)(most < slots ? most : slots)), dim3(kScoreThreads),
+                         ring + (p.B + 1) * sizeof(int), st, p);
+}
+
 size_t row_stride(int max_blocks) { return round_up((size_t)max_blocks, 4); }
 
 size_t select_ws(const hla_kv_cache *C, int B, int T, int H, int max_blocks) {
     if (check_cache(C, false, false) != HLA_OK || check_window(C, B, T, H, max_blocks) != HLA_OK || max_blocks > kMaxBlocks)
         return 0;
-    const size_t rows = (size_t)B * T * C->kv_heads, chunks = (max_blocks + kScoreBlocks - 1) / kScoreBlocks;
-    return rows * row_stride(max_blocks) * (sizeof(unsigned long long) + sizeof(float)) + round_up((size_t)B * C->kv_heads * chunks * sizeof(float), 16);
+    const size_t rows = (size_t)B * T * C->kv_heads, groups = (max_blocks + kGroupBlocks - 1) / kGroupBlocks;
+    return rows * row_stride(max_blocks) * (sizeof(unsigned long long) + sizeof(float)) + round_up((size_t)B * C->kv_heads * groups * sizeof(float), 16);
 }
 
 }  // namespace
@@ -447,7 +618,8 @@ extern "C" int attn_select_blocks(const hla_kv_cache *C, int B, int T, int H, in
     HLA_REQUIRE(max_blocks <= kMaxBlocks, HLA_ERR_UNSUPPORTED);
     HLA_REQUIRE(block_table && past_len && q && sel, HLA_ERR_INVALID_ARG);
     HLA_REQUIRE(n_select >= 1 && n_first >= 0 && n_last >= 0 && n_first <= n_select && n_last <= n_select - n_first, HLA_ERR_INVALID_ARG);
-    HLA_REQUIRE((long)B * C->kv_heads <= 65535, HLA_ERR_UNSUPPORTED);
+    // rows and groups are counted in 32 bits
+    HLA_REQUIRE((long)B * T * C->kv_heads < (1L << 31) && (long)B * C->kv_heads * ((max_blocks + kGroupBlocks - 1) / kGroupBlocks) < (1L << 31), HLA_ERR_UNSUPPORTED);
     HLA_REQUIRE(aligned16(block_table) && aligned16(past_len) && aligned16(q) && aligned16(sel), HLA_ERR_MISALIGNED);
     HLA_REQUIRE(ws && ws_bytes >= select_ws(C, B, T, H, max_blocks), HLA_ERR_WORKSPACE);
     HLA_REQUIRE(aligned16(ws), HLA_ERR_MISALIGNED);
@@ -457,17 +629,17 @@ extern "C" int attn_select_blocks(const hla_kv_cache *C, int B, int T, int H, in
     p.max_blocks = max_blocks; p.n_pages = C->n_pages; p.pshift = page_shift(C->page_size);
     p.n_select = n_select; p.n_first = n_first; p.n_last = n_last;
     p.stride = (int)row_stride(max_blocks);
-    p.chunks = (max_blocks + kScoreBlocks - 1) / kScoreBlocks;
+    p.groups = (max_blocks + kGroupBlocks - 1) / kGroupBlocks;
     const size_t rows = (size_t)B * T * p.Hkv;
     p.exact = static_cast<unsigned long long *>(ws);
     p.score = reinterpret_cast<float *>(p.exact + rows * p.stride);
     p.absmax = p.score + rows * p.stride;
     const cudaStream_t st = (cudaStream_t)stream;
     set_variant("attn_select<d%d>", p.d);
-    PdlChain chain(st, pdl_default(B * T));
-    const dim3 grid((unsigned)p.chunks, (unsigned)(B * p.Hkv));
-    e = launched(p.d == 128 ? launch_kernel(attn_score_kernel<128>, grid, dim3(kScoreThreads), 0, st, p)
-                            : launch_kernel(attn_score_kernel<64>, grid, dim3(kScoreThreads), 0, st, p));
+    // the choice always follows the scores programmatically (HLA_PDL=0 turns that off as everywhere)
+    PdlChain chain(st, pdl_default(1));
+    e = launched(p.d == 128 ? launch_score<128>(p, st) : launch_score<64>(p, st));
     if (e != HLA_OK) return e;
-    return launched(launch_kernel(attn_choose_kernel, dim3((unsigned)rows), dim3(kChooseThreads), 0, st, p));
+    return launched(p.d == 128 ? launch_kernel(attn_choose_kernel<128>, dim3((unsigned)rows), dim3(kChooseThreads), 0, st, p)
+                               : launch_kernel(attn_choose_kernel<64>, dim3((unsigned)rows), dim3(kChooseThreads), 0, st, p));
 }

@@ -131,7 +131,8 @@ def _p(t):
 def _stream(s):
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a Stream object around it (0.1 us instead of 2.9)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -295,17 +296,21 @@ def hla_decode_layer_routing(L, M, ws):
     return a.value, b.value
 
 
-def _tensors(fn, args):
-    """Refuse torch tensors that a kernel would misread: (name, tensor, dtype, least number of elements)."""
+def _device():
+    """The current CUDA device, or -2 (no tensor's) before CUDA is in use."""
     import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for name, t, dtype, n in args:
-        if t is None or isinstance(t, int):
-            continue
-        if t.dtype is not dtype or t.numel() < n or t.get_device() != dev or not t.is_contiguous():
-            raise HlaError(fn, HLA_ERR_INVALID_ARG,
-                           f"{name} must be a contiguous {dtype} tensor of at least {n} elements on the current "
-                           f"device (cuda:{dev}); got {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}, {t.device}")
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _tensor(fn, name, t, dtype, n, dev):
+    """The address of a torch tensor that a kernel may read as n values of dtype (others are refused), or t itself."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+        raise HlaError(fn, HLA_ERR_INVALID_ARG,
+                       f"{name} must be a contiguous {dtype} tensor of at least {n} elements on the current device; "
+                       f"got {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}, {t.device}")
+    return t.data_ptr()
 
 
 def make_kv_cache(dtype, n_pages, page_size, kv_heads, head_dim, k, v, k_scale=None, v_scale=None, k_min=None,
@@ -313,29 +318,29 @@ def make_kv_cache(dtype, n_pages, page_size, kv_heads, head_dim, k, v, k_scale=N
     """Build an hla_kv_cache descriptor; it keeps the tensors it was given alive."""
     import torch
     C = hla_kv_cache(dtype, n_pages, page_size, kv_heads, head_dim)
-    if min(n_pages, page_size, kv_heads, head_dim) >= 1:
-        kv = torch.float8_e4m3fn if dtype == HLA_E4M3 else torch.bfloat16
-        n, m = n_pages * kv_heads * page_size * head_dim, n_pages * kv_heads * head_dim
-        _tensors("make_kv_cache", [("k", k, kv, n), ("v", v, kv, n), ("k_scale", k_scale, torch.float32, kv_heads),
-                                   ("v_scale", v_scale, torch.float32, kv_heads), ("k_min", k_min, torch.bfloat16, m),
-                                   ("k_max", k_max, torch.bfloat16, m)])
-    C.tensors = dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale, k_min=k_min, k_max=k_max)
-    for name, t in C.tensors.items():
-        setattr(C, name, _p(t))
+    kv = torch.float8_e4m3fn if dtype == HLA_E4M3 else torch.bfloat16
+    n, m = n_pages * kv_heads * page_size * head_dim, n_pages * kv_heads * head_dim
+    dev = _device()
+    C.tensors = (k, v, k_scale, v_scale, k_min, k_max)
+    for name, t, dt, least in (("k", k, kv, n), ("v", v, kv, n), ("k_scale", k_scale, torch.float32, kv_heads),
+                               ("v_scale", v_scale, torch.float32, kv_heads), ("k_min", k_min, torch.bfloat16, m),
+                               ("k_max", k_max, torch.bfloat16, m)):
+        setattr(C, name, _tensor("make_kv_cache", name, t, dt, least, dev))
     return C
 
 
 def kv_cache_append(C, N, B, cu_seqlens, past_len, max_blocks, block_table, H, q, k, v, rope_dim,
                     rope_interleaved, inv_freq, q_out, stream=None):
     import torch
-    bf, i32, d, hk = torch.bfloat16, torch.int32, C.head_dim, C.kv_heads
-    _tensors("kv_cache_append", [
-        ("cu_seqlens", cu_seqlens, i32, B + 1), ("past_len", past_len, i32, B),
-        ("block_table", block_table, i32, B * max_blocks), ("q", q, bf, N * H * d), ("k", k, bf, N * hk * d),
-        ("v", v, bf, N * hk * d), ("inv_freq", inv_freq, torch.float64, rope_dim // 2), ("q_out", q_out, bf, N * H * d)])
-    return _check("kv_cache_append", load().kv_cache_append(
-        ctypes.byref(C), N, B, _p(cu_seqlens), _p(past_len), max_blocks, _p(block_table), H, _p(q), _p(k), _p(v),
-        rope_dim, rope_interleaved, _p(inv_freq), _p(q_out), _stream(stream)))
+    fn, bf, i32, dev = "kv_cache_append", torch.bfloat16, torch.int32, _device()
+    nq, nk = N * H * C.head_dim, N * C.kv_heads * C.head_dim
+    return _check(fn, load().kv_cache_append(
+        ctypes.byref(C), N, B, _tensor(fn, "cu_seqlens", cu_seqlens, i32, B + 1, dev),
+        _tensor(fn, "past_len", past_len, i32, B, dev), max_blocks,
+        _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev), H, _tensor(fn, "q", q, bf, nq, dev),
+        _tensor(fn, "k", k, bf, nk, dev), _tensor(fn, "v", v, bf, nk, dev), rope_dim, rope_interleaved,
+        _tensor(fn, "inv_freq", inv_freq, torch.float64, rope_dim // 2, dev), _tensor(fn, "q_out", q_out, bf, nq, dev),
+        _stream(stream)))
 
 
 def attn_paged_decode_workspace_size(C, B, T, H):
@@ -345,14 +350,12 @@ def attn_paged_decode_workspace_size(C, B, T, H):
 def attn_paged_decode(C, B, T, H, max_blocks, block_table, past_len, scale, q, o, o_dtype, ws, ws_bytes,
                       stream=None):
     import torch
-    n = B * T * H * C.head_dim
-    _tensors("attn_paged_decode", [
-        ("block_table", block_table, torch.int32, B * max_blocks), ("past_len", past_len, torch.int32, B),
-        ("q", q, torch.bfloat16, n), ("o", o, torch.bfloat16 if o_dtype == HLA_BF16 else torch.float32, n),
-        ("ws", ws, torch.uint8, ws_bytes)])
-    return _check("attn_paged_decode", load().attn_paged_decode(
-        ctypes.byref(C), B, T, H, max_blocks, _p(block_table), _p(past_len), scale, _p(q), _p(o), o_dtype, _p(ws),
-        ws_bytes, _stream(stream)))
+    fn, i32, dev, n = "attn_paged_decode", torch.int32, _device(), B * T * H * C.head_dim
+    return _check(fn, load().attn_paged_decode(
+        ctypes.byref(C), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
+        _tensor(fn, "past_len", past_len, i32, B, dev), scale, _tensor(fn, "q", q, torch.bfloat16, n, dev),
+        _tensor(fn, "o", o, torch.bfloat16 if o_dtype == HLA_BF16 else torch.float32, n, dev), o_dtype,
+        _tensor(fn, "ws", ws, torch.uint8, ws_bytes, dev), ws_bytes, _stream(stream)))
 
 
 def attn_select_blocks_workspace_size(C, B, T, H, max_blocks):
@@ -362,13 +365,13 @@ def attn_select_blocks_workspace_size(C, B, T, H, max_blocks):
 def attn_select_blocks(C, B, T, H, max_blocks, block_table, past_len, n_select, n_first, n_last, q, sel, ws,
                        ws_bytes, stream=None):
     import torch
-    _tensors("attn_select_blocks", [
-        ("block_table", block_table, torch.int32, B * max_blocks), ("past_len", past_len, torch.int32, B),
-        ("q", q, torch.bfloat16, B * T * H * C.head_dim), ("sel", sel, torch.int32, B * T * C.kv_heads * n_select),
-        ("ws", ws, torch.uint8, ws_bytes)])
-    return _check("attn_select_blocks", load().attn_select_blocks(
-        ctypes.byref(C), B, T, H, max_blocks, _p(block_table), _p(past_len), n_select, n_first, n_last, _p(q), _p(sel),
-        _p(ws), ws_bytes, _stream(stream)))
+    fn, i32, dev = "attn_select_blocks", torch.int32, _device()
+    return _check(fn, load().attn_select_blocks(
+        ctypes.byref(C), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
+        _tensor(fn, "past_len", past_len, i32, B, dev), n_select, n_first, n_last,
+        _tensor(fn, "q", q, torch.bfloat16, B * T * H * C.head_dim, dev),
+        _tensor(fn, "sel", sel, i32, B * T * C.kv_heads * n_select, dev),
+        _tensor(fn, "ws", ws, torch.uint8, ws_bytes, dev), ws_bytes, _stream(stream)))
 
 
 def attn_paged_sparse_workspace_size(C, B, T, H):
@@ -378,14 +381,14 @@ def attn_paged_sparse_workspace_size(C, B, T, H):
 def attn_paged_sparse(C, B, T, H, max_blocks, block_table, past_len, n_select, sel, scale, q, o, o_dtype, ws,
                       ws_bytes, stream=None):
     import torch
-    n = B * T * H * C.head_dim
-    _tensors("attn_paged_sparse", [
-        ("block_table", block_table, torch.int32, B * max_blocks), ("past_len", past_len, torch.int32, B),
-        ("sel", sel, torch.int32, B * T * C.kv_heads * n_select), ("q", q, torch.bfloat16, n),
-        ("o", o, torch.bfloat16 if o_dtype == HLA_BF16 else torch.float32, n), ("ws", ws, torch.uint8, ws_bytes)])
-    return _check("attn_paged_sparse", load().attn_paged_sparse(
-        ctypes.byref(C), B, T, H, max_blocks, _p(block_table), _p(past_len), n_select, _p(sel), scale, _p(q), _p(o),
-        o_dtype, _p(ws), ws_bytes, _stream(stream)))
+    fn, i32, dev, n = "attn_paged_sparse", torch.int32, _device(), B * T * H * C.head_dim
+    return _check(fn, load().attn_paged_sparse(
+        ctypes.byref(C), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
+        _tensor(fn, "past_len", past_len, i32, B, dev), n_select,
+        _tensor(fn, "sel", sel, i32, B * T * C.kv_heads * n_select, dev), scale,
+        _tensor(fn, "q", q, torch.bfloat16, n, dev),
+        _tensor(fn, "o", o, torch.bfloat16 if o_dtype == HLA_BF16 else torch.float32, n, dev), o_dtype,
+        _tensor(fn, "ws", ws, torch.uint8, ws_bytes, dev), ws_bytes, _stream(stream)))
 
 
 def hla_launch_count():

@@ -443,11 +443,11 @@ int attn_paged_decode(const hla_kv_cache *C, int B, int T, int H, int max_blocks
  *  Of the visible blocks j = 0 .. (past_len[b] + t) / page_size the first n_first and the last n_last are
  *  taken, and of the others those with the highest
  *    max over the kv head's query heads h of  sum_d max(q[b,t,h,d], 0) k_max[j,d] + min(q[b,t,h,d], 0) k_min[j,d],
- *  n_select in all (every visible one when there are no more).  The order is that of exact arithmetic up to
- *  fp64 rounding; equal scores go to the lower block, a NaN score is above all others, a block without a page
- *  scores -infinity.
+ *  n_select in all (every visible one when there are no more).  Scores are compared exactly, down to 2^-60 of
+ *  sum |q| x max |bound|; equal ones go to the lower block, a NaN score is above all others, a block without a
+ *  page scores -infinity.
  *  sel int32 [B, T, kv_heads, n_select]: the chosen blocks, ascending, then -1.  The cache's k and v are not
- *  used.  max_blocks <= 65536; n_first + n_last <= n_select; B * kv_heads <= 65535.
+ *  used.  max_blocks <= 65536; n_first + n_last <= n_select.
  * -------------------------------------------------------------------------*/
 size_t attn_select_blocks_workspace_size(const hla_kv_cache *C, int B, int T, int H, int max_blocks);
 int attn_select_blocks(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const int32_t *block_table,

@@ -94,7 +94,7 @@ def test_own_arguments_are_checked(lib):
                dict(n_first=2 ** 31 - 1, n_last=2 ** 31 - 1)):
         assert select(lib, C, **kw) == INVALID, kw
     assert select(lib, C, max_blocks=65537) == UNSUPPORTED
-    assert select(lib, cache(kv_heads=128), H=128, B=1024) == UNSUPPORTED
+    assert select(lib, cache(kv_heads=1024), H=1024, B=1024, max_blocks=65536) == UNSUPPORTED
     for kw in (dict(N=0), dict(B=0), dict(H=9), dict(cu=None), dict(out=None), dict(k=None), dict(v=None), dict(f=None), dict(rope=-16),
                dict(inter=2)):
         assert append(lib, C, **kw) == INVALID, kw
