@@ -18,8 +18,8 @@ namespace {
 
 constexpr int kGroupBlocks = 16;      // blocks scored together by a warp
 constexpr int kScoreThreads = 128;
-constexpr int kScoreStages = 3;       // groups in flight or in use per warp
-constexpr int kScoreCtas = 2;         // CTAs per SM
+constexpr int kScoreStages = 2;       // groups in flight or in use per warp
+constexpr int kScoreCtas = 3;         // CTAs per SM
 constexpr int kChooseThreads = 256;
 constexpr int kMaxBlocks = 65536;     // blocks per sequence (a bit each in shared memory)
 constexpr int kStaged = 6144;         // scores of a row kept in shared memory; longer rows are read through L2
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
         a.b = lo;
         a.groups = s_pre[lo + 1] - s_pre[lo];
         const int rem = x - s_pre[lo] * p.Hkv;
-        a.hk = rem / a.groups;
-        a.g = rem - a.hk * a.groups;
+        a.g = rem / p.Hkv;  // the heads of a group one after another: their bounds are neighbours in memory
+        a.hk = rem - a.g * p.Hkv;
         a.nb = visible_blocks(p, lo, p.T - 1);
         return a;
     };
@@ -144,9 +144,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
         }
         const unsigned has = __ballot_sync(ALL, pg >= 0);
         if (lane == 0) s_has[warp][stage] = has;
-        if (x + 1 < n) {
-            if (ahead.g + 1 < ahead.groups) ++ahead.g;
-            else ahead = place(begin + x + 1);
+        if (x + 1 < n && ++ahead.hk == p.Hkv) {
+            ahead.hk = 0;
+            if (++ahead.g == ahead.groups) ahead = place(begin + x + 1);
             pg = page_of(ahead);
         }
     };
@@ -160,7 +160,6 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
     const int parts = (p.G + 15) / 16;            // row tiles per token
     const bool one_tile = parts == 1 && per >= p.T;
     Place use = n > 0 ? place(begin) : Place{};
-    bool fresh = true;                            // the query fragments are not this unit's
     uint32_t qf[KS][4];
     // fragments of the row tile of tokens t0.. and part `part` of the heads
     auto load_q = [&](int t0, int part) {
@@ -177,6 +176,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
             }
         }
     };
+    if (one_tile && n > 0) load_q(0, 0);
     for (int x = 0, stage = 0, next = NS - 1; x < n; ++x) {
         cp_async_wait<NS - 2>();
         __syncwarp();
@@ -186,24 +186,15 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
         const int j0 = use.g * kGroupBlocks;
         const unsigned has = s_has[warp][stage];
 
-        // largest magnitude among the bounds, as the bits of a bf16 (a NaN's are the largest)
-        uint32_t big = 0;
-#pragma unroll
-        for (int y = 0; y < 2 * GB / 512; ++y) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(smem + (bmax - smem_u32(smem)) + (y * 32 + lane) * 16);
-            big = __vmaxu2(big, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
-        }
-        big = __reduce_max_sync(ALL, big >> 16 > (big & 0xffffu) ? big >> 16 : big & 0xffffu);
-        if (lane == 0) p.absmax[((size_t)use.b * p.Hkv + use.hk) * p.groups + use.g] = bf16_bits_to_float((uint16_t)big);
-
+        uint32_t big = 0;  // largest magnitude among the bounds, as the bits of a bf16 (a NaN's are the largest)
         for (int t0 = 0; t0 < p.T; t0 += per) {
             float keep[8];                        // of (token t0 + y / 16, block y % 16) for outputs y of this lane
 #pragma unroll
             for (int y = 0; y < 8; ++y) keep[y] = -INFINITY;
             for (int part = 0; part < parts; ++part) {
-                if (fresh || !one_tile) load_q(t0, part);
-                fresh = false;
-                float s[2][4] = {};
+                if (!one_tile) load_q(t0, part);
+                // four chains of sums per tile (even and odd steps of both halves): a chain's products wait for one another
+                float s[4][2][4] = {};
 #pragma unroll
                 for (int c = 0; c < KS; ++c) {
                     uint32_t f[4], g[4];
@@ -214,15 +205,18 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
                     const uint32_t dn[4] = {neg2(qf[c][0]), neg2(qf[c][1]), neg2(qf[c][2]), neg2(qf[c][3])};
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        mma_bf16_16816(s[y], up[0], up[1], up[2], up[3], f[2 * y], f[2 * y + 1]);
-                        mma_bf16_16816(s[y], dn[0], dn[1], dn[2], dn[3], g[2 * y], g[2 * y + 1]);
+                        mma_bf16_16816(s[2 * (c & 1)][y], up[0], up[1], up[2], up[3], f[2 * y], f[2 * y + 1]);
+                        mma_bf16_16816(s[2 * (c & 1) + 1][y], dn[0], dn[1], dn[2], dn[3], g[2 * y], g[2 * y + 1]);
                     }
+                    if (t0 == 0 && part == 0)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) big = __vmaxu2(big, __vmaxu2(f[y] & 0x7fff7fffu, g[y] & 0x7fff7fffu));
                 }
                 __syncwarp();
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s_tile[warp][i + 8 * (e >> 1)][8 * y + 2 * j + (e & 1)] = s[y][e];
+                    for (int e = 0; e < 4; ++e) s_tile[warp][i + 8 * (e >> 1)][8 * y + 2 * j + (e & 1)] = (s[0][y][e] + s[2][y][e]) + (s[1][y][e] + s[3][y][e]);
                 __syncwarp();
                 // maximum over the heads (a NaN stays)
                 const int rows = parts == 1 ? p.G : (p.G - part * 16 < 16 ? p.G - part * 16 : 16);
@@ -243,11 +237,14 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
                     p.score[((size_t)(use.b * p.T + t) * p.Hkv + use.hk) * p.stride + j0 + bl] = has >> bl & 1 ? keep[y] : -INFINITY;
             }
         }
-        if (use.g + 1 < use.groups) {
-            ++use.g;
-        } else if (x + 1 < n) {
-            use = place(begin + x + 1);
-            fresh = true;
+        big = __reduce_max_sync(ALL, big >> 16 > (big & 0xffffu) ? big >> 16 : big & 0xffffu);
+        if (lane == 0) p.absmax[((size_t)use.b * p.Hkv + use.hk) * p.groups + use.g] = bf16_bits_to_float((uint16_t)big);
+        if (x + 1 < n) {
+            if (++use.hk == p.Hkv) {
+                use.hk = 0;
+                if (++use.g == use.groups) use = place(begin + x + 1);
+            }
+            if (one_tile) load_q(0, 0);  // (on its way while the copies are waited for)
         }
         stage = stage + 1 == NS ? 0 : stage + 1;
         next = next + 1 == NS ? 0 : next + 1;
@@ -372,8 +369,8 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
     }
     auto score = [&](int x) -> float { return staged ? s_score[x] : fmaxf(row_score[x], -3e38f); };
 
-    // Bound on any score's error: 2^-14 sum |q| max |bound|.  A score is a chain of 2 d / 16 products of 16 terms; a
-    // sum of 17 values that keeps 23 bits of the largest errs by at most 17 2^-23 of it, 2 d / 16 <= 16 times over.
+    // Bound on any score's error: 2^-14 sum |q| max |bound|.  A score is 2 d / 16 products of 16 terms in four chains,
+    // added up; a sum of 17 values that keeps 23 bits of the largest errs by at most 17 2^-23 of it, 2 d / 16 <= 16 times over.
     const float size = absq * absb, err = size * 6.103515625e-05f;
 
     // [low, high]: the band in which fp32 does not decide.  The k-th highest score is in the bin of scores in which the
