@@ -336,6 +336,9 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
     // the scores; a block without a page below every other, but finite
     const float *row_score = p.score + (size_t)row * p.stride;
     const bool staged = nb <= kStaged;
+    const int groups = (visible_blocks(p, b, p.T - 1) + kGroupBlocks - 1) / kGroupBlocks;
+    const float *row_abs = p.absmax + ((size_t)b * p.Hkv + hk) * p.groups;
+    if (tid < groups) absb = row_abs[tid];  // in flight together with the scores
     float lo = INFINITY, hi = -INFINITY;
     for (int x = tid; x < nb; x += kChooseThreads) {
         const float v = fmaxf(row_score[x], -3e38f);
@@ -345,8 +348,7 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
             hi = fmaxf(hi, v);
         }
     }
-    const int groups = (visible_blocks(p, b, p.T - 1) + kGroupBlocks - 1) / kGroupBlocks;
-    for (int c = tid; c < groups; c += kChooseThreads) absb = max_nan(p.absmax[((size_t)b * p.Hkv + hk) * p.groups + c], absb);
+    for (int c = tid + kChooseThreads; c < groups; c += kChooseThreads) absb = max_nan(row_abs[c], absb);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
         absb = max_nan(__shfl_xor_sync(ALL, absb, m), absb);
