@@ -62,14 +62,17 @@ __device__ __forceinline__ int unit_tiles(const AttnParams &p, int past) {
     return (int)((len + p.tile - 1) / p.tile);
 }
 
-// Prefix sums of the sequences' tiles per unit into pre[0..B]; ends with a block barrier.
-__device__ __forceinline__ void tile_prefix(const AttnParams &p, int *pre) {
+// Prefix sums of the sequences' tiles per unit into pre[0..B], and their cached tokens into past[0..B-1] where
+// that is wanted; ends with a block barrier.
+__device__ __forceinline__ void tile_prefix(const AttnParams &p, int *pre, int *past = nullptr) {
     const int lane = threadIdx.x;
     if (lane < 32) {
         int base = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
-            int x = b < p.B ? unit_tiles(p, cached(p, b)) : 0;
+            const int c = b < p.B ? cached(p, b) : -1;
+            int x = unit_tiles(p, c);
+            if (past && b < p.B) past[b] = c;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, m);
@@ -115,7 +118,7 @@ __host__ __device__ constexpr int warp_keys() {
 // CTAs per SM, which bounds the registers per thread, and stages of the copy ring.
 template <int D, bool FP8>
 __host__ __device__ constexpr int ctas_per_sm() {
-    return D == 128 && !FP8 ? 2 : (D == 64 && FP8 ? 4 : 3);
+    return D == 128 ? 2 : (FP8 ? 4 : 3);
 }
 template <int D, bool FP8>
 __host__ __device__ constexpr int ring_stages() {
@@ -180,12 +183,11 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
     constexpr int REGION = warp_region<D, FP8>(), STAGE = 2 * KG * GB;
     constexpr int M = 16 * WR, WK = 4 / WR;
     constexpr int KS = D / 16, NT = D / 8;
-    constexpr int PITCH = D + 8;              // fp32 row pitch of the merge buffer
     constexpr uint32_t ONES = FP8 ? 0x3c003c00u : 0x3f803f80u;
     constexpr unsigned ALL = 0xffffffffu;
-    static_assert(NS >= 2 && 16 * PITCH * 4 <= REGION, "a warp merges its rows in its own stages");
+    static_assert(NS >= 2 && 16 * D * 4 <= STAGE, "a warp's part of a stage holds its 16 rows in fp32");
     extern __shared__ __align__(128) uint8_t smem[];
-    int *const s_pre = reinterpret_cast<int *>(smem + 4 * REGION);  // [B + 1]
+    int *const s_pre = reinterpret_cast<int *>(smem + 4 * REGION), *const s_past = s_pre + p.B + 1;  // [B + 1], [B]
     __shared__ int s_tok[4][NS][KG];          // first token of each staged group
     __shared__ float s_m[4][16], s_l[4][16];
 
@@ -193,133 +195,164 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
     const int j = lane & 3, i = lane >> 2;    // fragment column pair and row
     const int wr = warp % WR, kp = warp / WR; // 16 rows and share of the keys
     pdl_wait_trigger();
-    tile_prefix(p, s_pre);
+    tile_prefix(p, s_pre, s_past);
     const int total = s_pre[p.B] * p.units_per_b;
     const int share = cta_share(p, total, gridDim.x);
-    int at = (long)share * blockIdx.x < total ? share * (int)blockIdx.x : total;
-    const int end = share < total - at ? at + share : total;
+    const int begin = (long)share * blockIdx.x < total ? share * (int)blockIdx.x : total;
+    const int N = share < total - begin ? share : total - begin;  // this CTA's tiles
+    if (N == 0) return;
     const uint32_t ring = smem_u32(smem);
+    const int rows = p.sel ? p.G : p.T * p.G;
+
+    // The piece of a unit that tile t of all belongs to: the unit, and which of its nt tiles t is.
+    struct Unit {
+        int b, tq, hk, rt, nt, k;  // tq: the window token of the sparse form
+    };
+    auto unit_of = [&](int t) {
+        Unit u;
+        u.b = find_sequence(s_pre, p.B, p.units_per_b, t);
+        u.nt = s_pre[u.b + 1] - s_pre[u.b];
+        const int rem = t - s_pre[u.b] * p.units_per_b;
+        int x = rem / u.nt;
+        u.k = rem - x * u.nt;
+        u.rt = x % p.row_tiles;
+        x /= p.row_tiles;
+        u.hk = x % p.Hkv;
+        u.tq = x / p.Hkv;
+        return u;
+    };
+    // row r of a unit: token t, head h of q and o
+    auto row_at = [&](const Unit &u, int r) -> size_t {
+        const int t = p.sel ? u.tq : r / p.G, g = p.sel ? r : r % p.G;
+        return ((size_t)(u.b * p.T + t) * p.H + u.hk * p.G + g) * D;
+    };
+
+    // ---- copies.  They run through the CTA's tiles without regard to units.  The groups that this warp copies are
+    // numbered; lane l looks up group l of each 32, one batch ahead: where its 16 rows are (in units of 16 rows; -1:
+    // no keys), its first token, and how many of its rows hold a key for any row of the unit.
+    auto look = [&](int g0, int *at, int *tok, int *on) {
+        const int g = g0 + lane;
+        *at = -1;
+        *tok = kNoKeys;
+        *on = 0;
+        if (g >= N * KG) return;
+        const Unit u = unit_of(begin + g / KG);
+        const int key = u.k * TILE + warp * KW + g % KG * kGroup;
+        int blk = key >> p.pshift;
+        if (p.sel) blk = blk < p.n_select ? p.sel[((size_t)(u.b * p.T + u.tq) * p.Hkv + u.hk) * p.n_select + blk] : -1;
+        if (blk < 0 || blk >= p.max_blocks) return;
+        const int page = p.table[(size_t)u.b * p.max_blocks + blk];
+        if (page < 0 || page >= p.n_pages) return;
+        const int row = key & ((1 << p.pshift) - 1), t = (blk << p.pshift) + row;
+        const int seen = s_past[u.b] + (p.sel ? u.tq : p.T - 1) - t + 1;
+        *tok = t;
+        *on = seen < 0 ? 0 : seen < kGroup ? seen : kGroup;
+        if (*on) *at = ((page * p.Hkv + u.hk) << (p.pshift - 4)) + (row >> 4);
+    };
+    int at_now, tok_now, on_now, at_next, tok_next, on_next;
+    look(0, &at_now, &tok_now, &on_now);
+    look(32, &at_next, &tok_next, &on_next);
     // where this lane's 16-byte chunks of a group go: chunk x * 32 + lane
     uint32_t to[GB / 512];
 #pragma unroll
     for (int x = 0; x < GB / 512; ++x)
         to[x] = ring + warp * REGION + swizzled<RB>((x * 32 + lane) / CPR, lane % CPR);
-
-    while (at < end) {
-        // ---- the piece of a unit that this CTA runs: tiles [k0, k1) of nt
-        const int b = find_sequence(s_pre, p.B, p.units_per_b, at);
-        const int nt = s_pre[b + 1] - s_pre[b];
-        const int rem = at - s_pre[b] * p.units_per_b;
-        int u = rem / nt;
-        const int k0 = rem - u * nt;
-        const int k1 = nt - k0 < end - at ? nt : k0 + (end - at);
-        at += k1 - k0;
-        const int rt = u % p.row_tiles;
-        u /= p.row_tiles;
-        const int hk = u % p.Hkv;
-        const int tq = u / p.Hkv;             // sparse form: the window token
-        const int past = cached(p, b);
-        const int rows = p.sel ? p.G : p.T * p.G;
-        // last visible token of any row of the unit, and of the row with the fewest
-        const int lim_hi = p.sel ? past + tq : past + p.T - 1, lim_lo = p.sel ? past + tq : past;
-        const int32_t *list = p.sel ? p.sel + ((size_t)(b * p.T + tq) * p.Hkv + hk) * p.n_select : nullptr;
-        const int32_t *table = p.table + (size_t)b * p.max_blocks;
-
-        // row r of the unit: token t, head h of q and o
-        auto row_at = [&](int r) -> size_t {
-            const int t = p.sel ? tq : r / p.G, g = p.sel ? r : r % p.G;
-            return ((size_t)(b * p.T + t) * p.H + hk * p.G + g) * D;
-        };
-
-        // ---- copies.  Groups of this warp are numbered through the piece; lane l looks up group l of each 32.
-        const int n = k1 - k0;
-        auto look = [&](int g0, int *tok, int *pg) {
-            const int g = g0 + lane;
-            *tok = kNoKeys;
-            *pg = -1;
-            if (g >= n * KG) return;
-            const int key = (k0 + g / KG) * TILE + warp * KW + g % KG * kGroup;
-            int blk = key >> p.pshift;
-            if (p.sel) blk = blk < p.n_select ? list[blk] : -1;
-            if (blk < 0 || blk >= p.max_blocks) return;
-            const int page = table[blk];
-            if (page < 0 || page >= p.n_pages) return;
-            *pg = page;
-            *tok = (blk << p.pshift) + (key & ((1 << p.pshift) - 1));
-        };
-        int tok_now, pg_now, tok_next, pg_next;
-        look(0, &tok_now, &pg_now);
-        look(32, &tok_next, &pg_next);
-        auto issue = [&](int ti, int stage) {
+    auto issue = [&](int ti, int stage) {
 #pragma unroll
-            for (int g = 0; g < KG; ++g) {
-                const int src = (ti * KG + g) & 31;
-                const int tok = __shfl_sync(ALL, tok_now, src), pg = __shfl_sync(ALL, pg_now, src);
-                const uint32_t off = stage * STAGE + g * 2 * GB;
-                const size_t from = ((((size_t)(pg < 0 ? 0 : pg) * p.Hkv + hk) << p.pshift) + (tok & ((1 << p.pshift) - 1))) * RB + lane * 16;
-                if (tok + kGroup - 1 <= lim_hi) {
-                    const uint8_t *k = p.k + from, *v = p.v + from;
+        for (int g = 0; g < KG; ++g) {
+            const int src = (ti * KG + g) & 31;
+            const int from16 = __shfl_sync(ALL, at_now, src), on = __shfl_sync(ALL, on_now, src), tok = __shfl_sync(ALL, tok_now, src);
+            const uint32_t off = stage * STAGE + g * 2 * GB;
+            const size_t from = (size_t)(from16 < 0 ? 0 : from16) * GB + lane * 16;
+            const uint8_t *k = p.k + from, *v = p.v + from;
+            if (on == kGroup) {
 #pragma unroll
-                    for (int x = 0; x < GB / 512; ++x) {
-                        cp_async16_s(to[x] + off, k + x * 512);
-                        cp_async16_s(to[x] + off + GB, v + x * 512);
-                    }
-                } else {  // rows without a key are zero: a weight of zero must not meet what the page holds there
-                    const int on = tok > lim_hi ? 0 : lim_hi - tok + 1;
-#pragma unroll
-                    for (int x = 0; x < GB / 512; ++x) {
-                        const bool in = (x * 32 + lane) / CPR < on;
-                        const size_t f = in ? from + x * 512 : 0;
-                        cp_async16_or_zero(to[x] + off, p.k + f, in);
-                        cp_async16_or_zero(to[x] + off + GB, p.v + f, in);
-                    }
+                for (int x = 0; x < GB / 512; ++x) {
+                    cp_async16_s(to[x] + off, k + x * 512);
+                    cp_async16_s(to[x] + off + GB, v + x * 512);
                 }
-                if (lane == 0) s_tok[warp][stage][g] = tok;
-            }
-            if (((ti + 1) * KG & 31) == 0) {
-                tok_now = tok_next;
-                pg_now = pg_next;
-                look((ti + 1) * KG + 32, &tok_next, &pg_next);
-            }
-        };
+            } else {  // rows without a key are zero: a weight of zero must not meet what the page holds there
 #pragma unroll
-        for (int st = 0; st < NS - 1; ++st) {
-            if (st < n) issue(st, st);
-            cp_async_commit();
+                for (int x = 0; x < GB / 512; ++x) {
+                    const bool in = (x * 32 + lane) / CPR < on;
+                    cp_async16_or_zero(to[x] + off, in ? k + x * 512 : p.k, in);
+                    cp_async16_or_zero(to[x] + off + GB, in ? v + x * 512 : p.v, in);
+                }
+            }
+            if (lane == 0) s_tok[warp][stage][g] = tok;
         }
+        if (((ti + 1) * KG & 31) == 0) {
+            at_now = at_next;
+            tok_now = tok_next;
+            on_now = on_next;
+            look((ti + 1) * KG + 32, &at_next, &tok_next, &on_next);
+        }
+    };
 
-        // ---- query fragments.  bf16: element pairs (8 c + 2 j) of chunk c.  e4m3 keys come out of ldmatrix
-        // four bytes to a lane, so lane j takes elements 16 c + 4 j .. + 3 of k-step c, and the rows go to
-        // fp16 scaled by a power of two that puts their largest element in [2^14, 2^15): exact down to 2^-28
-        // of it; the factor comes back in the row's score scale.  Score scales are positive (a negative one is
-        // taken into the query), so that the running maximum is that of the unscaled products.
-        uint32_t qf[KS][4];
+    // ---- query rows as they are in memory.  bf16: element pairs (8 c + 2 j) of chunk c.  e4m3 keys come out of ldmatrix
+    // four bytes to a lane, so lane j takes elements 16 c + 4 j .. + 3 of k-step c.
+    uint32_t qf[KS][4];
+    auto load_q = [&](const Unit &u) {
+#pragma unroll
+        for (int hrow = 0; hrow < 2; ++hrow) {
+            const int r = u.rt * M + 16 * wr + 8 * hrow + i;
+            const bool on = r < rows;
+            const uint16_t *src = p.q + (on ? row_at(u, r) : 0);
+#pragma unroll
+            for (int c = 0; c < KS; ++c) {
+                if constexpr (!FP8) {
+                    qf[c][hrow] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * c + 2 * j) : 0u;
+                    qf[c][2 + hrow] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * c + 8 + 2 * j) : 0u;
+                } else {
+                    const uint2 w = on ? *reinterpret_cast<const uint2 *>(src + 16 * c + 4 * j) : make_uint2(0u, 0u);
+                    qf[c][hrow] = w.x;
+                    qf[c][2 + hrow] = w.y;
+                }
+            }
+        }
+    };
+
+    Unit u = unit_of(begin);
+    load_q(u);  // ahead of the copies in the memory system's queues
+#pragma unroll
+    for (int st = 0; st < NS - 1; ++st) {
+        if (st < N) issue(st, st);
+        cp_async_commit();
+    }
+
+    int stage = 0, ahead = NS - 1;
+    for (int done = 0; done < N;) {
+        // ---- the piece of a unit that this CTA runs: tiles [k0, k1) of nt
+        const int nt = u.nt, k0 = u.k, k1 = nt - k0 < N - done ? nt : k0 + (N - done), first = done;
+        done += k1 - k0;
+        const int rt = u.rt, hk = u.hk;
+        const int past = s_past[u.b];
+        // last visible token of any row of the unit, and of the row with the fewest
+        const int lim_hi = p.sel ? past + u.tq : past + p.T - 1, lim_lo = p.sel ? past + u.tq : past;
+
+        // ---- query fragments.  Score scales are positive (a negative one is taken into the query), so that the running
+        // maximum is that of the unscaled products.  With an 8-bit cache the rows go to fp16, scaled by a power of two
+        // that puts their largest element in [2^14, 2^15): exact down to 2^-28 of it; the factor comes back in the row's
+        // score scale.
         float sc[2];
         int lim[2];
         const float scale = p.scale * (FP8 ? p.k_scale[hk] : 1.f) * kLog2e;
 #pragma unroll
         for (int hrow = 0; hrow < 2; ++hrow) {
             const int r = rt * M + 16 * wr + 8 * hrow + i;
-            const bool on = r < rows;
-            const uint16_t *src = p.q + (on ? row_at(r) : 0);
-            lim[hrow] = !on ? -1 : (p.sel ? past + tq : past + r / p.G);
+            lim[hrow] = r >= rows ? -1 : (p.sel ? past + u.tq : past + r / p.G);
             sc[hrow] = fmaxf(fabsf(scale), 1e-37f);  // above zero, so that -infinity stays itself
             if constexpr (!FP8) {
                 const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
                 for (int c = 0; c < KS; ++c) {
-                    qf[c][hrow] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * c + 2 * j) ^ flip : 0u;
-                    qf[c][2 + hrow] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * c + 8 + 2 * j) ^ flip : 0u;
+                    qf[c][hrow] ^= flip;
+                    qf[c][2 + hrow] ^= flip;
                 }
             } else {
-                uint32_t raw[KS][2], big = 0;
+                uint32_t big = 0;
 #pragma unroll
-                for (int c = 0; c < KS; ++c) {
-                    const uint2 w = on ? *reinterpret_cast<const uint2 *>(src + 16 * c + 4 * j) : make_uint2(0u, 0u);
-                    raw[c][0] = w.x;
-                    raw[c][1] = w.y;
-                    big = __vmaxu2(big, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
-                }
+                for (int c = 0; c < KS; ++c) big = __vmaxu2(big, __vmaxu2(qf[c][hrow] & 0x7fff7fffu, qf[c][2 + hrow] & 0x7fff7fffu));
                 big = big >> 16 > (big & 0xffffu) ? big >> 16 : big & 0xffffu;
 #pragma unroll
                 for (int x = 1; x < 4; x <<= 1) {
@@ -335,9 +368,9 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
 #pragma unroll
                 for (int c = 0; c < KS; ++c)
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const __half2 h = __floats2half2_rn(bf16_lo(raw[c][z]) * up, bf16_hi(raw[c][z]) * up);
-                        qf[c][2 * z + hrow] = *reinterpret_cast<const uint32_t *>(&h);
+                    for (int z = 0; z < 4; z += 2) {
+                        const __half2 h = __floats2half2_rn(bf16_lo(qf[c][z + hrow]) * up, bf16_hi(qf[c][z + hrow]) * up);
+                        qf[c][z + hrow] = *reinterpret_cast<const uint32_t *>(&h);
                     }
             }
         }
@@ -348,12 +381,13 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
 #pragma unroll
         for (int t = 0; t <= NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
 
-        for (int it = 0, stage = 0, ahead = NS - 1; it < n; ++it) {
+        int last = 0;  // stage of the piece's last tile
+        for (int it = first; it < done; ++it) {
             cp_async_wait<NS - 2>();
             if (WR == 1) __syncwarp();
             else if (WR == 2) asm volatile("bar.sync %0, 64;" ::"r"(1 + kp) : "memory");
             else __syncthreads();
-            if (it + NS - 1 < n) issue(it + NS - 1, ahead);
+            if (it + NS - 1 < N) issue(it + NS - 1, ahead);
             cp_async_commit();
 
 #pragma unroll 1
@@ -497,19 +531,27 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
                     }
                 }
             }
+            last = stage;
             stage = stage + 1 == NS ? 0 : stage + 1;
             ahead = ahead + 1 == NS ? 0 : ahead + 1;
         }
-        cp_async_wait<0>();
+        const Unit now = u;
+        if (done < N) {  // the next unit's rows are on their way while this one is written out
+            u = unit_of(begin + done);
+            load_q(u);
+        }
 
-        // ---- the warps' parts together, and out: the unit whole, or a piece for the join.  Slot 2 c + 1 of CTA c
-        // holds a piece that begins its unit, slot 2 c any other.
+        // ---- the warps' parts together, each warp's in its part of the stage just read (the other stages are being filled
+        // for the next unit), and out: the unit whole, or a piece for the join.  Slot 2 c + 1 of CTA c holds a piece that
+        // begins its unit, slot 2 c any other.
         const bool whole = k0 == 0 && k1 == nt;
         const size_t slot = 2 * (size_t)blockIdx.x + (k0 == 0);
         const float vscale = FP8 ? p.v_scale[hk] : 1.f;
         if (WR == 1) __syncwarp();
         else __syncthreads();  // other warps read this warp's stages
-        float *buf = reinterpret_cast<float *>(smem + warp * REGION);
+        // 8-byte pairs of a row, permuted so that the eight rows of a store fall into different banks
+        auto pair_at = [](int r, int c) -> int { return r * D + 2 * (c ^ 4 * (r & 7)); };
+        float *const buf = reinterpret_cast<float *>(smem + warp * REGION + last * STAGE);
 #pragma unroll
         for (int hrow = 0; hrow < 2; ++hrow) {
             const int r = 8 * hrow + i;
@@ -521,7 +563,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-                *reinterpret_cast<float2 *>(buf + r * PITCH + 8 * t + 2 * j) = make_float2(acc[t][2 * hrow], acc[t][2 * hrow + 1]);
+                *reinterpret_cast<float2 *>(buf + pair_at(r, 4 * t + j)) = make_float2(acc[t][2 * hrow], acc[t][2 * hrow + 1]);
         }
         __syncthreads();
         for (int y = tid; y < M * (D / 4); y += kAttnThreads) {
@@ -536,13 +578,13 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
                 const int w = x * WR + (r >> 4);
                 if (s_m[w][rr] == -INFINITY) continue;
                 const float a = s_m[w][rr] == top && top != INFINITY ? 1.f : ex2(s_m[w][rr] - top);
-                const float4 f = *reinterpret_cast<const float4 *>(smem + w * REGION + (rr * PITCH + c) * 4);
+                const float4 f = *reinterpret_cast<const float4 *>(smem + w * REGION + last * STAGE + 4 * pair_at(rr, c / 2));
                 o.x += a * f.x; o.y += a * f.y; o.z += a * f.z; o.w += a * f.w;
                 ls += a * s_l[w][rr];
             }
             if (whole) {
                 const float inv = top == -INFINITY ? 0.f : vscale / ls;
-                const size_t dst = row_at(rt * M + r) + c;
+                const size_t dst = row_at(now, rt * M + r) + c;
                 store_out(p, dst, o.x * inv, o.y * inv);
                 store_out(p, dst + 2, o.z * inv, o.w * inv);
             } else {
@@ -550,8 +592,9 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
                 if (c == 0) *reinterpret_cast<float2 *>(p.part_ml + (slot * M + r) * 2) = make_float2(top, ls);
             }
         }
-        __syncthreads();  // the merge buffer and s_tok are free for the next piece
+        __syncthreads();  // the stage is free for the next tiles
     }
+    cp_async_wait<0>();
 }
 
 // Adds the pieces of the units that several CTAs share, in tile order, and writes zeros for the rows of
@@ -639,7 +682,7 @@ size_t attn_ws(const hla_kv_cache *C, int B, int T, int H, bool sparse) {
 template <int D, bool FP8, int WR>
 cudaError_t launch_attn(const AttnParams &p, int *grid, long most, cudaStream_t st) {
     constexpr size_t ring = 4 * (size_t)warp_region<D, FP8>();
-    const size_t smem = ring + (p.B + 1) * sizeof(int);
+    const size_t smem = ring + (2 * p.B + 1) * sizeof(int);
     // the shared-memory limit is a per-device attribute: raise it once on every device used
     static bool done[64] = {};
     int dev = 0;
@@ -647,7 +690,7 @@ cudaError_t launch_attn(const AttnParams &p, int *grid, long most, cudaStream_t 
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !done[dev]) {
         e = cudaFuncSetAttribute(attn_kernel<D, FP8, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(ring + (kMaxBatch + 1) * sizeof(int)));
+                                 (int)(ring + (2 * kMaxBatch + 1) * sizeof(int)));
         if (e != cudaSuccess) return e;
         if (dev < 64) done[dev] = true;
     }
@@ -705,7 +748,7 @@ int run_attn(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const i
                                 : (fp8 ? 4 * warp_keys<64, true>() : 4 * warp_keys<64, false>());
     const long per_unit = ((long)(sparse ? n_select : max_blocks) * C->page_size + p.tile - 1) / p.tile;
     const long most = (long)B * p.units_per_b * per_unit;  // tiles, if every sequence filled its table
-    HLA_REQUIRE(most < (1L << 31), HLA_ERR_UNSUPPORTED);
+    HLA_REQUIRE(most < (1L << 31) && (long)C->n_pages * C->kv_heads * (C->page_size / kGroup) < (1L << 31), HLA_ERR_UNSUPPORTED);
     const int D = C->head_dim;
     p.part_o = static_cast<float *>(ws);
     p.part_ml = p.part_o + (size_t)2 * attn_grid_limit() * M * D;
