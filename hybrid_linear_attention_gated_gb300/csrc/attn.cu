@@ -116,18 +116,18 @@ __host__ __device__ constexpr int warp_keys() {
     return D * (FP8 ? 1 : 2) <= 128 ? 32 : 16;
 }
 // CTAs per SM, which bounds the registers per thread, and stages of the copy ring.
-template <int D, bool FP8>
+template <int D, bool FP8, int WR>
 __host__ __device__ constexpr int ctas_per_sm() {
-    return D == 128 ? 2 : (FP8 ? 4 : 3);
+    return D == 128 ? 2 : (FP8 && WR == 1 ? 4 : 3);
 }
-template <int D, bool FP8>
+template <int D, bool FP8, int WR>
 __host__ __device__ constexpr int ring_stages() {
-    constexpr int tile_bytes = 8 * warp_keys<D, FP8>() * D * (FP8 ? 1 : 2), room = 216 * 1024 / ctas_per_sm<D, FP8>() - 3072;
+    constexpr int tile_bytes = 8 * warp_keys<D, FP8>() * D * (FP8 ? 1 : 2), room = 216 * 1024 / ctas_per_sm<D, FP8, WR>() - 3072;
     return room / tile_bytes < 6 ? room / tile_bytes : 6;
 }
-template <int D, bool FP8>
+template <int D, bool FP8, int WR>
 __host__ __device__ constexpr int warp_region() {  // shared memory of one warp's keys over all stages
-    return ring_stages<D, FP8>() * 2 * warp_keys<D, FP8>() * D * (FP8 ? 1 : 2);
+    return ring_stages<D, FP8, WR>() * 2 * warp_keys<D, FP8>() * D * (FP8 ? 1 : 2);
 }
 
 // B fragments (16 keys x 8 channels) of accumulator tiles t and t + 1 (t even) from a group's V rows: f[0], f[1]
@@ -175,12 +175,13 @@ __device__ __noinline__ bool strange_value(const uint8_t *v, int r0, int r1, int
 
 // WR: warps that divide the rows, 16 to a warp; the other 4 / WR ways divide the keys.
 template <int D, bool FP8, int WR>
-__global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_kernel(const AttnParams p) {
     constexpr int ES = FP8 ? 1 : 2, RB = D * ES, CPR = RB / 16;
     constexpr int KW = warp_keys<D, FP8>(), KG = KW / kGroup, TILE = 4 * KW;
-    constexpr int NS = ring_stages<D, FP8>();
+    constexpr int NS = ring_stages<D, FP8, WR>();
     constexpr int GB = kGroup * RB;           // bytes of one group's K (or V) rows
-    constexpr int REGION = warp_region<D, FP8>(), STAGE = 2 * KG * GB;
+    constexpr int REGION = warp_region<D, FP8, WR>(), STAGE = 2 * KG * GB;
+    constexpr int SG = KG * WR < 4 ? KG * WR : 4;  // groups that a warp scores at a time
     constexpr int M = 16 * WR, WK = 4 / WR;
     constexpr int KS = D / 16, NT = D / 8;
     constexpr uint32_t ONES = FP8 ? 0x3c003c00u : 0x3f803f80u;
@@ -391,19 +392,22 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
             cp_async_commit();
 
 #pragma unroll 1
-            for (int w = kp * WR; w < kp * WR + WR; ++w) {
-                const uint32_t kb = ring + w * REGION + stage * STAGE;
-                // ---- scores of KW keys: tile 2 g + x holds keys 8 x + 2 j, + 1 of group g
-                float s[2 * KG][4];
+            for (int step = 0; step < KG * WR / SG; ++step) {
+                // group g of the step: copied by warp w0 + g / KG, as its group g % KG
+                const int w0 = kp * WR + step * (SG / KG);
+                const uint32_t base_s = ring + w0 * REGION + stage * STAGE;
+                auto group_at = [&](int g) -> uint32_t { return base_s + g / KG * REGION + g % KG * 2 * GB; };
+                // ---- scores: tile 2 g + x holds keys 8 x + 2 j, + 1 of group g
+                float s[2 * SG][4];
 #pragma unroll
-                for (int t = 0; t < 2 * KG; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+                for (int t = 0; t < 2 * SG; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
                 if constexpr (!FP8) {
 #pragma unroll
                     for (int c = 0; c < KS; ++c)
 #pragma unroll
-                        for (int g = 0; g < KG; ++g) {
+                        for (int g = 0; g < SG; ++g) {
                             uint32_t f[4];  // keys 0-7: chunks 2c, 2c+1; keys 8-15: chunks 2c, 2c+1
-                            ldmatrix_x4(f, kb + 2 * g * GB + swizzled<RB>((lane & 7) + ((lane >> 4) << 3), 2 * c + ((lane >> 3) & 1)));
+                            ldmatrix_x4(f, group_at(g) + swizzled<RB>((lane & 7) + ((lane >> 4) << 3), 2 * c + ((lane >> 3) & 1)));
                             mma_bf16_16816(s[2 * g], qf[c][0], qf[c][1], qf[c][2], qf[c][3], f[0], f[1]);
                             mma_bf16_16816(s[2 * g + 1], qf[c][0], qf[c][1], qf[c][2], qf[c][3], f[2], f[3]);
                         }
@@ -411,9 +415,9 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
 #pragma unroll
                     for (int c = 0; c < KS; c += 2)
 #pragma unroll
-                        for (int g = 0; g < KG; ++g) {
+                        for (int g = 0; g < SG; ++g) {
                             uint32_t f[4];  // keys 0-7: chunks c, c+1; keys 8-15: chunks c, c+1
-                            ldmatrix_x4(f, kb + 2 * g * GB + swizzled<RB>((lane & 7) + ((lane >> 4) << 3), c + ((lane >> 3) & 1)));
+                            ldmatrix_x4(f, group_at(g) + swizzled<RB>((lane & 7) + ((lane >> 4) << 3), c + ((lane >> 3) & 1)));
 #pragma unroll
                             for (int z = 0; z < 4; ++z)
                                 mma_f16_16816(s[2 * g + (z >> 1)], qf[c + (z & 1)][0], qf[c + (z & 1)][1], qf[c + (z & 1)][2],
@@ -421,11 +425,11 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
                         }
                 }
                 // ---- mask, running maximum
-                int tok[KG];
+                int tok[SG];
                 float top[2] = {m[0], m[1]};
 #pragma unroll
-                for (int g = 0; g < KG; ++g) {
-                    tok[g] = s_tok[w][stage][g];
+                for (int g = 0; g < SG; ++g) {
+                    tok[g] = s_tok[w0 + g / KG][stage][g % KG];
                     if (tok[g] + kGroup - 1 > lim_lo) {  // some row does not see all 16
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
@@ -461,12 +465,12 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
                 // down to 2^-39 of the largest).  A bf16 output rounds by 2^-9 itself, so one rounding of each weight,
                 // which averages out over the keys, is below it; an fp32 output gets the rounded-off part in a second
                 // product, which leaves 2^-17.
-                uint32_t ph[KG][4], pl[KG][4];
+                uint32_t ph[SG][4], pl[SG][4];
 #pragma unroll
                 for (int hrow = 0; hrow < 2; ++hrow) {
                     const float base = (FP8 ? 14.f : 0.f) - mb[hrow];
 #pragma unroll
-                    for (int t = 0; t < 2 * KG; ++t) {
+                    for (int t = 0; t < 2 * SG; ++t) {
                         const float a = ex2(fmaf(s[t][2 * hrow], sc[hrow], base)), c = ex2(fmaf(s[t][2 * hrow + 1], sc[hrow], base));
                         uint32_t &h = ph[t >> 1][2 * (t & 1) + hrow], &r = pl[t >> 1][2 * (t & 1) + hrow];
                         if constexpr (!FP8) {
@@ -487,8 +491,8 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8>()) attn_kern
                 // hide an infinity or NaN of such a key's value: where one is there, these keys go one at a time and a
                 // row takes up only what it sees.
 #pragma unroll
-                for (int g = 0; g < KG; ++g) {
-                    const uint32_t vb = kb + 2 * g * GB + GB;
+                for (int g = 0; g < SG; ++g) {
+                    const uint32_t vb = group_at(g) + GB;
                     mma_pv<FP8>(acc[NT], ph[g], ONES, ONES);
                     if (!p.o_bf16) mma_pv<FP8>(acc[NT], pl[g], ONES, ONES);
                     bool odd = false;
@@ -681,7 +685,7 @@ size_t attn_ws(const hla_kv_cache *C, int B, int T, int H, bool sparse) {
 
 template <int D, bool FP8, int WR>
 cudaError_t launch_attn(const AttnParams &p, int *grid, long most, cudaStream_t st) {
-    constexpr size_t ring = 4 * (size_t)warp_region<D, FP8>();
+    constexpr size_t ring = 4 * (size_t)warp_region<D, FP8, WR>();
     const size_t smem = ring + (2 * p.B + 1) * sizeof(int);
     // the shared-memory limit is a per-device attribute: raise it once on every device used
     static bool done[64] = {};
@@ -695,7 +699,7 @@ cudaError_t launch_attn(const AttnParams &p, int *grid, long most, cudaStream_t 
         if (dev < 64) done[dev] = true;
     }
     // one wave of CTAs, and no more than the longest possible sequences have tiles
-    const int slots = ctas_per_sm<D, FP8>() * sm_count();
+    const int slots = ctas_per_sm<D, FP8, WR>() * sm_count();
     *grid = most < slots ? (int)most : slots;
     return launch_kernel(attn_kernel<D, FP8, WR>, dim3(*grid), dim3(kAttnThreads), smem, st, p);
 }
