@@ -19,6 +19,8 @@
 // Within a CTA a tile's keys are copied 16 or 32 to a warp, each warp into its own ring of cp.async stages.
 // With 16 query rows a warp also runs its own keys against all rows and meets the other warps only at the end
 // of a unit; with 32 or 64 rows, two or four warps take 16 rows each and run all keys that they copied together.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace hla {
@@ -118,7 +120,7 @@ __host__ __device__ constexpr int warp_keys() {
 // CTAs per SM, which bounds the registers per thread, and stages of the copy ring.
 template <int D, bool FP8, int WR>
 __host__ __device__ constexpr int ctas_per_sm() {
-    return D == 128 ? 2 : (FP8 && WR == 1 ? 4 : 3);
+    return D == 128 ? 2 : 3;
 }
 template <int D, bool FP8, int WR>
 __host__ __device__ constexpr int ring_stages() {
@@ -143,10 +145,8 @@ __device__ __forceinline__ void v_fragments(uint32_t (&f)[4], uint32_t vb, int t
         const int key = 2 * ((lane & 15) >> 2) + (lane & 1) + 4 * (lane & 2);
         uint32_t a, b;
         ldmatrix_trans8(a, b, vb + swizzled<RB>(key, t >> 1));
-        f[0] = e4m3x2_to_f16x2(a & 0xffffu);
-        f[1] = e4m3x2_to_f16x2(a >> 16);
-        f[2] = e4m3x2_to_f16x2(b & 0xffffu);
-        f[3] = e4m3x2_to_f16x2(b >> 16);
+        e4m3x4_to_f16x4(a, f[0], f[1]);
+        e4m3x4_to_f16x4(b, f[2], f[3]);
     }
 }
 
@@ -419,9 +419,12 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                             uint32_t f[4];  // keys 0-7: chunks c, c+1; keys 8-15: chunks c, c+1
                             ldmatrix_x4(f, group_at(g) + swizzled<RB>((lane & 7) + ((lane >> 4) << 3), c + ((lane >> 3) & 1)));
 #pragma unroll
-                            for (int z = 0; z < 4; ++z)
+                            for (int z = 0; z < 4; ++z) {
+                                uint32_t b0, b1;
+                                e4m3x4_to_f16x4(f[z], b0, b1);
                                 mma_f16_16816(s[2 * g + (z >> 1)], qf[c + (z & 1)][0], qf[c + (z & 1)][1], qf[c + (z & 1)][2],
-                                              qf[c + (z & 1)][3], e4m3x2_to_f16x2(f[z] & 0xffffu), e4m3x2_to_f16x2(f[z] >> 16));
+                                              qf[c + (z & 1)][3], b0, b1);
+                            }
                         }
                 }
                 // ---- mask, running maximum
@@ -465,75 +468,81 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                 // down to 2^-39 of the largest).  A bf16 output rounds by 2^-9 itself, so one rounding of each weight,
                 // which averages out over the keys, is below it; an fp32 output gets the rounded-off part in a second
                 // product, which leaves 2^-17.
-                uint32_t ph[SG][4], pl[SG][4];
+                auto weigh = [&](auto both) {
+                    constexpr bool LO = decltype(both)::value;  // a second product with what rounding took off
+                    uint32_t ph[SG][4], pl[LO ? SG : 1][4];
 #pragma unroll
-                for (int hrow = 0; hrow < 2; ++hrow) {
-                    const float base = (FP8 ? 14.f : 0.f) - mb[hrow];
+                    for (int hrow = 0; hrow < 2; ++hrow) {
+                        const float base = (FP8 ? 14.f : 0.f) - mb[hrow];
 #pragma unroll
-                    for (int t = 0; t < 2 * SG; ++t) {
-                        const float a = ex2(fmaf(s[t][2 * hrow], sc[hrow], base)), c = ex2(fmaf(s[t][2 * hrow + 1], sc[hrow], base));
-                        uint32_t &h = ph[t >> 1][2 * (t & 1) + hrow], &r = pl[t >> 1][2 * (t & 1) + hrow];
-                        if constexpr (!FP8) {
-                            h = pack_bf16x2(a, c);
-                            if (!p.o_bf16) r = pack_bf16x2(a - bf16_lo(h), c - bf16_hi(h));
-                        } else {
-                            const __half2 hh = __floats2half2_rn(a, c);
-                            h = *reinterpret_cast<const uint32_t *>(&hh);
-                            if (!p.o_bf16) {
-                                const float2 f = __half22float2(hh);
-                                const __half2 rr = __floats2half2_rn(a - f.x, c - f.y);
-                                r = *reinterpret_cast<const uint32_t *>(&rr);
-                            }
-                        }
-                    }
-                }
-                // ---- o += P V.  The window's own last keys are seen by some rows only, and a weight of zero does not
-                // hide an infinity or NaN of such a key's value: where one is there, these keys go one at a time and a
-                // row takes up only what it sees.
-#pragma unroll
-                for (int g = 0; g < SG; ++g) {
-                    const uint32_t vb = group_at(g) + GB;
-                    mma_pv<FP8>(acc[NT], ph[g], ONES, ONES);
-                    if (!p.o_bf16) mma_pv<FP8>(acc[NT], pl[g], ONES, ONES);
-                    bool odd = false;
-                    if (lim_lo < lim_hi && tok[g] + kGroup - 1 > lim_lo && tok[g] <= lim_hi)
-                        odd = strange_value<D, FP8>(smem + (vb - ring), lim_lo + 1 - tok[g], lim_hi - tok[g], lane);
-                    if (!odd) {
-#pragma unroll
-                        for (int t = 0; t < NT; t += 2) {
-                            uint32_t f[4];
-                            v_fragments<D, FP8>(f, vb, t, lane);
-                            mma_pv<FP8>(acc[t], ph[g], f[0], f[1]);
-                            mma_pv<FP8>(acc[t + 1], ph[g], f[2], f[3]);
-                            if (!p.o_bf16) {
-                                mma_pv<FP8>(acc[t], pl[g], f[0], f[1]);
-                                mma_pv<FP8>(acc[t + 1], pl[g], f[2], f[3]);
-                            }
-                        }
-                    } else {
-                        // first pass: the keys up to lim_lo, which all rows see; then key y alone
-                        for (int y = tok[g] > lim_lo ? tok[g] - 1 : lim_lo; y <= lim_hi && y < tok[g] + kGroup; ++y) {
-                            const bool all = y <= lim_lo || y < tok[g];
-                            auto keep = [&](int key) -> bool { return all ? tok[g] + key <= lim_lo : tok[g] + key == y; };
-                            const uint32_t lo = (keep(2 * j) ? 0xffffu : 0u) | (keep(2 * j + 1) ? 0xffff0000u : 0u),
-                                           hi = (keep(2 * j + 8) ? 0xffffu : 0u) | (keep(2 * j + 9) ? 0xffff0000u : 0u);
-#pragma unroll
-                            for (int t = 0; t < NT; t += 2) {
-                                uint32_t f[4];
-                                v_fragments<D, FP8>(f, vb, t, lane);
-#pragma unroll
-                                for (int z = 0; z < 2; ++z) {
-                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma_pv<FP8>(d, ph[g], f[2 * z] & lo, f[2 * z + 1] & hi);
-                                    if (!p.o_bf16) mma_pv<FP8>(d, pl[g], f[2 * z] & lo, f[2 * z + 1] & hi);
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (all || y <= lim[e >> 1]) acc[t + z][e] += d[e];
+                        for (int t = 0; t < 2 * SG; ++t) {
+                            const float a = ex2(fmaf(s[t][2 * hrow], sc[hrow], base)), c = ex2(fmaf(s[t][2 * hrow + 1], sc[hrow], base));
+                            const int w = 2 * (t & 1) + hrow;
+                            if constexpr (!FP8) {
+                                const uint32_t h = pack_bf16x2(a, c);
+                                ph[t >> 1][w] = h;
+                                if constexpr (LO) pl[t >> 1][w] = pack_bf16x2(a - bf16_lo(h), c - bf16_hi(h));
+                            } else {
+                                const __half2 h = __floats2half2_rn(a, c);
+                                ph[t >> 1][w] = *reinterpret_cast<const uint32_t *>(&h);
+                                if constexpr (LO) {
+                                    const float2 f = __half22float2(h);
+                                    const __half2 l = __floats2half2_rn(a - f.x, c - f.y);
+                                    pl[t >> 1][w] = *reinterpret_cast<const uint32_t *>(&l);
                                 }
                             }
                         }
                     }
-                }
+                    // o += P V.  The window's own last keys are seen by some rows only, and a weight of zero does not hide an
+                    // infinity or NaN of such a key's value: where one is there, these keys go one at a time and a row takes
+                    // up only what it sees.
+#pragma unroll
+                    for (int g = 0; g < SG; ++g) {
+                        const uint32_t vb = group_at(g) + GB;
+                        mma_pv<FP8>(acc[NT], ph[g], ONES, ONES);
+                        if constexpr (LO) mma_pv<FP8>(acc[NT], pl[g], ONES, ONES);
+                        bool odd = false;
+                        if (lim_lo < lim_hi && tok[g] + kGroup - 1 > lim_lo && tok[g] <= lim_hi)
+                            odd = strange_value<D, FP8>(smem + (vb - ring), lim_lo + 1 - tok[g], lim_hi - tok[g], lane);
+                        if (!odd) {
+#pragma unroll
+                            for (int t = 0; t < NT; t += 2) {
+                                uint32_t f[4];
+                                v_fragments<D, FP8>(f, vb, t, lane);
+                                mma_pv<FP8>(acc[t], ph[g], f[0], f[1]);
+                                mma_pv<FP8>(acc[t + 1], ph[g], f[2], f[3]);
+                                if constexpr (LO) {
+                                    mma_pv<FP8>(acc[t], pl[g], f[0], f[1]);
+                                    mma_pv<FP8>(acc[t + 1], pl[g], f[2], f[3]);
+                                }
+                            }
+                        } else {
+                            // first pass: the keys up to lim_lo, which all rows see; then key y alone
+                            for (int y = tok[g] > lim_lo ? tok[g] - 1 : lim_lo; y <= lim_hi && y < tok[g] + kGroup; ++y) {
+                                const bool all = y <= lim_lo || y < tok[g];
+                                auto keep = [&](int key) -> bool { return all ? tok[g] + key <= lim_lo : tok[g] + key == y; };
+                                const uint32_t lo = (keep(2 * j) ? 0xffffu : 0u) | (keep(2 * j + 1) ? 0xffff0000u : 0u),
+                                               hi = (keep(2 * j + 8) ? 0xffffu : 0u) | (keep(2 * j + 9) ? 0xffff0000u : 0u);
+#pragma unroll
+                                for (int t = 0; t < NT; t += 2) {
+                                    uint32_t f[4];
+                                    v_fragments<D, FP8>(f, vb, t, lane);
+#pragma unroll
+                                    for (int z = 0; z < 2; ++z) {
+                                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                        mma_pv<FP8>(d, ph[g], f[2 * z] & lo, f[2 * z + 1] & hi);
+                                        if constexpr (LO) mma_pv<FP8>(d, pl[g], f[2 * z] & lo, f[2 * z + 1] & hi);
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e)
+                                            if (all || y <= lim[e >> 1]) acc[t + z][e] += d[e];
+                                    }
+                                }
+                            }
+                        }
+                    }
+                };
+                if (p.o_bf16) weigh(std::false_type{});
+                else weigh(std::true_type{});
             }
             last = stage;
             stage = stage + 1 == NS ? 0 : stage + 1;

@@ -107,6 +107,18 @@ __device__ __forceinline__ void rotate(const AppendParams &p, int x, float (&a)[
     }
 }
 
+__device__ __forceinline__ uint4 e4m3x8_to_bf16x8(const uint2 t) {  // exact
+    uint32_t h[4], o[4];
+    e4m3x4_to_f16x4(t.x, h[0], h[1]);
+    e4m3x4_to_f16x4(t.y, h[2], h[3]);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&h[y]));
+        o[y] = pack_bf16x2(g.x, g.y);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // 8 values as the cache holds them; returns them as bf16 (an e4m3 value is one exactly).
 template <bool FP8>
 __device__ __forceinline__ uint4 store8(uint8_t *row, int c, float (&f)[8], float scale) {
@@ -119,16 +131,9 @@ __device__ __forceinline__ uint4 store8(uint8_t *row, int c, float (&f)[8], floa
         uint32_t r[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) r[y] = f32x2_to_e4m3x2(__fdiv_rn(f[2 * y], scale), __fdiv_rn(f[2 * y + 1], scale));
-        reinterpret_cast<uint2 *>(row)[c] = make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
-        uint4 w;
-        uint32_t *o = &w.x;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const uint32_t h = e4m3x2_to_f16x2(r[y]);
-            const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            o[y] = pack_bf16x2(g.x, g.y);
-        }
-        return w;
+        const uint2 t = make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
+        reinterpret_cast<uint2 *>(row)[c] = t;
+        return e4m3x8_to_bf16x8(t);
     }
 }
 
@@ -138,16 +143,7 @@ __device__ __forceinline__ uint4 load8(const uint8_t *row, int c) {
     if constexpr (!FP8) {
         return reinterpret_cast<const uint4 *>(row)[c];
     } else {
-        const uint2 t = reinterpret_cast<const uint2 *>(row)[c];
-        uint4 w;
-        uint32_t *o = &w.x;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const uint32_t h = e4m3x2_to_f16x2(((y & 2 ? t.y : t.x) >> (16 * (y & 1))) & 0xffffu);
-            const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            o[y] = pack_bf16x2(g.x, g.y);
-        }
-        return w;
+        return e4m3x8_to_bf16x8(reinterpret_cast<const uint2 *>(row)[c]);
     }
 }
 

@@ -53,11 +53,11 @@ inline int check_window(const hla_kv_cache *C, int B, int T, int H, int max_bloc
 
 // ----------------------------------------------------------------------------- device side
 
-// Two e4m3 values (the low 16 bits) as two fp16 values: exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-    uint32_t r;
-    asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(r) : "r"(two));
-    return r;
+// Four e4m3 values as fp16 (exact): bytes 0, 1 in lo and 2, 3 in hi.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t &lo, uint32_t &hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 // Two fp32 values as e4m3, rounded to nearest even and saturated at +-448 (NaN stays NaN); lo in the low byte.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
