@@ -55,10 +55,16 @@ __device__ __forceinline__ int cached(const AttnParams &p, int b) {
     return x < kNoKeys - 16 ? x : kNoKeys - 16;
 }
 
+// Entries of its list that the token at position pos reads: no more than the blocks it sees.
+__device__ __forceinline__ int listed(const AttnParams &p, int pos) {
+    const int n = (pos >> p.pshift) + 1;
+    return n < p.n_select ? n : p.n_select;
+}
+
 // Tiles of one unit of a sequence with `past` cached tokens.
 __device__ __forceinline__ int unit_tiles(const AttnParams &p, int past) {
     if (past < 0) return 0;
-    if (p.sel) return (int)((((long)p.n_select << p.pshift) + p.tile - 1) / p.tile);
+    if (p.sel) return (int)((((long)listed(p, past + p.T - 1) << p.pshift) + p.tile - 1) / p.tile);
     const long cap = (long)p.max_blocks << p.pshift;
     const long len = (long)past + p.T < cap ? (long)past + p.T : cap;
     return (int)((len + p.tile - 1) / p.tile);
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
         const Unit u = unit_of(begin + g / KG);
         const int key = u.k * TILE + warp * KW + g % KG * kGroup;
         int blk = key >> p.pshift;
-        if (p.sel) blk = blk < p.n_select ? p.sel[((size_t)(u.b * p.T + u.tq) * p.Hkv + u.hk) * p.n_select + blk] : -1;
+        if (p.sel) blk = blk < listed(p, s_past[u.b] + u.tq) ? p.sel[((size_t)(u.b * p.T + u.tq) * p.Hkv + u.hk) * p.n_select + blk] : -1;
         if (blk < 0 || blk >= p.max_blocks) return;
         const int page = p.table[(size_t)u.b * p.max_blocks + blk];
         if (page < 0 || page >= p.n_pages) return;
@@ -252,7 +258,6 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
     };
     int at_now, tok_now, on_now, at_next, tok_next, on_next;
     look(0, &at_now, &tok_now, &on_now);
-    look(32, &at_next, &tok_next, &on_next);
     // where this lane's 16-byte chunks of a group go: chunk x * 32 + lane
     uint32_t to[GB / 512];
 #pragma unroll
@@ -282,11 +287,12 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
             }
             if (lane == 0) s_tok[warp][stage][g] = tok;
         }
-        if (((ti + 1) * KG & 31) == 0) {
+        const int seen = (ti + 1) * KG;
+        if ((seen & 31) == 16) look(seen + 16, &at_next, &tok_next, &on_next);  // half a batch ahead
+        if ((seen & 31) == 0) {
             at_now = at_next;
             tok_now = tok_next;
             on_now = on_next;
-            look((ti + 1) * KG + 32, &at_next, &tok_next, &on_next);
         }
     };
 

@@ -14,8 +14,7 @@ namespace hla {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRowsPerPass = 16;  // cache rows whose angles are staged at a time
-constexpr int kMaxHalf = 64;      // channel pairs
+constexpr int kMaxQTokens = 4;    // tokens of q per CTA
 
 struct AppendParams {
     const uint16_t *q, *k, *v;
@@ -26,7 +25,7 @@ struct AppendParams {
     const int32_t *cu, *past, *table;
     const double *inv_freq;
     int N, B, H, Hkv, pshift, n_pages, max_blocks;
-    int half, interleaved;    // rotated channel pairs per head (0: none)
+    int half;                 // rotated channel pairs per head (0: none)
     int heads_per_cta, q_tokens, kv_ctas;
 };
 
@@ -64,9 +63,10 @@ __device__ __forceinline__ int touched_pages(const AppendParams &p, int b) {
 
 // Two 16-byte chunks of a head (channels 8 c0.. and 8 c1..) that are rotated together.  half == 0, or chunks behind
 // the rotated ones: unchanged.
+template <bool INTER>
 __device__ __forceinline__ void item_chunks(const AppendParams &p, int x, int *c0, int *c1) {
     const int hc = p.half >> 3;  // chunks of one half
-    if (!p.interleaved && x < hc) {
+    if (!INTER && x < hc) {
         *c0 = x;
         *c1 = x + hc;
     } else {  // the x-th pair of neighbouring chunks (the first 2 hc are the hc rotated items above)
@@ -83,13 +83,21 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
+// Place of a pair's (cos, sin) in its row: the eight pairs of an item lie one item count apart and a row is 64 bytes
+// longer than a round of the banks, so that the items and rows of a warp read side by side.
+template <int D>
+__device__ __forceinline__ int angle_at(int pair) {
+    return (pair & 7) * (D / 16) + (pair >> 3);
+}
+
 // Rotates the item's 16 channels; cs: (cos, sin) of the row's pairs.
+template <int D, bool INTER>
 __device__ __forceinline__ void rotate(const AppendParams &p, int x, float (&a)[8], float (&b)[8], const float2 *cs) {
     if (8 * x >= p.half) return;
-    if (p.interleaved) {
+    if constexpr (INTER) {
 #pragma unroll
         for (int y = 0; y < 8; y += 2) {
-            const float2 u = cs[8 * x + (y >> 1)], w = cs[8 * x + 4 + (y >> 1)];
+            const float2 u = cs[(y >> 1) * (D / 16) + x], w = cs[(4 + (y >> 1)) * (D / 16) + x];
             const float a0 = a[y], b0 = b[y];
             a[y] = a0 * u.x - a[y + 1] * u.y;
             a[y + 1] = a0 * u.y + a[y + 1] * u.x;
@@ -99,7 +107,7 @@ __device__ __forceinline__ void rotate(const AppendParams &p, int x, float (&a)[
     } else {
 #pragma unroll
         for (int y = 0; y < 8; ++y) {
-            const float2 u = cs[8 * x + y];
+            const float2 u = cs[y * (D / 16) + x];
             const float a0 = a[y];
             a[y] = a0 * u.x - b[y] * u.y;
             b[y] = a0 * u.y + b[y] * u.x;
@@ -176,13 +184,15 @@ struct Bounds {
     }
 };
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams p) {
+template <int D, bool FP8, bool INTER>
+__global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendParams p) {
     constexpr int ITEMS = D / 16;              // pairs of chunks per head row
     constexpr int LANES = kThreads / ITEMS;    // rows in flight
     constexpr int ES = FP8 ? 1 : 2;
-    __shared__ uint64_t s_turn[kMaxHalf];
-    __shared__ float2 s_cs[kRowsPerPass][kMaxHalf];
+    constexpr int MAXH = D / 2;                // channel pairs
+    __shared__ uint64_t s_turn[MAXH];
+    // angles of one pass of LANES cache rows, and of the next (or of the tokens of q)
+    __shared__ float2 s_cs[2][LANES][MAXH + 8];
     __shared__ uint32_t s_lo[4][ITEMS][8], s_hi[4][ITEMS][8];
     __shared__ int s_warp[4], s_b, s_j;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -190,14 +200,26 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
     pdl_wait_trigger();
     if (tid < p.half) s_turn[tid] = turn_fraction(p.inv_freq[tid]);
     int c0, c1;
-    item_chunks(p, item, &c0, &c1);
+    item_chunks<INTER>(p, item, &c0, &c1);
 
     if ((int)blockIdx.x >= p.kv_ctas) {
         // ---- q of some tokens: all heads
         const int n0 = (blockIdx.x - p.kv_ctas) * p.q_tokens;
-        const int nt = p.N - n0 < p.q_tokens ? p.N - n0 : p.q_tokens;
-        __shared__ int s_pos[kRowsPerPass];
-        __syncthreads();
+        const int nt = p.N - n0 < p.q_tokens ? p.N - n0 : p.q_tokens, rows = nt * p.H;
+        __shared__ int s_pos[kMaxQTokens];
+        // four rows at a time: their loads are in flight together, the first ones while the positions are found
+        uint4 wa[4], wb[4];
+        auto load = [&](int r0) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int r = r0 + y * LANES;
+                if (r >= rows) break;
+                const size_t o = ((size_t)n0 * p.H + r) * D;
+                wa[y] = ld_act_v4(p.q + o + 8 * c0);
+                wb[y] = ld_act_v4(p.q + o + 8 * c1);
+            }
+        };
+        load(rl);
         for (int x = 0; x < nt; ++x) {
             // the sequence of token n0 + x: the number of offsets cu[1..B] at or below it
             int n = 0;
@@ -212,20 +234,24 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
         __syncthreads();
         for (int x = tid; x < nt * p.half; x += kThreads) {
             const int t = x / p.half, h = x % p.half;
-            s_cs[t][h] = cos_sin(s_turn[h], s_pos[t]);
+            s_cs[0][t][angle_at<D>(h)] = cos_sin(s_turn[h], s_pos[t]);
         }
         __syncthreads();
-        for (int r = rl; r < nt * p.H; r += LANES) {
-            const int t = r / p.H;
-            if (s_pos[t] < 0) continue;  // no sequence's token, or an idle one's: left as it was
-            const size_t o = ((size_t)n0 * p.H + r) * D;
-            const uint4 wa = ld_act_v4(p.q + o + 8 * c0), wb = ld_act_v4(p.q + o + 8 * c1);
-            float a[8], b[8];
-            unpack8(wa, a);
-            unpack8(wb, b);
-            rotate(p, item, a, b, s_cs[t]);
-            *reinterpret_cast<uint4 *>(p.q_out + o + 8 * c0) = pack8(a);
-            *reinterpret_cast<uint4 *>(p.q_out + o + 8 * c1) = pack8(b);
+        for (int r0 = rl; r0 < rows; r0 += 4 * LANES) {
+            if (r0 != rl) load(r0);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int r = r0 + y * LANES, t = r / p.H;
+                if (r >= rows) break;
+                if (s_pos[t] < 0) continue;  // no sequence's token, or an idle one's: left as it was
+                const size_t o = ((size_t)n0 * p.H + r) * D;
+                float a[8], b[8];
+                unpack8(wa[y], a);
+                unpack8(wb[y], b);
+                rotate<D, INTER>(p, item, a, b, s_cs[0][t]);
+                *reinterpret_cast<uint4 *>(p.q_out + o + 8 * c0) = pack8(a);
+                *reinterpret_cast<uint4 *>(p.q_out + o + 8 * c1) = pack8(b);
+            }
         }
         return;
     }
@@ -277,36 +303,57 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
         const float ks = FP8 ? p.k_scale[h] : 1.f, vs = FP8 ? p.v_scale[h] : 1.f;
         Bounds bd;
         bd.clear();
+        // LANES rows a pass, one to a thread; the next pass's rows and angles are on their way during this one's work
+        uint4 ka, kb, va, vb;
+        auto load = [&](int r) {
+            if (r >= r1) return;
+            const size_t o = ((size_t)(t0 + r) * p.Hkv + h) * D;
+            ka = ld_act_v4(p.k + o + 8 * c0);
+            kb = ld_act_v4(p.k + o + 8 * c1);
+            va = ld_act_v4(p.v + o + 8 * c0);
+            vb = ld_act_v4(p.v + o + 8 * c1);
+        };
+        auto angles = [&](int buf, int rr) {
+            const int n = (r1 - rr < LANES ? r1 - rr : LANES) * p.half;
+            for (int x = tid; x < n; x += kThreads) {
+                const int r = x / p.half, y = x - r * p.half;
+                s_cs[buf][r][angle_at<D>(y)] = cos_sin(s_turn[y], start + rr + r);
+            }
+        };
+        const bool many = r1 - r0 > LANES;  // otherwise the angles of the one pass serve all heads
+        load(r0 + rl);
         if (bounds)  // keys that were there
             for (int r = rl; r < r0; r += LANES) bd.take(load8<FP8>(kp + r * (D * ES), c0), load8<FP8>(kp + r * (D * ES), c1));
-        for (int rr = r0; rr < r1; rr += kRowsPerPass) {
-            const int nr = r1 - rr < kRowsPerPass ? r1 - rr : kRowsPerPass;
-            if (h == h0 || r1 - r0 > kRowsPerPass) {  // angles of one pass serve all heads
-                __syncthreads();
-                for (int x = tid; x < nr * p.half; x += kThreads)
-                    s_cs[x / p.half][x % p.half] = cos_sin(s_turn[x % p.half], start + rr + x / p.half);
-                __syncthreads();
-            }
-            for (int r = rl; r < nr; r += LANES) {
-                const size_t o = ((size_t)(t0 + rr + r) * p.Hkv + h) * D;
-                const uint4 ka = ld_act_v4(p.k + o + 8 * c0), kb = ld_act_v4(p.k + o + 8 * c1);
-                const uint4 va = ld_act_v4(p.v + o + 8 * c0), vb = ld_act_v4(p.v + o + 8 * c1);
+        if (h == h0 || many) {
+            __syncthreads();  // (the last head's rows are done with the angles; s_turn is there)
+            angles(0, r0);
+            __syncthreads();
+        }
+        for (int rr = r0, buf = 0; rr < r1; rr += LANES, buf ^= 1) {
+            const int r = rr + rl;
+            const uint4 ca = ka, cb = kb, da = va, db = vb;
+            load(r + LANES);
+            if (r < r1) {
                 float a[8], c[8];
-                unpack8(ka, a);
-                unpack8(kb, c);
-                rotate(p, item, a, c, s_cs[r]);
-                uint8_t *krow = kp + (rr + r) * (D * ES), *vrow = vp + (rr + r) * (D * ES);
+                unpack8(ca, a);
+                unpack8(cb, c);
+                rotate<D, INTER>(p, item, a, c, s_cs[buf][rl]);
+                uint8_t *krow = kp + r * (D * ES), *vrow = vp + r * (D * ES);
                 const uint4 wa = store8<FP8>(krow, c0, a, ks), wb = store8<FP8>(krow, c1, c, ks);
                 if (bounds) bd.take(wa, wb);
                 if constexpr (!FP8) {
-                    reinterpret_cast<uint4 *>(vrow)[c0] = va;
-                    reinterpret_cast<uint4 *>(vrow)[c1] = vb;
+                    reinterpret_cast<uint4 *>(vrow)[c0] = da;
+                    reinterpret_cast<uint4 *>(vrow)[c1] = db;
                 } else {
-                    unpack8(va, a);
-                    unpack8(vb, c);
+                    unpack8(da, a);
+                    unpack8(db, c);
                     store8<true>(vrow, c0, a, vs);
                     store8<true>(vrow, c1, c, vs);
                 }
+            }
+            if (rr + LANES < r1) {
+                angles(buf ^ 1, rr + LANES);
+                __syncthreads();
             }
         }
         if (!bounds) continue;
@@ -334,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
                 hi = max2(hi, s_hi[w][it][y]);
             }
             int a, c;
-            item_chunks(p, it, &a, &c);
+            item_chunks<INTER>(p, it, &a, &c);
             const size_t o = ((size_t)pg * p.Hkv + h) * D + 8 * (y < 4 ? a : c) + 2 * (y & 3);
             *reinterpret_cast<uint32_t *>(p.k_min + o) = lo;
             *reinterpret_cast<uint32_t *>(p.k_max + o) = hi;
@@ -370,7 +417,7 @@ extern "C" int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_
     p.cu = cu_seqlens; p.past = past_len; p.table = block_table; p.inv_freq = inv_freq;
     p.N = N; p.B = B; p.H = H; p.Hkv = C->kv_heads; p.pshift = page_shift(C->page_size);
     p.n_pages = C->n_pages; p.max_blocks = max_blocks;
-    p.half = rope_dim / 2; p.interleaved = rope_interleaved;
+    p.half = rope_dim / 2;
     // n new tokens touch at most n pages, and at most n / page_size + 2
     const long by_size = (long)N / C->page_size + 2L * B, pages = N < by_size ? N : by_size;
     // heads of a page share its angles; one head per CTA until the pages alone fill the SMs
@@ -378,7 +425,7 @@ extern "C" int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_
     while (p.heads_per_cta < p.Hkv && pages * ((p.Hkv + 2 * p.heads_per_cta - 1) / (2 * p.heads_per_cta)) >= 8L * sm_count()) p.heads_per_cta *= 2;
     const long kv = pages * ((p.Hkv + p.heads_per_cta - 1) / p.heads_per_cta);
     p.q_tokens = 1;
-    while (p.q_tokens < kRowsPerPass && N / (2 * p.q_tokens) >= 8L * sm_count()) p.q_tokens *= 2;
+    while (p.q_tokens < kMaxQTokens && N / (2 * p.q_tokens) >= 3L * sm_count()) p.q_tokens *= 2;
     const long qc = (N + p.q_tokens - 1) / p.q_tokens;
     HLA_REQUIRE(kv + qc < (1L << 31), HLA_ERR_UNSUPPORTED);
     p.kv_ctas = (int)kv;
@@ -387,8 +434,12 @@ extern "C" int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_
     set_variant("kv_append<d%d,%s,rope%d%s>", D, fp8 ? "e4m3" : "bf16", rope_dim, rope_interleaved ? "i" : "");
     const cudaStream_t st = (cudaStream_t)stream;
     const dim3 grid((unsigned)(kv + qc));
-    return launched(D == 128 ? (fp8 ? launch_kernel(kv_append_kernel<128, true>, grid, dim3(kThreads), 0, st, p)
-                                    : launch_kernel(kv_append_kernel<128, false>, grid, dim3(kThreads), 0, st, p))
-                             : (fp8 ? launch_kernel(kv_append_kernel<64, true>, grid, dim3(kThreads), 0, st, p)
-                                    : launch_kernel(kv_append_kernel<64, false>, grid, dim3(kThreads), 0, st, p)));
+    auto go = [&](auto kernel) { return launched(launch_kernel(kernel, grid, dim3(kThreads), 0, st, p)); };
+    const bool in = rope_interleaved != 0;
+    if (D == 128) {
+        if (fp8) return in ? go(kv_append_kernel<128, true, true>) : go(kv_append_kernel<128, true, false>);
+        return in ? go(kv_append_kernel<128, false, true>) : go(kv_append_kernel<128, false, false>);
+    }
+    if (fp8) return in ? go(kv_append_kernel<64, true, true>) : go(kv_append_kernel<64, true, false>);
+    return in ? go(kv_append_kernel<64, false, true>) : go(kv_append_kernel<64, false, false>);
 }

@@ -95,7 +95,8 @@ def _row(q, keys, values, scale):
 
 
 def attend(q, k, v, table, past, scale, sel=None):
-    """o [B, T, H, d] of the T newest tokens, and the same sums over |v|.  sel [B, T, Hkv, n]: listed blocks only."""
+    """o [B, T, H, d] of the T newest tokens, and the same sums over |v|.  sel [B, T, Hkv, n]: listed blocks only,
+    and of a list no more entries than the token sees blocks."""
     q, k, v = f64(q), f64(k), f64(v)
     B, T, H, d = q.shape
     n_pages, Hkv, P, _ = k.shape
@@ -107,7 +108,7 @@ def attend(q, k, v, table, past, scale, sel=None):
             last = int(past[b]) + t
             for hk in range(Hkv):
                 blocks = range(min(table.shape[1], last // P + 1)) if sel is None else \
-                    [j for j in sel[b, t, hk] if 0 <= j < table.shape[1]]
+                    [j for j in sel[b, t, hk][:last // P + 1] if 0 <= j < table.shape[1]]
                 rows = [(int(table[b, j]), r) for j in blocks if 0 <= table[b, j] < n_pages
                         for r in range(P) if j * P + r <= last]
                 pg, r = np.array([x[0] for x in rows], int), np.array([x[1] for x in rows], int)

@@ -90,6 +90,9 @@ def test_attend_special_rows_and_lists():
     twice = at.attend(q, k, v, table, np.array([5]), 1.0, sel=np.array([[[[1, 1, 2]]]]))[0]
     table4 = np.array([[1, 1, 0, 3]])
     assert np.allclose(twice, at.attend(q, k, v, table4, np.array([5]), 1.0)[0])
+    # a token that sees two blocks reads two entries
+    short = at.attend(q, k, v, table, np.array([3]), 1.0, sel=np.array([[[[0, -1, 1]]]]))[0]
+    assert np.allclose(short, at.attend(q, k, v, table, np.array([1]), 1.0)[0])
 
 
 def test_scores_bound_every_key_and_selection_by_hand():
