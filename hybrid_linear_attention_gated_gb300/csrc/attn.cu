@@ -472,11 +472,13 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                 }
                 // ---- weights.  They meet V as bf16 (fp16 for an 8-bit cache, times 2^14 so that fp16 holds weights
                 // down to 2^-39 of the largest).  A bf16 output rounds by 2^-9 itself, so one rounding of each weight,
-                // which averages out over the keys, is below it; an fp32 output gets the rounded-off part in a second
-                // product, which leaves 2^-17.
+                // which averages out over the keys, is below it.  For an fp32 output the rounded-off part goes through
+                // further products, which leaves 2^-25 (fp16: 2^-23); with one less, 2^-17, the output was 1.4e-6 off,
+                // twice what fp32 arithmetic is.
                 auto weigh = [&](auto both) {
-                    constexpr bool LO = decltype(both)::value;  // a second product with what rounding took off
-                    uint32_t ph[SG][4], pl[LO ? SG : 1][4];
+                    // further products with what rounding took off: fp16 keeps 11 bits of a weight a time, bf16 8
+                    constexpr int EX = !decltype(both)::value ? 0 : FP8 ? 1 : 2;
+                    uint32_t ph[SG][4], pl[EX > 0 ? EX : 1][SG][4];
 #pragma unroll
                     for (int hrow = 0; hrow < 2; ++hrow) {
                         const float base = (FP8 ? 14.f : 0.f) - mb[hrow];
@@ -487,14 +489,19 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                             if constexpr (!FP8) {
                                 const uint32_t h = pack_bf16x2(a, c);
                                 ph[t >> 1][w] = h;
-                                if constexpr (LO) pl[t >> 1][w] = pack_bf16x2(a - bf16_lo(h), c - bf16_hi(h));
+                                if constexpr (EX > 0) {
+                                    const float a1 = a - bf16_lo(h), c1 = c - bf16_hi(h);
+                                    const uint32_t l = pack_bf16x2(a1, c1);
+                                    pl[0][t >> 1][w] = l;
+                                    pl[1][t >> 1][w] = pack_bf16x2(a1 - bf16_lo(l), c1 - bf16_hi(l));
+                                }
                             } else {
                                 const __half2 h = __floats2half2_rn(a, c);
                                 ph[t >> 1][w] = *reinterpret_cast<const uint32_t *>(&h);
-                                if constexpr (LO) {
+                                if constexpr (EX > 0) {
                                     const float2 f = __half22float2(h);
                                     const __half2 l = __floats2half2_rn(a - f.x, c - f.y);
-                                    pl[t >> 1][w] = *reinterpret_cast<const uint32_t *>(&l);
+                                    pl[0][t >> 1][w] = *reinterpret_cast<const uint32_t *>(&l);
                                 }
                             }
                         }
@@ -506,7 +513,8 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                     for (int g = 0; g < SG; ++g) {
                         const uint32_t vb = group_at(g) + GB;
                         mma_pv<FP8>(acc[NT], ph[g], ONES, ONES);
-                        if constexpr (LO) mma_pv<FP8>(acc[NT], pl[g], ONES, ONES);
+#pragma unroll
+                        for (int x = 0; x < EX; ++x) mma_pv<FP8>(acc[NT], pl[x][g], ONES, ONES);
                         bool odd = false;
                         if (lim_lo < lim_hi && tok[g] + kGroup - 1 > lim_lo && tok[g] <= lim_hi)
                             odd = strange_value<D, FP8>(smem + (vb - ring), lim_lo + 1 - tok[g], lim_hi - tok[g], lane);
@@ -517,9 +525,10 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                                 v_fragments<D, FP8>(f, vb, t, lane);
                                 mma_pv<FP8>(acc[t], ph[g], f[0], f[1]);
                                 mma_pv<FP8>(acc[t + 1], ph[g], f[2], f[3]);
-                                if constexpr (LO) {
-                                    mma_pv<FP8>(acc[t], pl[g], f[0], f[1]);
-                                    mma_pv<FP8>(acc[t + 1], pl[g], f[2], f[3]);
+#pragma unroll
+                                for (int x = 0; x < EX; ++x) {
+                                    mma_pv<FP8>(acc[t], pl[x][g], f[0], f[1]);
+                                    mma_pv<FP8>(acc[t + 1], pl[x][g], f[2], f[3]);
                                 }
                             }
                         } else {
@@ -537,7 +546,8 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                                     for (int z = 0; z < 2; ++z) {
                                         float d[4] = {0.f, 0.f, 0.f, 0.f};
                                         mma_pv<FP8>(d, ph[g], f[2 * z] & lo, f[2 * z + 1] & hi);
-                                        if constexpr (LO) mma_pv<FP8>(d, pl[g], f[2 * z] & lo, f[2 * z + 1] & hi);
+#pragma unroll
+                                        for (int x = 0; x < EX; ++x) mma_pv<FP8>(d, pl[x][g], f[2 * z] & lo, f[2 * z + 1] & hi);
 #pragma unroll
                                         for (int e = 0; e < 4; ++e)
                                             if (all || y <= lim[e >> 1]) acc[t + z][e] += d[e];

@@ -428,8 +428,8 @@ int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_t *cu_seqle
  *  A row that sees no key (an idle slot, no pages) is 0.  A position that a row does not see has no effect on
  *  it, whatever it holds.
  *  q bf16 [B, T, H, d]; o [B, T, H, d] (o_dtype: HLA_F32 or HLA_BF16).  Products on tensor cores with fp32
- *  sums; softmax statistics in fp32; the weights meet the values in 16 bits for a bf16 output and as two
- *  16-bit parts for an fp32 one.  The work is split over sequences and positions by the lengths on the
+ *  sums; softmax statistics in fp32; the weights meet the values in 16 bits for a bf16 output and in two or
+ *  three 16-bit parts, fp32's precision, for an fp32 one.  The work is split over sequences and positions by the lengths on the
  *  device, so one captured graph serves any lengths.  B <= 1024, T <= 8, H <= 1024.
  * -------------------------------------------------------------------------*/
 size_t attn_paged_decode_workspace_size(const hla_kv_cache *C, int B, int T, int H);

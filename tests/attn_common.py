@@ -102,10 +102,10 @@ def attention_tolerance(ref, mag, n_keys, d, score_size, o_dtype, cache_dtype):
     A score is a chain of d fp32 additions whose terms' magnitudes add up to score_size: off by d 2^-23 of it, and so is, to
     first order, the weight relative to itself, twice (numerator and sum); exp2 adds 2^-21.  A weight meets V rounded by half a
     step: bf16 2^-8, fp16 (8-bit cache) 2^-11 and for weights below 2^-28 nothing; an fp32 output keeps the rounded-off part to
-    the same relative precision again.  The sums over keys are chains of n_keys additions: n_keys 2^-23 of mag.  The output
+    the same relative precision again, twice with bf16.  The sums over keys are chains of n_keys additions: n_keys 2^-23 of mag.  The output
     rounds by 2^-8 (bf16) or 2^-24."""
     score = 2 * (d * 2.0 ** -23 * score_size + 2.0 ** -21)
     half = 2.0 ** -11 if cache_dtype == hla.HLA_E4M3 else 2.0 ** -8
     out_f32 = o_dtype == hla.HLA_F32
-    weight = half * half if out_f32 else half
+    weight = half ** (2 if cache_dtype == hla.HLA_E4M3 else 3) if out_f32 else half
     return (2.0 ** -24 if out_f32 else 2.0 ** -8) * np.abs(ref) + (score + weight + 2 * n_keys * 2.0 ** -23 + n_keys * 2.0 ** -28) * mag
