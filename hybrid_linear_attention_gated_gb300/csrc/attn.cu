@@ -45,6 +45,7 @@ struct AttnParams {
     int units_per_b;  // units of one sequence
     int min_share;    // least tiles per CTA
     int tile;         // keys per tile
+    uint32_t by_G, by_Hkv, by_row_tiles;  // for divided()
     int o_bf16;
 };
 
@@ -222,15 +223,15 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
         const int rem = t - s_pre[u.b] * p.units_per_b;
         int x = rem / u.nt;
         u.k = rem - x * u.nt;
-        u.rt = x % p.row_tiles;
-        x /= p.row_tiles;
-        u.hk = x % p.Hkv;
-        u.tq = x / p.Hkv;
+        const int y = divided(x, p.by_row_tiles);
+        u.rt = x - y * p.row_tiles;
+        u.tq = divided(y, p.by_Hkv);
+        u.hk = y - u.tq * p.Hkv;
         return u;
     };
     // row r of a unit: token t, head h of q and o
     auto row_at = [&](const Unit &u, int r) -> size_t {
-        const int t = p.sel ? u.tq : r / p.G, g = p.sel ? r : r % p.G;
+        const int t = p.sel ? u.tq : divided(r, p.by_G), g = p.sel ? r : r - t * p.G;
         return ((size_t)(u.b * p.T + t) * p.H + u.hk * p.G + g) * D;
     };
 
@@ -347,15 +348,15 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
 #pragma unroll
         for (int hrow = 0; hrow < 2; ++hrow) {
             const int r = rt * M + 16 * wr + 8 * hrow + i;
-            lim[hrow] = r >= rows ? -1 : (p.sel ? past + u.tq : past + r / p.G);
+            lim[hrow] = r >= rows ? -1 : past + (p.sel ? u.tq : divided(r, p.by_G));
             sc[hrow] = fmaxf(fabsf(scale), 1e-37f);  // above zero, so that -infinity stays itself
             if constexpr (!FP8) {
-                const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
+                if (scale < 0.f)
 #pragma unroll
-                for (int c = 0; c < KS; ++c) {
-                    qf[c][hrow] ^= flip;
-                    qf[c][2 + hrow] ^= flip;
-                }
+                    for (int c = 0; c < KS; ++c) {
+                        qf[c][hrow] ^= 0x80008000u;
+                        qf[c][2 + hrow] ^= 0x80008000u;
+                    }
             } else {
                 uint32_t big = 0;
 #pragma unroll
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                         bool odd = false;
                         if (lim_lo < lim_hi && tok[g] + kGroup - 1 > lim_lo && tok[g] <= lim_hi)
                             odd = strange_value<D, FP8>(smem + (vb - ring), lim_lo + 1 - tok[g], lim_hi - tok[g], lane);
-                        if (!odd) {
+                        if (__builtin_expect(!odd, 1)) {
 #pragma unroll
                             for (int t = 0; t < NT; t += 2) {
                                 uint32_t f[4];
@@ -772,6 +773,7 @@ int run_attn(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const i
     p.row_tiles = (rows + M - 1) / M;
     p.units_per_b = (sparse ? T : 1) * p.Hkv * p.row_tiles;
     p.min_share = 1;
+    p.by_G = divisor(p.G); p.by_Hkv = divisor(p.Hkv); p.by_row_tiles = divisor(p.row_tiles);
     p.o_bf16 = o_dtype == HLA_BF16;
     p.tile = C->head_dim == 128 ? (fp8 ? 4 * warp_keys<128, true>() : 4 * warp_keys<128, false>())
                                 : (fp8 ? 4 * warp_keys<64, true>() : 4 * warp_keys<64, false>());

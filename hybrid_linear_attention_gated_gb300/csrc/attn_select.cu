@@ -38,6 +38,7 @@ struct SelectParams {
     int max_blocks, n_pages, pshift;
     int n_select, n_first, n_last;
     int stride, groups;
+    uint32_t by_G, by_Hkv, by_T;  // for divided()
 };
 
 // Blocks that token t of a sequence sees.
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
         a.b = lo;
         a.groups = s_pre[lo + 1] - s_pre[lo];
         const int rem = x - s_pre[lo] * p.Hkv;
-        a.g = rem / p.Hkv;  // the heads of a group one after another: their bounds are neighbours in memory
+        a.g = divided(rem, p.by_Hkv);  // the heads of a group one after another: their bounds are neighbours in memory
         a.hk = rem - a.g * p.Hkv;
         a.nb = visible_blocks(p, lo, p.T - 1);
         return a;
@@ -166,7 +167,8 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
 #pragma unroll
         for (int hrow = 0; hrow < 2; ++hrow) {
             const int r = i + 8 * hrow;
-            const int t = t0 + (parts == 1 ? r / p.G : 0), g = parts == 1 ? r % p.G : part * 16 + r;
+            const int tl = divided(r, p.by_G);
+            const int t = t0 + (parts == 1 ? tl : 0), g = parts == 1 ? r - tl * p.G : part * 16 + r;
             const bool on = t < p.T && g < p.G && (parts > 1 || r < per * p.G);
             const uint16_t *src = p.q + (on ? ((size_t)(use.b * p.T + t) * p.H + use.hk * p.G + g) * D : 0);
 #pragma unroll
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
     constexpr int CPL = D / 32;                          // channels per lane
     constexpr unsigned ALL = 0xffffffffu;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.x, hk = row % p.Hkv, t = row / p.Hkv % p.T, b = row / p.Hkv / p.T;
+    const int row = blockIdx.x, bt = divided(row, p.by_Hkv), b = divided(bt, p.by_T), hk = row - bt * p.Hkv, t = bt - b * p.T;
     int32_t *sel = p.sel + (size_t)row * p.n_select;
 
     // what the score kernel does not write, before waiting for it: lengths and the query's size
@@ -628,6 +630,7 @@ extern "C" int attn_select_blocks(const hla_kv_cache *C, int B, int T, int H, in
     p.max_blocks = max_blocks; p.n_pages = C->n_pages; p.pshift = page_shift(C->page_size);
     p.n_select = n_select; p.n_first = n_first; p.n_last = n_last;
     p.stride = (int)row_stride(max_blocks);
+    p.by_G = divisor(p.G); p.by_Hkv = divisor(p.Hkv); p.by_T = divisor(T);
     p.groups = (max_blocks + kGroupBlocks - 1) / kGroupBlocks;
     const size_t rows = (size_t)B * T * p.Hkv;
     p.exact = static_cast<unsigned long long *>(ws);

@@ -26,7 +26,8 @@ struct AppendParams {
     const double *inv_freq;
     int N, B, H, Hkv, pshift, n_pages, max_blocks;
     int half;                 // rotated channel pairs per head (0: none)
-    int heads_per_cta, q_tokens, kv_ctas;
+    int heads_per_cta, q_tokens, kv_ctas, head_groups;
+    uint32_t by_half, by_H, by_head_groups;  // for divided()
 };
 
 // Fraction of a turn per position, in units of 2^-64 turn.
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendPara
         }
         __syncthreads();
         for (int x = tid; x < nt * p.half; x += kThreads) {
-            const int t = x / p.half, h = x % p.half;
+            const int t = divided(x, p.by_half), h = x - t * p.half;
             s_cs[0][t][angle_at<D>(h)] = cos_sin(s_turn[h], s_pos[t]);
         }
         __syncthreads();
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendPara
             if (r0 != rl) load(r0);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                const int r = r0 + y * LANES, t = r / p.H;
+                const int r = r0 + y * LANES, t = divided(r, p.by_H);
                 if (r >= rows) break;
                 if (s_pos[t] < 0) continue;  // no sequence's token, or an idle one's: left as it was
                 const size_t o = ((size_t)n0 * p.H + r) * D;
@@ -257,8 +258,7 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendPara
     }
 
     // ---- one touched page, some kv heads.  Which: the u-th of all sequences' touched pages.
-    const int groups = (p.Hkv + p.heads_per_cta - 1) / p.heads_per_cta;
-    const int u = blockIdx.x / groups, h0 = (blockIdx.x % groups) * p.heads_per_cta;
+    const int u = divided(blockIdx.x, p.by_head_groups), h0 = (blockIdx.x - u * p.head_groups) * p.heads_per_cta;
     const int h1 = h0 + p.heads_per_cta < p.Hkv ? h0 + p.heads_per_cta : p.Hkv;
     if (tid == 0) s_b = -1;
     int base = 0;
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendPara
         auto angles = [&](int buf, int rr) {
             const int n = (r1 - rr < LANES ? r1 - rr : LANES) * p.half;
             for (int x = tid; x < n; x += kThreads) {
-                const int r = x / p.half, y = x - r * p.half;
+                const int r = divided(x, p.by_half), y = x - r * p.half;
                 s_cs[buf][r][angle_at<D>(y)] = cos_sin(s_turn[y], start + rr + r);
             }
         };
@@ -423,11 +423,13 @@ extern "C" int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_
     // heads of a page share its angles; one head per CTA until the pages alone fill the SMs
     p.heads_per_cta = 1;
     while (p.heads_per_cta < p.Hkv && pages * ((p.Hkv + 2 * p.heads_per_cta - 1) / (2 * p.heads_per_cta)) >= 8L * sm_count()) p.heads_per_cta *= 2;
-    const long kv = pages * ((p.Hkv + p.heads_per_cta - 1) / p.heads_per_cta);
+    p.head_groups = (p.Hkv + p.heads_per_cta - 1) / p.heads_per_cta;
+    const long kv = pages * p.head_groups;
+    p.by_half = divisor(p.half ? p.half : 1); p.by_H = divisor(p.H); p.by_head_groups = divisor(p.head_groups);
     p.q_tokens = 1;
     while (p.q_tokens < kMaxQTokens && N / (2 * p.q_tokens) >= 3L * sm_count()) p.q_tokens *= 2;
     const long qc = (N + p.q_tokens - 1) / p.q_tokens;
-    HLA_REQUIRE(kv + qc < (1L << 31), HLA_ERR_UNSUPPORTED);
+    HLA_REQUIRE(kv * p.head_groups < (1L << 31) && kv + qc < (1L << 31), HLA_ERR_UNSUPPORTED);
     p.kv_ctas = (int)kv;
     const bool fp8 = C->dtype == HLA_E4M3;
     const int D = C->head_dim;

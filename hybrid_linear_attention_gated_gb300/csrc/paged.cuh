@@ -10,7 +10,7 @@ namespace hla {
 
 constexpr int kMaxBatch = 1024;         // sequences per call (their length prefix sums sit in shared memory)
 constexpr int kMaxWindowTokens = 8;     // tokens per sequence, as the KDA speculative window
-constexpr float kE4m3Max = 448.f;
+constexpr int kMaxKvHeads = 256;
 
 // ----------------------------------------------------------------------------- host side
 
@@ -27,7 +27,7 @@ inline int check_cache(const hla_kv_cache *C, bool need_kv, bool need_bounds) {
     HLA_REQUIRE(C->n_pages >= 1 && C->kv_heads >= 1 && C->page_size >= 1 && C->head_dim >= 1, HLA_ERR_INVALID_ARG);
     HLA_REQUIRE(C->dtype == HLA_BF16 || C->dtype == HLA_E4M3, C->dtype == HLA_F32 ? HLA_ERR_UNSUPPORTED : HLA_ERR_INVALID_ARG);
     HLA_REQUIRE(C->head_dim == 64 || C->head_dim == 128, HLA_ERR_UNSUPPORTED);
-    HLA_REQUIRE(page_shift(C->page_size) >= 0, HLA_ERR_UNSUPPORTED);
+    HLA_REQUIRE(page_shift(C->page_size) >= 0 && C->kv_heads <= kMaxKvHeads, HLA_ERR_UNSUPPORTED);
     if (need_kv) {
         HLA_REQUIRE(C->k && C->v, HLA_ERR_INVALID_ARG);
         HLA_REQUIRE(aligned16(C->k) && aligned16(C->v), HLA_ERR_MISALIGNED);
@@ -52,6 +52,10 @@ inline int check_window(const hla_kv_cache *C, int B, int T, int H, int max_bloc
 }
 
 // ----------------------------------------------------------------------------- device side
+
+// x / d for x d < 2^31 by a multiplication: a few instructions, where a short kernel pays for each one's fetch.
+__host__ __device__ constexpr uint32_t divisor(int d) { return (uint32_t)(((1ull << 31) + d - 1) / d); }
+__device__ __forceinline__ int divided(int x, uint32_t by) { return (int)__umulhi(2u * (uint32_t)x, by); }
 
 // Four e4m3 values as fp16 (exact): bytes 0, 1 in lo and 2, 3 in hi.
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t &lo, uint32_t &hi) {

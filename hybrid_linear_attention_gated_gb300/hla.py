@@ -132,7 +132,7 @@ def _stream(s):
     if s is None:
         import torch
         # the current stream's handle without a Stream object around it (0.1 us instead of 2.9)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -296,31 +296,36 @@ def hla_decode_layer_routing(L, M, ws):
     return a.value, b.value
 
 
-def _device():
-    """The current CUDA device, or -2 (no tensor's) before CUDA is in use."""
-    import torch
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+_torch = None
+
+
+def _torch_and_device():
+    """torch, and the current CUDA device, or -2 (no tensor's) before CUDA is in use."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch, _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else -2
 
 
 def _tensor(fn, name, t, dtype, n, dev):
     """The address of a torch tensor that a kernel may read as n values of dtype (others are refused), or t itself."""
     if t is None or isinstance(t, int):
         return t
-    if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
-        raise HlaError(fn, HLA_ERR_INVALID_ARG,
-                       f"{name} must be a contiguous {dtype} tensor of at least {n} elements on the current device; "
-                       f"got {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}, {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    raise HlaError(fn, HLA_ERR_INVALID_ARG,
+                   f"{name} must be a contiguous {dtype} tensor of at least {n} elements on the current device; "
+                   f"got {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}, {t.device}")
 
 
 def make_kv_cache(dtype, n_pages, page_size, kv_heads, head_dim, k, v, k_scale=None, v_scale=None, k_min=None,
                   k_max=None):
     """Build an hla_kv_cache descriptor; it keeps the tensors it was given alive."""
-    import torch
+    torch, dev = _torch_and_device()
     C = hla_kv_cache(dtype, n_pages, page_size, kv_heads, head_dim)
     kv = torch.float8_e4m3fn if dtype == HLA_E4M3 else torch.bfloat16
     n, m = n_pages * kv_heads * page_size * head_dim, n_pages * kv_heads * head_dim
-    dev = _device()
     C.tensors = (k, v, k_scale, v_scale, k_min, k_max)
     for name, t, dt, least in (("k", k, kv, n), ("v", v, kv, n), ("k_scale", k_scale, torch.float32, kv_heads),
                                ("v_scale", v_scale, torch.float32, kv_heads), ("k_min", k_min, torch.bfloat16, m),
@@ -331,8 +336,8 @@ def make_kv_cache(dtype, n_pages, page_size, kv_heads, head_dim, k, v, k_scale=N
 
 def kv_cache_append(C, N, B, cu_seqlens, past_len, max_blocks, block_table, H, q, k, v, rope_dim,
                     rope_interleaved, inv_freq, q_out, stream=None):
-    import torch
-    fn, bf, i32, dev = "kv_cache_append", torch.bfloat16, torch.int32, _device()
+    torch, dev = _torch_and_device()
+    fn, bf, i32 = "kv_cache_append", torch.bfloat16, torch.int32
     nq, nk = N * H * C.head_dim, N * C.kv_heads * C.head_dim
     return _check(fn, load().kv_cache_append(
         ctypes.byref(C), N, B, _tensor(fn, "cu_seqlens", cu_seqlens, i32, B + 1, dev),
@@ -349,8 +354,8 @@ def attn_paged_decode_workspace_size(C, B, T, H):
 
 def attn_paged_decode(C, B, T, H, max_blocks, block_table, past_len, scale, q, o, o_dtype, ws, ws_bytes,
                       stream=None):
-    import torch
-    fn, i32, dev, n = "attn_paged_decode", torch.int32, _device(), B * T * H * C.head_dim
+    torch, dev = _torch_and_device()
+    fn, i32, n = "attn_paged_decode", torch.int32, B * T * H * C.head_dim
     return _check(fn, load().attn_paged_decode(
         ctypes.byref(C), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
         _tensor(fn, "past_len", past_len, i32, B, dev), scale, _tensor(fn, "q", q, torch.bfloat16, n, dev),
@@ -364,8 +369,8 @@ def attn_select_blocks_workspace_size(C, B, T, H, max_blocks):
 
 def attn_select_blocks(C, B, T, H, max_blocks, block_table, past_len, n_select, n_first, n_last, q, sel, ws,
                        ws_bytes, stream=None):
-    import torch
-    fn, i32, dev = "attn_select_blocks", torch.int32, _device()
+    torch, dev = _torch_and_device()
+    fn, i32 = "attn_select_blocks", torch.int32
     return _check(fn, load().attn_select_blocks(
         ctypes.byref(C), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
         _tensor(fn, "past_len", past_len, i32, B, dev), n_select, n_first, n_last,
@@ -380,8 +385,8 @@ def attn_paged_sparse_workspace_size(C, B, T, H):
 
 def attn_paged_sparse(C, B, T, H, max_blocks, block_table, past_len, n_select, sel, scale, q, o, o_dtype, ws,
                       ws_bytes, stream=None):
-    import torch
-    fn, i32, dev, n = "attn_paged_sparse", torch.int32, _device(), B * T * H * C.head_dim
+    torch, dev = _torch_and_device()
+    fn, i32, n = "attn_paged_sparse", torch.int32, B * T * H * C.head_dim
     return _check(fn, load().attn_paged_sparse(
         ctypes.byref(C), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
         _tensor(fn, "past_len", past_len, i32, B, dev), n_select,

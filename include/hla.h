@@ -392,7 +392,7 @@ int hla_decode_layer_routing(const hla_layer *L, int M, const void *ws, const in
 typedef struct hla_kv_cache {
     int dtype;                 /* HLA_BF16, or HLA_E4M3 (8 bits, one scale per kv head) */
     int n_pages, page_size;    /* page_size 16, 32, 64 or 128 */
-    int kv_heads, head_dim;    /* head_dim 64 or 128 */
+    int kv_heads, head_dim;    /* kv_heads <= 256; head_dim 64 or 128 */
     void *k, *v;               /* [n_pages, kv_heads, page_size, head_dim] */
     const float *k_scale;      /* [kv_heads], HLA_E4M3 only: key = k_scale * stored */
     const float *v_scale;      /* [kv_heads], HLA_E4M3 only */

@@ -55,7 +55,7 @@ def test_descriptor_is_checked(lib, call):
     for kw in (dict(n_pages=0), dict(page_size=0), dict(kv_heads=0), dict(head_dim=0), dict(dtype=9), dict(k_min=None),
                dict(k_max=None)):
         assert call(lib, cache(**kw)) == INVALID, kw
-    for kw in (dict(page_size=48), dict(page_size=8), dict(page_size=256), dict(head_dim=96), dict(head_dim=256), dict(dtype=hla.HLA_F32)):
+    for kw in (dict(page_size=48), dict(page_size=8), dict(page_size=256), dict(head_dim=96), dict(head_dim=256), dict(kv_heads=257), dict(dtype=hla.HLA_F32)):
         assert call(lib, cache(**kw)) == UNSUPPORTED, kw
     assert call(lib, cache(k_min=FAKE + 2)) == MISALIGNED
     if call is select:
@@ -94,7 +94,6 @@ def test_own_arguments_are_checked(lib):
                dict(n_first=2 ** 31 - 1, n_last=2 ** 31 - 1)):
         assert select(lib, C, **kw) == INVALID, kw
     assert select(lib, C, max_blocks=65537) == UNSUPPORTED
-    assert select(lib, cache(kv_heads=1024), H=1024, B=1024, max_blocks=65536) == UNSUPPORTED
     for kw in (dict(N=0), dict(B=0), dict(H=9), dict(cu=None), dict(out=None), dict(k=None), dict(v=None), dict(f=None), dict(rope=-16),
                dict(inter=2)):
         assert append(lib, C, **kw) == INVALID, kw
