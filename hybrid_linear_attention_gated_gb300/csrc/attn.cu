@@ -21,103 +21,11 @@
 // of a unit; with 32 or 64 rows, two or four warps take 16 rows each and run all keys that they copied together.
 #include <type_traits>
 
-#include "paged.cuh"
+#include "attn.cuh"
+#include "tcgen05.cuh"
 
 namespace hla {
 namespace {
-
-constexpr int kGroup = 16;      // keys that are copied and masked together: never more than one page
-constexpr int kAttnThreads = 128;
-constexpr int kNoKeys = 1 << 30;  // token index of a group without keys: behind every row's last key
-constexpr float kLog2e = 1.44269504088896340736f;
-
-struct AttnParams {
-    const uint8_t *k, *v;
-    const float *k_scale, *v_scale;
-    const uint16_t *q;
-    void *o;
-    const int32_t *table, *past, *sel;  // sel: null for the dense form
-    float *part_o, *part_ml;
-    float scale;
-    int B, T, H, Hkv, G;
-    int max_blocks, n_pages, pshift, n_select;
-    int row_tiles;    // row tiles of a unit's rows
-    int units_per_b;  // units of one sequence
-    int min_share;    // least tiles per CTA
-    int tile;         // keys per tile
-    uint32_t by_G, by_Hkv, by_row_tiles;  // for divided()
-    int o_bf16;
-};
-
-// Cached tokens of sequence b; negative: an idle slot.  Held below 2^30 so that token indexes stay in 32 bits
-// (the table covers fewer).
-__device__ __forceinline__ int cached(const AttnParams &p, int b) {
-    const int x = p.past[b];
-    return x < kNoKeys - 16 ? x : kNoKeys - 16;
-}
-
-// Entries of its list that the token at position pos reads: no more than the blocks it sees.
-__device__ __forceinline__ int listed(const AttnParams &p, int pos) {
-    const int n = (pos >> p.pshift) + 1;
-    return n < p.n_select ? n : p.n_select;
-}
-
-// Tiles of one unit of a sequence with `past` cached tokens.
-__device__ __forceinline__ int unit_tiles(const AttnParams &p, int past) {
-    if (past < 0) return 0;
-    if (p.sel) return (int)((((long)listed(p, past + p.T - 1) << p.pshift) + p.tile - 1) / p.tile);
-    const long cap = (long)p.max_blocks << p.pshift;
-    const long len = (long)past + p.T < cap ? (long)past + p.T : cap;
-    return (int)((len + p.tile - 1) / p.tile);
-}
-
-// Prefix sums of the sequences' tiles per unit into pre[0..B], and their cached tokens into past[0..B-1] where
-// that is wanted; ends with a block barrier.
-__device__ __forceinline__ void tile_prefix(const AttnParams &p, int *pre, int *past = nullptr) {
-    const int lane = threadIdx.x;
-    if (lane < 32) {
-        int base = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const int b = b0 + lane;
-            const int c = b < p.B ? cached(p, b) : -1;
-            int x = unit_tiles(p, c);
-            if (past && b < p.B) past[b] = c;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, m);
-                if (lane >= m) x += y;
-            }
-            if (b < p.B) pre[b + 1] = base + x;
-            base += __shfl_sync(0xffffffffu, x, 31);
-        }
-        if (lane == 0) pre[0] = 0;
-    }
-    __syncthreads();
-}
-
-// Tiles that each CTA of the attention grid takes.
-__device__ __forceinline__ int cta_share(const AttnParams &p, int total, int grid) {
-    const int s = (int)(((long)total + grid - 1) / grid);
-    return s < p.min_share ? p.min_share : s;
-}
-
-// The sequence whose units hold tile t: pre[b] * units <= t < pre[b + 1] * units.
-__device__ __forceinline__ int find_sequence(const int *pre, int B, int units, int t) {
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] * units <= t) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
-__device__ __forceinline__ void store_out(const AttnParams &p, size_t at, float x, float y) {
-    if (p.o_bf16)
-        *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(p.o) + at) = pack_bf16x2(x, y);
-    else
-        *reinterpret_cast<float2 *>(reinterpret_cast<float *>(p.o) + at) = make_float2(x, y);
-}
 
 // Keys that a warp copies per stage: 32, or 16 where a key's row is 256 bytes.
 template <int D, bool FP8>
@@ -652,7 +560,7 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p, int M,
     const bool idle = (nt > 0 && c_first == c_last) || row >= (p.sel ? p.G : p.T * p.G);  // written whole, or no row
     if (idle && (blockIdx.x | blockIdx.y) != 0) return;
     pdl_wait_trigger();
-    if (idle) return;
+    if (idle || p.force_timeout) return;
     const int t = p.sel ? tq : row / p.G, g = p.sel ? row : row % p.G;
     const size_t to = ((size_t)(b * p.T + t) * p.H + hk * p.G + g) * D;
 
@@ -698,15 +606,21 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p, int M,
     else reinterpret_cast<float *>(p.o)[to + tid] = o * inv;
 }
 
-// Rows of a unit's tile: the smallest of 16, 32, 64 that holds them, 64 at most.
-int tile_rows(int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
+// Rows of a unit's tile: the smallest of 16, 32, 64 that holds them, 64 at most; 128 on tcgen05 (attn_tc.cu).
+int tile_rows(int rows, bool tc) { return tc ? kTcRows : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-int attn_grid_limit() { return 4 * sm_count(); }  // the most of any configuration
+// More than 32 rows of bf16 keys and a bf16 output go to tcgen05.
+bool use_tc(int rows, int dtype, int o_dtype) { return rows > 32 && dtype == HLA_BF16 && o_dtype == HLA_BF16; }
+
+int attn_grid_limit(bool tc) { return (tc ? 2 : 3) * sm_count(); }  // the most of any configuration
+
+size_t pieces_bytes(int M, bool tc, int d) { return (size_t)2 * attn_grid_limit(tc) * M * (d + 2) * sizeof(float); }
 
 size_t attn_ws(const hla_kv_cache *C, int B, int T, int H, bool sparse) {
     if (check_cache(C, false, false) != HLA_OK || check_window(C, B, T, H, 1) != HLA_OK) return 0;
-    const int G = H / C->kv_heads, M = tile_rows(sparse ? G : T * G);
-    return (size_t)2 * attn_grid_limit() * M * (C->head_dim + 2) * sizeof(float);
+    const int G = H / C->kv_heads, rows = sparse ? G : T * G;
+    const size_t a = pieces_bytes(tile_rows(rows, false), false, C->head_dim), b = pieces_bytes(kTcRows, true, C->head_dim);
+    return use_tc(rows, C->dtype, HLA_BF16) && b > a ? b : a;  // for either output type
 }
 
 template <int D, bool FP8, int WR>
@@ -769,26 +683,35 @@ int run_attn(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const i
     p.B = B; p.T = T; p.H = H; p.Hkv = C->kv_heads; p.G = H / C->kv_heads;
     p.max_blocks = max_blocks; p.n_pages = C->n_pages; p.pshift = page_shift(C->page_size);
     p.n_select = sparse ? n_select : 0;
-    const int rows = sparse ? p.G : T * p.G, M = tile_rows(rows);
+    const int rows = sparse ? p.G : T * p.G;
+    const bool tc = use_tc(rows, C->dtype, o_dtype);
+    const int M = tile_rows(rows, tc);
     p.row_tiles = (rows + M - 1) / M;
     p.units_per_b = (sparse ? T : 1) * p.Hkv * p.row_tiles;
     p.min_share = 1;
     p.by_G = divisor(p.G); p.by_Hkv = divisor(p.Hkv); p.by_row_tiles = divisor(p.row_tiles);
     p.o_bf16 = o_dtype == HLA_BF16;
-    p.tile = C->head_dim == 128 ? (fp8 ? 4 * warp_keys<128, true>() : 4 * warp_keys<128, false>())
+    p.tile = tc ? kTcTile
+             : C->head_dim == 128 ? (fp8 ? 4 * warp_keys<128, true>() : 4 * warp_keys<128, false>())
                                 : (fp8 ? 4 * warp_keys<64, true>() : 4 * warp_keys<64, false>());
     const long per_unit = ((long)(sparse ? n_select : max_blocks) * C->page_size + p.tile - 1) / p.tile;
     const long most = (long)B * p.units_per_b * per_unit;  // tiles, if every sequence filled its table
     HLA_REQUIRE(most < (1L << 31) && (long)C->n_pages * C->kv_heads * (C->page_size / kGroup) < (1L << 31), HLA_ERR_UNSUPPORTED);
     const int D = C->head_dim;
     p.part_o = static_cast<float *>(ws);
-    p.part_ml = p.part_o + (size_t)2 * attn_grid_limit() * M * D;
+    p.part_ml = p.part_o + (size_t)2 * attn_grid_limit(tc) * M * D;
+    if (tc) {
+        p.status = device_status_word();
+        HLA_REQUIRE(p.status, HLA_ERR_CUDA);
+        p.force_timeout = wait_timeout_forced();
+    }
 
     set_variant("attn_%s<d%d,%s,m%d>", sparse ? "sparse" : "paged", D, fp8 ? "e4m3" : "bf16", M);
     // the join always follows attn_kernel programmatically (HLA_PDL=0 turns that off as everywhere)
     PdlChain chain(st, pdl_default(1));
     int grid = 0;
-    cudaError_t ce = D == 128 ? (fp8 ? launch_rows<128, true>(M, p, &grid, most, st) : launch_rows<128, false>(M, p, &grid, most, st))
+    cudaError_t ce = tc ? launch_attn_tc(D, p, &grid, most, st)
+                     : D == 128 ? (fp8 ? launch_rows<128, true>(M, p, &grid, most, st) : launch_rows<128, false>(M, p, &grid, most, st))
                               : (fp8 ? launch_rows<64, true>(M, p, &grid, most, st) : launch_rows<64, false>(M, p, &grid, most, st));
     e = launched(ce);
     if (e != HLA_OK) return e;

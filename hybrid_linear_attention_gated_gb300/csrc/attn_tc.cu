@@ -1,0 +1,388 @@
+// The paged attention of more than 32 query rows per kv head (a speculative window of a model with few kv heads) on
+// tcgen05: from there on mma.sync, not memory, bounds the warps' form in attn.cu.
+//
+// A CTA owns 128 rows (padded), one per thread, and runs the same equal share of tiles as attn_kernel, 128 keys a
+// tile.  Per tile
+//     S = Q K^T        tcgen05.mma 128 x 128 x d, both operands K-major in shared memory, S in tensor memory;
+//     P = 2^(S - m)    a thread reads its row of S, keeps m and l, writes its row of P as bf16 to shared memory;
+//     O += P V         tcgen05.mma 128 x d x 128, V as it lies in the cache (its channels contiguous: MN-major).
+// O stays in tensor memory.  A row's m is raised, and O rescaled, only when a score passes it by 2^8: until then the
+// weights stay below 2^8, which bf16 and the fp32 sums hold as well as 1.
+//
+// Keys and values come through two stages of cp.async in the 128-byte swizzle: tile i + 1 is copied while tile i is
+// worked on.  One 128 x 128 tile of d = 128 takes the tensor core about 500 cycles, the 16384 exponentials 1024, and
+// HBM about 2800 for its 64 KB.
+//
+// The keys that all rows see (up to past) go through the tiles; the window's own T - 1 last keys, which a row sees in
+// part, are taken up on CUDA cores at the end of the unit, row by row, so that no weight of zero meets their values.
+//
+// Every wait is bounded (as in tc_gemm.cu): a wait that gives up sets the device status word, and after the next
+// block barrier every thread leaves the loop; the MMAs issued are waited for once more before tensor memory is freed.
+#include "attn.cuh"
+#include "tcgen05.cuh"
+
+namespace hla {
+namespace {
+
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s of %globaltimer per bounded wait
+constexpr uint32_t kSub = kTcRows * 128;     // bytes of 128 rows of one 128-byte-wide swizzled block
+
+template <int D>
+__host__ __device__ constexpr uint32_t tc_smem() {  // Q, 2 x K, 2 x V, P
+    return 5 * (D / 64) * kSub + 2 * kSub;
+}
+
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(const AttnParams p) {
+    constexpr int RB = 2 * D, CPR = RB / 16, GB = kGroup * RB, NB = D / 64, M = kTcRows;
+    constexpr uint32_t IS = idesc_bf16(M, kTcTile), IO = idesc_bf16(M, D, true);
+    constexpr unsigned ALL = 0xffffffffu;
+    extern __shared__ __align__(1024) uint8_t smem[];  // no static shared memory in front of it: two CTAs of d = 64 just fit
+    uint8_t *const sQ = smem, *const sK = sQ + NB * kSub, *const sV = sK + 2 * NB * kSub, *const sP = sV + 2 * NB * kSub;
+    uint64_t &bar_s = reinterpret_cast<uint64_t *>(sP + 2 * kSub)[0], &bar_o = (&bar_s)[1], &bar_end = (&bar_s)[2];
+    uint32_t &s_tmem = *reinterpret_cast<uint32_t *>(&bar_s + 3);
+    int (*const s_on)[8] = reinterpret_cast<int (*)[8]>(&bar_s + 4);  // [2]: rows with a key of each staged group
+    int *const s_pre = &s_on[2][0], *const s_past = s_pre + p.B + 1;  // [B + 1], [B]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    pdl_wait();
+    if (p.force_timeout) {
+        if (blockIdx.x == 0 && tid == 0) {
+            mbar_init(&bar_s, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            mbar_wait_for(&bar_s, 0, 1000000ull, p.status);  // nothing arrives: gives up after 1 ms
+            asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(&bar_s)) : "memory");
+        }
+        return;
+    }
+    tile_prefix(p, s_pre, s_past);
+    const int total = s_pre[p.B] * p.units_per_b;
+    const int share = cta_share(p, total, gridDim.x);
+    const int begin = (long)share * blockIdx.x < total ? share * (int)blockIdx.x : total;
+    const int N = share < total - begin ? share : total - begin;  // this CTA's tiles
+    if (N == 0) return;
+    const int rows = p.sel ? p.G : p.T * p.G;
+
+    if (tid == 0) {
+        mbar_init(&bar_s, 1);
+        mbar_init(&bar_o, 1);
+        mbar_init(&bar_end, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async();
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_u32(&s_tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();  // only now: a dependent that allocates tensor memory must not get it before this CTA
+    const uint32_t tm_s = s_tmem, tm_o = s_tmem + kTcTile;  // 128 columns of S, D of O
+    const uint32_t my_lanes = (uint32_t)(warp * 32) << 16;
+
+    struct Unit {
+        int b, tq, hk, rt, nt, k;
+    };
+    auto unit_of = [&](int t) {
+        Unit u;
+        u.b = find_sequence(s_pre, p.B, p.units_per_b, t);
+        u.nt = s_pre[u.b + 1] - s_pre[u.b];
+        const int rem = t - s_pre[u.b] * p.units_per_b;
+        const int x = rem / u.nt;
+        u.k = rem - x * u.nt;
+        const int y = divided(x, p.by_row_tiles);
+        u.rt = x - y * p.row_tiles;
+        u.tq = divided(y, p.by_Hkv);
+        u.hk = y - u.tq * p.Hkv;
+        return u;
+    };
+    auto row_at = [&](const Unit &u, int r) -> size_t {
+        const int t = p.sel ? u.tq : divided(r, p.by_G), g = p.sel ? r : r - t * p.G;
+        return ((size_t)(u.b * p.T + t) * p.H + u.hk * p.G + g) * D;
+    };
+    // page of logical block blk of sequence b, or -1
+    auto page_of = [&](int b, int blk) -> int {
+        if (blk < 0 || blk >= p.max_blocks) return -1;
+        const int page = p.table[(size_t)b * p.max_blocks + blk];
+        return page < p.n_pages ? page : -1;
+    };
+
+    // ---- copies, as in attn_kernel: two groups of 16 keys per warp and tile, lane l looks up group l of each 32
+    auto look = [&](int g0, int *at, int *on) {
+        const int g = g0 + lane;
+        *at = -1;
+        *on = 0;
+        if (g >= N * 2) return;
+        const Unit u = unit_of(begin + (g >> 1));
+        const int key = u.k * kTcTile + warp * 32 + (g & 1) * kGroup;
+        const int limit = s_past[u.b] + (p.sel ? u.tq : 0);  // last position that all rows see
+        int blk = key >> p.pshift;
+        if (p.sel) blk = blk < listed(p, limit) ? p.sel[((size_t)(u.b * p.T + u.tq) * p.Hkv + u.hk) * p.n_select + blk] : -1;
+        const int page = page_of(u.b, blk);
+        if (page < 0) return;
+        const int row = key & ((1 << p.pshift) - 1), seen = limit - ((blk << p.pshift) + row) + 1;
+        *on = seen < 0 ? 0 : seen < kGroup ? seen : kGroup;
+        if (*on) *at = ((page * p.Hkv + u.hk) << (p.pshift - 4)) + (row >> 4);
+    };
+    int at_now, on_now, at_next, on_next;
+    look(0, &at_now, &on_now);
+    uint32_t to[GB / 512];  // this lane's chunks of a group in a stage
+#pragma unroll
+    for (int x = 0; x < GB / 512; ++x) {
+        const int r = (x * 32 + lane) / CPR, c = (x * 32 + lane) % CPR;
+        to[x] = (c >> 3) * kSub + (warp * 32 + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
+    }
+    const uint32_t k_ring = smem_u32(sK), v_ring = smem_u32(sV);
+    auto issue = [&](int ti) {
+        const uint32_t st = (ti & 1) * NB * kSub;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int src = (ti * 2 + g) & 31;
+            const int from16 = __shfl_sync(ALL, at_now, src), on = __shfl_sync(ALL, on_now, src);
+            const size_t from = (size_t)(from16 < 0 ? 0 : from16) * GB + lane * 16;
+#pragma unroll
+            for (int x = 0; x < GB / 512; ++x) {
+                const bool in = (x * 32 + lane) / CPR < on;
+                const uint32_t d = st + to[x] + g * kGroup * 128;
+                cp_async16_or_zero(k_ring + d, in ? p.k + from + x * 512 : p.k, in);
+                cp_async16_or_zero(v_ring + d, in ? p.v + from + x * 512 : p.v, in);
+            }
+            if (lane == 0) s_on[ti & 1][2 * warp + g] = on;
+        }
+        const int seen = (ti + 1) * 2;
+        if ((seen & 31) == 16) look(seen + 16, &at_next, &on_next);
+        if ((seen & 31) == 0) {
+            at_now = at_next;
+            on_now = on_next;
+        }
+    };
+
+    issue(0);
+    cp_async_commit();
+    const float sc = fmaxf(fabsf(p.scale) * kLog2e, 1e-37f);  // a negative scale is taken into the query
+    bool ok = true, all_ok = true;                            // no wait of this thread, of any thread, has given up
+    for (int done = 0; done < N && all_ok;) {
+        const Unit u = unit_of(begin + done);
+        const int k0 = u.k, k1 = u.nt - k0 < N - done ? u.nt : k0 + (N - done), first = done;
+        done += k1 - k0;
+        const int past = s_past[u.b], lim_lo = p.sel ? past + u.tq : past, lim_hi = p.sel ? lim_lo : past + p.T - 1;
+        const int r = u.rt * M + tid;  // this thread's row of the unit
+        const bool live = r < rows;
+
+        // ---- Q: thread's own row into the K-major tile (the last unit's products with it are complete)
+        {
+            const uint16_t *src = p.q + (live ? row_at(u, r) : 0);
+            const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+            for (int c = 0; c < CPR; ++c) {
+                uint4 w = live ? ld_act_v4(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+                w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
+                *reinterpret_cast<uint4 *>(sQ + (c >> 3) * kSub + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) = w;
+            }
+        }
+        float mb = 0.f, l = 0.f;  // m times the scale
+        bool none = true;         // no score yet
+        for (int it = first; it < done; ++it) {
+            const int st = it & 1;
+            cp_async_wait<0>();
+            fence_async();
+            tc_fence_before();
+            all_ok = __syncthreads_and(ok);  // tile `it` is in shared memory, and every thread is done with tile it - 1
+            if (!all_ok) break;
+            if (tid == 0) {
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    const uint32_t off = (c >> 2) * kSub + (c & 3) * 32;
+                    umma_bf16(tm_s, sw128_desc(smem_u32(sQ) + off), sw128_desc(k_ring + st * NB * kSub + off), IS, c > 0);
+                }
+                umma_commit(&bar_s);
+            }
+            // the other stage and P are free once the previous tile's output product is complete
+            if (it > 0) ok &= mbar_wait_for(&bar_o, (it - 1) & 1, kWaitNs, p.status);
+            __syncwarp();
+            if (it + 1 < N) issue(it + 1);
+            cp_async_commit();
+            ok &= mbar_wait_for(&bar_s, it & 1, kWaitNs, p.status);
+            __syncwarp();
+            tc_fence_after();
+
+            // ---- this thread's row of S
+            uint32_t sr[kTcTile];
+#pragma unroll
+            for (int c = 0; c < kTcTile; c += 32) tmem_ld32(tm_s + my_lanes + c, sr + c);
+            tmem_wait_ld();
+            float mx = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const int on = s_on[st][g];
+                if (on < kGroup) {
+#pragma unroll
+                    for (int x = 0; x < kGroup; ++x)
+                        if (x >= on) sr[16 * g + x] = 0xff800000u;  // -infinity
+                }
+#pragma unroll
+                for (int x = 0; x < kGroup; ++x) mx = fmaxf(mx, __uint_as_float(sr[16 * g + x]));
+            }
+            const float t = mx * sc;
+            if (none && mx != -INFINITY) {
+                mb = t;
+                none = false;
+            }
+            const bool far = !none && t > mb + 8.f;
+            if (__any_sync(ALL, far)) {  // (never in the unit's first tile, where O is not there yet)
+                const float a = far ? ex2(mb - t) : 1.f;
+                if (far) mb = t;
+                l *= a;
+                uint32_t o[32];
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    tmem_ld32(tm_o + my_lanes + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * a);
+                    tmem_st32(tm_o + my_lanes + c, o);
+                }
+                tmem_wait_st();
+            }
+            // ---- weights: rounded once to bf16, as in attn_kernel for a bf16 output
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < kTcTile / 8; ++c) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float a = ex2(fmaf(__uint_as_float(sr[8 * c + 2 * x]), sc, -mb)),
+                                b = ex2(fmaf(__uint_as_float(sr[8 * c + 2 * x + 1]), sc, -mb));
+                    ls[x] += a + b;
+                    w[x] = pack_bf16x2(a, b);
+                }
+                *reinterpret_cast<uint4 *>(sP + (c >> 3) * kSub + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            fence_async();
+            tc_fence_before();
+            all_ok = __syncthreads_and(ok);
+            if (!all_ok) break;
+            if (tid == 0) {
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kTcTile / 16; ++c)
+                    umma_bf16(tm_o, sw128_desc(smem_u32(sP) + (c >> 2) * kSub + (c & 3) * 32),
+                              sw128_desc_mn(v_ring + st * NB * kSub + c * 2048, kSub), IO, it > first || c > 0);
+                umma_commit(&bar_o);
+            }
+        }
+        if (!all_ok) break;
+        ok &= mbar_wait_for(&bar_o, (done - 1) & 1, kWaitNs, p.status);
+        __syncwarp();
+        tc_fence_after();
+
+        // ---- this thread's row of O, and the window's own keys
+        uint32_t o[D];
+#pragma unroll
+        for (int c = 0; c < D; c += 32) tmem_ld32(tm_o + my_lanes + c, o + c);
+        tmem_wait_ld();
+        tc_fence_before();
+        const int lim = live ? past + (p.sel ? u.tq : divided(r, p.by_G)) : -1;
+        if (k1 == u.nt)
+            for (int c = lim_lo + 1; c <= lim_hi; ++c) {
+                const int pg = page_of(u.b, c >> p.pshift);
+                if (pg < 0 || c > lim) continue;
+                const size_t at = ((((size_t)pg * p.Hkv + u.hk) << p.pshift) + (c & ((1 << p.pshift) - 1))) * D;
+                const uint16_t *kr = reinterpret_cast<const uint16_t *>(p.k) + at, *vr = reinterpret_cast<const uint16_t *>(p.v) + at;
+                float s = 0.f;
+#pragma unroll 4
+                for (int x = 0; x < CPR; ++x) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(sQ + (x >> 3) * kSub + tid * 128 + (((x & 7) ^ (tid & 7)) << 4)),
+                                b = ld_act_v4(kr + 8 * x);
+                    s += bf16_lo(a.x) * bf16_lo(b.x) + bf16_hi(a.x) * bf16_hi(b.x);
+                    s += bf16_lo(a.y) * bf16_lo(b.y) + bf16_hi(a.y) * bf16_hi(b.y);
+                    s += bf16_lo(a.z) * bf16_lo(b.z) + bf16_hi(a.z) * bf16_hi(b.z);
+                    s += bf16_lo(a.w) * bf16_lo(b.w) + bf16_hi(a.w) * bf16_hi(b.w);
+                }
+                const float t = s * sc;
+                float a = 1.f;
+                if (t != -INFINITY && (none || t > mb)) {
+                    a = none ? 1.f : ex2(mb - t);
+                    mb = t;
+                    none = false;
+                }
+                const float w = ex2(t - mb);
+                l = l * a + w;
+#pragma unroll
+                for (int x = 0; x < CPR; ++x) {
+                    const uint4 b = ld_act_v4(vr + 8 * x);
+                    const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t &lo = o[8 * x + 2 * y], &hi = o[8 * x + 2 * y + 1];
+                        lo = __float_as_uint(fmaf(w, bf16_lo(bw[y]), __uint_as_float(lo) * a));
+                        hi = __float_as_uint(fmaf(w, bf16_hi(bw[y]), __uint_as_float(hi) * a));
+                    }
+                }
+            }
+        // ---- out: the unit whole, or a piece for the join (slots as in attn_kernel).  A row of NaN scores only has no
+        // maximum, but it has seen keys and is NaN.
+        const float top = l != l ? INFINITY : none ? -INFINITY : mb;
+        if (live && k0 == 0 && k1 == u.nt) {
+            const float inv = top == -INFINITY ? 0.f : 1.f / l;
+            uint16_t *dst = static_cast<uint16_t *>(p.o) + row_at(u, r);
+#pragma unroll
+            for (int c = 0; c < D; c += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    w[x] = pack_bf16x2(__uint_as_float(o[c + 2 * x]) * inv, __uint_as_float(o[c + 2 * x + 1]) * inv);
+                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else if (live) {
+            const size_t slot = (2 * (size_t)blockIdx.x + (k0 == 0)) * M + tid;
+#pragma unroll
+            for (int c = 0; c < D; c += 4)
+                *reinterpret_cast<uint4 *>(p.part_o + slot * D + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+            *reinterpret_cast<float2 *>(p.part_ml + slot * 2) = make_float2(top, l);
+        }
+    }
+    // After a wait that gave up, products may still run: they read operands that are in shared memory, so they end.
+    cp_async_wait<0>();
+    if (!all_ok && tid == 0) {
+        umma_commit(&bar_end);
+        mbar_wait_for(&bar_end, 0, 8 * kWaitNs, p.status);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(s_tmem) : "memory");
+}
+
+template <int D>
+cudaError_t launch(const AttnParams &p, int *grid, long most, cudaStream_t st) {
+    const size_t fixed = tc_smem<D>() + 32 + 64, smem = fixed + (2 * p.B + 1) * sizeof(int);
+    // the shared-memory limit is a per-device attribute: raise it once on every device used
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !done[dev]) {
+        e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(fixed + (2 * kMaxBatch + 1) * sizeof(int)));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) done[dev] = true;
+    }
+    const int slots = (D == 64 ? 2 : 1) * sm_count();
+    *grid = most < slots ? (int)most : slots;
+    return launch_kernel(attn_tc_kernel<D>, dim3(*grid), dim3(kAttnThreads), smem, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(int D, const AttnParams &p, int *grid, long most, cudaStream_t st) {
+    return D == 128 ? launch<128>(p, grid, most, st) : launch<64>(p, grid, most, st);
+}
+
+}  // namespace hla

@@ -54,6 +54,8 @@ def test_decode_matches_oracle(case, dtype, o_dtype):
     o = p.decode(o_dtype)
     rows = T * H // Hkv
     m = 16 if rows <= 16 else 32 if rows <= 32 else 64
+    if rows > 32 and dtype == hla.HLA_BF16 and o_dtype == hla.HLA_BF16:
+        m = 128  # tcgen05
     assert hla.hla_last_variant() == f"attn_paged<d{d},{'e4m3' if dtype == hla.HLA_E4M3 else 'bf16'},m{m}>"
     torch.cuda.synchronize()
     check(p, o, o_dtype)
@@ -67,7 +69,25 @@ def test_many_ragged_sequences(T, H, Hkv):
     g = np.random.default_rng(5)
     past = [int(x) for x in g.integers(-1, 700, size=70)]
     p = Problem(require_gpu(), past, T, H, Hkv, 64, 32, seed=9).upload()
-    check(p, p.decode(hla.HLA_F32), hla.HLA_F32)
+    for o_dtype in (hla.HLA_F32, hla.HLA_BF16):
+        check(p, p.decode(o_dtype), o_dtype)
+
+
+@pytest.mark.parametrize("d,T,H,Hkv,page", [(128, 8, 8, 1, 64), (64, 8, 32, 1, 16), (128, 5, 40, 2, 128), (64, 3, 16, 1, 32)])
+def test_tcgen05_rows_over_lengths(d, T, H, Hkv, page):
+    """More than 32 rows of a bf16 cache: lengths around the 128-key tiles, windows across page and tile borders, negative
+    scale, pieces joined across CTAs, and the status word stays clear."""
+    dev = require_gpu()
+    past = [0, 1, 120, 121, 126, 127, 128, 129, 255, 256, 511, 3000, -1, 900]
+    p = Problem(dev, past, T, H, Hkv, d, page, seed=d + T).upload()
+    for scale in (p.scale, -0.05, 0.7):
+        p.scale = scale
+        o = p.decode(hla.HLA_BF16)
+        assert hla.hla_last_variant().endswith("m128>")
+        torch.cuda.synchronize()
+        assert hla.hla_device_status() == 0
+        check(p, o, hla.HLA_BF16)
+        assert torch.equal(bits(o), bits(p.decode(hla.HLA_BF16)))
 
 
 @pytest.mark.parametrize("dtype", [hla.HLA_BF16, hla.HLA_E4M3])
@@ -114,10 +134,11 @@ def test_masked_places_may_hold_anything():
     problem's poison), whole foreign pages; a row sees its own infinities."""
     dev = require_gpu()
     for dtype in (hla.HLA_BF16, hla.HLA_E4M3):
-        for H, Hkv in ((4, 2), (16, 2), (16, 1)):  # 16-, 32- and 64-row tiles at T = 4
+        for H, Hkv in ((4, 2), (16, 2), (16, 1)):  # 16-, 32- and 64-row (or tcgen05) tiles at T = 4
             for past in (62, 64, 13):              # the window across a page and tile border, at its start, inside
                 p = Problem(dev, [past, 100], 4, H, Hkv, 64, 16, dtype, seed=past)
-                clean = Problem(dev, [past, 100], 4, H, Hkv, 64, 16, dtype, seed=past).upload().decode(hla.HLA_F32)
+                q = Problem(dev, [past, 100], 4, H, Hkv, 64, 16, dtype, seed=past).upload()
+                clean, clean16 = q.decode(hla.HLA_F32), q.decode(hla.HLA_BF16)
                 for t, what in ((2, float("nan")), (3, float("inf") if dtype == hla.HLA_BF16 else float("nan"))):
                     c = past + t
                     p.v[p.table[0, c // 16], :, c % 16] = torch.tensor(what).to(p.v.dtype)
@@ -129,6 +150,9 @@ def test_masked_places_may_hold_anything():
                 assert torch.allclose(o[0, :2], clean[0, :2], rtol=1e-4, atol=1e-5)
                 assert torch.equal(o[1], clean[1])
                 assert torch.isnan(o[0, 2:]).all()
+                o = p.decode(hla.HLA_BF16)
+                assert torch.isfinite(o[0, :2]).all() and torch.isnan(o[0, 2:]).all() and torch.equal(o[1], clean16[1])
+                assert torch.allclose(o[0, :2].float(), clean16[0, :2].float(), rtol=2.0 ** -6, atol=2.0 ** -8)
 
 
 def test_blocks_without_a_page_hold_no_keys():
@@ -209,24 +233,25 @@ def test_cache_beyond_32_bit_offsets():
     check(p, o, hla.HLA_F32)
 
 
-def test_one_captured_graph_serves_any_lengths_and_pages():
+@pytest.mark.parametrize("H,Hkv,o_dtype", [(8, 2, hla.HLA_F32), (40, 2, hla.HLA_BF16)])
+def test_one_captured_graph_serves_any_lengths_and_pages(H, Hkv, o_dtype):
     dev = require_gpu()
-    p = Problem(dev, [700, 300, 20], 2, 8, 2, 64, 32, seed=11, poison=False).upload()
-    o = torch.empty(3, 2, 8, 64, device=dev)
-    ws = torch.empty(hla.attn_paged_decode_workspace_size(p.C, 3, 2, 8), dtype=torch.uint8, device=dev)
+    p = Problem(dev, [700, 300, 20], 2, H, Hkv, 64, 32, seed=11, poison=False).upload()
+    o = torch.empty(3, 2, H, 64, device=dev, dtype=torch.float32 if o_dtype == hla.HLA_F32 else BF16)
+    ws = torch.empty(hla.attn_paged_decode_workspace_size(p.C, 3, 2, H), dtype=torch.uint8, device=dev)
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
-        p.decode(hla.HLA_F32, ws=ws, o=o)
+        p.decode(o_dtype, ws=ws, o=o)
     side.synchronize()
     graphs = []
     for _ in range(2):  # two graphs that share the workspace, replayed one after the other
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            p.decode(hla.HLA_F32, ws=ws, o=o)
+            p.decode(o_dtype, ws=ws, o=o)
         graphs.append(g)
     for past in ([700, 300, 20], [1, 640, -1], [0, 0, 0], [650, 2, 33]):
         p.D["past"].copy_(torch.tensor(past, dtype=I32))
-        eager = p.decode(hla.HLA_F32)
+        eager = p.decode(o_dtype)
         for g in graphs:
             ws.fill_(255)
             o.fill_(3.0)
