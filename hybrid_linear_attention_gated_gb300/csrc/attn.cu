@@ -8,7 +8,8 @@
 // Every cached row is needed once by the T x G query rows that share its kv head (G = H / Hkv), so the
 // step is bound by reading the cache: 2 d elements per key against 4 d T G operations.  The products
 // run on mma.sync (one pass of 16 rows costs 256 tensor cycles per 64 keys of d = 128, against about
-// 1400 cycles of an SM's share of HBM for their 32 KB), which takes the rows in tiles of 16, 32 or 64.
+// 1400 cycles of an SM's share of HBM for their 32 KB), which takes the rows in tiles of 16, 32 or 64;
+// attn_tc.cu takes more on tcgen05.
 //
 // Work split.  A tile is 64 or 128 keys of one unit; a unit is (sequence, kv head, row tile), and for the
 // sparse form (sequence, token, kv head, row tile).  The lengths live on the device, so the grid is
@@ -609,17 +610,19 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p, int M,
 // Rows of a unit's tile: the smallest of 16, 32, 64 that holds them, 64 at most; 128 on tcgen05 (attn_tc.cu).
 int tile_rows(int rows, bool tc) { return tc ? kTcRows : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-// More than 32 rows of bf16 keys and a bf16 output go to tcgen05.
-bool use_tc(int rows, int dtype, int o_dtype) { return rows > 32 && dtype == HLA_BF16 && o_dtype == HLA_BF16; }
+// More than 64 rows of bf16 keys and a bf16 output go to tcgen05.  Measured over 32 sequences of 180k to 240k tokens and
+// one kv head, tcgen05 / mma.sync: 128 rows, d 128 727 / 1453 us, d 64 516 / 811; at 64 rows (two kv heads, half the
+// length) 723 / 745 and 511 / 421: a tile of 128 rows costs the same half empty.
+bool use_tc(int rows, int dtype, int o_dtype) { return rows > 64 && dtype == HLA_BF16 && o_dtype == HLA_BF16; }
 
-int attn_grid_limit(bool tc) { return (tc ? 2 : 3) * sm_count(); }  // the most of any configuration
+int attn_grid_limit() { return 3 * sm_count(); }  // the most of any configuration
 
-size_t pieces_bytes(int M, bool tc, int d) { return (size_t)2 * attn_grid_limit(tc) * M * (d + 2) * sizeof(float); }
+size_t pieces_bytes(int M, int d) { return (size_t)2 * attn_grid_limit() * M * (d + 2) * sizeof(float); }
 
 size_t attn_ws(const hla_kv_cache *C, int B, int T, int H, bool sparse) {
     if (check_cache(C, false, false) != HLA_OK || check_window(C, B, T, H, 1) != HLA_OK) return 0;
     const int G = H / C->kv_heads, rows = sparse ? G : T * G;
-    const size_t a = pieces_bytes(tile_rows(rows, false), false, C->head_dim), b = pieces_bytes(kTcRows, true, C->head_dim);
+    const size_t a = pieces_bytes(tile_rows(rows, false), C->head_dim), b = pieces_bytes(kTcRows, C->head_dim);
     return use_tc(rows, C->dtype, HLA_BF16) && b > a ? b : a;  // for either output type
 }
 
@@ -699,7 +702,7 @@ int run_attn(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const i
     HLA_REQUIRE(most < (1L << 31) && (long)C->n_pages * C->kv_heads * (C->page_size / kGroup) < (1L << 31), HLA_ERR_UNSUPPORTED);
     const int D = C->head_dim;
     p.part_o = static_cast<float *>(ws);
-    p.part_ml = p.part_o + (size_t)2 * attn_grid_limit(tc) * M * D;
+    p.part_ml = p.part_o + (size_t)2 * attn_grid_limit() * M * D;
     if (tc) {
         p.status = device_status_word();
         HLA_REQUIRE(p.status, HLA_ERR_CUDA);

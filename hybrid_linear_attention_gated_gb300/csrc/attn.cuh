@@ -103,7 +103,7 @@ __device__ __forceinline__ void store_out(const AttnParams &p, size_t at, float 
 
 // attn_tc.cu: the same pieces on tcgen05, rows in tiles of 128.  *grid: CTAs launched, at most `most`.
 constexpr int kTcRows = 128;
-constexpr int kTcTile = 128;  // keys per tile
+constexpr int kTcTile = 64;   // keys per tile
 cudaError_t launch_attn_tc(int D, const AttnParams &p, int *grid, long most, cudaStream_t st);
 
 }  // namespace hla

@@ -1,17 +1,19 @@
-// The paged attention of more than 32 query rows per kv head (a speculative window of a model with few kv heads) on
-// tcgen05: from there on mma.sync, not memory, bounds the warps' form in attn.cu.
+// The paged attention of more than 64 query rows per kv head (a speculative window of a model with few kv heads) on
+// tcgen05: there mma.sync, not memory, bounds the warps' form in attn.cu.
 //
-// A CTA owns 128 rows (padded), one per thread, and runs the same equal share of tiles as attn_kernel, 128 keys a
+// A CTA owns 128 rows (padded), one per thread, and runs the same equal share of tiles as attn_kernel, 64 keys a
 // tile.  Per tile
-//     S = Q K^T        tcgen05.mma 128 x 128 x d, both operands K-major in shared memory, S in tensor memory;
+//     S = Q K^T        tcgen05.mma 128 x 64 x d, both operands K-major in shared memory, S in tensor memory;
 //     P = 2^(S - m)    a thread reads its row of S, keeps m and l, writes its row of P as bf16 to shared memory;
-//     O += P V         tcgen05.mma 128 x d x 128, V as it lies in the cache (its channels contiguous: MN-major).
+//     O += P V         tcgen05.mma 128 x d x 64, V as it lies in the cache (its channels contiguous: MN-major).
 // O stays in tensor memory.  A row's m is raised, and O rescaled, only when a score passes it by 2^8: until then the
 // weights stay below 2^8, which bf16 and the fp32 sums hold as well as 1.
 //
-// Keys and values come through two stages of cp.async in the 128-byte swizzle: tile i + 1 is copied while tile i is
-// worked on.  One 128 x 128 tile of d = 128 takes the tensor core about 500 cycles, the 16384 exponentials 1024, and
-// HBM about 2800 for its 64 KB.
+// Keys and values come through two stages of cp.async in the 128-byte swizzle.  A tile is a chain of short steps
+// (product, row of S, weights, product: about 3700 cycles for d = 128), so what counts is CTAs per SM that fill one
+// another's gaps: two of d = 128 and three of d = 64 with 64-key tiles and two stages (727 and 516 us for 128 rows over
+// 32 x 180k tokens, 4.1 and 2.9 TB/s) against one with 128-key tiles or four stages (1021 to 1200 us, 526 to 640).
+// What is left of the time is that chain.
 //
 // The keys that all rows see (up to past) go through the tiles; the window's own T - 1 last keys, which a row sees in
 // part, are taken up on CUDA cores at the end of the unit, row by row, so that no weight of zero meets their values.
@@ -25,26 +27,53 @@ namespace hla {
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s of %globaltimer per bounded wait
-constexpr uint32_t kSub = kTcRows * 128;     // bytes of 128 rows of one 128-byte-wide swizzled block
+constexpr uint32_t kSub = kTcRows * 128;     // bytes of 128 rows of one 128-byte-wide swizzled block (Q, P)
+constexpr uint32_t kKvSub = kTcTile * 128;   // of the 64 rows of a tile's K or V
+constexpr int kStages = 2;                   // tiles in shared memory: one on its way while one is worked on
 
 template <int D>
-__host__ __device__ constexpr uint32_t tc_smem() {  // Q, 2 x K, 2 x V, P
-    return 5 * (D / 64) * kSub + 2 * kSub;
+__host__ __device__ constexpr uint32_t tc_smem() {  // Q, K and V stages, P
+    return (D / 64) * kSub + 2 * kStages * (D / 64) * kKvSub + kSub;
+}
+template <int D>
+__host__ __device__ constexpr int tc_ctas() {  // per SM
+    return D == 64 ? 3 : 2;
+}
+template <int D>
+__host__ __device__ constexpr uint32_t tmem_columns() {  // 64 of S, D of O
+    return D == 64 ? 128 : 256;
+}
+
+// A bounded wait whose first polls do not read the clock (a read of %globaltimer takes longer than most waits here).
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, int *status) {
+    const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (done) return true;
+    }
+    return mbar_wait_for(bar, parity, kWaitNs, status);
 }
 
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 template <int D>
-__global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(const AttnParams p) {
     constexpr int RB = 2 * D, CPR = RB / 16, GB = kGroup * RB, NB = D / 64, M = kTcRows;
     constexpr uint32_t IS = idesc_bf16(M, kTcTile), IO = idesc_bf16(M, D, true);
     constexpr unsigned ALL = 0xffffffffu;
     extern __shared__ __align__(1024) uint8_t smem[];  // no static shared memory in front of it: two CTAs of d = 64 just fit
-    uint8_t *const sQ = smem, *const sK = sQ + NB * kSub, *const sV = sK + 2 * NB * kSub, *const sP = sV + 2 * NB * kSub;
-    uint64_t &bar_s = reinterpret_cast<uint64_t *>(sP + 2 * kSub)[0], &bar_o = (&bar_s)[1], &bar_end = (&bar_s)[2];
+    uint8_t *const sQ = smem, *const sK = sQ + NB * kSub, *const sV = sK + kStages * NB * kKvSub,
+            *const sP = sV + kStages * NB * kKvSub;
+    uint64_t &bar_s = reinterpret_cast<uint64_t *>(sP + kSub)[0], &bar_o = (&bar_s)[1], &bar_end = (&bar_s)[2];
     uint32_t &s_tmem = *reinterpret_cast<uint32_t *>(&bar_s + 3);
-    int (*const s_on)[8] = reinterpret_cast<int (*)[8]>(&bar_s + 4);  // [2]: rows with a key of each staged group
-    int *const s_pre = &s_on[2][0], *const s_past = s_pre + p.B + 1;  // [B + 1], [B]
+    int (*const s_on)[4] = reinterpret_cast<int (*)[4]>(&bar_s + 4);  // [kStages]: rows with a key of each staged group
+    int *const s_pre = &s_on[kStages][0], *const s_past = s_pre + p.B + 1;  // [B + 1], [B]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     pdl_wait();
@@ -73,14 +102,16 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(
         fence_async();
     }
     if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_u32(&s_tmem)) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "r"(tmem_columns<D>())
+                     : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_trigger();  // only now: a dependent that allocates tensor memory must not get it before this CTA
-    const uint32_t tm_s = s_tmem, tm_o = s_tmem + kTcTile;  // 128 columns of S, D of O
+    const uint32_t tm_s = s_tmem, tm_o = s_tmem + kTcTile;  // 64 columns of S, D of O
     const uint32_t my_lanes = (uint32_t)(warp * 32) << 16;
 
     struct Unit {
@@ -110,14 +141,13 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(
         return page < p.n_pages ? page : -1;
     };
 
-    // ---- copies, as in attn_kernel: two groups of 16 keys per warp and tile, lane l looks up group l of each 32
+    // ---- copies, as in attn_kernel: 16 keys per warp and tile, lane l looks up tile l of each 32
     auto look = [&](int g0, int *at, int *on) {
-        const int g = g0 + lane;
         *at = -1;
         *on = 0;
-        if (g >= N * 2) return;
-        const Unit u = unit_of(begin + (g >> 1));
-        const int key = u.k * kTcTile + warp * 32 + (g & 1) * kGroup;
+        if (g0 + lane >= N) return;
+        const Unit u = unit_of(begin + g0 + lane);
+        const int key = u.k * kTcTile + warp * kGroup;
         const int limit = s_past[u.b] + (p.sel ? u.tq : 0);  // last position that all rows see
         int blk = key >> p.pshift;
         if (p.sel) blk = blk < listed(p, limit) ? p.sel[((size_t)(u.b * p.T + u.tq) * p.Hkv + u.hk) * p.n_select + blk] : -1;
@@ -133,35 +163,43 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(
 #pragma unroll
     for (int x = 0; x < GB / 512; ++x) {
         const int r = (x * 32 + lane) / CPR, c = (x * 32 + lane) % CPR;
-        to[x] = (c >> 3) * kSub + (warp * 32 + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
+        to[x] = (c >> 3) * kKvSub + (warp * kGroup + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
     }
     const uint32_t k_ring = smem_u32(sK), v_ring = smem_u32(sV);
     auto issue = [&](int ti) {
-        const uint32_t st = (ti & 1) * NB * kSub;
+        const uint32_t st = ti % kStages * NB * kKvSub;
+        const int from16 = __shfl_sync(ALL, at_now, ti & 31), on = __shfl_sync(ALL, on_now, ti & 31);
+        const size_t from = (size_t)(from16 < 0 ? 0 : from16) * GB + lane * 16;
+        const uint8_t *k = p.k + from, *v = p.v + from;
+        if (on == kGroup) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const int src = (ti * 2 + g) & 31;
-            const int from16 = __shfl_sync(ALL, at_now, src), on = __shfl_sync(ALL, on_now, src);
-            const size_t from = (size_t)(from16 < 0 ? 0 : from16) * GB + lane * 16;
+            for (int x = 0; x < GB / 512; ++x) {
+                cp_async16_s(k_ring + st + to[x], k + x * 512);
+                cp_async16_s(v_ring + st + to[x], v + x * 512);
+            }
+        } else {
 #pragma unroll
             for (int x = 0; x < GB / 512; ++x) {
                 const bool in = (x * 32 + lane) / CPR < on;
-                const uint32_t d = st + to[x] + g * kGroup * 128;
-                cp_async16_or_zero(k_ring + d, in ? p.k + from + x * 512 : p.k, in);
-                cp_async16_or_zero(v_ring + d, in ? p.v + from + x * 512 : p.v, in);
+                cp_async16_or_zero(k_ring + st + to[x], in ? k + x * 512 : p.k, in);
+                cp_async16_or_zero(v_ring + st + to[x], in ? v + x * 512 : p.v, in);
             }
-            if (lane == 0) s_on[ti & 1][2 * warp + g] = on;
         }
-        const int seen = (ti + 1) * 2;
-        if ((seen & 31) == 16) look(seen + 16, &at_next, &on_next);
-        if ((seen & 31) == 0) {
+        if (lane == 0) s_on[ti % kStages][warp] = on;
+        if ((ti & 31) == 15) look(ti + 17, &at_next, &on_next);
+        if ((ti & 31) == 31) {
             at_now = at_next;
             on_now = on_next;
         }
     };
 
-    issue(0);
-    cp_async_commit();
+#pragma unroll
+    for (int x = 0; x < kStages - 1; ++x) {
+        if (x < N) issue(x);
+        cp_async_commit();
+    }
+    const uint64_t q_desc = sw128_desc(smem_u32(sQ)), k_desc = sw128_desc(k_ring), p_desc = sw128_desc(smem_u32(sP)),
+                   v_desc = sw128_desc_mn(v_ring, kKvSub);
     const float sc = fmaxf(fabsf(p.scale) * kLog2e, 1e-37f);  // a negative scale is taken into the query
     bool ok = true, all_ok = true;                            // no wait of this thread, of any thread, has given up
     for (int done = 0; done < N && all_ok;) {
@@ -186,8 +224,8 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(
         float mb = 0.f, l = 0.f;  // m times the scale
         bool none = true;         // no score yet
         for (int it = first; it < done; ++it) {
-            const int st = it & 1;
-            cp_async_wait<0>();
+            const int st = it % kStages;
+            cp_async_wait<kStages - 2>();
             fence_async();
             tc_fence_before();
             all_ok = __syncthreads_and(ok);  // tile `it` is in shared memory, and every thread is done with tile it - 1
@@ -196,17 +234,18 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
-                    const uint32_t off = (c >> 2) * kSub + (c & 3) * 32;
-                    umma_bf16(tm_s, sw128_desc(smem_u32(sQ) + off), sw128_desc(k_ring + st * NB * kSub + off), IS, c > 0);
+                    const uint32_t off = (c & 3) * 32;  // (a descriptor counts addresses in 16 bytes)
+                    umma_bf16(tm_s, q_desc + (((c >> 2) * kSub + off) >> 4),
+                              k_desc + (st * NB * kKvSub >> 4) + (((c >> 2) * kKvSub + off) >> 4), IS, c > 0);
                 }
                 umma_commit(&bar_s);
             }
-            // the other stage and P are free once the previous tile's output product is complete
-            if (it > 0) ok &= mbar_wait_for(&bar_o, (it - 1) & 1, kWaitNs, p.status);
+            // the previous tile's stage and P are free once its output product is complete
+            if (it > 0) ok &= wait_phase(&bar_o, (it - 1) & 1, p.status);
             __syncwarp();
-            if (it + 1 < N) issue(it + 1);
+            if (it + kStages - 1 < N) issue(it + kStages - 1);
             cp_async_commit();
-            ok &= mbar_wait_for(&bar_s, it & 1, kWaitNs, p.status);
+            ok &= wait_phase(&bar_s, it & 1, p.status);
             __syncwarp();
             tc_fence_after();
 
@@ -215,9 +254,9 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(
 #pragma unroll
             for (int c = 0; c < kTcTile; c += 32) tmem_ld32(tm_s + my_lanes + c, sr + c);
             tmem_wait_ld();
-            float mx = -INFINITY;
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
+            for (int g = 0; g < kTcTile / kGroup; ++g) {
                 const int on = s_on[st][g];
                 if (on < kGroup) {
 #pragma unroll
@@ -225,8 +264,9 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(
                         if (x >= on) sr[16 * g + x] = 0xff800000u;  // -infinity
                 }
 #pragma unroll
-                for (int x = 0; x < kGroup; ++x) mx = fmaxf(mx, __uint_as_float(sr[16 * g + x]));
+                for (int x = 0; x < kGroup; ++x) m4[x & 3] = fmaxf(m4[x & 3], __uint_as_float(sr[16 * g + x]));
             }
+            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             const float t = mx * sc;
             if (none && mx != -INFINITY) {
                 mb = t;
@@ -249,21 +289,21 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(
                 tmem_wait_st();
             }
             // ---- weights: rounded once to bf16, as in attn_kernel for a bf16 output
-            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 ls[4] = {};
+            const float2 sc2 = make_float2(sc, sc), mb2 = make_float2(-mb, -mb);
 #pragma unroll
             for (int c = 0; c < kTcTile / 8; ++c) {
                 uint32_t w[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float a = ex2(fmaf(__uint_as_float(sr[8 * c + 2 * x]), sc, -mb)),
-                                b = ex2(fmaf(__uint_as_float(sr[8 * c + 2 * x + 1]), sc, -mb));
-                    ls[x] += a + b;
-                    w[x] = pack_bf16x2(a, b);
+                    float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[8 * c + 2 * x]), __uint_as_float(sr[8 * c + 2 * x + 1])), sc2, mb2);
+                    y = make_float2(ex2(y.x), ex2(y.y));
+                    ls[x] = __fadd2_rn(ls[x], y);
+                    w[x] = pack_bf16x2(y.x, y.y);
                 }
-                *reinterpret_cast<uint4 *>(sP + (c >> 3) * kSub + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(sP + tid * 128 + ((c ^ (tid & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
             fence_async();
             tc_fence_before();
             all_ok = __syncthreads_and(ok);
@@ -272,13 +312,13 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < kTcTile / 16; ++c)
-                    umma_bf16(tm_o, sw128_desc(smem_u32(sP) + (c >> 2) * kSub + (c & 3) * 32),
-                              sw128_desc_mn(v_ring + st * NB * kSub + c * 2048, kSub), IO, it > first || c > 0);
+                    umma_bf16(tm_o, p_desc + (c * 32 >> 4), v_desc + (st * NB * kKvSub >> 4) + (c * 2048 >> 4), IO,
+                              it > first || c > 0);
                 umma_commit(&bar_o);
             }
         }
         if (!all_ok) break;
-        ok &= mbar_wait_for(&bar_o, (done - 1) & 1, kWaitNs, p.status);
+        ok &= wait_phase(&bar_o, (done - 1) & 1, p.status);
         __syncwarp();
         tc_fence_after();
 
@@ -357,12 +397,12 @@ __global__ void __launch_bounds__(kAttnThreads, D == 64 ? 2 : 1) attn_tc_kernel(
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(s_tmem) : "memory");
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "r"(tmem_columns<D>()) : "memory");
 }
 
 template <int D>
 cudaError_t launch(const AttnParams &p, int *grid, long most, cudaStream_t st) {
-    const size_t fixed = tc_smem<D>() + 32 + 64, smem = fixed + (2 * p.B + 1) * sizeof(int);
+    const size_t fixed = tc_smem<D>() + 32 + kStages * 16, smem = fixed + (2 * p.B + 1) * sizeof(int);
     // the shared-memory limit is a per-device attribute: raise it once on every device used
     static bool done[64] = {};
     int dev = 0;
@@ -374,7 +414,7 @@ cudaError_t launch(const AttnParams &p, int *grid, long most, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         if (dev < 64) done[dev] = true;
     }
-    const int slots = (D == 64 ? 2 : 1) * sm_count();
+    const int slots = tc_ctas<D>() * sm_count();
     *grid = most < slots ? (int)most : slots;
     return launch_kernel(attn_tc_kernel<D>, dim3(*grid), dim3(kAttnThreads), smem, st, p);
 }

@@ -49,9 +49,10 @@
  *    pipeline waits are bounded: a wait that gives up does not fail the launch
  *    but sets the device status word.  Every entry point that can reach that path
  *    (skinny_proj_splitk, skinny_proj_splitk_noalloc, skinny_proj_residual_rmsnorm,
- *    kda_qkvg_proj, moe_route_topk, moe_expert_forward, hla_decode_layer) can
- *    therefore return HLA_OK with invalid outputs; a caller that must know checks
- *    hla_device_status() after synchronising.
+ *    kda_qkvg_proj, moe_route_topk, moe_expert_forward, hla_decode_layer; and
+ *    attn_paged_decode and attn_paged_sparse with more than 64 query rows per kv head, a bf16 cache
+ *    and a bf16 output) can therefore return HLA_OK with invalid outputs; a caller that must know
+ *    checks hla_device_status() after synchronising.
  *  - Results are deterministic: every reduction runs in a fixed order, so the
  *    same inputs give bit-identical outputs run to run.
  */
@@ -508,12 +509,12 @@ int skinny_proj_splitk_noalloc(int M, int N, int K, const hla_bf16 *x, const hla
  * -------------------------------------------------------------------------*/
 unsigned long long hla_launch_count(void);
 /* Reads and clears the device status word: 0, or HLA_ERR_DEVICE_TIMEOUT when a bounded
- * device-side wait (the tensor-core projection's pipeline barriers) gave up since the last
- * read.  Synchronous (copies 4 bytes from the device); HLA_ERR_CUDA if that copy fails. */
+ * device-side wait (the pipeline barriers of the tensor-core projections and attention) gave up since the
+ * last read.  Synchronous (copies 4 bytes from the device); HLA_ERR_CUDA if that copy fails. */
 int hla_device_status(void);
 /* Test hook for the failure path, with no counterpart on the source pages.  While on != 0,
- * every tensor-core projection launch makes one of its bounded device waits give up (block 0
- * waits 1 ms on a barrier that nothing arrives at) and records HLA_ERR_DEVICE_TIMEOUT, and
+ * every tensor-core projection or attention launch makes one of its bounded device waits give up (block
+ * 0 waits 1 ms on a barrier that nothing arrives at) and records HLA_ERR_DEVICE_TIMEOUT, and
  * every block returns before it allocates tensor memory or issues a copy or an MMA; the
  * launch writes no output.  This lets a test check the status path without a real stall.
  * Takes effect for launches made after the call (a CUDA graph keeps what it captured);

@@ -54,7 +54,7 @@ def test_decode_matches_oracle(case, dtype, o_dtype):
     o = p.decode(o_dtype)
     rows = T * H // Hkv
     m = 16 if rows <= 16 else 32 if rows <= 32 else 64
-    if rows > 32 and dtype == hla.HLA_BF16 and o_dtype == hla.HLA_BF16:
+    if rows > 64 and dtype == hla.HLA_BF16 and o_dtype == hla.HLA_BF16:
         m = 128  # tcgen05
     assert hla.hla_last_variant() == f"attn_paged<d{d},{'e4m3' if dtype == hla.HLA_E4M3 else 'bf16'},m{m}>"
     torch.cuda.synchronize()
@@ -63,7 +63,7 @@ def test_decode_matches_oracle(case, dtype, o_dtype):
     assert torch.equal(bits(again), bits(o))  # fixed order of all sums
 
 
-@pytest.mark.parametrize("T,H,Hkv", [(1, 8, 2), (4, 16, 2), (8, 8, 1)])
+@pytest.mark.parametrize("T,H,Hkv", [(1, 8, 2), (4, 16, 2), (8, 8, 1), (8, 24, 2)])
 def test_many_ragged_sequences(T, H, Hkv):
     """More units than CTAs and fewer, with pieces joined across CTAs: every sequence against the oracle."""
     g = np.random.default_rng(5)
@@ -73,9 +73,9 @@ def test_many_ragged_sequences(T, H, Hkv):
         check(p, p.decode(o_dtype), o_dtype)
 
 
-@pytest.mark.parametrize("d,T,H,Hkv,page", [(128, 8, 8, 1, 64), (64, 8, 32, 1, 16), (128, 5, 40, 2, 128), (64, 3, 16, 1, 32)])
+@pytest.mark.parametrize("d,T,H,Hkv,page", [(128, 8, 9, 1, 64), (64, 8, 32, 1, 16), (128, 5, 40, 2, 128), (64, 3, 24, 1, 32)])
 def test_tcgen05_rows_over_lengths(d, T, H, Hkv, page):
-    """More than 32 rows of a bf16 cache: lengths around the 128-key tiles, windows across page and tile borders, negative
+    """More than 64 rows of a bf16 cache: lengths around the 64-key tiles, windows across page and tile borders, negative
     scale, pieces joined across CTAs, and the status word stays clear."""
     dev = require_gpu()
     past = [0, 1, 120, 121, 126, 127, 128, 129, 255, 256, 511, 3000, -1, 900]
@@ -134,7 +134,7 @@ def test_masked_places_may_hold_anything():
     problem's poison), whole foreign pages; a row sees its own infinities."""
     dev = require_gpu()
     for dtype in (hla.HLA_BF16, hla.HLA_E4M3):
-        for H, Hkv in ((4, 2), (16, 2), (16, 1)):  # 16-, 32- and 64-row (or tcgen05) tiles at T = 4
+        for H, Hkv in ((4, 2), (16, 2), (16, 1), (24, 1)):  # 16-, 32- and 64-row tiles, and tcgen05's, at T = 4
             for past in (62, 64, 13):              # the window across a page and tile border, at its start, inside
                 p = Problem(dev, [past, 100], 4, H, Hkv, 64, 16, dtype, seed=past)
                 q = Problem(dev, [past, 100], 4, H, Hkv, 64, 16, dtype, seed=past).upload()
@@ -189,7 +189,7 @@ def test_positions_behind_the_table_are_dropped():
 
 @pytest.mark.parametrize("dtype", [hla.HLA_BF16, hla.HLA_E4M3])
 @pytest.mark.parametrize("T,H,Hkv,d,page,n_sel", [(1, 8, 2, 128, 64, 5), (3, 12, 4, 64, 16, 9), (2, 40, 2, 128, 32, 3),
-                                                  (1, 48, 1, 64, 128, 2)])
+                                                  (1, 48, 1, 64, 128, 2), (2, 144, 2, 64, 16, 6)])
 def test_sparse_matches_oracle(T, H, Hkv, d, page, n_sel, dtype):
     """Arbitrary lists: unsorted, repeated, behind the token, outside the table, empty."""
     dev = require_gpu()
@@ -198,7 +198,9 @@ def test_sparse_matches_oracle(T, H, Hkv, d, page, n_sel, dtype):
     sel = g.integers(-2, 15, size=(4, T, Hkv, n_sel))
     sel[1, 0, 0] = -1                       # nothing listed
     sel[0, -1, -1] = 2                      # one block, n_sel times
-    o = p.decode(hla.HLA_F32, torch.from_numpy(sel).to(I32).to(dev))
+    lists = torch.from_numpy(sel).to(I32).to(dev)
+    check(p, p.decode(hla.HLA_BF16, lists), hla.HLA_BF16, sel)
+    o = p.decode(hla.HLA_F32, lists)
     assert hla.hla_last_variant().startswith("attn_sparse<")
     check(p, o, hla.HLA_F32, sel)
     assert torch.all(o[2] == 0) and torch.all(o[1, 0, :H // Hkv] == 0)
@@ -233,7 +235,7 @@ def test_cache_beyond_32_bit_offsets():
     check(p, o, hla.HLA_F32)
 
 
-@pytest.mark.parametrize("H,Hkv,o_dtype", [(8, 2, hla.HLA_F32), (40, 2, hla.HLA_BF16)])
+@pytest.mark.parametrize("H,Hkv,o_dtype", [(8, 2, hla.HLA_F32), (80, 2, hla.HLA_BF16)])
 def test_one_captured_graph_serves_any_lengths_and_pages(H, Hkv, o_dtype):
     dev = require_gpu()
     p = Problem(dev, [700, 300, 20], 2, H, Hkv, 64, 32, seed=11, poison=False).upload()
@@ -302,3 +304,21 @@ def test_inside_a_launch_chain():
     finally:
         hla.hla_chain_end()
     assert torch.equal(o, want)
+
+
+def test_forced_wait_timeout_is_reported_and_nothing_is_written():
+    """A tcgen05 launch whose wait gives up reports it once through the status word and leaves the output alone; the
+    next launch is right."""
+    dev = require_gpu()
+    p = Problem(dev, [300, 70], 8, 16, 1, 64, 32, seed=15).upload()
+    torch.cuda.synchronize()
+    assert hla.hla_device_status() == 0
+    try:
+        hla.hla_test_force_wait_timeout(1)
+        o = p.decode(hla.HLA_BF16)
+        torch.cuda.synchronize()
+    finally:
+        hla.hla_test_force_wait_timeout(0)
+    assert hla.hla_device_status() == 6 and hla.hla_device_status() == 0  # HLA_ERR_DEVICE_TIMEOUT, then cleared
+    assert torch.all(o == 7.0)
+    check(p, p.decode(hla.HLA_BF16), hla.HLA_BF16)
