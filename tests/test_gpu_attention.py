@@ -277,15 +277,27 @@ def test_two_streams_at_once_with_their_own_workspaces():
             assert torch.equal(a, b)
 
 
+def test_largest_batch_and_most_heads_per_kv_head():
+    """1024 sequences (some idle), and 512 query heads on one kv head (four tcgen05 row tiles, eight of 64)."""
+    dev = require_gpu()
+    g = np.random.default_rng(16)
+    past = [int(x) for x in g.integers(-1, 40, size=1024)]
+    p = Problem(dev, past, 1, 2, 1, 64, 16, seed=16).upload()
+    check(p, p.decode(hla.HLA_F32), hla.HLA_F32)
+    p = Problem(dev, [90, 700], 1, 512, 1, 64, 32, seed=17).upload()
+    for o_dtype in (hla.HLA_BF16, hla.HLA_F32):
+        check(p, p.decode(o_dtype), o_dtype)
+
+
 def test_output_and_workspace_stay_inside_their_bounds():
     dev = require_gpu()
-    for T, H, Hkv, d in ((1, 8, 2, 128), (5, 8, 2, 64), (8, 16, 1, 128)):
+    for T, H, Hkv, d, o_dtype in ((1, 8, 2, 128, 0), (5, 8, 2, 64, 0), (8, 16, 1, 128, 0), (8, 12, 1, 128, 1), (7, 10, 1, 64, 1)):
         p = Problem(dev, [500, 33], T, H, Hkv, d, 16, seed=13).upload()
         n = hla.attn_paged_decode_workspace_size(p.C, 2, T, H)
         ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device=dev)
         elems = 2 * T * H * d
-        o = torch.full((elems + 1024,), 5.0, device=dev)
-        hla.attn_paged_decode(p.C, 2, T, H, p.max_blocks, p.D["table"], p.D["past"], p.scale, p.D["q"], o, hla.HLA_F32, ws, n)
+        o = torch.full((elems + 1024,), 5.0, device=dev, dtype=BF16 if o_dtype == hla.HLA_BF16 else torch.float32)
+        hla.attn_paged_decode(p.C, 2, T, H, p.max_blocks, p.D["table"], p.D["past"], p.scale, p.D["q"], o, o_dtype, ws, n)
         torch.cuda.synchronize()
         assert torch.all(ws[n:] == 0x5A) and torch.all(o[elems:] == 5.0) and not torch.any(o[:elems] == 5.0)
 

@@ -125,6 +125,28 @@ def test_append_many_sequences_and_long_prompts():
     a.check(*a.run())
 
 
+def test_largest_batch():
+    """1024 sequences through the append and the block choice."""
+    dev = require_gpu()
+    g = np.random.default_rng(9)
+    a = Append(dev, [int(x) for x in g.integers(-1, 60, 1024)], [int(x) for x in g.integers(0, 3, 1024)], H=2, Hkv=1, d=64, page=16,
+               rope=64, seed=9)
+    a.check(*a.run())
+    p = bounded(Problem(dev, [int(x) for x in g.integers(-1, 300, 1024)], 1, 2, 1, 64, 16, seed=9, poison=False), 9)
+    select_check(p, 5, 1, 1)
+
+
+def test_block_choice_keeps_inside_its_buffers():
+    dev = require_gpu()
+    p = bounded(Problem(dev, [900, -1, 40], 2, 4, 2, 64, 16, seed=11, poison=False), 11)
+    n, m = hla.attn_select_blocks_workspace_size(p.C, 3, 2, 4, p.max_blocks), 3 * 2 * 2 * 7
+    ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device=dev)
+    sel = torch.full((m + 64,), -7, dtype=I32, device=dev)
+    hla.attn_select_blocks(p.C, 3, 2, 4, p.max_blocks, p.D["table"], p.D["past"], 7, 1, 1, p.D["q"], sel, ws, n)
+    torch.cuda.synchronize()
+    assert torch.all(ws[n:] == 0x5A) and torch.all(sel[m:] == -7) and torch.all(sel[:m] >= -1)
+
+
 def test_append_in_place_and_again():
     """q rotated in its own buffer; the same append twice gives the same cache."""
     dev = require_gpu()
