@@ -24,7 +24,7 @@ constexpr int kChooseThreads = 256;
 constexpr int kMaxBlocks = 65536;     // blocks per sequence (a bit each in shared memory)
 constexpr int kStaged = 6144;         // scores of a row kept in shared memory; longer rows are read through L2
 constexpr int kListed = 1024;         // blocks near the border kept in shared memory
-constexpr int kBins = 1024;           // of a row's scores, to find the n-th highest
+constexpr int kBins = 2048;           // of a row's scores, to find the n-th highest
 constexpr int kFewInBin = 64;         // a bin with no more scores is not split again
 
 struct SelectParams {
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
     __shared__ float s_f[4][kWarps];
     __shared__ int s_near, s_sure, s_bin, s_count;
     int *const s_hist = reinterpret_cast<int *>(s_key);  // [kBins], before the keys
-    static_assert(kBins * sizeof(int) <= sizeof(s_key) && kBins == 4 * kChooseThreads, "four bins per thread");
+    static_assert(kBins * sizeof(int) <= sizeof(s_key) && kBins == 8 * kChooseThreads, "eight bins per thread");
     constexpr int CPL = D / 32;                          // channels per lane
     constexpr unsigned ALL = 0xffffffffu;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -373,9 +373,10 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
     }
     auto score = [&](int x) -> float { return staged ? s_score[x] : fmaxf(row_score[x], -3e38f); };
 
-    // Bound on any score's error: 2^-14 sum |q| max |bound|.  A score is 2 d / 16 products of 16 terms in four chains,
-    // added up; a sum of 17 values that keeps 23 bits of the largest errs by at most 17 2^-23 of it, 2 d / 16 <= 16 times over.
-    const float size = absq * absb, err = size * 6.103515625e-05f;
+    // Bound on any score's error: 2^-16 sum |q| max |bound|.  A score is four chains of at most 4 products of 16 terms,
+    // added up; a sum of 17 values that keeps 23 bits of the largest errs by at most 17 2^-23 of it, 4 times over in each
+    // chain, and the chains' sizes add up to the score's: 68 2^-23, and 3 2^-24 for the last additions.
+    const float size = absq * absb, err = size * 1.52587890625e-05f;
 
     // [low, high]: the band in which fp32 does not decide.  The k-th highest score is in the bin of scores in which the
     // count from above reaches k; a bin with many scores is split again until it is as narrow as the error.
@@ -392,9 +393,10 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
                 if (v >= lo && v <= hi) atomicAdd(&s_hist[(int)fminf((v - lo) * inv, kBins - 1)], 1);
             }
             __syncthreads();
-            // counts from the highest bin down: thread tid has bins kBins - 4 - 4 tid .. kBins - 1 - 4 tid
-            const int4 c = reinterpret_cast<const int4 *>(s_hist)[kBins / 4 - 1 - tid];
-            const int sum = c.x + c.y + c.z + c.w;
+            // counts from the highest bin down: thread tid has bins kBins - 8 - 8 tid .. kBins - 1 - 8 tid
+            int4 *const mine = reinterpret_cast<int4 *>(s_hist) + kBins / 4 - 2 - 2 * tid;
+            const int4 c = mine[1], d = mine[0];
+            const int sum = (c.x + c.y + c.z + c.w) + (d.x + d.y + d.z + d.w);
             int before = sum;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
@@ -407,16 +409,21 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
             for (int w = 0; w < kWarps; ++w) before += w < warp ? s_red[w] : 0;
             before -= sum;
             if (before < need && need <= before + sum) {  // one thread's
-                int at = kBins - 1 - 4 * tid, n = c.w;
-                if (need > before + n) { before += n; --at; n = c.z; }
-                if (need > before + n) { before += n; --at; n = c.y; }
-                if (need > before + n) { before += n; --at; n = c.x; }
+                const int each[8] = {c.w, c.z, c.y, c.x, d.w, d.z, d.y, d.x};
+                int at = kBins - 1 - 8 * tid, n = each[0];
+#pragma unroll
+                for (int y = 1; y < 8; ++y)
+                    if (need > before + n) {
+                        before += n;
+                        --at;
+                        n = each[y];
+                    }
                 s_bin = at;
                 s_count = n;
             }
-            reinterpret_cast<int4 *>(s_hist)[kBins / 4 - 1 - tid] = make_int4(0, 0, 0, 0);
+            mine[0] = mine[1] = make_int4(0, 0, 0, 0);
             __syncthreads();
-            // The bin's ends, wider by more than the rounding of a bin number, 1024 2^-22.  (That of lo itself, 2^-23 of
+            // The bin's ends, wider by more than the rounding of a bin number, 2048 2^-22.  (That of lo itself, 2^-23 of
             // a score, is far below the error.)
             const float l = fmaxf(lo, lo + (s_bin - 0.01f) / inv), h = fminf(hi, lo + (s_bin + 1.01f) / inv);
             if (!(l > lo || h < hi)) break;
