@@ -54,6 +54,14 @@ __device__ __forceinline__ uint32_t relu2(uint32_t x) {  // max(x, 0) of two bf1
     const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&x), z);
     return *reinterpret_cast<const uint32_t *>(&r);
 }
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of two bf16 each, NaN kept
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
 __device__ __forceinline__ uint32_t neg2(uint32_t x) {  // min(x, 0) of two bf16, NaN kept
     const __nv_bfloat162 z = __float2bfloat162_rn(0.f);
     const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&x), z);
@@ -132,16 +140,26 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
     // The place and pages of the group that is copied next are looked up one step ahead.
     Place ahead = n > 0 ? place(begin) : Place{};
     int pg = n > 0 ? page_of(ahead) : -1;
-    auto issue = [&](int x, int stage) {
-        const uint32_t bmax = ring + stage * 2 * GB, bmin = bmax + GB;
+    uint32_t to[GB / 512];  // where this lane's chunks of a group go: chunk y * 32 + lane
 #pragma unroll
-        for (int y = 0; y < GB / 512; ++y) {
-            const int r = (y * 32 + lane) / CPR, c = lane % CPR;
-            const int rp = __shfl_sync(ALL, pg, r);
-            const size_t o = rp >= 0 ? ((size_t)rp * p.Hkv + ahead.hk) * D + c * 8 : 0;
-            const uint32_t at = swizzled<RB>(r, c);
-            cp_async16_or_zero(bmax + at, p.k_max + o, rp >= 0);
-            cp_async16_or_zero(bmin + at, p.k_min + o, rp >= 0);
+    for (int y = 0; y < GB / 512; ++y) to[y] = ring + swizzled<RB>((y * 32 + lane) / CPR, lane % CPR);
+    auto issue = [&](int x, int stage) {
+        const uint32_t off = stage * 2 * GB;
+        if (__all_sync(ALL, pg >= 0)) {
+#pragma unroll
+            for (int y = 0; y < GB / 512; ++y) {
+                const size_t o = (size_t)(__shfl_sync(ALL, pg, (y * 32 + lane) / CPR) * p.Hkv + ahead.hk) * D + lane % CPR * 8;
+                cp_async16_s(to[y] + off, p.k_max + o);
+                cp_async16_s(to[y] + off + GB, p.k_min + o);
+            }
+        } else {
+#pragma unroll
+            for (int y = 0; y < GB / 512; ++y) {
+                const int rp = __shfl_sync(ALL, pg, (y * 32 + lane) / CPR);
+                const size_t o = rp >= 0 ? (size_t)(rp * p.Hkv + ahead.hk) * D + lane % CPR * 8 : 0;
+                cp_async16_or_zero(to[y] + off, p.k_max + o, rp >= 0);
+                cp_async16_or_zero(to[y] + off + GB, p.k_min + o, rp >= 0);
+            }
         }
         const unsigned has = __ballot_sync(ALL, pg >= 0);
         if (lane == 0) s_has[warp][stage] = has;
@@ -187,9 +205,10 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
         const uint32_t bmax = ring + stage * 2 * GB, bmin = bmax + GB;
         const int j0 = use.g * kGroupBlocks;
         const unsigned has = s_has[warp][stage];
+        uint32_t top = 0, low = 0;  // largest k_max and smallest k_min of the group, or 0
 
-        uint32_t big = 0;  // largest magnitude among the bounds, as the bits of a bf16 (a NaN's are the largest)
         for (int t0 = 0; t0 < p.T; t0 += per) {
+            const int tokens = p.T - t0 < per ? p.T - t0 : per;
             float keep[8];                        // of (token t0 + y / 16, block y % 16) for outputs y of this lane
 #pragma unroll
             for (int y = 0; y < 8; ++y) keep[y] = -INFINITY;
@@ -212,7 +231,10 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
                     }
                     if (t0 == 0 && part == 0)
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) big = __vmaxu2(big, __vmaxu2(f[y] & 0x7fff7fffu, g[y] & 0x7fff7fffu));
+                        for (int y = 0; y < 4; ++y) {
+                            top = max2(top, f[y]);
+                            low = min2(low, g[y]);
+                        }
                 }
                 __syncwarp();
 #pragma unroll
@@ -225,8 +247,8 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
 #pragma unroll
                 for (int y = 0; y < 8; ++y) {
                     const int o = y * 32 + lane, tl = o >> 4, bl = o & 15;
-                    if (tl >= per || t0 + tl >= p.T) break;
-                    for (int g = 0; g < rows; ++g) {
+                    if (2 * y >= tokens) break;  // (the whole warp)
+                    for (int g = 0; g < rows && tl < tokens; ++g) {
                         const float v = s_tile[warp][(parts == 1 ? tl * p.G : 0) + g][bl];
                         keep[y] = v > keep[y] || v != v ? v : keep[y];
                     }
@@ -235,10 +257,13 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
                 const int o = y * 32 + lane, tl = o >> 4, bl = o & 15, t = t0 + tl;
-                if (tl < per && t < p.T && j0 + bl < use.nb)
+                if (2 * y >= tokens) break;
+                if (tl < tokens && j0 + bl < use.nb)
                     p.score[((size_t)(use.b * p.T + t) * p.Hkv + use.hk) * p.stride + j0 + bl] = has >> bl & 1 ? keep[y] : -INFINITY;
             }
         }
+        // the largest magnitude (k_min <= k_max, so no other is larger), as the bits of a bf16 (a NaN's are the largest)
+        uint32_t big = max2(top, low ^ 0x80008000u) & 0x7fff7fffu;
         big = __reduce_max_sync(ALL, big >> 16 > (big & 0xffffu) ? big >> 16 : big & 0xffffu);
         if (lane == 0) p.absmax[((size_t)use.b * p.Hkv + use.hk) * p.groups + use.g] = bf16_bits_to_float((uint16_t)big);
         if (x + 1 < n) {
@@ -627,7 +652,8 @@ extern "C" int attn_select_blocks(const hla_kv_cache *C, int B, int T, int H, in
     HLA_REQUIRE(block_table && past_len && q && sel, HLA_ERR_INVALID_ARG);
     HLA_REQUIRE(n_select >= 1 && n_first >= 0 && n_last >= 0 && n_first <= n_select && n_last <= n_select - n_first, HLA_ERR_INVALID_ARG);
     // rows and groups are counted in 32 bits
-    HLA_REQUIRE((long)B * T * C->kv_heads < (1L << 31) && (long)B * C->kv_heads * ((max_blocks + kGroupBlocks - 1) / kGroupBlocks) < (1L << 31), HLA_ERR_UNSUPPORTED);
+    HLA_REQUIRE((long)C->n_pages * C->kv_heads < (1L << 31) && (long)B * T * C->kv_heads < (1L << 31) &&
+                    (long)B * C->kv_heads * ((max_blocks + kGroupBlocks - 1) / kGroupBlocks) < (1L << 31), HLA_ERR_UNSUPPORTED);
     HLA_REQUIRE(aligned16(block_table) && aligned16(past_len) && aligned16(q) && aligned16(sel), HLA_ERR_MISALIGNED);
     HLA_REQUIRE(ws && ws_bytes >= select_ws(C, B, T, H, max_blocks), HLA_ERR_WORKSPACE);
     HLA_REQUIRE(aligned16(ws), HLA_ERR_MISALIGNED);
