@@ -20,6 +20,12 @@
 // Within a CTA a tile's keys are copied 16 or 32 to a warp, each warp into its own ring of cp.async stages.
 // With 16 query rows a warp also runs its own keys against all rows and meets the other warps only at the end
 // of a unit; with 32 or 64 rows, two or four warps take 16 rows each and run all keys that they copied together.
+//
+// Measured (CUDA graph, d = 128, 32 query heads on 8 kv heads): 64 sequences of 500 to 15500 tokens, bf16, 310 us and
+// 30000 to 65000 tokens, e4m3, 913 us, both 6.8 TB/s, at or above the copy rate; one sequence of 1021 tokens 7.6 us
+// (this kernel about 4, the join the rest), all of it dependent loads.  CTAs per SM and keys per step were swept: 32
+// keys and 3 CTAs of d = 64, 2 of d = 128 (registers: more CTAs spill or lose the second accumulator set).
+
 #include <type_traits>
 
 #include "attn.cuh"

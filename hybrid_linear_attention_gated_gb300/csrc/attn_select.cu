@@ -11,6 +11,9 @@
 // only fp32's word on most blocks: with e a bound on the error of any score and t the n-th highest fp32 score,
 // blocks above t + 2 e are in and blocks below t - 2 e are out; the few between are scored again exactly and
 // ranked.
+// Measured (CUDA graph, pages of 64, 32 query heads on 8 kv heads of 128, 64 blocks chosen): one sequence of 131001
+// tokens 12.7 us, latency; 32 sequences x 2 tokens, 20000 to 90000 tokens, 35.4 us, of which the scores take about 25 (4.5
+// TB/s: about 900 instructions per group of 8 KB and warp set the pace) and the choice the rest.
 #include "paged.cuh"
 
 namespace hla {

@@ -8,6 +8,8 @@
 //
 // Every value is read and written once, so the step is bound by memory, and at decode sizes by latency.  One grid
 // does both halves: blocks that own a touched page for some kv heads, and blocks that own some tokens of q.
+// Measured (CUDA graph, 32 query and 8 kv heads of 128): one token 3.95 us; 64 x 4 tokens, e4m3, 7.2 us; 60 single
+// tokens and 4 chunks of 512 14.8 us; 8 prompts of 4093 tokens 129 us, 6.2 TB/s of reads and writes.
 #include "paged.cuh"
 
 namespace hla {
@@ -420,13 +422,14 @@ extern "C" int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_
     p.half = rope_dim / 2;
     // n new tokens touch at most n pages, and at most n / page_size + 2
     const long by_size = (long)N / C->page_size + 2L * B, pages = N < by_size ? N : by_size;
-    // heads of a page share its angles; one head per CTA until the pages alone fill the SMs
+    // Heads of a page share its angles; one head per CTA until the pages alone fill the SMs several times: two heads per
+    // CTA take prompts from 133 to 131 us, but a mixed batch, whose longest CTA sets the pace, from 18 to 26.
     p.heads_per_cta = 1;
     while (p.heads_per_cta < p.Hkv && pages * ((p.Hkv + 2 * p.heads_per_cta - 1) / (2 * p.heads_per_cta)) >= 8L * sm_count()) p.heads_per_cta *= 2;
     p.head_groups = (p.Hkv + p.heads_per_cta - 1) / p.heads_per_cta;
     const long kv = pages * p.head_groups;
     p.by_half = divisor(p.half ? p.half : 1); p.by_H = divisor(p.H); p.by_head_groups = divisor(p.head_groups);
-    p.q_tokens = 1;
+    p.q_tokens = 1;  // four rows in flight per thread want four tokens of 32 heads, once there are tokens enough
     while (p.q_tokens < kMaxQTokens && N / (2 * p.q_tokens) >= 3L * sm_count()) p.q_tokens *= 2;
     const long qc = (N + p.q_tokens - 1) / p.q_tokens;
     HLA_REQUIRE(kv * p.head_groups < (1L << 31) && kv + qc < (1L << 31), HLA_ERR_UNSUPPORTED);

@@ -110,8 +110,9 @@ int hla_version(void);
  * per host thread: a second hla_chain_begin, or hla_chain_end without one, returns
  * HLA_ERR_INVALID_ARG.  Every entry point that launches several kernels (hla_decode_layer,
  * kda_qkvg_proj, skinny_proj_splitk and its no-allocation form, skinny_proj_residual_rmsnorm,
- * moe_route_topk, moe_expert_forward) chains its own kernels at up to 32 tokens (the environment
- * variable HLA_PDL=0 / 1 turns that off / on at any size) and, inside a caller's chain on the same
+ * moe_route_topk, moe_expert_forward) chains its own kernels at up to 32 tokens, and attn_paged_decode,
+ * attn_paged_sparse and attn_select_blocks theirs at any size (the environment variable HLA_PDL=0 / 1
+ * turns that off / on at any size) and, inside a caller's chain on the same
  * stream, continues it.  Its first kernel follows whatever the caller queued before it.
  * -------------------------------------------------------------------------*/
 int hla_chain_begin(hla_stream stream);
