@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
     }
     // After a wait that gave up, products may still run: they read operands that are in shared memory, so they end.
     cp_async_wait<0>();
+    all_ok = __syncthreads_and(ok && all_ok);
     if (!all_ok && tid == 0) {
         umma_commit(&bar_end);
         mbar_wait_for(&bar_end, 0, 8 * kWaitNs, p.status);
