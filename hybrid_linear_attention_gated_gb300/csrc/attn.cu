@@ -24,7 +24,7 @@
 // Measured (CUDA graph, d = 128, 32 query heads on 8 kv heads): 64 sequences of 500 to 15500 tokens, bf16, 310 us and
 // 30000 to 65000 tokens, e4m3, 913 us, both 6.8 TB/s, at or above the copy rate; one sequence of 1021 tokens 7.6 us
 // (this kernel about 4, the join the rest), all of it dependent loads.  CTAs per SM and keys per step were swept: 32
-// keys and 3 CTAs of d = 64, 2 of d = 128 (registers: more CTAs spill or lose the second accumulator set).
+// keys and 3 CTAs of d = 64, 2 of d = 128 (accumulators, query and scores take 255 registers a thread there).
 
 #include <type_traits>
 
@@ -46,7 +46,7 @@ __host__ __device__ constexpr int ctas_per_sm() {
 }
 template <int D, bool FP8, int WR>
 __host__ __device__ constexpr int ring_stages() {
-    constexpr int tile_bytes = 8 * warp_keys<D, FP8>() * D * (FP8 ? 1 : 2), room = 216 * 1024 / ctas_per_sm<D, FP8, WR>() - 3072;
+    constexpr int tile_bytes = 8 * warp_keys<D, FP8>() * D * (FP8 ? 1 : 2), room = 216 * 1024 / ctas_per_sm<D, FP8, WR>() - 3 * 1024;
     return room / tile_bytes < 6 ? room / tile_bytes : 6;
 }
 template <int D, bool FP8, int WR>
@@ -387,8 +387,8 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                     }
                 }
                 // ---- weights.  They meet V as bf16 (fp16 for an 8-bit cache, times 2^14 so that fp16 holds weights
-                // down to 2^-39 of the largest).  A bf16 output rounds by 2^-9 itself, so one rounding of each weight,
-                // which averages out over the keys, is below it.  For an fp32 output the rounded-off part goes through
+                // down to 2^-39 of the largest).  A bf16 output rounds by 2^-8 itself; one rounding of each weight, 2^-8
+                // as well, averages out over the keys to less.  For an fp32 output the rounded-off part goes through
                 // further products, which leaves 2^-25 (fp16: 2^-23); with one less, 2^-17, the output was 1.4e-6 off,
                 // twice what fp32 arithmetic is.
                 auto weigh = [&](auto both) {

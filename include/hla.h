@@ -385,10 +385,12 @@ int hla_decode_layer_routing(const hla_layer *L, int M, const void *ws, const in
  * The cache is a pool of pages of page_size tokens; a block table int32 [B, max_blocks] names the page
  * of each block of page_size consecutive positions of a sequence.  A table entry outside [0, n_pages)
  * holds no page: nothing is read or written there, and its positions hold no keys.  Pages may be shared
- * by sequences for reading; a page that a call appends to belongs to one sequence of that call.
+ * by sequences for reading; a page that a call appends to belongs to one block of one sequence of that call.
  * past_len int32 [B] counts the tokens cached before a step's new ones (committed_len of
  * spec_accept_prefix, say), so one array serves the append and the attention of a step; a negative
- * entry marks an idle slot.  Positions at or behind max_blocks * page_size are dropped.
+ * entry marks an idle slot.  Positions at or behind max_blocks * page_size are dropped; past_len[b] plus the
+ * new tokens stays below 2^31.  max_blocks * page_size < 2^30, n_pages * kv_heads * page_size / 16 < 2^31.
+ * Outputs and workspaces overlap no other argument, but for q_out.
  * All pointers are device pointers; the descriptor itself is read during the call only.
  * -------------------------------------------------------------------------*/
 typedef struct hla_kv_cache {
@@ -413,9 +415,9 @@ typedef struct hla_kv_cache {
  *  Bounds (when k_min and k_max are set): of every page that got a token, over its stored keys at positions
  *  below past_len[b] + new tokens, whatever the page held before; a NaN key makes its channel's bounds NaN.
  *  N: rows of q [N, H, d], k, v [N, kv_heads, d], q_out [N, H, d] (may be q itself), all bf16.  Rows at or
- *  behind cu_seqlens[B], and the rows of idle sequences, are left as they were.
+ *  behind cu_seqlens[B], and the rows of idle sequences, are left as they were (q of dropped tokens is rotated).
  *  cu_seqlens int32 [B + 1] (device, non-decreasing); inv_freq fp64 [rope_dim / 2].
- *  1 <= B <= 1024, max_blocks * page_size < 2^30, H a multiple of kv_heads, H <= 1024.
+ *  N >= 1, 1 <= B <= 1024, H a multiple of kv_heads, H <= 1024.
  * -------------------------------------------------------------------------*/
 int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_t *cu_seqlens, const int32_t *past_len,
                     int max_blocks, const int32_t *block_table, int H, const hla_bf16 *q, const hla_bf16 *k,
@@ -431,8 +433,10 @@ int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_t *cu_seqle
  *  it, whatever it holds.
  *  q bf16 [B, T, H, d]; o [B, T, H, d] (o_dtype: HLA_F32 or HLA_BF16).  Products on tensor cores with fp32
  *  sums; softmax statistics in fp32; the weights meet the values in 16 bits for a bf16 output and in two or
- *  three 16-bit parts, fp32's precision, for an fp32 one.  The work is split over sequences and positions by the lengths on the
- *  device, so one captured graph serves any lengths.  B <= 1024, T <= 8, H <= 1024.
+ *  three 16-bit parts, fp32's precision, for an fp32 one.  The work is split over sequences and positions by
+ *  the lengths on the device, so one captured graph serves any lengths.
+ *  B <= 1024, T <= 8, H <= 1024; scale finite, of either sign.  B full tables may hold less than 2^31 tiles of
+ *  64 keys, over all kv heads and each 64 query rows of one (HLA_ERR_UNSUPPORTED otherwise).
  * -------------------------------------------------------------------------*/
 size_t attn_paged_decode_workspace_size(const hla_kv_cache *C, int B, int T, int H);
 int attn_paged_decode(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const int32_t *block_table,
@@ -446,8 +450,9 @@ int attn_paged_decode(const hla_kv_cache *C, int B, int T, int H, int max_blocks
  *  taken, and of the others those with the highest
  *    max over the kv head's query heads h of  sum_d max(q[b,t,h,d], 0) k_max[j,d] + min(q[b,t,h,d], 0) k_min[j,d],
  *  n_select in all (every visible one when there are no more).  Scores are compared exactly, down to 2^-60 of
- *  sum |q| x max |bound|; equal ones go to the lower block, a NaN score is above all others, a block without a
- *  page scores -infinity.
+ *  sum |q| x max |bound| (in fp64 where that is below 1e-20, above 1e37 or not finite); equal ones go to the
+ *  lower block, a NaN score is above all others, a block without a page scores -infinity.  The bounds are those
+ *  of kv_cache_append or others with k_min <= k_max (or NaN), and stand for keys under a positive k_scale.
  *  sel int32 [B, T, kv_heads, n_select]: the chosen blocks, ascending, then -1.  The cache's k and v are not
  *  used.  max_blocks <= 65536; n_first + n_last <= n_select.
  * -------------------------------------------------------------------------*/
@@ -458,10 +463,11 @@ int attn_select_blocks(const hla_kv_cache *C, int B, int T, int H, int max_block
 
 /* ---------------------------------------------------------------------------
  * attn_paged_decode over listed blocks: token t of sequence b, for the query heads of kv head h, sees the
- * positions of the blocks sel[b, t, h, 0 .. n_select-1], up to past_len[b] + t.  Entries outside
- * [0, max_blocks) are skipped, blocks behind the token hold nothing for it, and a block listed twice counts
- * twice.  Other arguments as attn_paged_decode.  Listing every visible block once gives attn_paged_decode's
- * sum, in another order.
+ * positions of the blocks sel[b, t, h, 0 .. n_select-1], up to past_len[b] + t.  Of a list no more entries are
+ * read than the token sees blocks, (past_len[b] + t) / page_size + 1: a list that attn_select_blocks wrote holds
+ * -1 behind them.  Of those read, entries outside [0, max_blocks) are skipped, blocks behind the token hold
+ * nothing for it, and a block listed twice counts twice.  n_select * page_size < 2^30.  Other arguments as
+ * attn_paged_decode.  Listing every visible block once gives attn_paged_decode's sum, in another order.
  * -------------------------------------------------------------------------*/
 size_t attn_paged_sparse_workspace_size(const hla_kv_cache *C, int B, int T, int H);
 int attn_paged_sparse(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const int32_t *block_table,

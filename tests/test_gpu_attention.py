@@ -334,3 +334,52 @@ def test_forced_wait_timeout_is_reported_and_nothing_is_written():
     assert hla.hla_device_status() == 6 and hla.hla_device_status() == 0  # HLA_ERR_DEVICE_TIMEOUT, then cleared
     assert torch.all(o == 7.0)
     check(p, p.decode(hla.HLA_BF16), hla.HLA_BF16)
+
+
+def test_sequences_that_share_a_prefix():
+    """Four sequences on the same first pages, each with its own last one, through the dense, listed and chosen forms."""
+    dev = require_gpu()
+    for H, Hkv, o_dtype in ((8, 2, hla.HLA_F32), (36, 1, hla.HLA_BF16)):
+        p = Problem(dev, [70, 75, 64, 79], 2, H, Hkv, 64, 16, seed=18, poison=False)
+        p.table[1:, :4] = p.table[0, :4]
+        p.upload()
+        check(p, p.decode(o_dtype), o_dtype)
+        sel = np.tile(np.array([3, 0, 4]), (4, 2, Hkv, 1))
+        check(p, p.decode(o_dtype, torch.from_numpy(sel).to(I32).to(dev)), o_dtype, sel)
+
+
+def test_largest_batch_on_tcgen05():
+    """1024 windows of 8 tokens, 72 rows each, some idle: every CTA runs many short units."""
+    dev = require_gpu()
+    g = np.random.default_rng(19)
+    for d in (64, 128):
+        p = Problem(dev, [int(x) for x in g.integers(-1, 9, size=1024)], 8, 9, 1, d, 16, seed=19).upload()
+        check(p, p.decode(hla.HLA_BF16), hla.HLA_BF16)
+        assert hla.hla_last_variant().endswith("m128>")
+
+
+def test_stream_argument():
+    """The stream given by object or by handle, with another one current."""
+    dev = require_gpu()
+    p = Problem(dev, [300, 40], 2, 8, 2, 64, 16, seed=20).upload()
+    want = p.decode(hla.HLA_F32)
+    ws = torch.empty(hla.attn_paged_decode_workspace_size(p.C, 2, 2, 8), dtype=torch.uint8, device=dev)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        o = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        p.decode(hla.HLA_F32, stream=stream, ws=ws, o=o)
+        side.synchronize()
+        assert torch.equal(o, want)
+
+
+def test_a_list_is_read_up_to_the_blocks_the_token_sees():
+    """Entries behind those are not read: neither a visible block there nor a further mention counts."""
+    dev = require_gpu()
+    p = Problem(dev, [17, 3], 1, 4, 2, 64, 16, seed=21).upload()
+    lists = torch.tensor([[-1, 1, 0, 0], [0, 0, 0, 0]], dtype=I32).view(2, 1, 1, 4).repeat(1, 1, 2, 1)
+    short = torch.tensor([[-1, 1, -1, -1], [0, -1, -1, -1]], dtype=I32).view(2, 1, 1, 4).repeat(1, 1, 2, 1)
+    a, b = p.decode(hla.HLA_F32, lists.to(dev)), p.decode(hla.HLA_F32, short.to(dev))
+    assert torch.equal(a, b)
+    check(p, a, hla.HLA_F32, short.numpy())
