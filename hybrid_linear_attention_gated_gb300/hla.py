@@ -48,6 +48,7 @@ class hla_kv_cache(ctypes.Structure):
     _fields_ = [("dtype", c_int), ("n_pages", c_int), ("page_size", c_int), ("kv_heads", c_int),
                 ("head_dim", c_int), ("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("k_min", P),
                 ("k_max", P)]
+    device = None  # of the tensors that make_kv_cache was given
 
 
 CACHE = ctypes.POINTER(hla_kv_cache)
@@ -319,6 +320,12 @@ def _tensor(fn, name, t, dtype, n, dev):
                    f"got {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}, {t.device}")
 
 
+def _cache(fn, C, dev):
+    if C.device is None or C.device == dev:
+        return ctypes.byref(C)
+    raise HlaError(fn, HLA_ERR_INVALID_ARG, f"the cache is on device {C.device}, the current device is {dev}")
+
+
 def make_kv_cache(dtype, n_pages, page_size, kv_heads, head_dim, k, v, k_scale=None, v_scale=None, k_min=None,
                   k_max=None):
     """Build an hla_kv_cache descriptor; it keeps the tensors it was given alive."""
@@ -327,6 +334,7 @@ def make_kv_cache(dtype, n_pages, page_size, kv_heads, head_dim, k, v, k_scale=N
     kv = torch.float8_e4m3fn if dtype == HLA_E4M3 else torch.bfloat16
     n, m = n_pages * kv_heads * page_size * head_dim, n_pages * kv_heads * head_dim
     C.tensors = (k, v, k_scale, v_scale, k_min, k_max)
+    C.device = dev if any(isinstance(t, torch.Tensor) for t in C.tensors) else None
     for name, t, dt, least in (("k", k, kv, n), ("v", v, kv, n), ("k_scale", k_scale, torch.float32, kv_heads),
                                ("v_scale", v_scale, torch.float32, kv_heads), ("k_min", k_min, torch.bfloat16, m),
                                ("k_max", k_max, torch.bfloat16, m)):
@@ -340,7 +348,7 @@ def kv_cache_append(C, N, B, cu_seqlens, past_len, max_blocks, block_table, H, q
     fn, bf, i32 = "kv_cache_append", torch.bfloat16, torch.int32
     nq, nk = N * H * C.head_dim, N * C.kv_heads * C.head_dim
     return _check(fn, load().kv_cache_append(
-        ctypes.byref(C), N, B, _tensor(fn, "cu_seqlens", cu_seqlens, i32, B + 1, dev),
+        _cache(fn, C, dev), N, B, _tensor(fn, "cu_seqlens", cu_seqlens, i32, B + 1, dev),
         _tensor(fn, "past_len", past_len, i32, B, dev), max_blocks,
         _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev), H, _tensor(fn, "q", q, bf, nq, dev),
         _tensor(fn, "k", k, bf, nk, dev), _tensor(fn, "v", v, bf, nk, dev), rope_dim, rope_interleaved,
@@ -357,7 +365,7 @@ def attn_paged_decode(C, B, T, H, max_blocks, block_table, past_len, scale, q, o
     torch, dev = _torch_and_device()
     fn, i32, n = "attn_paged_decode", torch.int32, B * T * H * C.head_dim
     return _check(fn, load().attn_paged_decode(
-        ctypes.byref(C), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
+        _cache(fn, C, dev), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
         _tensor(fn, "past_len", past_len, i32, B, dev), scale, _tensor(fn, "q", q, torch.bfloat16, n, dev),
         _tensor(fn, "o", o, torch.bfloat16 if o_dtype == HLA_BF16 else torch.float32, n, dev), o_dtype,
         _tensor(fn, "ws", ws, torch.uint8, ws_bytes, dev), ws_bytes, _stream(stream)))
@@ -372,7 +380,7 @@ def attn_select_blocks(C, B, T, H, max_blocks, block_table, past_len, n_select, 
     torch, dev = _torch_and_device()
     fn, i32 = "attn_select_blocks", torch.int32
     return _check(fn, load().attn_select_blocks(
-        ctypes.byref(C), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
+        _cache(fn, C, dev), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
         _tensor(fn, "past_len", past_len, i32, B, dev), n_select, n_first, n_last,
         _tensor(fn, "q", q, torch.bfloat16, B * T * H * C.head_dim, dev),
         _tensor(fn, "sel", sel, i32, B * T * C.kv_heads * n_select, dev),
@@ -388,7 +396,7 @@ def attn_paged_sparse(C, B, T, H, max_blocks, block_table, past_len, n_select, s
     torch, dev = _torch_and_device()
     fn, i32, n = "attn_paged_sparse", torch.int32, B * T * H * C.head_dim
     return _check(fn, load().attn_paged_sparse(
-        ctypes.byref(C), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
+        _cache(fn, C, dev), B, T, H, max_blocks, _tensor(fn, "block_table", block_table, i32, B * max_blocks, dev),
         _tensor(fn, "past_len", past_len, i32, B, dev), n_select,
         _tensor(fn, "sel", sel, i32, B * T * C.kv_heads * n_select, dev), scale,
         _tensor(fn, "q", q, torch.bfloat16, n, dev),

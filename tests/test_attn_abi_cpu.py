@@ -128,3 +128,17 @@ def test_binding_refuses_tensors_a_kernel_would_misread(lib):
     if torch.cuda.is_available():
         with pytest.raises(hla.HlaError):
             hla.attn_paged_decode(C, 2, 1, 8, 4, table.int(), FAKE, 1.0, FAKE, FAKE, 0, FAKE, 1 << 40, stream=0)  # a host tensor
+
+
+def test_binding_refuses_a_cache_of_another_device(lib):
+    """The descriptor's tensors are on the device that was current when it was made."""
+    C = cache()
+    assert C.device is None
+    C.device = 5
+    for call in (lambda: hla.kv_cache_append(C, 1, 1, FAKE, FAKE, 4, FAKE, 8, FAKE, FAKE, FAKE, 0, 0, None, FAKE, stream=0),
+                 lambda: hla.attn_paged_decode(C, 1, 1, 8, 4, FAKE, FAKE, 1.0, FAKE, FAKE, 0, FAKE, 1 << 40, stream=0),
+                 lambda: hla.attn_select_blocks(C, 1, 1, 8, 4, FAKE, FAKE, 2, 0, 0, FAKE, FAKE, FAKE, 1 << 40, stream=0),
+                 lambda: hla.attn_paged_sparse(C, 1, 1, 8, 4, FAKE, FAKE, 2, FAKE, 1.0, FAKE, FAKE, 0, FAKE, 1 << 40, stream=0)):
+        with pytest.raises(hla.HlaError) as e:
+            call()
+        assert e.value.status == INVALID and "device 5" in str(e.value)
