@@ -12,8 +12,8 @@
 // blocks above t + 2 e are in and blocks below t - 2 e are out; the few between are scored again exactly and
 // ranked.
 // Measured (CUDA graph, pages of 64, 32 query heads on 8 kv heads of 128, 64 blocks chosen): one sequence of 131001
-// tokens 12.7 us, latency; 32 sequences x 2 tokens, 20000 to 90000 tokens, 35.4 us, of which the scores take about 25 (4.5
-// TB/s: about 900 instructions per group of 8 KB and warp set the pace) and the choice the rest.
+// tokens 10.9 us, latency; 32 sequences x 2 tokens, 20000 to 90000 tokens, 30.2 us, of which the scores take about 19 (5.9
+// TB/s) and the choice the rest: dependent steps (scores in, counts, border, output) of about 1 us each.
 #include "paged.cuh"
 
 namespace hla {
@@ -25,7 +25,7 @@ constexpr int kScoreStages = 2;       // groups in flight or in use per warp
 constexpr int kScoreCtas = 3;         // CTAs per SM
 constexpr int kChooseThreads = 256;
 constexpr int kMaxBlocks = 65536;     // blocks per sequence (a bit each in shared memory)
-constexpr int kStaged = 6144;         // scores of a row kept in shared memory; longer rows are read through L2
+constexpr int kStaged = 6144;         // most scores of a row in shared memory; longer rows are read through L2
 constexpr int kListed = 1024;         // blocks near the border kept in shared memory
 constexpr int kBins = 2048;           // of a row's scores, to find the n-th highest
 constexpr int kFewInBin = 64;         // a bin with no more scores is not split again
@@ -41,6 +41,7 @@ struct SelectParams {
     int max_blocks, n_pages, pshift;
     int n_select, n_first, n_last;
     int stride, groups;
+    int staged;                   // scores of a row that attn_choose_kernel keeps in shared memory
     uint32_t by_G, by_Hkv, by_T;  // for divided()
 };
 
@@ -71,6 +72,17 @@ __device__ __forceinline__ uint32_t neg2(uint32_t x) {  // min(x, 0) of two bf16
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+__device__ __forceinline__ float max_keep_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t at) {
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+    return w;
+}
+
 // Prefix sums of the sequences' groups per kv head into pre[0..B]; ends with a block barrier.
 __device__ __forceinline__ void group_prefix(const SelectParams &p, int *pre) {
     const int lane = threadIdx.x;
@@ -97,15 +109,20 @@ __host__ __device__ constexpr int score_ring() {  // shared memory of one warp's
     return kScoreStages * 2 * kGroupBlocks * 2 * D;
 }
 
-// Scores of groups of 16 blocks of one (sequence, kv head) for all T x G queries.  The rows go in tiles of 16
-// that hold whole groups of G heads (or a part of one, for G > 16).
-template <int D>
+// Scores of groups of 16 blocks of one (sequence, kv head) for all T x G queries.  The blocks are the products' 16 rows
+// and the queries their 8 columns, NQ times: a tile of 8 NQ queries holds whole groups of G heads (or a part of one).
+// The order of channels within a sum is free, so lane (i, j) takes channels 32 c + 8 j .. + 7 of rows i and i + 8 and of
+// query i, four of them for each of two products: 16 bytes to a load of q or of shared memory.
+// NQ = 1, for at most 8 queries, against 2 there: 32 sequences x 2 tokens of 4 heads 2.6 us less.  The operands loaded from
+// global memory into registers ahead of their use, without shared memory, are no faster (32.1 us with either) and slower
+// for one sequence (14.1 against 12.1).
+template <int D, int NQ>
 __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(const SelectParams p) {
-    constexpr int RB = 2 * D, CPR = RB / 16, KS = D / 16, GB = kGroupBlocks * RB, NS = kScoreStages;
+    constexpr int ROWS = 8 * NQ, RB = 2 * D, CPR = RB / 16, KS = D / 16, GB = kGroupBlocks * RB, NS = kScoreStages;
     constexpr unsigned ALL = 0xffffffffu;
     extern __shared__ __align__(128) uint8_t smem[];
     int *const s_pre = reinterpret_cast<int *>(smem + 4 * score_ring<D>());  // [B + 1]
-    __shared__ float s_tile[4][16][17];
+    __shared__ float s_tile[4][ROWS][17];
     __shared__ unsigned s_has[4][NS];  // blocks of each staged group that have a page
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = lane >> 2, j = lane & 3;
     pdl_wait_trigger();
@@ -143,25 +160,29 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
     // The place and pages of the group that is copied next are looked up one step ahead.
     Place ahead = n > 0 ? place(begin) : Place{};
     int pg = n > 0 ? page_of(ahead) : -1;
-    uint32_t to[GB / 512];  // where this lane's chunks of a group go: chunk y * 32 + lane
-#pragma unroll
-    for (int y = 0; y < GB / 512; ++y) to[y] = ring + swizzled<RB>((y * 32 + lane) / CPR, lane % CPR);
+    // This lane's 16-byte chunks of a group: row y ROWS_IN + lane / CPR, chunk lane % CPR, for every y
+    constexpr int ROWS_IN = 32 / CPR;
+    const uint8_t *const from_max = reinterpret_cast<const uint8_t *>(p.k_max) + lane % CPR * 16;
+    const uint8_t *const from_min = reinterpret_cast<const uint8_t *>(p.k_min) + lane % CPR * 16;
+    const uint32_t to = ring + lane / CPR * RB + ((lane % CPR ^ (lane / CPR & 1) << 2) << 4);
     auto issue = [&](int x, int stage) {
-        const uint32_t off = stage * 2 * GB;
+        const uint32_t dst = to + stage * 2 * GB;
+        const uint32_t row = pg * p.Hkv + ahead.hk;
         if (__all_sync(ALL, pg >= 0)) {
 #pragma unroll
             for (int y = 0; y < GB / 512; ++y) {
-                const size_t o = (size_t)(__shfl_sync(ALL, pg, (y * 32 + lane) / CPR) * p.Hkv + ahead.hk) * D + lane % CPR * 8;
-                cp_async16_s(to[y] + off, p.k_max + o);
-                cp_async16_s(to[y] + off + GB, p.k_min + o);
+                const size_t o = (size_t)__shfl_sync(ALL, row, y * ROWS_IN + lane / CPR) * RB;
+                cp_async16_s(dst + y * 512, from_max + o);
+                cp_async16_s(dst + y * 512 + GB, from_min + o);
             }
         } else {
 #pragma unroll
             for (int y = 0; y < GB / 512; ++y) {
-                const int rp = __shfl_sync(ALL, pg, (y * 32 + lane) / CPR);
-                const size_t o = rp >= 0 ? (size_t)(rp * p.Hkv + ahead.hk) * D + lane % CPR * 8 : 0;
-                cp_async16_or_zero(to[y] + off, p.k_max + o, rp >= 0);
-                cp_async16_or_zero(to[y] + off + GB, p.k_min + o, rp >= 0);
+                const bool in = __shfl_sync(ALL, pg, y * ROWS_IN + lane / CPR) >= 0;
+                const uint32_t r = __shfl_sync(ALL, row, y * ROWS_IN + lane / CPR);
+                const size_t o = in ? (size_t)r * RB : 0;
+                cp_async16_or_zero(dst + y * 512, from_max + o, in);
+                cp_async16_or_zero(dst + y * 512 + GB, from_min + o, in);
             }
         }
         const unsigned has = __ballot_sync(ALL, pg >= 0);
@@ -178,87 +199,91 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) attn_score_kernel(c
         cp_async_commit();
     }
 
-    const int per = p.G <= 16 ? 16 / p.G : 1;     // tokens per row tile
-    const int parts = (p.G + 15) / 16;            // row tiles per token
-    const bool one_tile = parts == 1 && per >= p.T;
+    const int per = NQ == 1 ? p.T : p.G <= ROWS ? ROWS / p.G : 1;  // tokens per query tile
+    const int parts = NQ == 1 ? 1 : (p.G + ROWS - 1) / ROWS;       // query tiles per token
+    const bool one_tile = NQ == 1 || (parts == 1 && per >= p.T);
     Place use = n > 0 ? place(begin) : Place{};
-    uint32_t qf[KS][4];
-    // fragments of the row tile of tokens t0.. and part `part` of the heads
+    uint4 qf[KS / 2][NQ];
+    // fragments of the query tile of tokens t0.. and part `part` of the heads
     auto load_q = [&](int t0, int part) {
 #pragma unroll
-        for (int hrow = 0; hrow < 2; ++hrow) {
-            const int r = i + 8 * hrow;
+        for (int y = 0; y < NQ; ++y) {
+            const int r = i + 8 * y;
             const int tl = divided(r, p.by_G);
-            const int t = t0 + (parts == 1 ? tl : 0), g = parts == 1 ? r - tl * p.G : part * 16 + r;
+            const int t = t0 + (parts == 1 ? tl : 0), g = parts == 1 ? r - tl * p.G : part * ROWS + r;
             const bool on = t < p.T && g < p.G && (parts > 1 || r < per * p.G);
-            const uint16_t *src = p.q + (on ? ((size_t)(use.b * p.T + t) * p.H + use.hk * p.G + g) * D : 0);
+            const uint16_t *src = p.q + (on ? ((size_t)(use.b * p.T + t) * p.H + use.hk * p.G + g) * D + 8 * j : 0);
 #pragma unroll
-            for (int c = 0; c < KS; ++c) {
-                qf[c][hrow] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * c + 2 * j) : 0u;
-                qf[c][2 + hrow] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * c + 8 + 2 * j) : 0u;
-            }
+            for (int c = 0; c < KS / 2; ++c)
+                qf[c][y] = on ? *reinterpret_cast<const uint4 *>(src + 32 * c) : make_uint4(0u, 0u, 0u, 0u);
         }
     };
+    // chunk 4 c + j of row i sits at 4 (c ^ (i & 1)) + j, so that two rows' four chunks are in different banks
+    const uint32_t at0 = ring + i * RB + j * 16 + (i & 1) * 64, at1 = ring + i * RB + j * 16 + (~i & 1) * 64;
     if (one_tile && n > 0) load_q(0, 0);
     for (int x = 0, stage = 0, next = NS - 1; x < n; ++x) {
         cp_async_wait<NS - 2>();
         __syncwarp();
         if (x + NS - 1 < n) issue(x + NS - 1, next);
         cp_async_commit();
-        const uint32_t bmax = ring + stage * 2 * GB, bmin = bmax + GB;
+        const uint32_t stage_off = stage * 2 * GB;
         const int j0 = use.g * kGroupBlocks;
         const unsigned has = s_has[warp][stage];
         uint32_t top = 0, low = 0;  // largest k_max and smallest k_min of the group, or 0
 
         for (int t0 = 0; t0 < p.T; t0 += per) {
             const int tokens = p.T - t0 < per ? p.T - t0 : per;
-            float keep[8];                        // of (token t0 + y / 16, block y % 16) for outputs y of this lane
+            float keep[ROWS / 2];                 // of (token t0 + y / 16, block y % 16) for outputs y of this lane
 #pragma unroll
-            for (int y = 0; y < 8; ++y) keep[y] = -INFINITY;
+            for (int y = 0; y < ROWS / 2; ++y) keep[y] = -INFINITY;
             for (int part = 0; part < parts; ++part) {
                 if (!one_tile) load_q(t0, part);
                 // four chains of sums per tile (even and odd steps of both halves): a chain's products wait for one another
-                float s[4][2][4] = {};
+                float s[4][NQ][4] = {};
 #pragma unroll
-                for (int c = 0; c < KS; ++c) {
-                    uint32_t f[4], g[4];
-                    const uint32_t at = swizzled<RB>((lane & 7) + ((lane >> 4) << 3), 2 * c + ((lane >> 3) & 1));
-                    ldmatrix_x4(f, bmax + at);
-                    ldmatrix_x4(g, bmin + at);
-                    const uint32_t up[4] = {relu2(qf[c][0]), relu2(qf[c][1]), relu2(qf[c][2]), relu2(qf[c][3])};
-                    const uint32_t dn[4] = {neg2(qf[c][0]), neg2(qf[c][1]), neg2(qf[c][2]), neg2(qf[c][3])};
+                for (int c = 0; c < KS / 2; ++c) {  // 32 channels: lane j has 8 j .. 8 j + 7, four of them for each product
+                    const uint32_t at = (c & 1 ? at1 : at0) + (c >> 1) * 128;
+                    uint4 f[2], g[2];  // of rows i and i + 8
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        mma_bf16_16816(s[2 * (c & 1)][y], up[0], up[1], up[2], up[3], f[2 * y], f[2 * y + 1]);
-                        mma_bf16_16816(s[2 * (c & 1) + 1][y], dn[0], dn[1], dn[2], dn[3], g[2 * y], g[2 * y + 1]);
+                    for (int h = 0; h < 2; ++h) {
+                        f[h] = lds_v4(at + stage_off + h * 8 * RB);
+                        g[h] = lds_v4(at + stage_off + GB + h * 8 * RB);
+                    }
+#pragma unroll
+                    for (int y = 0; y < NQ; ++y) {
+                        const uint4 w = qf[c][y];
+                        mma_bf16_16816(s[0][y], f[0].x, f[1].x, f[0].y, f[1].y, relu2(w.x), relu2(w.y));
+                        mma_bf16_16816(s[1][y], g[0].x, g[1].x, g[0].y, g[1].y, neg2(w.x), neg2(w.y));
+                        mma_bf16_16816(s[2][y], f[0].z, f[1].z, f[0].w, f[1].w, relu2(w.z), relu2(w.w));
+                        mma_bf16_16816(s[3][y], g[0].z, g[1].z, g[0].w, g[1].w, neg2(w.z), neg2(w.w));
                     }
                     if (t0 == 0 && part == 0)
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            top = max2(top, f[y]);
-                            low = min2(low, g[y]);
+                        for (int h = 0; h < 2; ++h) {
+                            top = max2(max2(max2(max2(top, f[h].x), f[h].y), f[h].z), f[h].w);
+                            low = min2(min2(min2(min2(low, g[h].x), g[h].y), g[h].z), g[h].w);
                         }
                 }
                 __syncwarp();
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                for (int y = 0; y < NQ; ++y)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s_tile[warp][i + 8 * (e >> 1)][8 * y + 2 * j + (e & 1)] = (s[0][y][e] + s[2][y][e]) + (s[1][y][e] + s[3][y][e]);
+                    for (int e = 0; e < 4; ++e) s_tile[warp][8 * y + 2 * j + (e & 1)][i + 8 * (e >> 1)] = (s[0][y][e] + s[2][y][e]) + (s[1][y][e] + s[3][y][e]);
                 __syncwarp();
                 // maximum over the heads (a NaN stays)
-                const int rows = parts == 1 ? p.G : (p.G - part * 16 < 16 ? p.G - part * 16 : 16);
+                const int rows = parts == 1 ? p.G : (p.G - part * ROWS < ROWS ? p.G - part * ROWS : ROWS);
 #pragma unroll
-                for (int y = 0; y < 8; ++y) {
+                for (int y = 0; y < ROWS / 2; ++y) {
                     const int o = y * 32 + lane, tl = o >> 4, bl = o & 15;
                     if (2 * y >= tokens) break;  // (the whole warp)
                     for (int g = 0; g < rows && tl < tokens; ++g) {
                         const float v = s_tile[warp][(parts == 1 ? tl * p.G : 0) + g][bl];
-                        keep[y] = v > keep[y] || v != v ? v : keep[y];
+                        keep[y] = max_keep_nan(v, keep[y]);
                     }
                 }
             }
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
+            for (int y = 0; y < ROWS / 2; ++y) {
                 const int o = y * 32 + lane, tl = o >> 4, bl = o & 15, t = t0 + tl;
                 if (2 * y >= tokens) break;
                 if (tl < tokens && j0 + bl < use.nb)
@@ -301,12 +326,13 @@ __device__ __forceinline__ int block_sum(int x, int *s_red) {
     for (int w = 0; w < kWarps; ++w) all += s_red[w];
     return all;
 }
-// One CTA per (sequence, token, kv head).  The steps are short and latency-bound (about 3 us for 2048 blocks): few
-// barriers, and loops kept rolled, since code that runs once is fetched once.
+// One CTA per (sequence, token, kv head).  The steps are short and latency-bound (5 to 6 us for 1000 to 2000 blocks): few
+// barriers, loads of a step all on their way before the first is used, and loops kept rolled otherwise, since code that
+// runs once is fetched once.  Four CTAs per SM: with 80 registers a thread, three, 512 rows take two waves (3.5 us more).
 template <int D>
-__global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const SelectParams p) {
-    __shared__ float s_score[kStaged];
-    __shared__ uint32_t s_bits[kMaxBlocks / 32];       // the choice
+__global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const SelectParams p) {
+    extern __shared__ float s_score[];                 // as many as a row may have, kStaged at most
+    uint32_t *const s_bits = reinterpret_cast<uint32_t *>(s_score) + p.staged;  // the choice, a bit per block
     __shared__ unsigned long long s_key[kListed];
     __shared__ int s_blk[kListed];
     __shared__ int s_red[kWarps];
@@ -365,17 +391,25 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
 
     // the scores; a block without a page below every other, but finite
     const float *row_score = p.score + (size_t)row * p.stride;
-    const bool staged = nb <= kStaged;
+    const bool staged = nb <= p.staged;
     const int groups = (visible_blocks(p, b, p.T - 1) + kGroupBlocks - 1) / kGroupBlocks;
     const float *row_abs = p.absmax + ((size_t)b * p.Hkv + hk) * p.groups;
     if (tid < groups) absb = row_abs[tid];  // in flight together with the scores
     float lo = INFINITY, hi = -INFINITY;
-    for (int x = tid; x < nb; x += kChooseThreads) {
-        const float v = fmaxf(row_score[x], -3e38f);
-        if (staged) s_score[x] = v;
-        if (x >= e0 && x < e1) {
-            lo = fminf(lo, v);
-            hi = fmaxf(hi, v);
+#pragma unroll 1
+    for (int x0 = tid; x0 < nb; x0 += 8 * kChooseThreads) {
+        float r[8];  // all on their way before the first is stored
+#pragma unroll
+        for (int y = 0; y < 8; ++y) r[y] = x0 + y * kChooseThreads < nb ? row_score[x0 + y * kChooseThreads] : 0.f;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const int x = x0 + y * kChooseThreads;
+            const float v = fmaxf(r[y], -3e38f);
+            if (staged && x < nb) s_score[x] = v;
+            if (x >= e0 && x < e1) {
+                lo = fminf(lo, v);
+                hi = fmaxf(hi, v);
+            }
         }
     }
     for (int c = tid + kChooseThreads; c < groups; c += kChooseThreads) absb = max_nan(row_abs[c], absb);
@@ -484,43 +518,66 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
     __syncthreads();
     const int near = s_near, want = k - s_sure;
     if (want > 0 && near > want) {
-        // Exact scores of the blocks in the band as integers in their order, a warp to a (block, head).  A product of two
+        // Exact scores of the blocks in the band as integers in their order, a warp to a block.  A product of two
         // bf16 is exact in fp32 and, times a power of two that holds the sum below 2^62, in 64-bit fixed point down to
         // 2^-37 of the largest: integer sums, so equal scores are equal whatever the order.  Where the size is out of
         // fp32's comfort (infinities and NaN too) the sum is fp64's.
         const int shift = usable ? 61 - ilogbf(size) : 0;  // 2^shift size < 2^62
         const float s1 = exp2f((float)(shift / 2)), s2 = exp2f((float)(shift - shift / 2));
-        auto exact = [&](int x, int g) -> unsigned long long {
+        // The highest of the heads' scores of block x, four heads at a time.
+        auto exact = [&](int x) -> unsigned long long {
+            float q[4][CPL], up[CPL], dn[CPL];
+            unsigned long long best = 0;
             const int pg = table[x];
-            if (pg < 0 || pg >= p.n_pages) return 1;
-            float q[CPL], up[CPL], dn[CPL];
-            channels(qrow + (size_t)g * D, q);
-            channels(p.k_max + ((size_t)pg * p.Hkv + hk) * D + lane * CPL, up);
-            channels(p.k_min + ((size_t)pg * p.Hkv + hk) * D + lane * CPL, dn);
-            if (usable) {
-                long long s = 0;
+            const bool has = pg >= 0 && pg < p.n_pages;
+            const size_t row = ((size_t)(has ? pg : 0) * p.Hkv + hk) * D + lane * CPL;
+#pragma unroll 1
+            for (int g = 0; g < p.G; g += 4) {
 #pragma unroll
-                for (int c = 0; c < CPL; ++c)
-                    s += __float2ll_rn(__fmul_rn(__fmul_rn(__fmul_rn(q[c], q[c] > 0.f ? up[c] : dn[c]), s1), s2));
+                for (int y = 0; y < 4; ++y) channels(qrow + (size_t)(g + y < p.G ? g + y : g) * D, q[y]);
+                if (g == 0) {
+                    channels(p.k_max + row, up);
+                    channels(p.k_min + row, dn);
+                }
+                if (usable) {
+                    long long s[4] = {};
 #pragma unroll
-                for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(ALL, s, m);
-                return (unsigned long long)s ^ 1ull << 63;
+                    for (int y = 0; y < 4; ++y)
+#pragma unroll
+                        for (int c = 0; c < CPL; ++c)
+                            s[y] += __float2ll_rn(__fmul_rn(__fmul_rn(__fmul_rn(q[y][c], q[y][c] > 0.f ? up[c] : dn[c]), s1), s2));
+#pragma unroll
+                    for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) s[y] += __shfl_xor_sync(ALL, s[y], m);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const unsigned long long o = (unsigned long long)s[y] ^ 1ull << 63;
+                        best = o > best ? o : best;
+                    }
+                } else {
+#pragma unroll 1
+                    for (int y = 0; y < 4; ++y) {
+                        double s = 0.0;
+#pragma unroll
+                        for (int c = 0; c < CPL; ++c) {
+                            const float w = y == 0 ? q[0][c] : y == 1 ? q[1][c] : y == 2 ? q[2][c] : q[3][c];
+                            s += (double)(w < 0.f ? 0.f : w) * (double)up[c] + (double)(w > 0.f ? 0.f : w) * (double)dn[c];
+                        }
+#pragma unroll
+                        for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(ALL, s, m);
+                        const unsigned long long o = ordered(s);
+                        best = o > best ? o : best;
+                    }
+                }
             }
-            double s = 0.0;
-#pragma unroll
-            for (int c = 0; c < CPL; ++c)
-                s += (double)(q[c] < 0.f ? 0.f : q[c]) * (double)up[c] + (double)(q[c] > 0.f ? 0.f : q[c]) * (double)dn[c];
-#pragma unroll
-            for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(ALL, s, m);
-            return ordered(s);
+            return has ? best : 1;
         };
         if (near <= kListed) {  // ranked one against another
-            for (int c = tid; c < near; c += kChooseThreads) s_key[c] = 0;
-            __syncthreads();
 #pragma unroll 1
-            for (int c = warp; c < near * p.G; c += kWarps) {
-                const unsigned long long o = exact(s_blk[c / p.G], c % p.G);
-                if (lane == 0) atomicMax(&s_key[c / p.G], o);
+            for (int c = warp; c < near; c += kWarps) {
+                const unsigned long long o = exact(s_blk[c]);
+                if (lane == 0) s_key[c] = o;
             }
             __syncthreads();
             for (int c = tid; c < near; c += kChooseThreads) {
@@ -534,14 +591,8 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
             unsigned long long *key = p.exact + (size_t)row * p.stride;
 #pragma unroll 1
             for (int x = e0 + warp; x < e1; x += kWarps) {
-                unsigned long long best = 0;
-                if (in_band(score(x)))
-#pragma unroll 1
-                    for (int g = 0; g < p.G; ++g) {
-                        const unsigned long long o = exact(x, g);
-                        best = o > best ? o : best;
-                    }
-                if (lane == 0) key[x] = best;
+                const unsigned long long o = in_band(score(x)) ? exact(x) : 0;
+                if (lane == 0) key[x] = o;
             }
             __syncthreads();
             // the want-th highest key: the largest klo with count(key >= klo) >= want
@@ -607,7 +658,7 @@ __global__ void __launch_bounds__(kChooseThreads) attn_choose_kernel(const Selec
     }
 }
 
-template <int D>
+template <int D, int NQ>
 cudaError_t launch_score(const SelectParams &p, cudaStream_t st) {
     constexpr size_t ring = 4 * (size_t)score_ring<D>();
     // the shared-memory limit is a per-device attribute: raise it once on every device used
@@ -616,13 +667,13 @@ cudaError_t launch_score(const SelectParams &p, cudaStream_t st) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !done[dev]) {
-        e = cudaFuncSetAttribute(attn_score_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(ring + (kMaxBatch + 1) * sizeof(int)));
+        e = cudaFuncSetAttribute(attn_score_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(ring + (kMaxBatch + 1) * sizeof(int)));
         if (e != cudaSuccess) return e;
         if (dev < 64) done[dev] = true;
     }
     const long most = ((long)p.B * p.Hkv * p.groups + 3) / 4;  // a group per warp
     const int slots = kScoreCtas * sm_count();
-    return launch_kernel(attn_score_kernel<D>, dim3((unsigned)(most < slots ? most : slots)), dim3(kScoreThreads),
+    return launch_kernel(attn_score_kernel<D, NQ>, dim3((unsigned)(most < slots ? most : slots)), dim3(kScoreThreads),
                          ring + (p.B + 1) * sizeof(int), st, p);
 }
 
@@ -668,6 +719,7 @@ extern "C" int attn_select_blocks(const hla_kv_cache *C, int B, int T, int H, in
     p.stride = (int)row_stride(max_blocks);
     p.by_G = divisor(p.G); p.by_Hkv = divisor(p.Hkv); p.by_T = divisor(T);
     p.groups = (max_blocks + kGroupBlocks - 1) / kGroupBlocks;
+    p.staged = max_blocks < kStaged ? max_blocks : kStaged;
     const size_t rows = (size_t)B * T * p.Hkv;
     p.exact = static_cast<unsigned long long *>(ws);
     p.score = reinterpret_cast<float *>(p.exact + rows * p.stride);
@@ -676,8 +728,10 @@ extern "C" int attn_select_blocks(const hla_kv_cache *C, int B, int T, int H, in
     set_variant("attn_select<d%d>", p.d);
     // the choice always follows the scores programmatically (HLA_PDL=0 turns that off as everywhere)
     PdlChain chain(st, pdl_default(1));
-    e = launched(p.d == 128 ? launch_score<128>(p, st) : launch_score<64>(p, st));
+    e = launched(p.T * p.G <= 8 ? p.d == 128 ? launch_score<128, 1>(p, st) : launch_score<64, 1>(p, st)
+                               : p.d == 128 ? launch_score<128, 2>(p, st) : launch_score<64, 2>(p, st));
     if (e != HLA_OK) return e;
-    return launched(p.d == 128 ? launch_kernel(attn_choose_kernel<128>, dim3((unsigned)rows), dim3(kChooseThreads), 0, st, p)
-                               : launch_kernel(attn_choose_kernel<64>, dim3((unsigned)rows), dim3(kChooseThreads), 0, st, p));
+    const size_t smem = p.staged * sizeof(float) + (max_blocks + 31) / 32 * sizeof(uint32_t);
+    return launched(p.d == 128 ? launch_kernel(attn_choose_kernel<128>, dim3((unsigned)rows), dim3(kChooseThreads), smem, st, p)
+                               : launch_kernel(attn_choose_kernel<64>, dim3((unsigned)rows), dim3(kChooseThreads), smem, st, p));
 }
