@@ -23,11 +23,9 @@ constexpr int kGroupBlocks = 16;      // blocks scored together by a warp
 constexpr int kScoreThreads = 128;
 constexpr int kScoreStages = 2;       // groups in flight or in use per warp
 constexpr int kScoreCtas = 3;         // CTAs per SM
-constexpr int kChooseThreads = 256;
 constexpr int kMaxBlocks = 65536;     // blocks per sequence (a bit each in shared memory)
 constexpr int kStaged = 6144;         // most scores of a row in shared memory; longer rows are read through L2
 constexpr int kListed = 1024;         // blocks near the border kept in shared memory
-constexpr int kBins = 2048;           // of a row's scores, to find the n-th highest
 constexpr int kFewInBin = 64;         // a bin with no more scores is not split again
 
 struct SelectParams {
@@ -314,8 +312,7 @@ __device__ __forceinline__ unsigned long long ordered(double x) {
 }
 __device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }  // a NaN stays
 
-constexpr int kWarps = kChooseThreads / 32;
-
+template <int WARPS>
 __device__ __forceinline__ int block_sum(int x, int *s_red) {
     x = __reduce_add_sync(0xffffffffu, x);
     __syncthreads();
@@ -323,23 +320,26 @@ __device__ __forceinline__ int block_sum(int x, int *s_red) {
     __syncthreads();
     int all = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) all += s_red[w];
+    for (int w = 0; w < WARPS; ++w) all += s_red[w];
     return all;
 }
 // One CTA per (sequence, token, kv head).  The steps are short and latency-bound (5 to 6 us for 1000 to 2000 blocks): few
 // barriers, loads of a step all on their way before the first is used, and loops kept rolled otherwise, since code that
-// runs once is fetched once.  Four CTAs per SM: with 80 registers a thread, three, 512 rows take two waves (3.5 us more).
-template <int D>
-__global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const SelectParams p) {
+// runs once is fetched once.  At 80 registers a thread, three CTAs of 256 to an SM, 512 rows take two waves (3.5 us more).
+// 256 threads while all rows run at once, 128, with less work in all, behind that: against 256 there, 1024 rows 36.0 us
+// (scores and choice) for 39.6 and 2048 rows 59.3 for 67.0; against 128, 8 rows 11.0 for 12.8 and 512 rows 30.3 for 31.8.
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) attn_choose_kernel(const SelectParams p) {
     extern __shared__ float s_score[];                 // as many as a row may have, kStaged at most
     uint32_t *const s_bits = reinterpret_cast<uint32_t *>(s_score) + p.staged;  // the choice, a bit per block
-    __shared__ unsigned long long s_key[kListed];
+    constexpr int WARPS = THREADS / 32, BINS = 8 * THREADS;  // bins of a row's scores, to find the n-th highest
+    __shared__ __align__(16) unsigned long long s_key[kListed];
     __shared__ int s_blk[kListed];
-    __shared__ int s_red[kWarps];
-    __shared__ float s_f[4][kWarps];
+    __shared__ int s_red[WARPS];
+    __shared__ float s_f[4][WARPS];
     __shared__ int s_near, s_sure, s_bin, s_count;
-    int *const s_hist = reinterpret_cast<int *>(s_key);  // [kBins], before the keys
-    static_assert(kBins * sizeof(int) <= sizeof(s_key) && kBins == 8 * kChooseThreads, "eight bins per thread");
+    int *const s_hist = reinterpret_cast<int *>(s_key);  // [BINS], before the keys
+    static_assert(BINS * sizeof(int) <= sizeof(s_key), "the bins lie in the keys' place");
     constexpr int CPL = D / 32;                          // channels per lane
     constexpr unsigned ALL = 0xffffffffu;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
     float absq = 0.f, absb = 0.f;
     if (choose) {
 #pragma unroll 1
-        for (int g = warp; g < p.G; g += kWarps) {
+        for (int g = warp; g < p.G; g += WARPS) {
             float f[CPL], a = 0.f;
             channels(qrow + (size_t)g * D, f);
 #pragma unroll
@@ -375,17 +375,17 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
             for (int m = 16; m > 0; m >>= 1) a += __shfl_xor_sync(ALL, a, m);
             absq = max_nan(a, absq);
         }
-        for (int x = tid; x < words; x += kChooseThreads) {  // bits e0.. e1 - 1 open, the others in
+        for (int x = tid; x < words; x += THREADS) {  // bits e0.. e1 - 1 open, the others in
             const int f = e0 - 32 * x, l = e1 - 32 * x, last = nb - 32 * x;
             auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ALL : (1u << n) - 1u; };
             s_bits[x] = below(f) | (below(last) & ~below(l));
         }
-        for (int x = tid; x < kBins; x += kChooseThreads) s_hist[x] = 0;
+        for (int x = tid; x < BINS; x += THREADS) s_hist[x] = 0;
         if (tid == 0) s_near = s_sure = 0;
     }
     pdl_wait_trigger();
     if (!choose) {
-        for (int x = tid; x < p.n_select; x += kChooseThreads) sel[x] = x < nb ? x : -1;
+        for (int x = tid; x < p.n_select; x += THREADS) sel[x] = x < nb ? x : -1;
         return;
     }
 
@@ -397,13 +397,13 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
     if (tid < groups) absb = row_abs[tid];  // in flight together with the scores
     float lo = INFINITY, hi = -INFINITY;
 #pragma unroll 1
-    for (int x0 = tid; x0 < nb; x0 += 8 * kChooseThreads) {
+    for (int x0 = tid; x0 < nb; x0 += 8 * THREADS) {
         float r[8];  // all on their way before the first is stored
 #pragma unroll
-        for (int y = 0; y < 8; ++y) r[y] = x0 + y * kChooseThreads < nb ? row_score[x0 + y * kChooseThreads] : 0.f;
+        for (int y = 0; y < 8; ++y) r[y] = x0 + y * THREADS < nb ? row_score[x0 + y * THREADS] : 0.f;
 #pragma unroll
         for (int y = 0; y < 8; ++y) {
-            const int x = x0 + y * kChooseThreads;
+            const int x = x0 + y * THREADS;
             const float v = fmaxf(r[y], -3e38f);
             if (staged && x < nb) s_score[x] = v;
             if (x >= e0 && x < e1) {
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
             }
         }
     }
-    for (int c = tid + kChooseThreads; c < groups; c += kChooseThreads) absb = max_nan(row_abs[c], absb);
+    for (int c = tid + THREADS; c < groups; c += THREADS) absb = max_nan(row_abs[c], absb);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
         absb = max_nan(__shfl_xor_sync(ALL, absb, m), absb);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
     }
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
         absq = max_nan(s_f[0][w], absq);
         absb = max_nan(s_f[1][w], absb);
         lo = fminf(lo, s_f[2][w]);
@@ -449,14 +449,14 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
         int need = k;  // rank wanted among the scores in [lo, hi]
         while (hi - lo > err) {
             // (infinite for a range of zero to fp32: then NaN and infinity all go to the last bin)
-            const float inv = (kBins - 1) / (hi - lo);
-            for (int x = e0 + tid; x < e1; x += kChooseThreads) {
+            const float inv = (BINS - 1) / (hi - lo);
+            for (int x = e0 + tid; x < e1; x += THREADS) {
                 const float v = score(x);
-                if (v >= lo && v <= hi) atomicAdd(&s_hist[(int)fminf((v - lo) * inv, kBins - 1)], 1);
+                if (v >= lo && v <= hi) atomicAdd(&s_hist[(int)fminf((v - lo) * inv, BINS - 1)], 1);
             }
             __syncthreads();
-            // counts from the highest bin down: thread tid has bins kBins - 8 - 8 tid .. kBins - 1 - 8 tid
-            int4 *const mine = reinterpret_cast<int4 *>(s_hist) + kBins / 4 - 2 - 2 * tid;
+            // counts from the highest bin down: thread tid has bins BINS - 8 - 8 tid .. BINS - 1 - 8 tid
+            int4 *const mine = reinterpret_cast<int4 *>(s_hist) + BINS / 4 - 2 - 2 * tid;
             const int4 c = mine[1], d = mine[0];
             const int sum = (c.x + c.y + c.z + c.w) + (d.x + d.y + d.z + d.w);
             int before = sum;
@@ -468,11 +468,11 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
             if (lane == 31) s_red[warp] = before;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) before += w < warp ? s_red[w] : 0;
+            for (int w = 0; w < WARPS; ++w) before += w < warp ? s_red[w] : 0;
             before -= sum;
             if (before < need && need <= before + sum) {  // one thread's
                 const int each[8] = {c.w, c.z, c.y, c.x, d.w, d.z, d.y, d.x};
-                int at = kBins - 1 - 8 * tid, n = each[0];
+                int at = BINS - 1 - 8 * tid, n = each[0];
 #pragma unroll
                 for (int y = 1; y < 8; ++y)
                     if (need > before + n) {
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
             }
             mine[0] = mine[1] = make_int4(0, 0, 0, 0);
             __syncthreads();
-            // The bin's ends, wider by more than the rounding of a bin number, 2048 2^-22.  (That of lo itself, 2^-23 of
+            // The bin's ends, wider by more than the rounding of a bin number, at most 2048 2^-22.  (That of lo itself, 2^-23 of
             // a score, is far below the error.)
             const float l = fmaxf(lo, lo + (s_bin - 0.01f) / inv), h = fminf(hi, lo + (s_bin + 1.01f) / inv);
             if (!(l > lo || h < hi)) break;
@@ -493,8 +493,8 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
             hi = h;
             if (s_count <= kFewInBin) break;
             int above = 0;  // (the widened end may take in scores of the bin above)
-            for (int x = e0 + tid; x < e1; x += kChooseThreads) above += score(x) > hi;
-            need = k - block_sum(above, s_red);
+            for (int x = e0 + tid; x < e1; x += THREADS) above += score(x) > hi;
+            need = k - block_sum<WARPS>(above, s_red);
         }
         low = lo - 2.f * err;
         high = hi + 2.f * err;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
     auto in_band = [&](float v) -> bool { return !usable || (v >= low && v <= high); };
     if (k > 0) {
         int sure = 0;
-        for (int x = e0 + tid; x < e1; x += kChooseThreads) {
+        for (int x = e0 + tid; x < e1; x += THREADS) {
             const float v = score(x);
             if (in_band(v)) {
                 const int at = atomicAdd(&s_near, 1);  // any order: they are ranked by score and index below
@@ -575,12 +575,12 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
         };
         if (near <= kListed) {  // ranked one against another
 #pragma unroll 1
-            for (int c = warp; c < near; c += kWarps) {
+            for (int c = warp; c < near; c += WARPS) {
                 const unsigned long long o = exact(s_blk[c]);
                 if (lane == 0) s_key[c] = o;
             }
             __syncthreads();
-            for (int c = tid; c < near; c += kChooseThreads) {
+            for (int c = tid; c < near; c += THREADS) {
                 const unsigned long long o = s_key[c];
                 const int x = s_blk[c];
                 int rank = 0;
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
         } else {  // many equals (keys never written, say): by block in the workspace, 0 for those outside the band
             unsigned long long *key = p.exact + (size_t)row * p.stride;
 #pragma unroll 1
-            for (int x = e0 + warp; x < e1; x += kWarps) {
+            for (int x = e0 + warp; x < e1; x += WARPS) {
                 const unsigned long long o = in_band(score(x)) ? exact(x) : 0;
                 if (lane == 0) key[x] = o;
             }
@@ -600,32 +600,32 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
             while (klo < khi) {
                 const unsigned long long mid = khi - (khi - klo) / 2;
                 int n = 0;
-                for (int x = e0 + tid; x < e1; x += kChooseThreads) n += key[x] >= mid;
-                if (block_sum(n, s_red) >= want) klo = mid;
+                for (int x = e0 + tid; x < e1; x += THREADS) n += key[x] >= mid;
+                if (block_sum<WARPS>(n, s_red) >= want) klo = mid;
                 else khi = mid - 1;
             }
             int above = 0;
-            for (int x = e0 + tid; x < e1; x += kChooseThreads) {
+            for (int x = e0 + tid; x < e1; x += THREADS) {
                 if (key[x] > klo) {
                     ++above;
                     atomicOr(&s_bits[x >> 5], 1u << (x & 31));
                 }
             }
             // and the lowest indexes among its equals: those below the largest cut that takes `equal` of them
-            const int equal = want - block_sum(above, s_red);
+            const int equal = want - block_sum<WARPS>(above, s_red);
             int clo = e0, chi = e1;
             while (clo < chi) {
                 const int mid = chi - (chi - clo) / 2;
                 int n = 0;
-                for (int x = e0 + tid; x < mid; x += kChooseThreads) n += key[x] == klo;
-                if (block_sum(n, s_red) <= equal) clo = mid;
+                for (int x = e0 + tid; x < mid; x += THREADS) n += key[x] == klo;
+                if (block_sum<WARPS>(n, s_red) <= equal) clo = mid;
                 else chi = mid - 1;
             }
-            for (int x = e0 + tid; x < clo; x += kChooseThreads)
+            for (int x = e0 + tid; x < clo; x += THREADS)
                 if (key[x] == klo) atomicOr(&s_bits[x >> 5], 1u << (x & 31));
         }
     } else if (want > 0) {  // the whole band
-        for (int x = e0 + tid; x < e1; x += kChooseThreads)
+        for (int x = e0 + tid; x < e1; x += THREADS)
             if (in_band(score(x))) atomicOr(&s_bits[x >> 5], 1u << (x & 31));
     }
     __syncthreads();
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
     // the chosen indexes in ascending order
     int base = 0;
 #pragma unroll 1
-    for (int w0 = 0; w0 < words; w0 += kChooseThreads) {
+    for (int w0 = 0; w0 < words; w0 += THREADS) {
         const uint32_t m = w0 + tid < words ? s_bits[w0 + tid] : 0u;
         int n = __popc(m);
         const int mine = n;
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kChooseThreads, 4) attn_choose_kernel(const Se
         __syncthreads();
         int at = base + n - mine;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             at += w < warp ? s_red[w] : 0;
             base += s_red[w];
         }
@@ -732,6 +732,7 @@ extern "C" int attn_select_blocks(const hla_kv_cache *C, int B, int T, int H, in
                                : p.d == 128 ? launch_score<128, 2>(p, st) : launch_score<64, 2>(p, st));
     if (e != HLA_OK) return e;
     const size_t smem = p.staged * sizeof(float) + (max_blocks + 31) / 32 * sizeof(uint32_t);
-    return launched(p.d == 128 ? launch_kernel(attn_choose_kernel<128>, dim3((unsigned)rows), dim3(kChooseThreads), smem, st, p)
-                               : launch_kernel(attn_choose_kernel<64>, dim3((unsigned)rows), dim3(kChooseThreads), smem, st, p));
+    auto choose = [&](auto kernel, int threads) { return launched(launch_kernel(kernel, dim3((unsigned)rows), dim3(threads), smem, st, p)); };
+    if (rows <= 4u * sm_count()) return p.d == 128 ? choose(attn_choose_kernel<128, 256>, 256) : choose(attn_choose_kernel<64, 256>, 256);
+    return p.d == 128 ? choose(attn_choose_kernel<128, 128>, 128) : choose(attn_choose_kernel<64, 128>, 128);
 }

@@ -291,6 +291,17 @@ def test_select_long_rows(kind):
     select_check(bounded(p, 3, kind), 64, 1, 2)
 
 
+@pytest.mark.parametrize("kind", ["random", "equal", "few", "near", "huge"])
+@pytest.mark.parametrize("d,H,Hkv", [(128, 4, 2), (64, 10, 2)])
+def test_select_more_rows_than_run_at_once(kind, d, H, Hkv):
+    """800 rows, on sequences that share their pages, some with more equals than are listed in shared memory."""
+    p = Problem(require_gpu(), [17000], 8, H, Hkv, d, 16, seed=5, poison=False)
+    p.B, p.past = 50, [17000 - 340 * b for b in range(50)]
+    p.table = p.table.repeat(50, 1)
+    p.q = torch.randn((50, 8, H, d), generator=inputs.generator(6)).to(BF16)
+    select_check(bounded(p, 5, kind), 24, 1, 2)
+
+
 # ----------------------------------------------------------------------------- together
 
 
