@@ -22,7 +22,7 @@
 // of a unit; with 32 or 64 rows, two or four warps take 16 rows each and run all keys that they copied together.
 //
 // Measured (CUDA graph, d = 128, 32 query heads on 8 kv heads): 64 sequences of 500 to 15500 tokens, bf16, 310 us and
-// 30000 to 65000 tokens, e4m3, 913 us, both 6.8 TB/s, at or above the copy rate; one sequence of 1021 tokens 7.6 us
+// 30000 to 65000 tokens, e4m3, 913 us, both 6.8 TB/s, at or above the copy rate; one sequence of 1021 tokens 7.4 us
 // (this kernel about 4, the join the rest), all of it dependent loads.  CTAs per SM and keys per step were swept: 32
 // keys and 3 CTAs of d = 64, 2 of d = 128 (accumulators, query and scores take 255 registers a thread there).
 
@@ -120,10 +120,10 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
     pdl_wait_trigger();
     tile_prefix(p, s_pre, s_past);
     const int total = s_pre[p.B] * p.units_per_b;
-    const int share = cta_share(p, total, gridDim.x);
-    const int begin = (long)share * blockIdx.x < total ? share * (int)blockIdx.x : total;
+    const int share = cta_share(total, gridDim.x);
+    const int begin = share * (int)blockIdx.x;
+    if ((long)share * blockIdx.x >= total) return;
     const int N = share < total - begin ? share : total - begin;  // this CTA's tiles
-    if (N == 0) return;
     const uint32_t ring = smem_u32(smem);
     const int rows = p.sel ? p.G : p.T * p.G;
 
@@ -543,31 +543,55 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
 }
 
 // Adds the pieces of the units that several CTAs share, in tile order, and writes zeros for the rows of
-// sequences without tiles.  One block per (unit, row of the unit).  Launched as a programmatic dependent of
-// attn_kernel: what it needs first are the lengths, which that kernel does not write, so the blocks find out
-// before their wait whether they have anything to do; block 0 always waits, so that the kernel does not
-// complete before attn_kernel.
+// sequences without tiles.  Launched as a programmatic dependent of attn_kernel: what it needs first are the
+// lengths, which that kernel does not write, so the blocks find out before their wait whether they have anything
+// to do; block 0 always waits, so that the kernel does not complete before attn_kernel.
+// A block takes one row of a unit, the blockIdx.x-th of all (by_end = 0), or with more units than CTAs in
+// attn_kernel's grid, of the unit that CTA blockIdx.x begins and does not finish, if there is one: 1024 sequences
+// of 200 to 600 tokens 262 us in all, 319 by unit.
 template <int D>
-__global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p, int M, int grid) {
+__global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p, int M, int grid, int by_end) {
     extern __shared__ int s_pre[];  // [B + 1]
     __shared__ float s_w[D];
     __shared__ float s_red[2][D / 32];
     const int tid = threadIdx.x;
     tile_prefix(p, s_pre);
-    const int b = blockIdx.x / p.units_per_b;
-    int u = blockIdx.x % p.units_per_b;
-    const int r = blockIdx.y, nt = s_pre[b + 1] - s_pre[b];
-    const int share = cta_share(p, s_pre[p.B] * p.units_per_b, grid);
+    const int r = blockIdx.y, total_tiles = s_pre[p.B] * p.units_per_b, share = cta_share(total_tiles, grid);
+    int b = 0, u = 0;
+    bool mine = true, empty = false;  // a unit to write; sequences without tiles (by_end)
+    if (!by_end) {
+        b = blockIdx.x / p.units_per_b;
+        u = blockIdx.x - b * p.units_per_b;
+    } else {
+        const long end = ((long)blockIdx.x + 1) * share;
+        mine = end < total_tiles;
+        if (mine) {
+            b = find_sequence(s_pre, p.B, p.units_per_b, (int)end - 1);
+            u = ((int)end - 1 - s_pre[b] * p.units_per_b) / (s_pre[b + 1] - s_pre[b]);
+        }
+        for (int x = blockIdx.x; x < p.B; x += gridDim.x) empty |= s_pre[x + 1] == s_pre[x];
+    }
+    const int nt = s_pre[b + 1] - s_pre[b];
     const int first = s_pre[b] * p.units_per_b + u * nt;
     const int c_first = first / share, c_last = (first + nt - 1) / share;
     const int rt = u % p.row_tiles;
     u /= p.row_tiles;
     const int hk = u % p.Hkv, tq = u / p.Hkv;
     const int row = rt * M + r;
-    const bool idle = (nt > 0 && c_first == c_last) || row >= (p.sel ? p.G : p.T * p.G);  // written whole, or no row
-    if (idle && (blockIdx.x | blockIdx.y) != 0) return;
+    // written whole, no row, or another block's
+    if ((nt > 0 && c_first == c_last) || row >= (p.sel ? p.G : p.T * p.G) || (by_end && c_first != blockIdx.x)) mine = false;
+    if (!mine && !empty && (blockIdx.x | blockIdx.y) != 0) return;
     pdl_wait_trigger();
-    if (idle || p.force_timeout) return;
+    if (p.force_timeout) return;
+    if (empty)
+        for (int x = blockIdx.x; x < p.B; x += gridDim.x)
+            if (s_pre[x + 1] == s_pre[x])
+                for (int y = blockIdx.y; y < p.T * p.H; y += gridDim.y) {
+                    const size_t to = ((size_t)x * p.T * p.H + y) * D + tid;
+                    if (p.o_bf16) reinterpret_cast<uint16_t *>(p.o)[to] = 0;
+                    else reinterpret_cast<float *>(p.o)[to] = 0.f;
+                }
+    if (!mine) return;
     const int t = p.sel ? tq : row / p.G, g = p.sel ? row : row % p.G;
     const size_t to = ((size_t)(b * p.T + t) * p.H + hk * p.G + g) * D;
 
@@ -697,15 +721,16 @@ int run_attn(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const i
     const int M = tile_rows(rows, tc);
     p.row_tiles = (rows + M - 1) / M;
     p.units_per_b = (sparse ? T : 1) * p.Hkv * p.row_tiles;
-    p.min_share = 1;
     p.by_G = divisor(p.G); p.by_Hkv = divisor(p.Hkv); p.by_row_tiles = divisor(p.row_tiles);
     p.o_bf16 = o_dtype == HLA_BF16;
-    p.tile = tc ? kTcTile
+    const int tile = tc ? kTcTile
              : C->head_dim == 128 ? (fp8 ? 4 * warp_keys<128, true>() : 4 * warp_keys<128, false>())
                                 : (fp8 ? 4 * warp_keys<64, true>() : 4 * warp_keys<64, false>());
-    const long per_unit = ((long)(sparse ? n_select : max_blocks) * C->page_size + p.tile - 1) / p.tile;
+    const long per_unit = ((long)(sparse ? n_select : max_blocks) * C->page_size + tile - 1) / tile;
+    p.tshift = __builtin_ctz(tile);
     const long most = (long)B * p.units_per_b * per_unit;  // tiles, if every sequence filled its table
-    HLA_REQUIRE(most < (1L << 31) && (long)C->n_pages * C->kv_heads * (C->page_size / kGroup) < (1L << 31), HLA_ERR_UNSUPPORTED);
+    // (share * CTA, up to a grid above it, stays in 32 bits)
+    HLA_REQUIRE(most < 2000000000L && (long)C->n_pages * C->kv_heads * (C->page_size / kGroup) < (1L << 31), HLA_ERR_UNSUPPORTED);
     const int D = C->head_dim;
     p.part_o = static_cast<float *>(ws);
     p.part_ml = p.part_o + (size_t)2 * attn_grid_limit() * M * D;
@@ -724,10 +749,11 @@ int run_attn(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const i
                               : (fp8 ? launch_rows<64, true>(M, p, &grid, most, st) : launch_rows<64, false>(M, p, &grid, most, st));
     e = launched(ce);
     if (e != HLA_OK) return e;
-    const dim3 jg((unsigned)(B * p.units_per_b), (unsigned)(rows < M ? rows : M));
+    const bool by_end = B * p.units_per_b > grid;
+    const dim3 jg((unsigned)(by_end ? grid : B * p.units_per_b), (unsigned)(rows < M ? rows : M));
     const size_t js = (B + 1) * sizeof(int);
-    ce = D == 128 ? launch_kernel(attn_join_kernel<128>, jg, dim3(128), js, st, p, M, grid)
-                  : launch_kernel(attn_join_kernel<64>, jg, dim3(64), js, st, p, M, grid);
+    ce = D == 128 ? launch_kernel(attn_join_kernel<128>, jg, dim3(128), js, st, p, M, grid, (int)by_end)
+                  : launch_kernel(attn_join_kernel<64>, jg, dim3(64), js, st, p, M, grid, (int)by_end);
     return launched(ce);
 }
 

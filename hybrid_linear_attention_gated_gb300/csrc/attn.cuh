@@ -23,8 +23,7 @@ struct AttnParams {
     int max_blocks, n_pages, pshift, n_select;
     int row_tiles;    // row tiles of a unit's rows
     int units_per_b;  // units of one sequence
-    int min_share;    // least tiles per CTA
-    int tile;         // keys per tile
+    int tshift;       // log2 of keys per tile
     uint32_t by_G, by_Hkv, by_row_tiles;  // for divided()
     int o_bf16;
     int *status;       // attn_tc_kernel: the device status word
@@ -47,40 +46,43 @@ __device__ __forceinline__ int listed(const AttnParams &p, int pos) {
 // Tiles of one unit of a sequence with `past` cached tokens.
 __device__ __forceinline__ int unit_tiles(const AttnParams &p, int past) {
     if (past < 0) return 0;
-    if (p.sel) return (int)((((long)listed(p, past + p.T - 1) << p.pshift) + p.tile - 1) / p.tile);
-    const long cap = (long)p.max_blocks << p.pshift;
-    const long len = (long)past + p.T < cap ? (long)past + p.T : cap;
-    return (int)((len + p.tile - 1) / p.tile);
+    const int cap = p.max_blocks << p.pshift;  // (below 2^30, as the cached tokens and the listed ones)
+    const int len = p.sel ? listed(p, past + p.T - 1) << p.pshift : past + p.T < cap ? past + p.T : cap;
+    return (len + (1 << p.tshift) - 1) >> p.tshift;
+}
+
+// (out of line: a short call's time goes into fetching its instructions, and these would lie among them)
+static __device__ __noinline__ void many_prefix(const AttnParams &p, int *pre, int *past) {
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+        const int c = cached(p, b);
+        if (past) past[b] = c;
+        pre[b + 1] = unit_tiles(p, c);
+    }
+    block_prefix(pre, p.B);
 }
 
 // Prefix sums of the sequences' tiles per unit into pre[0..B], and their cached tokens into past[0..B-1] where
 // that is wanted; ends with a block barrier.
 __device__ __forceinline__ void tile_prefix(const AttnParams &p, int *pre, int *past = nullptr) {
     const int lane = threadIdx.x;
-    if (lane < 32) {
-        int base = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const int b = b0 + lane;
-            const int c = b < p.B ? cached(p, b) : -1;
-            int x = unit_tiles(p, c);
-            if (past && b < p.B) past[b] = c;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, m);
-                if (lane >= m) x += y;
-            }
-            if (b < p.B) pre[b + 1] = base + x;
-            base += __shfl_sync(0xffffffffu, x, 31);
+    if (p.B <= 32) {
+        if (lane < 32) {
+            const int c = lane < p.B ? cached(p, lane) : -1;
+            if (past && lane < p.B) past[lane] = c;
+            const int x = warp_prefix(unit_tiles(p, c), lane);
+            if (lane < p.B) pre[lane + 1] = x;
+            if (lane == 0) pre[0] = 0;
         }
-        if (lane == 0) pre[0] = 0;
+    } else {
+        many_prefix(p, pre, past);
     }
     __syncthreads();
 }
 
 // Tiles that each CTA of the attention grid takes.
-__device__ __forceinline__ int cta_share(const AttnParams &p, int total, int grid) {
-    const int s = (int)(((long)total + grid - 1) / grid);
-    return s < p.min_share ? p.min_share : s;
+__device__ __forceinline__ int cta_share(int total, int grid) {
+    const int s = (int)(((unsigned)total + grid - 1u) / (unsigned)grid);
+    return s < 1 ? 1 : s;
 }
 
 // The sequence whose units hold tile t: pre[b] * units <= t < pre[b + 1] * units.

@@ -84,20 +84,16 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t at) {
 // Prefix sums of the sequences' groups per kv head into pre[0..B]; ends with a block barrier.
 __device__ __forceinline__ void group_prefix(const SelectParams &p, int *pre) {
     const int lane = threadIdx.x;
-    if (lane < 32) {
-        int base = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const int b = b0 + lane;
-            int x = b < p.B ? (visible_blocks(p, b, p.T - 1) + kGroupBlocks - 1) / kGroupBlocks : 0;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, m);
-                if (lane >= m) x += y;
-            }
-            if (b < p.B) pre[b + 1] = base + x;
-            base += __shfl_sync(0xffffffffu, x, 31);
+    auto groups = [&](int b) { return (visible_blocks(p, b, p.T - 1) + kGroupBlocks - 1) / kGroupBlocks; };
+    if (p.B <= 32) {
+        if (lane < 32) {
+            const int x = warp_prefix(lane < p.B ? groups(lane) : 0, lane);
+            if (lane < p.B) pre[lane + 1] = x;
+            if (lane == 0) pre[0] = 0;
         }
-        if (lane == 0) pre[0] = 0;
+    } else {
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) pre[b + 1] = groups(b);
+        block_prefix(pre, p.B);
     }
     __syncthreads();
 }

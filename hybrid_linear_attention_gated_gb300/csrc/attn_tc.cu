@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
     }
     tile_prefix(p, s_pre, s_past);
     const int total = s_pre[p.B] * p.units_per_b;
-    const int share = cta_share(p, total, gridDim.x);
+    const int share = cta_share(total, gridDim.x);
     const int begin = (long)share * blockIdx.x < total ? share * (int)blockIdx.x : total;
     const int N = share < total - begin ? share : total - begin;  // this CTA's tiles
     if (N == 0) return;

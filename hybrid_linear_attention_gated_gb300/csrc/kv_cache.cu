@@ -8,8 +8,8 @@
 //
 // Every value is read and written once, so the step is bound by memory, and at decode sizes by latency.  One grid
 // does both halves: blocks that own a touched page for some kv heads, and blocks that own some tokens of q.
-// Measured (CUDA graph, 32 query and 8 kv heads of 128): one token 3.95 us; 64 x 4 tokens, e4m3, 7.2 us; 60 single
-// tokens and 4 chunks of 512 14.8 us; 8 prompts of 4093 tokens 129 us, 6.2 TB/s of reads and writes.
+// Measured (CUDA graph, 32 query and 8 kv heads of 128): one token 3.4 us; 64 x 4 tokens, e4m3, 6.7 us; 60 single
+// tokens and 4 chunks of 512 14.7 us; 8 prompts of 4093 tokens 129 us, 6.2 TB/s of reads and writes.
 #include "paged.cuh"
 
 namespace hla {
@@ -325,7 +325,18 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendPara
         const bool many = r1 - r0 > LANES;  // otherwise the angles of the one pass serve all heads
         load(r0 + rl);
         if (bounds)  // keys that were there
-            for (int r = rl; r < r0; r += LANES) bd.take(load8<FP8>(kp + r * (D * ES), c0), load8<FP8>(kp + r * (D * ES), c1));
+#pragma unroll 1
+            for (int r = rl; r < r0; r += 2 * LANES) {
+                uint4 oa[2], ob[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int x = r + y * LANES < r0 ? r + y * LANES : r;
+                    oa[y] = load8<FP8>(kp + x * (D * ES), c0);
+                    ob[y] = load8<FP8>(kp + x * (D * ES), c1);
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) bd.take(oa[y], ob[y]);
+            }
         if (h == h0 || many) {
             __syncthreads();  // (the last head's rows are done with the angles; s_turn is there)
             angles(0, r0);

@@ -57,6 +57,29 @@ inline int check_window(const hla_kv_cache *C, int B, int T, int H, int max_bloc
 __host__ __device__ constexpr uint32_t divisor(int d) { return (uint32_t)(((1ull << 31) + d - 1) / d); }
 __device__ __forceinline__ int divided(int x, uint32_t by) { return (int)__umulhi(2u * (uint32_t)x, by); }
 
+// Inclusive prefix sums over a warp's lanes.
+__device__ __forceinline__ int warp_prefix(int x, int lane) {
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, m);
+        if (lane >= m) x += y;
+    }
+    return x;
+}
+// Turns the counts pre[1..n] that the block's threads have just written into prefix sums pre[0..n].  A lane of the first
+// warp sums an odd number of neighbours (different banks across the lanes).  The caller's block barrier ends it.
+__device__ __forceinline__ void block_prefix(int *pre, int n) {
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int each = ((n + 31) / 32) | 1, first = threadIdx.x * each, last = first + each < n ? first + each : n;
+        int sum = 0;
+        for (int b = first; b < last; ++b) sum += pre[b + 1];
+        sum = warp_prefix(sum, threadIdx.x) - sum;
+        for (int b = first; b < last; ++b) pre[b + 1] = sum += pre[b + 1];
+        if (threadIdx.x == 0) pre[0] = 0;
+    }
+}
+
 // Four e4m3 values as fp16 (exact): bytes 0, 1 in lo and 2, 3 in hi.
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t &lo, uint32_t &hi) {
     asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"

@@ -435,7 +435,7 @@ int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_t *cu_seqle
  *  sums; softmax statistics in fp32; the weights meet the values in 16 bits for a bf16 output and in two or
  *  three 16-bit parts, fp32's precision, for an fp32 one.  The work is split over sequences and positions by
  *  the lengths on the device, so one captured graph serves any lengths.
- *  B <= 1024, T <= 8, H <= 1024; scale finite, of either sign.  B full tables may hold less than 2^31 tiles of
+ *  B <= 1024, T <= 8, H <= 1024; scale finite, of either sign.  B full tables may hold less than 2e9 tiles of
  *  64 keys, over all kv heads and each 64 query rows of one (HLA_ERR_UNSUPPORTED otherwise).
  * -------------------------------------------------------------------------*/
 size_t attn_paged_decode_workspace_size(const hla_kv_cache *C, int B, int T, int H);

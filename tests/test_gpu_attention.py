@@ -383,3 +383,19 @@ def test_a_list_is_read_up_to_the_blocks_the_token_sees():
     a, b = p.decode(hla.HLA_F32, lists.to(dev)), p.decode(hla.HLA_F32, short.to(dev))
     assert torch.equal(a, b)
     check(p, a, hla.HLA_F32, short.numpy())
+
+
+@pytest.mark.parametrize("dtype", [hla.HLA_BF16, hla.HLA_E4M3])
+@pytest.mark.parametrize("o_dtype", [hla.HLA_BF16, hla.HLA_F32])
+@pytest.mark.parametrize("T,H,Hkv,d", [(1, 8, 8, 128), (2, 16, 8, 64), (8, 9, 1, 128), (3, 40, 4, 64)])
+def test_more_units_than_run_at_once(T, H, Hkv, d, o_dtype, dtype):
+    """Sequences of no, few and thousands of tokens in one call: units of many CTAs, many units of one, and none."""
+    dev = require_gpu()
+    g = np.random.default_rng(22)
+    past = [int(x) for x in g.integers(-1, 60, size=640 // Hkv)]
+    past[0], past[7], past[-1] = -1, 3000, 1500
+    past[20:30] = [-1] * 10
+    p = Problem(dev, past, T, H, Hkv, d, 32, dtype, seed=22).upload()
+    check(p, p.decode(o_dtype), o_dtype)
+    sel = g.integers(-1, 95, size=(len(past), T, Hkv, 12))
+    check(p, p.decode(o_dtype, torch.from_numpy(sel).to(I32).to(dev)), o_dtype, sel)
