@@ -33,7 +33,7 @@ struct SelectParams {
     const int32_t *table, *past;
     int32_t *sel;
     float *score;                 // [B, T, Hkv, stride]
-    unsigned long long *exact;    // [B, T, Hkv, stride]: fp64 scores of the blocks near the border, when too many to list
+    unsigned long long *exact;    // [B, T, Hkv, stride]: exact scores, as ordered integers, of the blocks near the border when too many to list
     float *absmax;                // [B, Hkv, groups]: largest magnitude among the bounds of each group of 16 blocks
     int B, T, H, Hkv, G, d;
     int max_blocks, n_pages, pshift;
@@ -54,14 +54,6 @@ __device__ __forceinline__ int visible_blocks(const SelectParams &p, int b, int 
 __device__ __forceinline__ uint32_t relu2(uint32_t x) {  // max(x, 0) of two bf16, NaN kept
     const __nv_bfloat162 z = __float2bfloat162_rn(0.f);
     const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&x), z);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of two bf16 each, NaN kept
-    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 __device__ __forceinline__ uint32_t neg2(uint32_t x) {  // min(x, 0) of two bf16, NaN kept

@@ -158,15 +158,6 @@ __device__ __forceinline__ uint4 load8(const uint8_t *row, int c) {
     }
 }
 
-__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // of two bf16, NaN kept
-    const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
 // (lo, hi) of 16 channels, taking up the item's two chunks.
 struct Bounds {
     uint32_t lo[8], hi[8];

@@ -57,6 +57,15 @@ inline int check_window(const hla_kv_cache *C, int B, int T, int H, int max_bloc
 __host__ __device__ constexpr uint32_t divisor(int d) { return (uint32_t)(((1ull << 31) + d - 1) / d); }
 __device__ __forceinline__ int divided(int x, uint32_t by) { return (int)__umulhi(2u * (uint32_t)x, by); }
 
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // of two bf16, NaN kept
+    const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
 // Inclusive prefix sums over a warp's lanes.
 __device__ __forceinline__ int warp_prefix(int x, int lane) {
 #pragma unroll
