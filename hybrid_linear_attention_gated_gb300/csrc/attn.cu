@@ -22,7 +22,7 @@
 // of a unit; with 32 or 64 rows, two or four warps take 16 rows each and run all keys that they copied together.
 //
 // Measured (CUDA graph, d = 128, 32 query heads on 8 kv heads): 64 sequences of 500 to 15500 tokens, bf16, 310 us and
-// 30000 to 65000 tokens, e4m3, 913 us, both 6.8 TB/s, at or above the copy rate; one sequence of 1021 tokens 7.4 us
+// 30000 to 65000 tokens, e4m3, 913 us, both 6.8 TB/s, at or above the copy rate; one sequence of 1021 tokens 6.0 us
 // (this kernel about 4, the join the rest), all of it dependent loads.  CTAs per SM and keys per step were swept: 32
 // keys and 3 CTAs of d = 64, 2 of d = 128 (accumulators, query and scores take 255 registers a thread there).
 
@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p, int M,
     const int t = p.sel ? tq : row / p.G, g = p.sel ? row : row % p.G;
     const size_t to = ((size_t)(b * p.T + t) * p.H + hk * p.G + g) * D;
 
-    // a quarter of the block to a piece, 4 channels to a thread, and 4 pieces ahead: one after another, a load each, the
-    // pieces of 128 rows of 16000 tokens take 3 to 5 us longer
+    // A quarter of the block to a piece, 4 channels to a thread, 4 pieces a thread on their way at once and the first ones
+    // before their weights are known: one sequence at 1k 6.0 us, with a channel to a thread and piece after piece 7.4.
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f, top = -INFINITY;
     const int ch = 4 * (tid % (D / 4));
@@ -606,7 +606,14 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p, int M,
     // slot of piece x of the unit
     auto slot = [&](int x) -> size_t { return 2 * (size_t)(c_first + x) + (x == 0); };
     for (int x0 = 0; x0 < n; x0 += D) {  // the sums so far rescaled to the new maximum, as within a CTA
-        const int x = x0 + tid;
+        const int x = x0 + tid, lim = n - x0 < D ? n - x0 : D, y1 = tid / (D / 4);
+        float4 f[kAhead];  // the next pieces of this thread's, on their way before the last are used
+        auto load = [&](int y0) {
+#pragma unroll
+            for (int y = 0; y < kAhead; ++y)
+                if (y0 + 4 * y < lim) f[y] = *reinterpret_cast<const float4 *>(p.part_o + (slot(x0 + y0 + 4 * y) * M + r) * D + ch);
+        };
+        load(y1);
         float2 ml = make_float2(-INFINITY, 0.f);
         if (x < n) ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot(x) * M + r) * 2);
         float mx = ml.x;
@@ -630,13 +637,9 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p, int M,
         total *= old;
 #pragma unroll
         for (int y = 0; y < D / 32; ++y) total += s_red[1][y];
-        const int lim = n - x0 < D ? n - x0 : D;
 #pragma unroll 1
-        for (int y0 = tid / (D / 4); y0 < lim; y0 += 4 * kAhead) {
-            float4 f[kAhead];  // all on their way before the first is used
-#pragma unroll
-            for (int y = 0; y < kAhead; ++y)
-                f[y] = *reinterpret_cast<const float4 *>(p.part_o + (slot(x0 + (y0 + 4 * y < lim ? y0 + 4 * y : y0)) * M + r) * D + ch);
+        for (int y0 = y1; y0 < lim; y0 += 4 * kAhead) {
+            if (y0 != y1) load(y0);
 #pragma unroll
             for (int y = 0; y < kAhead; ++y) {
                 const float w = y0 + 4 * y < lim ? s_w[y0 + 4 * y] : 0.f;
