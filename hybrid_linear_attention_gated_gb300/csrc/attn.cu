@@ -666,8 +666,9 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p, int M,
 int tile_rows(int rows, bool tc) { return tc ? kTcRows : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 // More than 64 rows of bf16 keys and a bf16 output go to tcgen05.  Measured over 32 sequences of 180k to 240k tokens and
-// one kv head, tcgen05 / mma.sync: 128 rows, d 128 727 / 1453 us, d 64 516 / 811; at 64 rows (two kv heads, half the
-// length) 723 / 745 and 511 / 421: a tile of 128 rows costs the same half empty.
+// one kv head, tcgen05 / mma.sync: 128 rows, d 128 640 / 1406 us, d 64 434 / 763.  A tile of 128 rows costs the same half
+// empty: 64 rows (four kv heads of 45k to 60k tokens) take 649 / 727 and 438 / 398, and 4 sequences of 3k to 4k tokens
+// 27 / 24 and 19 / 14.
 bool use_tc(int rows, int dtype, int o_dtype) { return rows > 64 && dtype == HLA_BF16 && o_dtype == HLA_BF16; }
 
 int attn_grid_limit() { return 3 * sm_count(); }  // the most of any configuration

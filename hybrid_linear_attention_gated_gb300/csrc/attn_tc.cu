@@ -11,12 +11,14 @@
 //
 // Keys and values come through two stages of cp.async in the 128-byte swizzle.  A tile is a chain of short steps
 // (product, row of S, weights, product: about 3700 cycles for d = 128), so what counts is CTAs per SM that fill one
-// another's gaps: two of d = 128 and three of d = 64 with 64-key tiles and two stages (727 and 516 us for 128 rows over
-// 32 x 180k tokens, 4.1 and 2.9 TB/s) against one with 128-key tiles or four stages (1021 to 1200 us, 526 to 640).
-// What is left of the time is that chain.
+// another's gaps: two of d = 128 and three of d = 64 with 64-key tiles and two stages (when compared, 727 and 516 us for
+// 128 rows over 32 sequences of 180k to 240k tokens) against one with 128-key tiles or four stages (1021 to 1200 us, 526
+// to 640).  Now 640 and 434 us, 4.6 and 3.4 TB/s; what is left of the time is that chain.
 //
 // The keys that all rows see (up to past) go through the tiles; the window's own T - 1 last keys, which a row sees in
 // part, are taken up on CUDA cores at the end of the unit, row by row, so that no weight of zero meets their values.
+// They are fetched into shared memory together: read by each row from global memory, one after another, they made 8-token
+// windows of 4 sequences of 6k to 8k tokens 44 us for 33.
 //
 // Every wait is bounded (as in tc_gemm.cu): a wait that gives up sets the device status word, and after the next
 // block barrier every thread leaves the loop; the MMAs issued are waited for once more before tensor memory is freed.
@@ -320,26 +322,40 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
         if (!all_ok) break;
         ok &= wait_phase(&bar_o, (done - 1) & 1, p.status);
         __syncwarp();
-        tc_fence_after();
 
-        // ---- this thread's row of O, and the window's own keys
+        // ---- the window's own keys: their rows go to P's place, which is free since its last product is complete
+        const bool window = k1 == u.nt && lim_hi > lim_lo;
+        int *const s_page = reinterpret_cast<int *>(sP + (kMaxWindowTokens - 1) * 2 * RB);
+        if (window) {
+#pragma unroll 1
+            for (int x = tid; x < (lim_hi - lim_lo) * 2 * CPR; x += kAttnThreads) {
+                const int own = x / (2 * CPR), c = lim_lo + 1 + own, pg = page_of(u.b, c >> p.pshift);
+                if (x % (2 * CPR) == 0) s_page[own] = pg;
+                if (pg < 0) continue;
+                const size_t at = ((((size_t)pg * p.Hkv + u.hk) << p.pshift) + (c & ((1 << p.pshift) - 1))) * RB + x % CPR * 16;
+                *reinterpret_cast<uint4 *>(sP + x * 16) = ld_act_v4((x % (2 * CPR) < CPR ? p.k : p.v) + at);
+            }
+            __syncthreads();
+        }
+
+        // ---- this thread's row of O, and those keys
+        tc_fence_after();
         uint32_t o[D];
 #pragma unroll
         for (int c = 0; c < D; c += 32) tmem_ld32(tm_o + my_lanes + c, o + c);
         tmem_wait_ld();
         tc_fence_before();
         const int lim = live ? past + (p.sel ? u.tq : divided(r, p.by_G)) : -1;
-        if (k1 == u.nt)
-            for (int c = lim_lo + 1; c <= lim_hi; ++c) {
-                const int pg = page_of(u.b, c >> p.pshift);
-                if (pg < 0 || c > lim) continue;
-                const size_t at = ((((size_t)pg * p.Hkv + u.hk) << p.pshift) + (c & ((1 << p.pshift) - 1))) * D;
-                const uint16_t *kr = reinterpret_cast<const uint16_t *>(p.k) + at, *vr = reinterpret_cast<const uint16_t *>(p.v) + at;
+        if (window)
+            for (int c = lim_lo + 1; c <= lim_hi && c <= lim; ++c) {
+                const int own = c - lim_lo - 1;
+                if (s_page[own] < 0) continue;
+                const uint8_t *const kr = sP + own * 2 * RB, *const vr = kr + RB;
                 float s = 0.f;
 #pragma unroll 4
                 for (int x = 0; x < CPR; ++x) {
                     const uint4 a = *reinterpret_cast<const uint4 *>(sQ + (x >> 3) * kSub + tid * 128 + (((x & 7) ^ (tid & 7)) << 4)),
-                                b = ld_act_v4(kr + 8 * x);
+                                b = *reinterpret_cast<const uint4 *>(kr + 16 * x);
                     s += bf16_lo(a.x) * bf16_lo(b.x) + bf16_hi(a.x) * bf16_hi(b.x);
                     s += bf16_lo(a.y) * bf16_lo(b.y) + bf16_hi(a.y) * bf16_hi(b.y);
                     s += bf16_lo(a.z) * bf16_lo(b.z) + bf16_hi(a.z) * bf16_hi(b.z);
@@ -356,7 +372,7 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
                 l = l * a + w;
 #pragma unroll
                 for (int x = 0; x < CPR; ++x) {
-                    const uint4 b = ld_act_v4(vr + 8 * x);
+                    const uint4 b = *reinterpret_cast<const uint4 *>(vr + 16 * x);
                     const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
