@@ -387,13 +387,17 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                     }
                 }
                 // ---- weights.  They meet V as bf16 (fp16 for an 8-bit cache, times 2^14 so that fp16 holds weights
-                // down to 2^-39 of the largest).  A bf16 output rounds by 2^-8 itself; one rounding of each weight, 2^-8
-                // as well, averages out over the keys to less.  For an fp32 output the rounded-off part goes through
-                // further products, which leaves 2^-25 (fp16: 2^-23); with one less, 2^-17, the output was 1.4e-6 off,
-                // twice what fp32 arithmetic is.
-                auto weigh = [&](auto both) {
+                // down to 2^-39 of the largest), and what rounding took off goes through further products as long as the
+                // output can show it.  One bf16 part, 2^-8, is as coarse as a bf16 output: 1.95e-3 off the exact result
+                // over 64 x 8k tokens where the output's rounding alone is 1.67e-3.  With two, 2^-16, that rounding is all that
+                // is left: 16 rows, which the cache bounds, have two (64 x 8k tokens 311 -> 315 us, 32 x 210k of d 64 493 ->
+                // 497).  More rows, which the products bound, keep one (32 rows of d 128 501 -> 527, of d 64 496 -> 590, 64 of
+                // d 128 718 -> 960).  fp16's 2^-11 adds 1%.  An fp32 output takes three parts (fp16: two), 2^-24; with two
+                // bf16 ones it was 1.4e-6 off, twice what fp32 arithmetic is.
+                auto weigh = [&](auto f32) {
                     // further products with what rounding took off: fp16 keeps 11 bits of a weight a time, bf16 8
-                    constexpr int EX = !decltype(both)::value ? 0 : FP8 ? 1 : 2;
+                    constexpr bool F32 = decltype(f32)::value;
+                    constexpr int EX = F32 ? (FP8 ? 1 : 2) : !FP8 && WR == 1 ? 1 : 0;
                     uint32_t ph[SG][4], pl[EX > 0 ? EX : 1][SG][4];
 #pragma unroll
                     for (int hrow = 0; hrow < 2; ++hrow) {
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                                     const float a1 = a - bf16_lo(h), c1 = c - bf16_hi(h);
                                     const uint32_t l = pack_bf16x2(a1, c1);
                                     pl[0][t >> 1][w] = l;
-                                    pl[1][t >> 1][w] = pack_bf16x2(a1 - bf16_lo(l), c1 - bf16_hi(l));
+                                    if constexpr (EX > 1) pl[1][t >> 1][w] = pack_bf16x2(a1 - bf16_lo(l), c1 - bf16_hi(l));
                                 }
                             } else {
                                 const __half2 h = __floats2half2_rn(a, c);

@@ -432,9 +432,10 @@ int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_t *cu_seqle
  *  A row that sees no key (an idle slot, no pages) is 0.  A position that a row does not see has no effect on
  *  it, whatever it holds.
  *  q bf16 [B, T, H, d]; o [B, T, H, d] (o_dtype: HLA_F32 or HLA_BF16).  Products on tensor cores with fp32
- *  sums; softmax statistics in fp32; the weights meet the values in 16 bits for a bf16 output and in two or
- *  three 16-bit parts, fp32's precision, for an fp32 one.  The work is split over sequences and positions by
- *  the lengths on the device, so one captured graph serves any lengths.
+ *  sums; softmax statistics in fp32.  The weights meet the values in 16-bit parts: as many as fp32 holds for an fp32
+ *  output; for a bf16 one two bf16 parts (2^-16) up to 16 query rows per kv head and one (2^-8, as the output) above,
+ *  and one fp16 part (2^-11) with an 8-bit cache.  The work is split over sequences and positions by the lengths on
+ *  the device, so one captured graph serves any lengths.
  *  B <= 1024, T <= 8, H <= 1024; scale finite, of either sign.  B full tables may hold less than 2e9 tiles of
  *  64 keys, over all kv heads and each 64 query rows of one (HLA_ERR_UNSUPPORTED otherwise).
  * -------------------------------------------------------------------------*/

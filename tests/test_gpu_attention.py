@@ -399,3 +399,25 @@ def test_more_units_than_run_at_once(T, H, Hkv, d, o_dtype, dtype):
     check(p, p.decode(o_dtype), o_dtype)
     sel = g.integers(-1, 95, size=(len(past), T, Hkv, 12))
     check(p, p.decode(o_dtype, torch.from_numpy(sel).to(I32).to(dev)), o_dtype, sel)
+
+
+@pytest.mark.parametrize("dtype", [hla.HLA_BF16, hla.HLA_E4M3])
+@pytest.mark.parametrize("T,H,Hkv,d", [(1, 8, 8, 128), (1, 32, 8, 64), (4, 16, 4, 128), (2, 24, 3, 128), (5, 3, 1, 64)])
+def test_a_bf16_output_is_off_by_its_rounding_alone(T, H, Hkv, d, dtype):
+    """Up to 16 rows: the weights lose nothing that the output would show."""
+    p = Problem(require_gpu(), [1500, 700, 2100, 33], T, H, Hkv, d, 64, dtype, seed=23).upload()
+    k, v = p.values()
+    lists = np.tile(np.arange(0, 34, 2), (4, T, Hkv, 1))
+    for sel in (None, lists):
+        ref, _ = oracle.attention.attend(p.q.double().numpy(), k, v, p.table.numpy(), p.past, p.scale, sel)
+        o = f64(p.decode(hla.HLA_BF16, None if sel is None else torch.from_numpy(sel).to(I32).to(p.dev)))
+        size, rounding = np.linalg.norm(ref), np.linalg.norm(torch.from_numpy(ref).to(BF16).double().numpy() - ref)
+        # An error e before the output's rounding shifts a value's distance from its rounded self by |e| at most, and adds |e|.
+        # Two bf16 parts hold a weight to 2^-16, and independent errors of weights over values of either sign add up to that
+        # much of the output (twice that with what fp32 sums and scores err); fp16 holds 2^-11 worst, which is one error
+        # among independent others: a square root of squares.
+        err = np.linalg.norm(o - ref)
+        if dtype == hla.HLA_BF16:
+            assert err <= rounding + 2 * 2.0 ** -15 * size, (err / size, rounding / size)
+        else:
+            assert err <= np.hypot(rounding, 2.0 ** -11 * size) + 2 * 2.0 ** -15 * size, (err / size, rounding / size)
