@@ -290,7 +290,9 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
                 }
                 tmem_wait_st();
             }
-            // ---- weights: rounded once to bf16, as in attn_kernel for a bf16 output
+            // ---- weights: rounded once to bf16, as in attn_kernel for more than 16 rows, and summed as they are then: a row
+            // that one key dominates keeps that key's value (weights of 2^8 at most are no powers of two, so the sum before
+            // rounding is up to 2^-8 off theirs)
             float2 ls[4] = {};
             const float2 sc2 = make_float2(sc, sc), mb2 = make_float2(-mb, -mb);
 #pragma unroll
@@ -300,8 +302,8 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
                 for (int x = 0; x < 4; ++x) {
                     float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[8 * c + 2 * x]), __uint_as_float(sr[8 * c + 2 * x + 1])), sc2, mb2);
                     y = make_float2(ex2(y.x), ex2(y.y));
-                    ls[x] = __fadd2_rn(ls[x], y);
                     w[x] = pack_bf16x2(y.x, y.y);
+                    ls[x] = __fadd2_rn(ls[x], make_float2(bf16_lo(w[x]), bf16_hi(w[x])));
                 }
                 *reinterpret_cast<uint4 *>(sP + tid * 128 + ((c ^ (tid & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }

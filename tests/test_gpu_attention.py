@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle
-from hybrid_linear_attention_gated_gb300 import hla
+from hybrid_linear_attention_gated_gb300 import hla, inputs
 from tests.attn_common import BF16, I32, Problem, attention_tolerance, bits
 from tests.gpu_common import f64, require_gpu
 
@@ -421,3 +421,25 @@ def test_a_bf16_output_is_off_by_its_rounding_alone(T, H, Hkv, d, dtype):
             assert err <= rounding + 2 * 2.0 ** -15 * size, (err / size, rounding / size)
         else:
             assert err <= np.hypot(rounding, 2.0 ** -11 * size) + 2 * 2.0 ** -15 * size, (err / size, rounding / size)
+
+
+@pytest.mark.parametrize("dtype", [hla.HLA_BF16, hla.HLA_E4M3])
+@pytest.mark.parametrize("T,H,Hkv,d", [(1, 8, 2, 128), (4, 16, 2, 64), (8, 8, 1, 128), (8, 9, 1, 128), (8, 16, 1, 64)])
+def test_equal_values_come_back_as_they_are(T, H, Hkv, d, dtype):
+    """Numerator and denominator hold the same rounded weights: over keys whose values are all alike an output is that value,
+    whatever the scores (a few keys dominate here, and their weights are no powers of two).  Where they differ, the largest
+    mantissa shows it first: a step of its own is 2^-8 of it."""
+    p = Problem(require_gpu(), [3000], T, H, Hkv, d, 64, dtype, seed=24, poison=False)
+    # sequences on the same pages: several tiles for every CTA, over which a row's maximum rises
+    p.B, p.past = 64, [3000 - 40 * b for b in range(64)]
+    p.table = p.table.repeat(64, 1)
+    p.q = torch.randn((64, T, H, d), generator=inputs.generator(25)).to(BF16)
+    value = 255 / 128 if dtype == hla.HLA_BF16 else 1.875
+    p.v = torch.full_like(p.v.float(), value).to(p.v.dtype)
+    if dtype == hla.HLA_E4M3:
+        p.v_scale[:] = 1
+    p.upload()
+    for scale in (4 * d ** -0.5, 16 * d ** -0.5, 40 * d ** -0.5):
+        p.scale = scale
+        o = p.decode(hla.HLA_BF16)
+        assert torch.all(o == value), (scale, torch.unique(o.float(), return_counts=True))
