@@ -33,14 +33,29 @@ constexpr uint32_t kSub = kTcRows * 128;     // bytes of 128 rows of one 128-byt
 constexpr uint32_t kKvSub = kTcTile * 128;   // of the 64 rows of a tile's K or V
 constexpr int kStages = 2;                   // tiles in shared memory: one on its way while one is worked on
 
+// Sequences whose prefix sums of tiles and lengths a CTA keeps: all that there can be, or with more only every 2nd, 4th,
+// 8th or 16th prefix sum, from which the lengths themselves lead on.
 template <int D>
-__host__ __device__ constexpr uint32_t tc_smem() {  // Q, K and V stages, P
-    return (D / 64) * kSub + 2 * kStages * (D / 64) * kKvSub + kSub;
+__host__ __device__ constexpr int kept() {
+    return D == 64 ? kMaxBatch : 112;
+}
+template <int D>
+__host__ __device__ constexpr uint32_t tc_smem(int B) {  // Q, K and V stages, P; barriers and the tensor memory's address; s_on; s_pre, s_past
+    return (D / 64) * kSub + 2 * kStages * (D / 64) * kKvSub + kSub + 32 + kStages * 16 + (2 * (B < kept<D>() ? B : kept<D>()) + 1) * 4;
 }
 template <int D>
 __host__ __device__ constexpr int tc_ctas() {  // per SM
     return D == 64 ? 3 : 2;
 }
+// A CTA's shared memory is rounded up to 128 bytes and costs 1 KB more.  With 8 bytes per sequence in it, two CTAs of
+// d = 128 fitted up to 119 sequences only: 128 rows over 6.7 million tokens 681 us for 119 of them, 1067 for 120 and 1267
+// for 1024 (now 683 and 877).
+template <int D>
+constexpr bool fits() {
+    return tc_ctas<D>() * ((tc_smem<D>(kMaxBatch) + 127) / 128 * 128 + 1024) <= 228 * 1024;
+}
+static_assert(fits<64>() && fits<128>(), "tc_ctas CTAs on an SM, whatever the batch");
+static_assert((kMaxBatch + 1) * sizeof(int) <= kSub, "the prefix sums of all sequences pass through P's place");
 template <int D>
 __host__ __device__ constexpr uint32_t tmem_columns() {  // 64 of S, D of O
     return D == 64 ? 128 : 256;
@@ -69,13 +84,13 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
     constexpr int RB = 2 * D, CPR = RB / 16, GB = kGroup * RB, NB = D / 64, M = kTcRows;
     constexpr uint32_t IS = idesc_bf16(M, kTcTile), IO = idesc_bf16(M, D, true);
     constexpr unsigned ALL = 0xffffffffu;
-    extern __shared__ __align__(1024) uint8_t smem[];  // no static shared memory in front of it: two CTAs of d = 64 just fit
+    extern __shared__ __align__(1024) uint8_t smem[];  // (and no static shared memory in front of it)
     uint8_t *const sQ = smem, *const sK = sQ + NB * kSub, *const sV = sK + kStages * NB * kKvSub,
             *const sP = sV + kStages * NB * kKvSub;
     uint64_t &bar_s = reinterpret_cast<uint64_t *>(sP + kSub)[0], &bar_o = (&bar_s)[1], &bar_end = (&bar_s)[2];
     uint32_t &s_tmem = *reinterpret_cast<uint32_t *>(&bar_s + 3);
     int (*const s_on)[4] = reinterpret_cast<int (*)[4]>(&bar_s + 4);  // [kStages]: rows with a key of each staged group
-    int *const s_pre = &s_on[kStages][0], *const s_past = s_pre + p.B + 1;  // [B + 1], [B]
+    int *const s_pre = &s_on[kStages][0], *const s_past = s_pre + p.B + 1;  // [B + 1], [B]; with more than kept: [kept + 1], none
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     pdl_wait();
@@ -88,8 +103,19 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
         }
         return;
     }
-    tile_prefix(p, s_pre, s_past);
-    const int total = s_pre[p.B] * p.units_per_b;
+    // s_pre[x]: tiles per unit of the sequences before sequence x << skip.  s_past: all lengths, if they fit
+    int skip = 0;
+    if constexpr (kept<D>() < kMaxBatch)
+        while (p.B > kept<D>() << skip) ++skip;
+    const int nx = (p.B + (1 << skip) - 1) >> skip;
+    int *const pre = skip ? reinterpret_cast<int *>(sP) : s_pre;  // (P's place is not in use yet)
+    tile_prefix(p, pre, skip ? nullptr : s_past);
+    if (skip) {
+        for (int x = tid; x <= nx; x += kAttnThreads) s_pre[x] = pre[x << skip < p.B ? x << skip : p.B];
+        __syncthreads();
+    }
+    auto past_of = [&](int b) -> int { return skip ? cached(p, b) : s_past[b]; };
+    const int total = s_pre[nx] * p.units_per_b;
     const int share = cta_share(total, gridDim.x);
     const int begin = (long)share * blockIdx.x < total ? share * (int)blockIdx.x : total;
     const int N = share < total - begin ? share : total - begin;  // this CTA's tiles
@@ -121,9 +147,16 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
     };
     auto unit_of = [&](int t) {
         Unit u;
-        u.b = find_sequence(s_pre, p.B, p.units_per_b, t);
-        u.nt = s_pre[u.b + 1] - s_pre[u.b];
-        const int rem = t - s_pre[u.b] * p.units_per_b;
+        const int x0 = find_sequence(s_pre, nx, p.units_per_b, t);
+        int at = s_pre[x0];  // tiles per unit before sequence u.b
+        u.b = x0 << skip;
+        u.nt = skip ? unit_tiles(p, past_of(u.b)) : s_pre[x0 + 1] - at;
+        if (skip)
+            while (u.b + 1 < p.B && (at + u.nt) * p.units_per_b <= t) {
+                at += u.nt;
+                u.nt = unit_tiles(p, past_of(++u.b));
+            }
+        const int rem = t - at * p.units_per_b;
         const int x = rem / u.nt;
         u.k = rem - x * u.nt;
         const int y = divided(x, p.by_row_tiles);
@@ -150,7 +183,7 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
         if (g0 + lane >= N) return;
         const Unit u = unit_of(begin + g0 + lane);
         const int key = u.k * kTcTile + warp * kGroup;
-        const int limit = s_past[u.b] + (p.sel ? u.tq : 0);  // last position that all rows see
+        const int limit = past_of(u.b) + (p.sel ? u.tq : 0);  // last position that all rows see
         int blk = key >> p.pshift;
         if (p.sel) blk = blk < listed(p, limit) ? p.sel[((size_t)(u.b * p.T + u.tq) * p.Hkv + u.hk) * p.n_select + blk] : -1;
         const int page = page_of(u.b, blk);
@@ -208,7 +241,7 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
         const Unit u = unit_of(begin + done);
         const int k0 = u.k, k1 = u.nt - k0 < N - done ? u.nt : k0 + (N - done), first = done;
         done += k1 - k0;
-        const int past = s_past[u.b], lim_lo = p.sel ? past + u.tq : past, lim_hi = p.sel ? lim_lo : past + p.T - 1;
+        const int past = past_of(u.b), lim_lo = p.sel ? past + u.tq : past, lim_hi = p.sel ? lim_lo : past + p.T - 1;
         const int r = u.rt * M + tid;  // this thread's row of the unit
         const bool live = r < rows;
 
@@ -421,21 +454,19 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
 
 template <int D>
 cudaError_t launch(const AttnParams &p, int *grid, long most, cudaStream_t st) {
-    const size_t fixed = tc_smem<D>() + 32 + kStages * 16, smem = fixed + (2 * p.B + 1) * sizeof(int);
     // the shared-memory limit is a per-device attribute: raise it once on every device used
     static bool done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !done[dev]) {
-        e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(fixed + (2 * kMaxBatch + 1) * sizeof(int)));
+        e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc_smem<D>(kMaxBatch));
         if (e != cudaSuccess) return e;
         if (dev < 64) done[dev] = true;
     }
     const int slots = tc_ctas<D>() * sm_count();
     *grid = most < slots ? (int)most : slots;
-    return launch_kernel(attn_tc_kernel<D>, dim3(*grid), dim3(kAttnThreads), smem, st, p);
+    return launch_kernel(attn_tc_kernel<D>, dim3(*grid), dim3(kAttnThreads), tc_smem<D>(p.B), st, p);
 }
 
 }  // namespace

@@ -443,3 +443,30 @@ def test_equal_values_come_back_as_they_are(T, H, Hkv, d, dtype):
         p.scale = scale
         o = p.decode(hla.HLA_BF16)
         assert torch.all(o == value), (scale, torch.unique(o.float(), return_counts=True))
+
+
+def test_tcgen05_keeps_its_pace_with_the_batch():
+    """The time per cached token does not jump where a batch grows: 119 and 120 sequences, and 800, on the same pages.  (Two
+    CTAs to an SM or one is a factor of 1.6; units that end and begin cost the larger batch some of its time.)"""
+    dev = require_gpu()
+
+    def us_per_token(B, n, d):
+        p = Problem(dev, [n], 8, 16, 1, d, 64, seed=26, poison=False)
+        p.B, p.past, p.table = B, [n] * B, p.table.repeat(B, 1)
+        p.q = p.q.repeat(B, 1, 1, 1)
+        p.upload()
+        o = torch.empty(B, 8, 16, d, dtype=BF16, device=dev)
+        ws = torch.empty(hla.attn_paged_decode_workspace_size(p.C, B, 8, 16), dtype=torch.uint8, device=dev)
+        times = []
+        for _ in range(12):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            p.decode(hla.HLA_BF16, ws=ws, o=o)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b) * 1e3)
+        return sorted(times[3:])[4] / (B * n)
+
+    for d in (128, 64):
+        small, large, many = us_per_token(119, 24000, d), us_per_token(120, 24000, d), us_per_token(800, 24000, d)
+        assert large < 1.2 * small and many < 1.2 * small, (d, small, large, many)
