@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) attn_choose_kernel(co
                     }
                 }
             }
-            return has ? best : 1;
+            return has ? best : usable ? 1 : ordered(-INFINITY);  // (below every finite score; among others -infinity is a score)
         };
         if (near <= kListed) {  // ranked one against another
 #pragma unroll 1

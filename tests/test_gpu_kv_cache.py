@@ -268,6 +268,21 @@ def test_select_with_infinities_and_nan():
         select_check(p, 6, 0, 1)
 
 
+@pytest.mark.parametrize("blocks", [20, 1500])
+def test_blocks_without_a_page_tie_with_scores_of_minus_infinity(blocks):
+    """An infinite query channel against negative bounds: every score is -infinity, so the lowest blocks are chosen, those
+    without a page among them (few blocks, and more than are listed in shared memory)."""
+    p = Problem(require_gpu(), [16 * blocks - 1], 1, 4, 2, 64, 16, seed=12, poison=False)
+    p.q[..., 0] = float("inf")
+    p.k_min, p.k_max = (torch.randn((p.n_pages, 2, 64), generator=inputs.generator(n)).to(BF16) for n in (1, 2))
+    p.k_min, p.k_max = torch.minimum(p.k_min, p.k_max), torch.maximum(p.k_min, p.k_max)
+    p.k_min[..., 0], p.k_max[..., 0] = -2.0, -1.0
+    p.table[0, 1], p.table[0, 2], p.table[0, 9] = -1, p.n_pages, -7
+    p.upload()
+    for n, first, last in ((5, 0, 0), (2, 0, 1), (11, 1, 2)):
+        select_check(p, n, first, last)
+
+
 def test_select_extremes():
     dev = require_gpu()
     p = bounded(Problem(dev, [999], 1, 4, 2, 64, 16, seed=2, poison=False), 2)
