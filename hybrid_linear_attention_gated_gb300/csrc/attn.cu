@@ -298,9 +298,10 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
             }
         }
 
-        // m: running maximum of the products; mb: times the scale, 0 while there is none.  The last accumulator tile
-        // is the sum of the weights as they meet V (a product with ones).
-        float m[2] = {-INFINITY, -INFINITY}, mb[2] = {0.f, 0.f}, acc[NT + 1][4];
+        // m: running maximum of the products; base: the same, 0 while there is none.  Weights are powers of the difference
+        // s - base times the scale, not of a difference of scaled products, whose rounding passes 2^127 from scores of 2^31
+        // on.  The last accumulator tile is the sum of the weights as they meet V (a product with ones).
+        float m[2] = {-INFINITY, -INFINITY}, base[2] = {0.f, 0.f}, acc[NT + 1][4];
 #pragma unroll
         for (int t = 0; t <= NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
 
@@ -375,10 +376,9 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                 if (__any_sync(ALL, top[0] > m[0] || top[1] > m[1])) {
 #pragma unroll
                     for (int hrow = 0; hrow < 2; ++hrow) {
-                        const float now = top[hrow] == -INFINITY ? 0.f : top[hrow] * sc[hrow];
-                        const float a = m[hrow] == -INFINITY ? 0.f : (m[hrow] == top[hrow] ? 1.f : ex2(mb[hrow] - now));
+                        const float a = m[hrow] == -INFINITY ? 0.f : (m[hrow] == top[hrow] ? 1.f : ex2((m[hrow] - top[hrow]) * sc[hrow]));
                         m[hrow] = top[hrow];
-                        mb[hrow] = now;
+                        base[hrow] = top[hrow] == -INFINITY ? 0.f : top[hrow];
 #pragma unroll
                         for (int t = 0; t <= NT; ++t) {
                             acc[t][2 * hrow] *= a;
@@ -401,10 +401,10 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                     uint32_t ph[SG][4], pl[EX > 0 ? EX : 1][SG][4];
 #pragma unroll
                     for (int hrow = 0; hrow < 2; ++hrow) {
-                        const float base = (FP8 ? 14.f : 0.f) - mb[hrow];
 #pragma unroll
                         for (int t = 0; t < 2 * SG; ++t) {
-                            const float a = ex2(fmaf(s[t][2 * hrow], sc[hrow], base)), c = ex2(fmaf(s[t][2 * hrow + 1], sc[hrow], base));
+                            const float x = s[t][2 * hrow] - base[hrow], y = s[t][2 * hrow + 1] - base[hrow];
+                            const float a = FP8 ? ex2(fmaf(x, sc[hrow], 14.f)) : ex2(x * sc[hrow]), c = FP8 ? ex2(fmaf(y, sc[hrow], 14.f)) : ex2(y * sc[hrow]);
                             const int w = 2 * (t & 1) + hrow;
                             if constexpr (!FP8) {
                                 const uint32_t h = pack_bf16x2(a, c);
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
             if (j == 0) {
                 // fmaxf passes over NaN scores: such a row may have no maximum, but it has seen keys and is NaN
                 const float l = acc[NT][2 * hrow];
-                s_m[warp][r] = l != l ? INFINITY : (m[hrow] == -INFINITY ? -INFINITY : mb[hrow]);
+                s_m[warp][r] = l != l ? INFINITY : (m[hrow] == -INFINITY ? -INFINITY : fmaxf(m[hrow] * sc[hrow], -3e38f));
                 s_l[warp][r] = l;
             }
 #pragma unroll

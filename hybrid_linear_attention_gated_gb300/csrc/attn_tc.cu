@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
                 *reinterpret_cast<uint4 *>(sQ + (c >> 3) * kSub + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) = w;
             }
         }
-        float mb = 0.f, l = 0.f;  // m times the scale
+        float m = 0.f, l = 0.f;   // of the products; weights are powers of (s - m) sc, as in attn_kernel
         bool none = true;         // no score yet
         for (int it = first; it < done; ++it) {
             const int st = it % kStages;
@@ -302,15 +302,14 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
                 for (int x = 0; x < kGroup; ++x) m4[x & 3] = fmaxf(m4[x & 3], __uint_as_float(sr[16 * g + x]));
             }
             const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-            const float t = mx * sc;
             if (none && mx != -INFINITY) {
-                mb = t;
+                m = mx;
                 none = false;
             }
-            const bool far = !none && t > mb + 8.f;
+            const bool far = !none && (mx - m) * sc > 8.f;
             if (__any_sync(ALL, far)) {  // (never in the unit's first tile, where O is not there yet)
-                const float a = far ? ex2(mb - t) : 1.f;
-                if (far) mb = t;
+                const float a = far ? ex2((m - mx) * sc) : 1.f;
+                if (far) m = mx;
                 l *= a;
                 uint32_t o[32];
 #pragma unroll
@@ -327,13 +326,13 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
             // that one key dominates keeps that key's value (weights of 2^8 at most are no powers of two, so the sum before
             // rounding is up to 2^-8 off theirs)
             float2 ls[4] = {};
-            const float2 sc2 = make_float2(sc, sc), mb2 = make_float2(-mb, -mb);
+            const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
 #pragma unroll
             for (int c = 0; c < kTcTile / 8; ++c) {
                 uint32_t w[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[8 * c + 2 * x]), __uint_as_float(sr[8 * c + 2 * x + 1])), sc2, mb2);
+                    float2 y = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(sr[8 * c + 2 * x]), __uint_as_float(sr[8 * c + 2 * x + 1])), m2), sc2);
                     y = make_float2(ex2(y.x), ex2(y.y));
                     w[x] = pack_bf16x2(y.x, y.y);
                     ls[x] = __fadd2_rn(ls[x], make_float2(bf16_lo(w[x]), bf16_hi(w[x])));
@@ -396,14 +395,13 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
                     s += bf16_lo(a.z) * bf16_lo(b.z) + bf16_hi(a.z) * bf16_hi(b.z);
                     s += bf16_lo(a.w) * bf16_lo(b.w) + bf16_hi(a.w) * bf16_hi(b.w);
                 }
-                const float t = s * sc;
                 float a = 1.f;
-                if (t != -INFINITY && (none || t > mb)) {
-                    a = none ? 1.f : ex2(mb - t);
-                    mb = t;
+                if (s != -INFINITY && (none || s > m)) {
+                    a = none ? 1.f : ex2((m - s) * sc);
+                    m = s;
                     none = false;
                 }
-                const float w = ex2(t - mb);
+                const float w = ex2((s - m) * sc);
                 l = l * a + w;
 #pragma unroll
                 for (int x = 0; x < CPR; ++x) {
@@ -419,7 +417,7 @@ __global__ void __launch_bounds__(kAttnThreads, tc_ctas<D>()) attn_tc_kernel(con
             }
         // ---- out: the unit whole, or a piece for the join (slots as in attn_kernel).  A row of NaN scores only has no
         // maximum, but it has seen keys and is NaN.
-        const float top = l != l ? INFINITY : none ? -INFINITY : mb;
+        const float top = l != l ? INFINITY : none ? -INFINITY : fmaxf(m * sc, -3e38f);
         if (live && k0 == 0 && k1 == u.nt) {
             const float inv = top == -INFINITY ? 0.f : 1.f / l;
             uint16_t *dst = static_cast<uint16_t *>(p.o) + row_at(u, r);

@@ -470,3 +470,33 @@ def test_tcgen05_keeps_its_pace_with_the_batch():
     for d in (128, 64):
         small, large, many = us_per_token(119, 24000, d), us_per_token(120, 24000, d), us_per_token(800, 24000, d)
         assert large < 1.2 * small and many < 1.2 * small, (d, small, large, many)
+
+
+@pytest.mark.parametrize("dtype", [hla.HLA_BF16, hla.HLA_E4M3])
+@pytest.mark.parametrize("T,H,Hkv,d", [(1, 8, 2, 128), (4, 16, 2, 64), (8, 8, 1, 128), (8, 9, 1, 128), (8, 16, 1, 64)])
+def test_scores_beyond_the_precision_of_their_differences(T, H, Hkv, d, dtype):
+    """Scores of 2^31 and far beyond, exact in fp32: one product each.  The highest key of a row takes all, so the row is that
+    key's value; the fp32 spacing of such scores is no weight."""
+    dev = require_gpu()
+    for past, top in (([300, 40, 0], 2.0 ** 31), ([2500, 100, 7], 2.0 ** 36), ([900, 333, 64], 2.0 ** 120)):
+        p = Problem(dev, past, T, H, Hkv, d, 16, dtype, seed=27, poison=False)
+        # keys of 1 to 1.9375 (bf16 and e4m3 both hold 1, 1.125, ...) over 2^(x) in one channel, the others zero
+        g = inputs.generator(28)
+        p.k = torch.zeros(p.k.shape)
+        p.k[..., 3] = -(1 + torch.randint(0, 8, p.k.shape[:-1], generator=g) / 8)
+        for b in range(3):  # one key per kv head above all others, seen by every token of the window
+            for h in range(Hkv):
+                c = (past[b] * (h + 1) * 5) // 7 % (past[b] + 1)
+                p.k[p.table[b, c // 16], h, c % 16, 3] = 2.0
+        p.k = p.k.to(p.v.dtype)
+        p.q = torch.zeros(p.q.shape, dtype=BF16)
+        p.q[..., 3] = top
+        p.scale = 1.0
+        if dtype == hla.HLA_E4M3:
+            p.k_scale[:] = 1
+        p.upload()
+        k, v = p.values()
+        ref, _ = oracle.attention.attend(p.q.double().numpy(), k, v, p.table.numpy(), p.past, 1.0)
+        for o_dtype, half in ((hla.HLA_F32, 2.0 ** -23), (hla.HLA_BF16, 2.0 ** -8)):
+            # a weight of 1 and zeros: the value, times its scale in fp32
+            assert np.all(np.abs(f64(p.decode(o_dtype)) - ref) <= half * np.abs(ref)), (top, o_dtype)
