@@ -3,13 +3,14 @@
 //
 // Rotation: channel pair (x, y) of frequency f at position p becomes (x cos a - y sin a, x sin a + y cos a) with
 // a = p f.  Far positions lose their angle in fp32, so a is kept as a fraction of a turn in 64 bits:
-// F = round(2^64 frac(f / 2 pi)), and p F modulo 2^64 is exact; its top 32 bits go to sincospif.  (fp64 would do
-// too, but a page's keys take one angle per pair and token, and the fp64 rate of this part is far below that.)
+// F = 2^64 frac(f / 2 pi), from f's own bits in integers, and p F modulo 2^64 is exact; its top 32 bits, less the nearest
+// quarter, give the sine and cosine.  (fp64 would do too, but a page's keys take one angle per pair and token, and the fp64
+// rate of this part is far below that.)
 //
 // Every value is read and written once, so the step is bound by memory, and at decode sizes by latency.  One grid
 // does both halves: blocks that own a touched page for some kv heads, and blocks that own some tokens of q.
-// Measured (CUDA graph, 32 query and 8 kv heads of 128): one token 3.4 us; 64 x 4 tokens, e4m3, 6.7 us; 60 single
-// tokens and 4 chunks of 512 14.7 us; 8 prompts of 4093 tokens 129 us, 6.2 TB/s of reads and writes.
+// Measured (CUDA graph, 32 query and 8 kv heads of 128): one token 3.5 us; 64 x 4 tokens, e4m3, 6.1 us; 60 single
+// tokens and 4 chunks of 512 14.3 us; 8 prompts of 4093 tokens 129 us, 6.2 TB/s of reads and writes.
 #include "paged.cuh"
 
 namespace hla {
@@ -32,17 +33,37 @@ struct AppendParams {
     uint32_t by_half, by_H, by_head_groups;  // for divided()
 };
 
-// Fraction of a turn per position, in units of 2^-64 turn.
+// Fraction of a turn per position, in units of 2^-64 turn, cut off: the fp64 value m 2^e times 2^128 / 2 pi in integers.
 __device__ __forceinline__ uint64_t turn_fraction(double inv_freq) {
-    double t = inv_freq * 0.15915494309189533577;  // 1 / 2 pi
-    t -= floor(t);
-    return (uint64_t)__double2ull_rn(t * 9223372036854775808.0) << 1;  // 2^63 t fits; t = 1 wraps to 0
+    const uint64_t bits = (uint64_t)__double_as_longlong(inv_freq), hi = 0x28be60db9391054aull, lo = 0x7f09d5f47d4d3770ull;
+    const int ex = (int)(bits >> 52 & 0x7ff);
+    const uint64_t m = (bits & 0xfffffffffffffull) | (ex ? 1ull << 52 : 0ull);
+    const uint64_t w0 = m * lo, x = __umul64hi(m, lo), y = m * hi, w1 = x + y, w2 = __umul64hi(m, hi) + (w1 < x);
+    const int s = 64 + 1075 - (ex ? ex : 1);  // the product, w2 w1 w0, in units of 2^-64 turn: shifted right by s
+    uint64_t u = 0;
+    if (s >= 128) u = s < 192 ? w2 >> (s - 128) : 0;
+    else if (s > 64) u = w2 << (128 - s) | w1 >> (s - 64);
+    else if (s > 0) u = s == 64 ? w1 : w1 << (64 - s) | w0 >> s;
+    return bits >> 63 ? 0 - u : u;
 }
+// The angle in units of 2^-32 turn, rounded, is taken to within an eighth of a turn of a quarter before it meets fp32, whose
+// 24 bits would otherwise leave 2^-26 of a turn.  There the Taylor series of sine and cosine end soon: what follows the last
+// terms here is below 2^-28 of the sums.
 __device__ __forceinline__ float2 cos_sin(uint64_t turns, int pos) {
-    const int32_t top = (int32_t)((turns * (uint64_t)(uint32_t)pos) >> 32);
-    float s, c;
-    sincospif((float)top * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns in [-1, 1]
-    return make_float2(c, s);
+    const uint32_t top = (uint32_t)((turns * (uint64_t)(uint32_t)pos + 0x80000000ull) >> 32);
+    const uint32_t quarter = (top + 0x20000000u) >> 30;
+    const float a = (float)(int32_t)(top - (quarter << 30)) * 1.4629180792671596e-09f, q = a * a;  // 2 pi / 2^32
+    float s = fmaf(q, 1.f / 362880.f, -1.f / 5040.f);
+    s = fmaf(s, q, 1.f / 120.f);
+    s = fmaf(s, q, -1.f / 6.f);
+    s = fmaf(s * q, a, a);
+    float c = fmaf(q, -1.f / 3628800.f, 1.f / 40320.f);
+    c = fmaf(c, q, -1.f / 720.f);
+    c = fmaf(c, q, 1.f / 24.f);
+    c = fmaf(c, q, -0.5f);
+    c = fmaf(c, q, 1.f);
+    const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
+    return make_float2((quarter + 1) & 2 ? -x : x, quarter & 2 ? -y : y);
 }
 
 // First token and number of new tokens of sequence b, clamped to the N rows there are; 0 for an idle slot.

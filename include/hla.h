@@ -410,8 +410,8 @@ typedef struct hla_kv_cache {
  *  Rotation of the first rope_dim channels of every head (0: none, inv_freq NULL): pair i of position p
  *  turns by p * inv_freq[i], (x, y) -> (x cos - y sin, x sin + y cos).  Pair i is channels (i, i + rope_dim/2),
  *  or (2i, 2i + 1) with rope_interleaved = 1.  rope_dim % 16 == 0.  Angles are exact to 2^-32 of a turn at
- *  any position.  q_out = the rotated q; k and v are rounded once, to bf16 or to e4m3 of value / scale
- *  (saturating at +-448, infinities too).
+ *  any position (|inv_freq| below 2^40), and their sines and cosines to 2^-21 of themselves beyond that.  q_out = the
+ *  rotated q; k and v are rounded once, to bf16 or to e4m3 of value / scale (saturating at +-448, infinities too).
  *  Bounds (when k_min and k_max are set): of every page that got a token, over its stored keys at positions
  *  below past_len[b] + new tokens, whatever the page held before; a NaN key makes its channel's bounds NaN.
  *  N: rows of q [N, H, d], k, v [N, kv_heads, d], q_out [N, H, d] (may be q itself), all bf16.  Rows at or

@@ -1,6 +1,8 @@
 """Appending to the paged cache (rotation, both cache types, key bounds), block choice, and the operators together,
 against the fp64 oracle."""
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -180,6 +182,46 @@ def test_far_positions_keep_their_angles():
         ref = oracle.attention.rotate(q[n].double().numpy(), 1, turns, False)
         # the frequency itself is an fp64 value: its rounding, 2^-53 relative, times 5e8 positions is 2^-22 radian at 6
         assert np.all(np.abs(f64(out[n]) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -18)
+
+
+def test_angles_near_quarter_turns():
+    """Where a sine or cosine is nearly zero its bf16 value shows the angle's absolute error, here at the positions below 2^31
+    that come nearest to a quarter turn (denominators of the continued fraction of quarters per position)."""
+    dev = require_gpu()
+    pi = Fraction(314159265358979323846264338327950288419716939937510, 10 ** 50)
+    f = [1.0, 0.75, 0.1, 10000.0 ** (-1 / 64), 10000.0 ** (-3 / 8), 6.0, -37.25, 1e-3]
+    past = []
+    for x in f:
+        a, q0, q1 = abs(Fraction(x)) * 2 / pi, 1, 0
+        while True:
+            whole = a.numerator // a.denominator
+            q0, q1 = q1, whole * q1 + q0
+            if q1 >= 2 ** 31 - 1:
+                break
+            past += [q1] * (q1 > 0)
+            a = 1 / (a - whole)
+    B, d = len(past), 64
+    q = torch.zeros(B, 1, d, dtype=BF16)
+    q[..., 0:16:2] = 1  # (1, 0) turns to (cos, sin)
+    cache = torch.zeros(1, 1, 16, d, dtype=BF16, device=dev)
+    C = hla.make_kv_cache(hla.HLA_BF16, 1, 16, 1, d, cache, cache.clone())
+    out = torch.empty_like(q, device=dev)
+    kv = torch.zeros(B, 1, d, dtype=BF16, device=dev)
+    hla.kv_cache_append(C, B, B, torch.arange(B + 1, dtype=I32, device=dev), torch.tensor(past, dtype=I32, device=dev), 1,
+                        torch.full((B, 1), -1, dtype=I32, device=dev), 1, q.to(dev), kv, kv, 16, 1,
+                        torch.tensor(f, dtype=torch.float64, device=dev), out)
+    got, near = f64(out)[:, 0, :16].reshape(B, 8, 2), 0
+    for b, pos in enumerate(past):
+        for i, x in enumerate(f):
+            quarters = Fraction(x) * pos * 2 / pi
+            whole = round(quarters)
+            rest = float(quarters - whole) * np.pi / 2  # from the nearest quarter turn
+            c, s = np.cos(rest), np.sin(rest)
+            ref = np.array([(c, s), (-s, c), (-c, -s), (s, -c)][whole % 4])
+            near += abs(s) < 1e-5
+            # bf16 2^-8, fp32 sine and cosine 2^-21, and 2^-32 of a turn is 1.5e-9 radian, below 2^-29
+            assert np.all(np.abs(got[b, i] - ref) <= (2.0 ** -8 + 2.0 ** -21) * np.abs(ref) + 2.0 ** -29), (pos, x, got[b, i], ref)
+    assert near > 40
 
 
 def test_append_drops_tokens_without_a_page_or_behind_the_table():
