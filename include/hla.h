@@ -521,10 +521,12 @@ unsigned long long hla_launch_count(void);
  * last read.  Synchronous (copies 4 bytes from the device); HLA_ERR_CUDA if that copy fails. */
 int hla_device_status(void);
 /* Test hook for the failure path, with no counterpart on the source pages.  While on != 0,
- * every tensor-core projection or attention launch makes one of its bounded device waits give up (block
+ * every launch that has bounded device waits (the tensor-core projections, and the attention of more
+ * than 64 query rows per kv head with a bf16 cache and output) makes one of them give up (block
  * 0 waits 1 ms on a barrier that nothing arrives at) and records HLA_ERR_DEVICE_TIMEOUT, and
  * every block returns before it allocates tensor memory or issues a copy or an MMA; the
- * launch writes no output.  This lets a test check the status path without a real stall.
+ * launch writes no output.  Other launches are not affected.  This lets a test check the status
+ * path without a real stall.
  * Takes effect for launches made after the call (a CUDA graph keeps what it captured);
  * process-wide, not thread-safe with concurrent launches.  Always returns HLA_OK. */
 int hla_test_force_wait_timeout(int on);

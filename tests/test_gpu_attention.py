@@ -500,3 +500,21 @@ def test_scores_beyond_the_precision_of_their_differences(T, H, Hkv, d, dtype):
         for o_dtype, half in ((hla.HLA_F32, 2.0 ** -23), (hla.HLA_BF16, 2.0 ** -8)):
             # a weight of 1 and zeros: the value, times its scale in fp32
             assert np.all(np.abs(f64(p.decode(o_dtype)) - ref) <= half * np.abs(ref)), (top, o_dtype)
+
+
+@pytest.mark.parametrize("T,H,dtype,o_dtype", [(8, 8, hla.HLA_BF16, hla.HLA_BF16), (8, 16, hla.HLA_E4M3, hla.HLA_BF16),
+                                               (8, 16, hla.HLA_BF16, hla.HLA_F32)])
+def test_forms_without_bounded_waits_ignore_the_forced_timeout(T, H, dtype, o_dtype):
+    """At most 64 rows, an 8-bit cache or an fp32 output: the hook changes nothing and the status word stays clear."""
+    dev = require_gpu()
+    p = Problem(dev, [300, 70], T, H, 1, 64, 32, dtype, seed=29).upload()
+    want = p.decode(o_dtype)
+    torch.cuda.synchronize()
+    try:
+        hla.hla_test_force_wait_timeout(1)
+        o = p.decode(o_dtype)
+        torch.cuda.synchronize()
+    finally:
+        hla.hla_test_force_wait_timeout(0)
+    assert hla.hla_device_status() == 0
+    assert torch.equal(bits(o), bits(want))
