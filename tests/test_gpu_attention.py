@@ -518,3 +518,17 @@ def test_forms_without_bounded_waits_ignore_the_forced_timeout(T, H, dtype, o_dt
         hla.hla_test_force_wait_timeout(0)
     assert hla.hla_device_status() == 0
     assert torch.equal(bits(o), bits(want))
+
+
+@pytest.mark.parametrize("B", [112, 113, 224, 225, 449, 897])
+def test_tcgen05_finds_its_sequences_in_any_batch(B):
+    """Around the batches from which a CTA keeps every 2nd, 4th, ... prefix sum: idle sequences alone, in runs and at the ends,
+    lengths of nothing to many tiles."""
+    g = np.random.default_rng(B)
+    past = [int(x) for x in g.integers(-1, 200, size=B)]
+    past[B // 3:B // 3 + 19], past[0], past[1], past[-2:] = [-1] * 19, -1, 1700, [900, -1]
+    for T, H, sparse in ((8, 9, False), (1, 66, True)):
+        p = Problem(require_gpu(), past, T, H, 1, 128, 64, seed=B).upload()
+        sel = g.integers(-1, 28, size=(B, T, 1, 5)) if sparse else None
+        check(p, p.decode(hla.HLA_BF16, None if sel is None else torch.from_numpy(sel).to(I32).to(p.dev)), hla.HLA_BF16, sel)
+        assert hla.hla_last_variant().endswith("m128>")
