@@ -464,11 +464,14 @@ int attn_select_blocks(const hla_kv_cache *C, int B, int T, int H, int max_block
 
 /* ---------------------------------------------------------------------------
  * attn_paged_decode over listed blocks: token t of sequence b, for the query heads of kv head h, sees the
- * positions of the blocks sel[b, t, h, 0 .. n_select-1], up to past_len[b] + t.  Of a list no more entries are
- * read than the token sees blocks, (past_len[b] + t) / page_size + 1: a list that attn_select_blocks wrote holds
- * -1 behind them.  Of those read, entries outside [0, max_blocks) are skipped, blocks behind the token hold
- * nothing for it, and a block listed twice counts twice.  n_select * page_size < 2^30.  Other arguments as
- * attn_paged_decode.  Listing every visible block once gives attn_paged_decode's sum, in another order.
+ * positions of the blocks sel[b, t, h, 0 .. n_select-1], up to past_len[b] + t.
+ *  Lists are written as attn_select_blocks writes them: distinct visible blocks in front, in any order, and -1
+ *  behind them.  Of a list the first n = (past_len[b] + t) / page_size + 1 entries count, as many as the token sees
+ *  blocks; the rest is not read.  Among these n an entry outside [0, max_blocks) is skipped, a block behind the
+ *  token holds nothing for it and a block listed twice counts twice, but each of them takes a place: a list that has
+ *  them in front of visible blocks may lose those behind its n-th entry.
+ *  n_select * page_size < 2^30.  Other arguments as attn_paged_decode.  Listing every visible block once gives
+ *  attn_paged_decode's sum, in another order.
  * -------------------------------------------------------------------------*/
 size_t attn_paged_sparse_workspace_size(const hla_kv_cache *C, int B, int T, int H);
 int attn_paged_sparse(const hla_kv_cache *C, int B, int T, int H, int max_blocks, const int32_t *block_table,
