@@ -429,8 +429,8 @@ int kv_cache_append(const hla_kv_cache *C, int N, int B, const int32_t *cu_seqle
  * cache, the T tokens' own keys appended before.
  *  Token t of sequence b sees positions 0 .. past_len[b] + t:
  *    o[b, t, h] = sum_c softmax_c(scale q[b, t, h] . k_c) v_c,   k_c, v_c of kv head h / (H / kv_heads).
- *  A row that sees no key (an idle slot, no pages) is 0.  A position that a row does not see has no effect on
- *  it, whatever it holds.
+ *  A row that sees no key (an idle slot, no pages) is 0, and so is one whose scores are all -infinity.  A position
+ *  that a row does not see has no effect on it, whatever it holds.
  *  q bf16 [B, T, H, d]; o [B, T, H, d] (o_dtype: HLA_F32 or HLA_BF16).  Products on tensor cores with fp32
  *  sums; softmax statistics in fp32.  The weights meet the values in 16-bit parts: as many as fp32 holds for an fp32
  *  output; for a bf16 one two bf16 parts (2^-16) up to 16 query rows per kv head and one (2^-8, as the output) above,

@@ -532,3 +532,20 @@ def test_tcgen05_finds_its_sequences_in_any_batch(B):
         sel = g.integers(-1, 28, size=(B, T, 1, 5)) if sparse else None
         check(p, p.decode(hla.HLA_BF16, None if sel is None else torch.from_numpy(sel).to(I32).to(p.dev)), hla.HLA_BF16, sel)
         assert hla.hla_last_variant().endswith("m128>")
+
+
+@pytest.mark.parametrize("dtype", [hla.HLA_BF16, hla.HLA_E4M3])
+@pytest.mark.parametrize("T,H,Hkv,d", [(1, 8, 2, 128), (4, 8, 1, 64), (8, 8, 1, 128), (8, 9, 1, 128), (8, 16, 1, 64)])
+def test_rows_of_scores_of_minus_infinity(T, H, Hkv, d, dtype):
+    """An infinite query channel against negative keys: rows all of whose scores are -infinity are zero, beside rows that are
+    not, whole units and joined ones."""
+    p = Problem(require_gpu(), [900, 20, 0], T, H, Hkv, d, 16, dtype, seed=33)
+    p.k[..., 0] = torch.where(torch.isnan(p.k[..., 0].float()), p.k[..., 0].float(), -2.0).to(p.k.dtype)
+    plain = p.upload().decode(hla.HLA_BF16)
+    p.q[:, :, ::2, 0] = float("inf")
+    p.upload()
+    for o_dtype in (hla.HLA_BF16, hla.HLA_F32):
+        o = p.decode(o_dtype)
+        assert torch.all(o[:, :, ::2] == 0)
+        if o_dtype == hla.HLA_BF16:
+            assert torch.equal(bits(o[:, :, 1::2]), bits(plain[:, :, 1::2]))
