@@ -380,7 +380,10 @@ int hla_decode_layer_routing(const hla_layer *L, int M, const void *ws, const in
  * Paged key-value cache of the softmax-attention layers that a hybrid model interleaves with its KDA
  * layers.  [KIMI-WEBINAR] names the pair: a fixed-size recurrent state next to an attention cache that
  * grows with the sequence; [VLLM-K3] Part 1 sec. 1 (split of a long cache and join of the parts).  The
- * pages give no layout or kernel for it.
+ * pages give no layout or kernel for it.  The form here is grouped-query attention, keys and values of one
+ * width, for hybrid models that have it; the latent cache of K3's own attention layers is another format.
+ * kv_cache_append takes prompt chunks too, but attention is for windows of up to 8 tokens a sequence only:
+ * there is none for the tokens of a chunk.
  *
  * The cache is a pool of pages of page_size tokens; a block table int32 [B, max_blocks] names the page
  * of each block of page_size consecutive positions of a sequence.  A table entry outside [0, n_pages)
