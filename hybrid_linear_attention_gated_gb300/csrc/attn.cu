@@ -21,9 +21,9 @@
 // With 16 query rows a warp also runs its own keys against all rows and meets the other warps only at the end
 // of a unit; with 32 or 64 rows, two or four warps take 16 rows each and run all keys that they copied together.
 //
-// Measured (CUDA graph, d = 128, 32 query heads on 8 kv heads): 64 sequences of 500 to 15500 tokens, bf16, 310 us and
-// 30000 to 65000 tokens, e4m3, 913 us, both 6.8 TB/s, at or above the copy rate; one sequence of 1021 tokens 6.0 us
-// (this kernel about 4, the join the rest), all of it dependent loads.  CTAs per SM and keys per step were swept: 32
+// Measured (CUDA graph, d = 128, 32 query heads on 8 kv heads): 64 sequences of 500 to 15500 tokens, bf16, 314 us (6.7
+// TB/s) and 30000 to 65000 tokens, e4m3, 908 us (6.8 TB/s), both the copy rate; one sequence of 1021 tokens 6.1 us
+// (this kernel about 4, the join the rest; 10 us called one at a time from Python), all of it dependent loads.  CTAs per SM and keys per step were swept: 32
 // keys and 3 CTAs of d = 64, 2 of d = 128 (accumulators, query and scores take 255 registers a thread there).
 
 #include <type_traits>
@@ -670,9 +670,10 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p, int M,
 int tile_rows(int rows, bool tc) { return tc ? kTcRows : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 // More than 64 rows of bf16 keys and a bf16 output go to tcgen05.  Measured over 32 sequences of 180k to 240k tokens and
-// one kv head, tcgen05 / mma.sync: 128 rows, d 128 640 / 1406 us, d 64 434 / 763.  A tile of 128 rows costs the same half
-// empty: 64 rows (four kv heads of 45k to 60k tokens) take 649 / 727 and 438 / 398, and 4 sequences of 3k to 4k tokens
-// 27 / 24 and 19 / 14.
+// one kv head, tcgen05 / mma.sync: 128 rows, d 128 647 / 1419 us, d 64 444 / 787.  A tile of 128 rows costs the same half
+// empty: 64 rows (two kv heads of 90k to 120k tokens) take 643 / 728 and 441 / 405, and 4 sequences of 3k to 4k tokens
+// 28 / 24 and 19 / 14.  (Short calls of 128 rows lose too, 26 / 22 and 22 / 16 over 4 x 6k to 8k tokens, but lengths are not
+// known at launch.)
 bool use_tc(int rows, int dtype, int o_dtype) { return rows > 64 && dtype == HLA_BF16 && o_dtype == HLA_BF16; }
 
 int attn_grid_limit() { return 3 * sm_count(); }  // the most of any configuration

@@ -6,14 +6,15 @@
 //     S = Q K^T        tcgen05.mma 128 x 64 x d, both operands K-major in shared memory, S in tensor memory;
 //     P = 2^(S - m)    a thread reads its row of S, keeps m and l, writes its row of P as bf16 to shared memory;
 //     O += P V         tcgen05.mma 128 x d x 64, V as it lies in the cache (its channels contiguous: MN-major).
-// O stays in tensor memory.  A row's m is raised, and O rescaled, only when a score passes it by 2^8: until then the
-// weights stay below 2^8, which bf16 and the fp32 sums hold as well as 1.
+// O stays in tensor memory.  A row's m is raised, and O rescaled, only when a score passes it by 2^8 (a known way to spare
+// rescaling: any m near the maximum will do, since it cancels): until then the weights stay below 2^8, which bf16 and the
+// fp32 sums hold as well as 1.
 //
 // Keys and values come through two stages of cp.async in the 128-byte swizzle.  A tile is a chain of short steps
 // (product, row of S, weights, product: about 3700 cycles for d = 128), so what counts is CTAs per SM that fill one
 // another's gaps: two of d = 128 and three of d = 64 with 64-key tiles and two stages (when compared, 727 and 516 us for
 // 128 rows over 32 sequences of 180k to 240k tokens) against one with 128-key tiles or four stages (1021 to 1200 us, 526
-// to 640).  Now 640 and 434 us, 4.6 and 3.4 TB/s; what is left of the time is that chain.
+// to 640).  Now 647 and 444 us, 5.3 and 3.9 TB/s; what is left of the time is that chain.
 //
 // The keys that all rows see (up to past) go through the tiles; the window's own T - 1 last keys, which a row sees in
 // part, are taken up on CUDA cores at the end of the unit, row by row, so that no weight of zero meets their values.
