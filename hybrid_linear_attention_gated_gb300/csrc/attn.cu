@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                 // output can show it.  One bf16 part, 2^-8, is as coarse as a bf16 output: 1.95e-3 off the exact result
                 // over 64 x 8k tokens where the output's rounding alone is 1.67e-3.  With two, 2^-16, that rounding is all that
                 // is left: 16 rows, which the cache bounds, have two (64 x 8k tokens 311 -> 315 us, 32 x 210k of d 64 493 ->
-                // 497).  More rows, which the products bound, keep one (32 rows of d 128 501 -> 527, of d 64 496 -> 590, 64 of
+                // 497).  More rows, which the products bound, keep one (with two: 32 rows of d 128 501 -> 527, of d 64 496 -> 590, 64 of
                 // d 128 718 -> 960).  fp16's 2^-11 adds 1%.  An fp32 output takes three parts (fp16: two), 2^-24; with two
                 // bf16 ones it was 1.4e-6 off, twice what fp32 arithmetic is.
                 auto weigh = [&](auto f32) {
@@ -401,10 +401,12 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                     uint32_t ph[SG][4], pl[EX > 0 ? EX : 1][SG][4];
 #pragma unroll
                     for (int hrow = 0; hrow < 2; ++hrow) {
+                        const float2 minus = make_float2(-base[hrow], -base[hrow]), scale2 = make_float2(sc[hrow], sc[hrow]);
 #pragma unroll
                         for (int t = 0; t < 2 * SG; ++t) {
-                            const float x = s[t][2 * hrow] - base[hrow], y = s[t][2 * hrow + 1] - base[hrow];
-                            const float a = FP8 ? ex2(fmaf(x, sc[hrow], 14.f)) : ex2(x * sc[hrow]), c = FP8 ? ex2(fmaf(y, sc[hrow], 14.f)) : ex2(y * sc[hrow]);
+                            float2 x = __fadd2_rn(make_float2(s[t][2 * hrow], s[t][2 * hrow + 1]), minus);
+                            x = FP8 ? __ffma2_rn(x, scale2, make_float2(14.f, 14.f)) : __fmul2_rn(x, scale2);
+                            const float a = ex2(x.x), c = ex2(x.y);
                             const int w = 2 * (t & 1) + hrow;
                             if constexpr (!FP8) {
                                 const uint32_t h = pack_bf16x2(a, c);
@@ -670,8 +672,8 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p, int M,
 int tile_rows(int rows, bool tc) { return tc ? kTcRows : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 // More than 64 rows of bf16 keys and a bf16 output go to tcgen05.  Measured over 32 sequences of 180k to 240k tokens and
-// one kv head, tcgen05 / mma.sync: 128 rows, d 128 647 / 1419 us, d 64 444 / 787.  A tile of 128 rows costs the same half
-// empty: 64 rows (two kv heads of 90k to 120k tokens) take 643 / 728 and 441 / 405, and 4 sequences of 3k to 4k tokens
+// one kv head, tcgen05 / mma.sync: 128 rows, d 128 647 / 1407 us, d 64 444 / 770.  A tile of 128 rows costs the same half
+// empty: 64 rows (two kv heads of 90k to 120k tokens) take 643 / 721 and 441 / 397, and 4 sequences of 3k to 4k tokens
 // 28 / 24 and 19 / 14.  (Short calls of 128 rows lose too, 26 / 22 and 22 / 16 over 4 x 6k to 8k tokens, but lengths are not
 // known at launch.)
 bool use_tc(int rows, int dtype, int o_dtype) { return rows > 64 && dtype == HLA_BF16 && o_dtype == HLA_BF16; }
