@@ -389,11 +389,11 @@ __global__ void __launch_bounds__(kAttnThreads, ctas_per_sm<D, FP8, WR>()) attn_
                 // ---- weights.  They meet V as bf16 (fp16 for an 8-bit cache, times 2^14 so that fp16 holds weights
                 // down to 2^-39 of the largest), and what rounding took off goes through further products as long as the
                 // output can show it.  One bf16 part, 2^-8, is as coarse as a bf16 output: 1.95e-3 off the exact result
-                // over 64 x 8k tokens where the output's rounding alone is 1.67e-3.  With two, 2^-16, that rounding is all that
-                // is left: 16 rows, which the cache bounds, have two (64 x 8k tokens 311 -> 315 us, 32 x 210k of d 64 493 ->
-                // 497).  More rows, which the products bound, keep one (with two: 32 rows of d 128 501 -> 527, of d 64 496 -> 590, 64 of
-                // d 128 718 -> 960).  fp16's 2^-11 adds 1%.  An fp32 output takes three parts (fp16: two), 2^-24; with two
-                // bf16 ones it was 1.4e-6 off, twice what fp32 arithmetic is.
+                // over 64 x 8k tokens where the output's rounding alone is 1.67e-3.  With two, 2^-16, that rounding is all
+                // that is left: 16 rows, which the cache bounds, have two (64 x 8k tokens 309 -> 314 us, 32 x 210k of d 64
+                // 493 -> 497).  More rows, which the products bound, keep one (with two 32 rows of d 128 501 -> 527, of d 64
+                // 496 -> 590, 64 of d 128 718 -> 960).  fp16's 2^-11 adds 1% to the error.  An fp32 output takes three parts
+                // (fp16: two), 2^-24; with two bf16 ones it was 1.4e-6 off, twice what fp32 arithmetic is.
                 auto weigh = [&](auto f32) {
                     // further products with what rounding took off: fp16 keeps 11 bits of a weight a time, bf16 8
                     constexpr bool F32 = decltype(f32)::value;
