@@ -256,8 +256,9 @@ def _exact_scales(x, rows):
         cols = slice(b * BLOCK, min(K, (b + 1) * BLOCK))
         top = x[:, cols].abs().amax(1)
         top = torch.nn.functional.pad(top, (0, small.shape[0] * rows - M)).view(-1, rows).amax(1)
-        power = torch.ceil(torch.log2((top / E4M3_MAX).clamp(min=2.0 ** -126)))
-        small[:, b] = torch.exp2(power)
+        power = torch.floor(torch.log2((top / E4M3_MAX).clamp(min=2.0 ** -126)))
+        low = torch.exp2(power)  # one step below the scale, or the scale itself where 448 of it reach the top
+        small[:, b] = torch.where(low * E4M3_MAX < top, 2.0 * low, low)
         full[:, cols] = small[:, b].repeat_interleave(rows)[:M, None]
     return full, small
 
