@@ -196,7 +196,8 @@ def _quantize(x, rows=1):
         x = torch.nn.functional.pad(x, (0, k * BLOCK - K, 0, m * rows - M))
     x = x.view(m, rows, k, BLOCK)
     part, power = torch.frexp(x.abs().amax((1, 3)))  # part in [0.5, 1): 448 is 0.875 * 2^9
-    scale = torch.ldexp(torch.ones_like(part), (power - 9 + (part > 0.875)).clamp(min=-126))
+    power = torch.where(part > 0, power - 9 + (part > 0.875), -126).clamp(min=-126)
+    scale = torch.ldexp(torch.ones_like(part), power)
     q = (x / scale[:, None, :, None]).view(m * rows, k * BLOCK)[:M, :K].contiguous()
     return q.to(torch.float8_e4m3fn), scale
 
