@@ -1,0 +1,190 @@
+// What the kernels over e4m3 values with block scales share: conversion, tiles, instructions, launches.
+//
+// A block is 128 consecutive values along K (of one row of activations, or of 128 rows of a weight matrix) with one
+// fp32 scale; the product of a block is exact in the tensor core's fp32 accumulator up to its own additions, and the
+// scales are applied to it outside, in fp32.
+#pragma once
+
+#include <cuda.h>
+
+#include "tcgen05.cuh"
+
+namespace hla {
+
+constexpr int kFp8Block = 128;                      // values per scale along K: one 128-byte swizzle atom
+constexpr uint64_t kFp8WaitNs = 2000000000ull;      // 2 s of %globaltimer per bounded wait
+
+// 2-D map over a row-major [rows, K] matrix of bytes, box = 128 columns x box_rows rows, 128-byte swizzle; what lies
+// outside the matrix reads as zeros.
+bool byte_tile_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t K, uint32_t box_rows);
+
+// ----------------------------------------------------------------------------- conversion
+
+// Bits of the smallest power of two 2^e, e >= -126, with 448 * 2^e >= top (448 = 1.75 * 2^8); NaN for NaN and infinities.
+__device__ __forceinline__ float fp8_scale_of(float top) {
+    const uint32_t b = __float_as_uint(top);
+    const int e = static_cast<int>(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u);
+    if (b >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+    return __uint_as_float(static_cast<uint32_t>(e < 1 ? 1 : e) << 23);
+}
+
+// 1 / 2^e for the normal powers of two that fp8_scale_of gives (2^-126 .. 2^120); NaN stays NaN.
+__device__ __forceinline__ float fp8_inverse(float scale) {
+    return scale == scale ? __uint_as_float(0x7F000000u - __float_as_uint(scale)) : scale;
+}
+
+// Two values as e4m3, to nearest even, the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) { return e4m3x2(a, b) | e4m3x2(c, d) << 16; }
+
+// Larger magnitude, NaN if either is (fmaxf drops it): magnitudes order like their bits, NaN above infinity.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+    const uint32_t x = __float_as_uint(a) & 0x7FFFFFFFu, y = __float_as_uint(b) & 0x7FFFFFFFu;
+    return __uint_as_float(x > y ? x : y);
+}
+
+// ----------------------------------------------------------------------------- tensor cores
+
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator, e4m3 A and B, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// D = A x B^T over one block of 128 along K (four instructions of 32).
+__device__ __forceinline__ void umma_block(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem, uint32_t idesc) {
+    const uint64_t da = sw128_desc(a_smem), db = sw128_desc(b_smem);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) umma_e4m3(d_tmem, da + 2 * kk, db + 2 * kk, idesc, kk > 0);
+}
+
+__device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ bool fp8_wait(uint64_t *bar, uint32_t parity, int *status, uint64_t limit = kFp8WaitNs) {
+    return mbar_wait_for(bar, parity, limit, status);
+}
+
+// COLS consecutive 32-bit tensor-memory columns of this thread's lane, without waiting for them.
+template <int COLS>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[COLS]) {
+    static_assert(COLS == 8 || COLS == 16 || COLS % 32 == 0, "columns per load");
+    if constexpr (COLS == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "r"(taddr));
+    } else if constexpr (COLS == 16) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+              "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+            : "r"(taddr));
+    } else {
+#pragma unroll
+        for (int c = 0; c < COLS; c += 32) tmem_ld32(taddr + c, v + c);
+    }
+}
+
+// Allocate / free `columns` (a power of two from 32) of tensor memory; one whole warp.
+__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t taddr, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(columns) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float peer_float(const float *p, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+// A barrier among `threads` threads of the block (whole warps).
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// The CTAs whose bounded waits are made to give up (hla_test_force_wait_timeout): CTA 0 waits for a barrier at which
+// nothing arrives, and every CTA returns before it allocates, copies or multiplies.
+__device__ __forceinline__ void forced_timeout(uint64_t *bar, int *status) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        mbar_init(bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fp8_wait(bar, 0, status, 1000000ull);
+        asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    }
+}
+
+// ----------------------------------------------------------------------------- launches
+
+// Raises a kernel's shared-memory limit once on every device used (`done` belongs to the kernel).
+template <typename K>
+inline cudaError_t allow_smem(K kernel, size_t bytes, bool (&done)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) done[dev] = true;
+    return e;
+}
+
+// As launch_kernel, in clusters of `cluster` blocks, or as a cooperative launch.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_kernel_as(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                                    int cluster, bool cooperative, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[3];
+    int n = 0;
+    if (pdl_for(st)) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    if (cooperative) {
+        attr[n].id = cudaLaunchAttributeCooperative;
+        attr[n++].val.cooperative = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+    if (e == cudaSuccess) pdl_launched(st);
+    return e;
+}
+
+}  // namespace hla

@@ -35,7 +35,7 @@
 #include <cstdlib>
 #include <mutex>
 
-#include "tcgen05.cuh"
+#include "fp8.cuh"
 
 namespace hla {
 
@@ -292,6 +292,18 @@ int launch_tc(const TcParams &p, const void *W, const void *x, cudaStream_t st) 
 }
 
 }  // namespace
+
+bool byte_tile_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t K, uint32_t box_rows) {
+    EncodeTiledFn enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {K, rows};
+    const cuuint64_t strides[1] = {K};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kFp8Block), box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 int *device_status_word() {
     void *p = nullptr;

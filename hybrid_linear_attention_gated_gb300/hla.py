@@ -91,6 +91,8 @@ SIGNATURES = {
     "attn_paged_sparse_workspace_size": (c_size_t, [CACHE] + [c_int] * 3),
     "attn_paged_sparse": (c_int, [CACHE] + [c_int] * 4 + [P, P, c_int, P, c_float, P, P, c_int, P,
                                                           c_size_t, P]),
+    "fp8_quantize": (c_int, [c_int, c_int, P, c_int, c_int, P, P, P]),
+    "fp8_matmul": (c_int, [c_int] * 3 + [P] * 6 + [c_int, P]),
     "skinny_proj_splitk_noalloc": (c_int, [c_int] * 3 + [P] * 4 + [c_int, c_int, P]),
     "hla_launch_count": (ctypes.c_ulonglong, []),
     "hla_device_status": (c_int, []),
@@ -402,6 +404,29 @@ def attn_paged_sparse(C, B, T, H, max_blocks, block_table, past_len, n_select, s
         _tensor(fn, "q", q, torch.bfloat16, n, dev),
         _tensor(fn, "o", o, torch.bfloat16 if o_dtype == HLA_BF16 else torch.float32, n, dev), o_dtype,
         _tensor(fn, "ws", ws, torch.uint8, ws_bytes, dev), ws_bytes, _stream(stream)))
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def fp8_quantize(M, K, x, x_dtype, rows_per_scale, q, scale, stream=None):
+    torch, dev = _torch_and_device()
+    fn = "fp8_quantize"
+    return _check(fn, load().fp8_quantize(
+        M, K, _tensor(fn, "x", x, torch.bfloat16 if x_dtype == HLA_BF16 else torch.float32, M * K, dev), x_dtype,
+        rows_per_scale, _tensor(fn, "q", q, torch.float8_e4m3fn, M * K, dev),
+        _tensor(fn, "scale", scale, torch.float32, -(-M // max(rows_per_scale, 1)) * _blocks(K), dev), _stream(stream)))
+
+
+def fp8_matmul(M, N, K, x, x_scale, W, w_scale, residual, y, y_dtype, stream=None):
+    torch, dev = _torch_and_device()
+    fn, e4m3, f32 = "fp8_matmul", torch.float8_e4m3fn, torch.float32
+    return _check(fn, load().fp8_matmul(
+        M, N, K, _tensor(fn, "x", x, e4m3, M * K, dev), _tensor(fn, "x_scale", x_scale, f32, M * _blocks(K), dev),
+        _tensor(fn, "W", W, e4m3, N * K, dev), _tensor(fn, "w_scale", w_scale, f32, _blocks(N) * _blocks(K), dev),
+        _tensor(fn, "residual", residual, torch.bfloat16, M * N, dev),
+        _tensor(fn, "y", y, torch.bfloat16 if y_dtype == HLA_BF16 else f32, M * N, dev), y_dtype, _stream(stream)))
 
 
 def hla_launch_count():

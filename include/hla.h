@@ -377,6 +377,31 @@ int hla_decode_layer_routing(const hla_layer *L, int M, const void *ws, const in
                              const float **topk_w);
 
 /* ---------------------------------------------------------------------------
+ * Operators over 8-bit values with a scale for each block of 128.  [KIMI-WEBINAR] and [VLLM-K3] Part 1 sec. 3: streaming
+ * weights through memory is the low-batch limit; 8-bit weights halve what is streamed.  The pages give no 8-bit format;
+ * the one here is e4m3 (4 exponent bits of bias 7, 3 mantissa bits, no infinity, largest value 448) with one fp32 scale
+ * for each block of 128 values along K: of one row for activations, of 128 rows for weights.  A value is stored * scale.
+ * The last block of a row, and the last 128 rows, may be shorter.
+ * -------------------------------------------------------------------------*/
+
+/* Conversion.  x [M, K] bf16 or fp32 (x_dtype) -> q e4m3 [M, K], scale fp32 [ceil(M / rows_per_scale), ceil(K / 128)].
+ *  scale = the smallest power of two 2^e, e >= -126, with max|x| <= 448 * 2^e over the block; q = x / scale (exact)
+ *  rounded to the nearest e4m3 value, ties to even.  A block that holds a NaN or an infinity has a NaN scale and NaN
+ *  values.  rows_per_scale 1 (activations) or 128 (weights; a stack of matrices with a multiple of 128 rows each is one
+ *  matrix).  M >= 1, K >= 1, K % 16 == 0.  q and scale overlap nothing else. */
+int fp8_quantize(int M, int K, const void *x, int x_dtype, int rows_per_scale, uint8_t *q, float *scale, hla_stream stream);
+
+/* Product y = x W^T (+ residual).
+ *  y[m, n] = sum_b (x_scale[m, b] * w_scale[n / 128, b]) * sum_{k in block b} x[m, k] * W[n, k]  (+ residual[m, n])
+ *  x e4m3 [M, K], x_scale fp32 [M, ceil(K / 128)]; W e4m3 [N, K], w_scale fp32 [ceil(N / 128), ceil(K / 128)]; any
+ *  scales, not only powers of two (their product is formed in fp32); residual bf16 [M, N] or NULL; y [M, N] fp32 or bf16
+ *  (y_dtype), which may be the residual itself when it is bf16.  Products and sums fp32, one rounding to y's type.
+ *  M, N, K >= 1, K % 16 == 0.  No workspace: K is cut inside a thread-block cluster.  Runs on tcgen05 with bounded waits
+ *  at any size (hla_device_status). */
+int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_scale, const uint8_t *W, const float *w_scale,
+               const hla_bf16 *residual, void *y, int y_dtype, hla_stream stream);
+
+/* ---------------------------------------------------------------------------
  * Paged key-value cache of the softmax-attention layers that a hybrid model interleaves with its KDA
  * layers.  [KIMI-WEBINAR] names the pair: a fixed-size recurrent state next to an attention cache that
  * grows with the sequence; [VLLM-K3] Part 1 sec. 1 (split of a long cache and join of the parts).  The

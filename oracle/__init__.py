@@ -18,10 +18,12 @@ defining equations by eye; speed is not a goal.  Modules:
   hybrid decode layer.
 * ``attention`` -- softmax attention over a paged key-value cache, the append
   with position rotation, and block choice by key bounds.
+* ``fp8``      -- e4m3 values with block scales: conversion, matrix product, and
+  the mixture-of-experts layer.
 
 Parity status: every function is pinned by the ``-m "not gpu"`` tests in
 ``tests/test_oracle_*.py`` (closed forms, hand-worked examples under
 ``tests/golden/``, brute force and invariants).  No function is unpinned.
 """
 
-from . import numerics, kda, moe, layer, attention  # noqa: F401
+from . import numerics, kda, moe, layer, attention, fp8  # noqa: F401

@@ -1,0 +1,58 @@
+"""Refusals of the 8-bit entry points on the host, before any launch."""
+
+import pytest
+import torch
+
+from hybrid_linear_attention_gated_gb300 import build, hla
+
+OK, INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE = range(5)
+FAKE = 0x10000  # never dereferenced: validation fails before any launch
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return hla.load()
+
+
+def quantize(lib, **kw):
+    a = dict(M=4, K=256, x=FAKE, x_dtype=hla.HLA_BF16, rows=1, q=FAKE, scale=FAKE)
+    a.update(kw)
+    return lib.fp8_quantize(*a.values(), None)
+
+
+def matmul(lib, **kw):
+    a = dict(M=4, N=256, K=256, x=FAKE, xs=FAKE, W=FAKE, ws=FAKE, residual=None, y=FAKE, y_dtype=hla.HLA_BF16)
+    a.update(kw)
+    return lib.fp8_matmul(*a.values(), None)
+
+
+def test_quantize_refusals(lib):
+    for kw in (dict(M=0), dict(M=-1), dict(K=0), dict(x=None), dict(q=None), dict(scale=None), dict(x_dtype=hla.HLA_E4M3), dict(x_dtype=7)):
+        assert quantize(lib, **kw) == INVALID, kw
+    for kw in (dict(K=24), dict(K=250), dict(rows=0), dict(rows=2), dict(rows=64), dict(M=2**31 - 1, K=2**31 - 16, rows=128)):
+        assert quantize(lib, **kw) == UNSUPPORTED, kw
+    for kw in (dict(x=FAKE + 8), dict(q=FAKE + 4), dict(scale=FAKE + 4)):
+        assert quantize(lib, **kw) == MISALIGNED, kw
+
+
+def test_matmul_refusals(lib):
+    for kw in (dict(M=0), dict(N=0), dict(K=0), dict(x=None), dict(xs=None), dict(W=None), dict(ws=None), dict(y=None),
+               dict(y_dtype=hla.HLA_E4M3), dict(K=-16)):
+        assert matmul(lib, **kw) == INVALID, kw
+    for kw in (dict(K=40), dict(K=8)):
+        assert matmul(lib, **kw) == UNSUPPORTED, kw
+    for kw in (dict(x=FAKE + 8), dict(xs=FAKE + 4), dict(W=FAKE + 1), dict(ws=FAKE + 8), dict(residual=FAKE + 2), dict(y=FAKE + 2)):
+        assert matmul(lib, **kw) == MISALIGNED, kw
+
+
+def test_binding_checks_tensors(lib):
+    e4m3, bf = torch.float8_e4m3fn, torch.bfloat16
+    x, q, s = torch.zeros(4, 256, dtype=bf), torch.zeros(4, 256, dtype=e4m3), torch.zeros(4, 2)
+    good = dict(M=4, K=256, x=x, x_dtype=hla.HLA_BF16, rows_per_scale=1, q=q, scale=s, stream=0)
+    # host tensors are on no CUDA device; types, sizes and strides are refused the same way
+    for kw in (dict(), dict(x=x.float()), dict(q=q[:3]), dict(x=x.t()), dict(scale=s[:, :1])):
+        with pytest.raises(hla.HlaError):
+            hla.fp8_quantize(**{**good, **kw})
+    with pytest.raises(hla.HlaError):
+        hla.fp8_matmul(4, 4, 256, q, s, q, s[:1], None, torch.zeros(4, 4, dtype=bf), hla.HLA_BF16, stream=0)
