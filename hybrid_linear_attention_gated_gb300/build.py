@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libhla.so")
 SOURCES = ["api.cu", "kda.cu", "gemm.cu", "moe.cu", "layer.cu", "noalloc.cu", "tc_gemm.cu",
-           "kv_cache.cu", "attn.cu", "attn_tc.cu", "attn_select.cu", "fp8_quant.cu", "fp8_matmul.cu"]
+           "kv_cache.cu", "attn.cu", "attn_tc.cu", "attn_select.cu", "fp8_quant.cu", "fp8_matmul.cu", "moe_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -453,7 +453,7 @@ extern "C" int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_
                 HLA_ERR_MISALIGNED);
     MatmulParams p = {};
     p.M = M; p.N = N; p.K = K;
-    p.KB = (K + kFp8Block - 1) / kFp8Block;
+    p.KB = K / kFp8Block + (K % kFp8Block != 0);
     p.xs = x_scale; p.ws = w_scale; p.residual = residual; p.y = y; p.y_bf16 = y_dtype == HLA_BF16;
     p.status = device_status_word();
     HLA_REQUIRE(p.status, HLA_ERR_CUDA);

@@ -151,7 +151,7 @@ extern "C" int fp8_quantize(int M, int K, const void *x, int x_dtype, int rows_p
     HLA_REQUIRE(aligned16(x) && aligned16(q) && aligned16(scale), HLA_ERR_MISALIGNED);
     QuantParams p;
     p.x = x; p.q = q; p.scale = scale; p.M = M; p.K = K;
-    p.KB = (K + kFp8Block - 1) / kFp8Block;
+    p.KB = K / kFp8Block + (K % kFp8Block != 0);
     const cudaStream_t st = (cudaStream_t)stream;
     const bool bf = x_dtype == HLA_BF16;
     set_variant("fp8_quantize<%s,rows%d>", bf ? "bf16" : "f32", rows_per_scale);

@@ -1,0 +1,814 @@
+// The whole mixture-of-experts layer for up to 64 tokens over 8-bit weights with block scales, in two kernels.
+//
+//   logits = x W_r^T, the k largest, w = sigmoid / sum; xq = e4m3 blocks of x;
+//   h = SiLU(xq Wg^T) * (xq Wu^T) per chosen and shared expert, hq = e4m3 blocks of h;  y = residual + sum w (hq Wd^T).
+//
+// Bound by HBM: the weights of the distinct chosen experts, 3 Hd I bytes each, are read once; everything else is small.
+//
+//  1. `moe_prep_kernel`: the router's logits (mma.sync, clusters of four CTAs cut K) beside the conversion of x, and the second
+//     kernel's counters set to zero.
+//  2. `moe_fp8_kernel`, one CTA per SM, a cooperative launch: every CTA derives the choice and the list of active experts from
+//     the logits, and streams an equal, contiguous share of all gate and up tiles, then, after one grid barrier, of all down
+//     tiles.  A tile is 128 weight rows x 128 of K.  The weight rows lie on the lanes of tcgen05 and all tokens of the
+//     batch on the columns (16, 32 or 64): tokens that did not choose the expert cost nothing that the memory does not hide, and
+//     nothing has to be gathered.  Products of one block of K are read back and added, scaled, to sums in registers.
+//     Items cut between CTAs leave their parts in the workspace, and the CTA that comes last adds them in order: no CTA waits
+//     for a part, and the order does not depend on who comes last.  Down tiles run through all experts of one block of output
+//     rows, so that the mixture over experts is one sum in registers.  The copying thread runs ahead across the
+//     barrier: the first down tiles, which depend on no other CTA, are on their way before it.
+//
+// Every wait is bounded (see tc_gemm.cu): a wait that gives up sets the device status word, and what follows still passes
+// every block barrier and the grid barrier's count, without waiting.
+#include "fp8.cuh"
+
+namespace hla {
+namespace {
+
+constexpr int kMaxExperts = 1024;   // routed and shared together
+constexpr int kMaxTopK = 16;
+constexpr int kMaxTokens = 64;
+
+// ----------------------------------------------------------------------------- workspace
+
+struct MoeSpace {
+    size_t logits, xq, xs, hq, hs, part, count, total;
+};
+
+inline int tokens_padded(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+inline int moe_units_most(const hla_moe_fp8 *L, int M) {
+    const long r = (long)M * L->top_k;
+    return (int)(r < L->n_experts ? r : L->n_experts) + L->n_shared;
+}
+
+MoeSpace moe_space(const hla_moe_fp8 *L, int M) {
+    const size_t NT = tokens_padded(M), U = moe_units_most(L, M), G = sm_count();
+    MoeSpace s;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t r = at;
+        at += round_up(bytes, 256);
+        return r;
+    };
+    s.logits = take((size_t)M * L->n_experts * 4);
+    s.xq = take((size_t)M * L->hidden);
+    s.xs = take(NT * (L->hidden / kFp8Block) * 4);
+    s.hq = take(U * NT * L->inter);
+    s.hs = take(U * NT * (L->inter / kFp8Block) * 4);
+    s.part = take(G * 2 * 2 * NT * 128 * 4);
+    s.count = take((2 * G + 1) * 4);
+    s.total = at;
+    return s;
+}
+
+// ----------------------------------------------------------------------------- first kernel
+
+constexpr int kPrepThreads = 256;
+constexpr int kPrepCluster = 4;
+constexpr int kPrepExperts = 8;     // experts per cluster: the columns of one mma.sync
+constexpr int kPrepAhead = 7;       // K steps of 32 whose weights are loaded at once
+
+struct PrepParams {
+    int M, Hd, E, NT, router_clusters, counters;
+    const uint16_t *x, *Wr;
+    float *logits;
+    uint8_t *xq;
+    float *xs;
+    int *count;
+};
+
+__global__ void __launch_bounds__(kPrepThreads) __cluster_dims__(kPrepCluster, 1, 1) moe_prep_kernel(const PrepParams p) {
+    __shared__ float s_part[kPrepThreads / 32][kMaxTokens][kPrepExperts];
+    __shared__ float s_sum[kMaxTokens][kPrepExperts];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cluster = blockIdx.x / kPrepCluster, rank = blockIdx.x % kPrepCluster;
+    if (cluster >= p.router_clusters) {  // conversion of x: 8 lanes a block of 128
+        pdl_wait_trigger();
+        const int KB = p.Hd / kFp8Block;
+        const long b = ((long)(cluster - p.router_clusters) * kPrepCluster + rank) * (kPrepThreads / 8) + (tid >> 3);
+        if (cluster == p.router_clusters && rank == 0)
+            for (int i = tid; i < p.counters; i += kPrepThreads) p.count[i] = 0;
+        const bool live = b < (long)p.M * KB;
+        const int m = live ? (int)(b / KB) : 0, kb = live ? (int)(b - (long)m * KB) : 0;
+        const size_t at = (size_t)m * p.Hd + kb * kFp8Block + (tid & 7) * 16;
+        const uint4 a = ld_act_v4(p.x + at), c = ld_act_v4(p.x + at + 8);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max_magnitude(top, max_magnitude(bf16_lo(w[i]), bf16_hi(w[i])));
+#pragma unroll
+        for (int s = 4; s; s >>= 1) top = max_magnitude(top, __shfl_xor_sync(~0u, top, s));
+        const float sc = fp8_scale_of(top), inv = fp8_inverse(sc);
+        if (live) {
+            uint32_t r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r[i] = e4m3x4(bf16_lo(w[2 * i]) * inv, bf16_hi(w[2 * i]) * inv, bf16_lo(w[2 * i + 1]) * inv, bf16_hi(w[2 * i + 1]) * inv);
+            *reinterpret_cast<uint4 *>(p.xq + at) = make_uint4(r[0], r[1], r[2], r[3]);
+            if ((tid & 7) == 0) p.xs[(size_t)kb * p.NT + m] = sc;
+        }
+        return;
+    }
+    // Logits of 8 experts: the cluster's warps cut K into shares of whole steps of 32.  Lane (g, t) holds 8 values of K for
+    // expert g and for tokens g and g + 8; the same permutation of K on both sides leaves the product as it is.
+    const int g = lane >> 2, t = lane & 3, e0 = cluster * kPrepExperts;
+    const int share = rank * (kPrepThreads / 32) + warp, shares = kPrepCluster * (kPrepThreads / 32), steps = p.Hd / 32;
+    const int s0 = (int)((long)steps * share / shares), s1 = (int)((long)steps * (share + 1) / shares);
+    const int e = e0 + g < p.E ? e0 + g : p.E - 1;
+    const uint16_t *const wr = p.Wr + (size_t)e * p.Hd + t * 8;
+    uint4 w[kPrepAhead];
+#pragma unroll
+    for (int i = 0; i < kPrepAhead; ++i)
+        if (s0 + i < s1) w[i] = ld_weight_v4(wr + (s0 + i) * 32);
+    pdl_wait_trigger();
+    float acc[kMaxTokens / 16][4] = {};
+    for (int s = s0; s < s1; s += kPrepAhead) {
+        if (s > s0) {
+#pragma unroll
+            for (int i = 0; i < kPrepAhead; ++i)
+                if (s + i < s1) w[i] = ld_weight_v4(wr + (s + i) * 32);
+        }
+#pragma unroll
+        for (int mt = 0; mt < kMaxTokens / 16; ++mt) {
+            if (mt * 16 >= p.M) break;
+            const int ma = mt * 16 + g, mb = ma + 8;
+            const uint16_t *const xa = p.x + (size_t)(ma < p.M ? ma : 0) * p.Hd + t * 8, *const xb = p.x + (size_t)(mb < p.M ? mb : 0) * p.Hd + t * 8;
+            uint4 a[kPrepAhead], b[kPrepAhead];
+#pragma unroll
+            for (int i = 0; i < kPrepAhead; ++i)
+                if (s + i < s1) {
+                    a[i] = ld_act_v4(xa + (s + i) * 32);
+                    b[i] = ld_act_v4(xb + (s + i) * 32);
+                }
+#pragma unroll
+            for (int i = 0; i < kPrepAhead; ++i)
+                if (s + i < s1) {
+                    mma_bf16_16816(acc[mt], a[i].x, b[i].x, a[i].y, b[i].y, w[i].x, w[i].y);
+                    mma_bf16_16816(acc[mt], a[i].z, b[i].z, a[i].w, b[i].w, w[i].z, w[i].w);
+                }
+        }
+    }
+#pragma unroll
+    for (int mt = 0; mt < kMaxTokens / 16; ++mt) {
+        if (mt * 16 >= p.M) break;
+        *reinterpret_cast<float2 *>(&s_part[warp][mt * 16 + g][2 * t]) = make_float2(acc[mt][0], acc[mt][1]);
+        *reinterpret_cast<float2 *>(&s_part[warp][mt * 16 + g + 8][2 * t]) = make_float2(acc[mt][2], acc[mt][3]);
+    }
+    __syncthreads();
+    for (int i = tid; i < p.M * kPrepExperts; i += kPrepThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPrepThreads / 32; ++k) v += (&s_part[k][0][0])[i];
+        (&s_sum[0][0])[i] = v;
+    }
+    cluster_sync();
+    for (int i = rank * kPrepThreads + tid; i < p.M * kPrepExperts; i += kPrepCluster * kPrepThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPrepCluster; ++k) v += peer_float(&s_sum[0][0] + i, k);
+        const int m = i / kPrepExperts, n = e0 + i % kPrepExperts;
+        if (n < p.E) p.logits[(size_t)m * p.E + n] = v;
+    }
+    cluster_sync();
+}
+
+// ----------------------------------------------------------------------------- second kernel
+
+constexpr int kMoeThreads = 384;    // copies, products, two warps of the choice only, two groups of four warps of sums
+constexpr int kSumThreads = 256;
+constexpr int kSumWarp0 = 4;
+
+struct MoeMaps {
+    CUtensorMap x, h, gate, up, down, sgate, sup, sdown;
+};
+
+struct MoeParams {
+    int M, Hd, I, E, k, n_shared;
+    const float *logits, *xs;
+    const float *gate_s, *up_s, *down_s, *sgate_s, *sup_s, *sdown_s;
+    const uint16_t *residual;
+    uint16_t *y;
+    int32_t *topk_idx;
+    float *topk_w;
+    uint8_t *hq;
+    float *hs, *part;
+    int *count;                // [G] parts of cut gate/up items, [G] parts of cut output blocks, [1] grid barrier
+    int *status;
+    int force_timeout;
+};
+
+template <int NT>
+struct Moe {
+    static constexpr int kSlots = NT == 16 ? 12 : NT == 32 ? 10 : 8;  // even: gate and up tiles alternate
+    static constexpr int kAcc = 4;                                    // accumulators of 2 NT columns
+    static constexpr uint32_t kTile = 128 * 128, kTokens = NT * 128, kScales = NT * 4;
+    static constexpr uint32_t kColumns = kAcc * 2 * NT;
+    static constexpr int kHalf = NT / 2;                              // tokens of a group of four warps
+    static constexpr size_t kTables = NT * kMaxTopK * 8 + kMaxExperts * 2 + kMaxExperts / 8 + NT * 4 + NT * 16 + 64;
+    static_assert((2 * kSlots + 2 * kAcc + 2) * 8 % 16 == 0 && NT % 4 == 0, "vectors of four in the tables");
+    static constexpr size_t kSmem = 1024 + kSlots * (kTile + kTokens + kScales) + (2 * kSlots + 2 * kAcc + 2) * 8 + 16 + kTables;
+};
+
+// A share of one phase: units of one block of K, [t0, t1) of T for this CTA among `ctas`.
+struct Share {
+    long T;
+    int ctas;
+    __device__ __forceinline__ long start(int c) const { return T * c / ctas; }
+    __device__ __forceinline__ int owner(long t) const { return (int)(((t + 1) * ctas - 1) / T); }
+};
+
+// Position in the order of the gate/up items: unit, block of 128 of the inner width, block of K.
+struct GateAt {
+    int u, ib, kb;
+    __device__ __forceinline__ void set(long t, int nI, int KB) {
+        const long item = t / KB;
+        kb = (int)(t - item * KB);
+        u = (int)(item / nI);
+        ib = (int)(item - (long)u * nI);
+    }
+    __device__ __forceinline__ void next(int nI, int KB) {
+        if (++kb == KB) {
+            kb = 0;
+            if (++ib == nI) ib = 0, ++u;
+        }
+    }
+};
+// Position in the order of the down items: block of output rows, unit, block of K.
+struct DownAt {
+    int rb, u, kb;
+    __device__ __forceinline__ void set(long t, int U, int KB) {
+        const long per = (long)U * KB;
+        rb = (int)(t / per);
+        const int r = (int)(t - rb * per);
+        u = r / KB;
+        kb = r - u * KB;
+    }
+    __device__ __forceinline__ void next(int U, int KB) {
+        if (++kb == KB) {
+            kb = 0;
+            if (++u == U) u = 0, ++rb;
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t ordered(float v) {  // larger floats have larger keys; none is 0
+    const uint32_t b = __float_as_uint(v), k = b & 0x80000000u ? ~b : b | 0x80000000u;
+    return k ? k : 1u;
+}
+__device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
+
+// The k largest of a token's logits by one warp, ties to the lower index: lane j gets the jth index and its logit.
+template <int PER>
+__device__ __forceinline__ void choose(const float *logits, int E, int k, int lane, int *idx, float *logit) {
+    uint32_t key[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = i * 32 + lane;
+        key[i] = e < E ? ordered(__ldcg(logits + e)) : 0u;
+    }
+    for (int j = 0; j < k; ++j) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) top = max(top, key[i]);
+        const uint32_t best = __reduce_max_sync(~0u, top);
+        uint32_t at = ~0u;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i)
+            if (key[i] == best) at = i * 32 + lane;
+        at = __reduce_min_sync(~0u, at);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (at == static_cast<uint32_t>(i * 32 + lane)) key[i] = 0u;
+        if (lane == j) {
+            *idx = (int)at;
+            *logit = unordered(best);
+        }
+    }
+}
+
+__device__ __forceinline__ int load_acquire(const int *p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+template <int NT>
+__global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_constant__ MoeMaps maps, const MoeParams p) {
+    using F = Moe<NT>;
+    constexpr int NS = F::kSlots, NB = F::kAcc, H = F::kHalf;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *const sA = smem, *const sB = smem + NS * F::kTile;
+    float *const sS = reinterpret_cast<float *>(sB + NS * F::kTokens);
+    uint64_t *const full = reinterpret_cast<uint64_t *>(sS + NS * NT);
+    uint64_t *const empty = full + NS, *const acc_full = empty + NS, *const acc_empty = acc_full + NB, *const done = acc_empty + NB;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(done + 2);  // 16-byte aligned, as the tables behind it
+    int *const s_int = reinterpret_cast<int *>(tmem_slot + 1);       // units, products issued, last part?
+    float *const s_weight = reinterpret_cast<float *>(tmem_slot + 4);  // [NT] of the unit at hand, NaN where not chosen
+    float *const s_top = s_weight + NT;                               // [NT][4]
+    uint32_t *const s_active = reinterpret_cast<uint32_t *>(s_top + NT * 4);  // bit e: some token chose expert e
+    int *const s_idx = reinterpret_cast<int *>(s_active + kMaxExperts / 32);  // [NT][k]
+    float *const s_w = reinterpret_cast<float *>(s_idx + NT * kMaxTopK);
+    uint16_t *const s_unit = reinterpret_cast<uint16_t *>(s_w + NT * kMaxTopK);  // routed units' experts
+
+    if (p.force_timeout) {
+        forced_timeout(done, p.status);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1 + kSumThreads / 32);
+        }
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], kSumThreads / 32);
+        }
+        mbar_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async();
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, F::kColumns);
+    for (int i = tid; i < kMaxExperts / 32; i += kMoeThreads) s_active[i] = 0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait_trigger();
+
+    // ---- the choice, by every CTA for itself; the first one writes it out
+    for (int m = warp; m < p.M; m += kMoeThreads / 32) {
+        int idx = 0;
+        float logit = 0.f;
+        if (p.E <= 256) choose<8>(p.logits + (size_t)m * p.E, p.E, p.k, lane, &idx, &logit);
+        else choose<32>(p.logits + (size_t)m * p.E, p.E, p.k, lane, &idx, &logit);
+        const float score = 1.f / (1.f + expf(-logit));
+        float sum = 0.f;
+        for (int j = 0; j < p.k; ++j) sum += __shfl_sync(~0u, score, j);
+        if (lane < p.k) {
+            const float w = score / sum;
+            s_idx[m * p.k + lane] = idx;
+            s_w[m * p.k + lane] = w;
+            atomicOr(&s_active[idx >> 5], 1u << (idx & 31));
+            if (blockIdx.x == 0) {
+                if (p.topk_idx) p.topk_idx[m * p.k + lane] = idx;
+                if (p.topk_w) p.topk_w[m * p.k + lane] = w;
+            }
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < p.E; e += kMoeThreads) {
+        if (!(s_active[e >> 5] >> (e & 31) & 1)) continue;
+        int at = __popc(s_active[e >> 5] & ((1u << (e & 31)) - 1));
+        for (int i = 0; i < e >> 5; ++i) at += __popc(s_active[i]);
+        s_unit[at] = (uint16_t)e;
+    }
+    if (tid == 0) {
+        int n = 0;
+        for (int i = 0; i < (p.E + 31) / 32; ++i) n += __popc(s_active[i]);
+        s_int[0] = n;
+    }
+    __syncthreads();
+    // units: the shared experts, then the active ones in order
+    const int U = s_int[0] + p.n_shared, G = gridDim.x, c = blockIdx.x;
+    const int nI = p.I / 128, nR = p.Hd / 128, KB1 = p.Hd / kFp8Block, KB2 = p.I / kFp8Block;
+    Share s1, s2;
+    s1.T = (long)U * nI * KB1;
+    s2.T = (long)nR * U * KB2;
+    s1.ctas = s1.T < G ? (int)s1.T : G;
+    s2.ctas = s2.T < G ? (int)s2.T : G;
+    const long a0 = c < s1.ctas ? s1.start(c) : 0, a1 = c < s1.ctas ? s1.start(c + 1) : 0;
+    const long b0 = c < s2.ctas ? s2.start(c) : 0, b1 = c < s2.ctas ? s2.start(c + 1) : 0;
+    int *const barrier = p.count + 2 * G;
+    long issued = 0;  // slots filled
+
+    if (warp == 0 && lane == 0) {
+        // ---- copies
+        bool ok = true;
+        GateAt at;
+        at.set(a0, nI, KB1);
+        for (long t = a0; t < a1 && ok; ++t, at.next(nI, KB1)) {
+            const bool sh = at.u < p.n_shared;
+            const int row = (sh ? at.u : s_unit[at.u - p.n_shared]) * p.I + at.ib * 128, col = at.kb * kFp8Block;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int s = (int)(issued % NS);
+                if (issued >= NS && !(ok = fp8_wait(&empty[s], (uint32_t)(issued / NS - 1) & 1, p.status))) break;
+                mbar_expect_tx(&full[s], F::kTile + (half ? 0 : F::kTokens + F::kScales));
+                tma_tile(sA + s * F::kTile, half ? (sh ? &maps.sup : &maps.up) : (sh ? &maps.sgate : &maps.gate), col, row, &full[s]);
+                if (!half) {
+                    tma_tile(sB + s * F::kTokens, &maps.x, col, 0, &full[s]);
+                    bulk_g2s(sS + s * NT, p.xs + (size_t)at.kb * NT, F::kScales, &full[s]);
+                }
+                ++issued;
+            }
+        }
+        // the first down tiles go out before the grid barrier, their tokens and scales after it
+        const long n2 = b1 - b0, first = issued;
+        const int pre = (int)(n2 < NS ? n2 : NS);
+        DownAt w, h;
+        w.set(b0, U, KB2);
+        h = w;
+        const auto weights = [&](int s) {
+            const bool sh = w.u < p.n_shared;
+            mbar_expect_tx(&full[s], F::kTile + F::kTokens + F::kScales);
+            tma_tile(sA + s * F::kTile, sh ? &maps.sdown : &maps.down, w.kb * kFp8Block,
+                     (sh ? w.u : s_unit[w.u - p.n_shared]) * p.Hd + w.rb * 128, &full[s]);
+            w.next(U, KB2);
+        };
+        const auto tokens = [&](int s) {
+            tma_tile(sB + s * F::kTokens, &maps.h, h.kb * kFp8Block, h.u * NT, &full[s]);
+            bulk_g2s(sS + s * NT, p.hs + ((size_t)h.u * KB2 + h.kb) * NT, F::kScales, &full[s]);
+            h.next(U, KB2);
+        };
+        int sent = 0;
+        for (; sent < pre && ok; ++sent) {
+            const long i = first + sent;
+            const int s = (int)(i % NS);
+            if (i >= NS && !(ok = fp8_wait(&empty[s], (uint32_t)(i / NS - 1) & 1, p.status))) break;
+            weights(s);
+        }
+        if (n2 > 0 && ok) {
+            const uint64_t began = global_ns();
+            while (load_acquire(barrier) < G)
+                if (global_ns() - began > kFp8WaitNs) {
+                    atomicExch(p.status, HLA_ERR_DEVICE_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+            fence_async();
+        }
+        for (int i = 0; i < sent; ++i) tokens((int)((first + i) % NS));  // after a barrier that gave up, too: the fills complete
+        issued += sent;
+        for (long t = sent; t < n2 && ok; ++t) {
+            const int s = (int)(issued % NS);
+            if (issued >= NS && !(ok = fp8_wait(&empty[s], (uint32_t)(issued / NS - 1) & 1, p.status))) break;
+            weights(s);
+            tokens(s);
+            ++issued;
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ---- products
+        bool ok = true;
+        long g = 0, slot = 0;
+        for (long t = a0; t < a1; ++t, ++g, slot += 2) {
+            const int b = (int)(g % NB), s = (int)(slot % NS);
+            if (g >= NB && !(ok = fp8_wait(&acc_empty[b], (uint32_t)(g / NB - 1) & 1, p.status))) break;
+            if (!(ok = fp8_wait(&full[s], (uint32_t)(slot / NS) & 1, p.status))) break;
+            tc_fence_after();
+            umma_block(tmem + b * 2 * NT, smem_u32(sA + s * F::kTile), smem_u32(sB + s * F::kTokens), idesc_e4m3(128, NT));
+            if (!(ok = fp8_wait(&full[s + 1], (uint32_t)(slot / NS) & 1, p.status))) break;
+            tc_fence_after();
+            umma_block(tmem + b * 2 * NT + NT, smem_u32(sA + (s + 1) * F::kTile), smem_u32(sB + s * F::kTokens), idesc_e4m3(128, NT));
+            umma_commit(&empty[s]);
+            umma_commit(&empty[s + 1]);
+            umma_commit(&acc_full[b]);
+        }
+        for (long t = b0; t < b1 && ok; ++t, ++g, ++slot) {
+            const int b = (int)(g % NB), s = (int)(slot % NS);
+            if (g >= NB && !(ok = fp8_wait(&acc_empty[b], (uint32_t)(g / NB - 1) & 1, p.status))) break;
+            if (!(ok = fp8_wait(&full[s], (uint32_t)(slot / NS) & 1, p.status))) break;
+            tc_fence_after();
+            umma_block(tmem + b * 2 * NT, smem_u32(sA + s * F::kTile), smem_u32(sB + s * F::kTokens), idesc_e4m3(128, NT));
+            umma_commit(&empty[s]);
+            umma_commit(&acc_full[b]);
+        }
+        s_int[1] = ok;
+        umma_commit(done);
+        if (!fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
+    } else if (warp >= kSumWarp0) {
+        // ---- sums: group `grp` of four warps has tokens [grp * H, grp * H + H) of every weight row
+        const int grp = warp >= kSumWarp0 + 4, q4 = warp & 3, row = q4 * 32 + lane, m0 = grp * H;
+        const int st = tid - kSumWarp0 * 32;
+        const uint32_t my = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + m0;
+        constexpr size_t kPart = 2 * NT * 128;  // floats of a part
+        bool ok = true;
+        long g = 0, slot = 0;
+        // wait for an accumulator and the scales that came with it
+        const auto ready = [&](int b, int s) {
+            ok = __all_sync(~0u, ok && fp8_wait(&acc_full[b], (uint32_t)(g / NB) & 1, p.status) &&
+                                     fp8_wait(&full[s], (uint32_t)(slot / NS) & 1, p.status));
+            tc_fence_after();
+            return ok;
+        };
+        // leaves a part behind (already stored): true in the CTA that comes last, whose parts are all there
+        const auto last_part = [&](int *count, int parts) {
+            __threadfence();
+            named_sync(1, kSumThreads);
+            if (st == 0) {
+                const int before = atomicAdd(count, 1);
+                __threadfence();
+                s_int[2] = before == parts - 1;
+            }
+            named_sync(1, kSumThreads);
+            return s_int[2] != 0;
+        };
+        {
+            float ga[H], ua[H];
+            GateAt at;
+            at.set(a0, nI, KB1);
+            long begin = a0;  // of the segment
+            const auto scales_at = [&](const GateAt &x, float *sg, float *su) {
+                const bool sh = x.u < p.n_shared;
+                const size_t i = ((size_t)(sh ? x.u : s_unit[x.u - p.n_shared]) * nI + x.ib) * KB1 + x.kb;
+                *sg = __ldg((sh ? p.sgate_s : p.gate_s) + i);
+                *su = __ldg((sh ? p.sup_s : p.up_s) + i);
+            };
+            float sg = 0.f, su = 0.f;
+            if (a0 < a1) scales_at(at, &sg, &su);
+            for (long t = a0; t < a1; ++t, ++g, slot += 2) {
+                if (t == begin) {
+#pragma unroll
+                    for (int j = 0; j < H; ++j) ga[j] = ua[j] = 0.f;
+                }
+                GateAt nx = at;
+                nx.next(nI, KB1);
+                float ng = 0.f, nu = 0.f;
+                if (t + 1 < a1) scales_at(nx, &ng, &nu);
+                const int b = (int)(g % NB), s = (int)(slot % NS);
+                if (ready(b, s)) {
+                    uint32_t vg[H], vu[H];
+                    tmem_ld<H>(my + b * 2 * NT, vg);
+                    tmem_ld<H>(my + b * 2 * NT + NT, vu);
+                    tmem_wait_ld();
+                    const float *const sc = sS + s * NT + m0;
+#pragma unroll
+                    for (int j = 0; j < H; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(sc + j);
+                        const float x[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            ga[j + i] = fmaf(__uint_as_float(vg[j + i]), x[i] * sg, ga[j + i]);
+                            ua[j + i] = fmaf(__uint_as_float(vu[j + i]), x[i] * su, ua[j + i]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&acc_empty[b]);
+                        mbar_arrive(&empty[s]);
+                        mbar_arrive(&empty[s + 1]);
+                    }
+                }
+                if (at.kb == KB1 - 1 || t + 1 == a1) {
+                    // the segment ends: a whole item, or a part of one
+                    const long i0 = t - at.kb, i1 = i0 + KB1;
+                    bool whole = begin == i0 && t + 1 == i1;
+                    if (!whole) {
+                        float *const mine = p.part + ((size_t)c * 2 + (begin != a0)) * kPart;
+#pragma unroll
+                        for (int j = 0; j < H; ++j) {
+                            __stcg(mine + (m0 + j) * 128 + row, ga[j]);
+                            __stcg(mine + (NT + m0 + j) * 128 + row, ua[j]);
+                        }
+                        const int c0 = s1.owner(i0), c1 = s1.owner(i1 - 1);
+                        if ((whole = last_part(p.count + c0, c1 - c0 + 1))) {
+#pragma unroll
+                            for (int j = 0; j < H; ++j) ga[j] = ua[j] = 0.f;
+                            for (int k = c0; k <= c1; ++k) {
+                                const float *const their = p.part + ((size_t)k * 2 + (k == c0 && s1.start(c0) != i0)) * kPart;
+#pragma unroll
+                                for (int j = 0; j < H; ++j) {
+                                    ga[j] += __ldcg(their + (m0 + j) * 128 + row);
+                                    ua[j] += __ldcg(their + (NT + m0 + j) * 128 + row);
+                                }
+                            }
+                        }
+                    }
+                    if (whole) {
+                        // h of 128 columns: every token that chose this expert, its own scale, times its weight in the mixture
+                        const bool sh = at.u < p.n_shared;
+                        if (st < NT) {
+                            float w = sh ? 1.f : -1.f;  // -1: not chosen
+                            if (!sh && st < p.M) {
+                                const int e = s_unit[at.u - p.n_shared];
+                                for (int j = 0; j < p.k; ++j)
+                                    if (s_idx[st * p.k + j] == e) w = s_w[st * p.k + j];
+                            }
+                            s_weight[st] = st < p.M ? w : -1.f;
+                        }
+                        named_sync(1, kSumThreads);
+#pragma unroll
+                        for (int j = 0; j < H; ++j) {
+                            if (s_weight[m0 + j] == -1.f) continue;  // the same for the whole group
+                            const float hv = silu_f(ga[j]) * ua[j];
+                            ga[j] = hv;
+                            const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(hv) & 0x7FFFFFFFu);
+                            if (lane == 0) s_top[(m0 + j) * 4 + q4] = __uint_as_float(top);
+                        }
+                        named_sync(2 + grp, 128);
+#pragma unroll
+                        for (int j = 0; j < H; ++j) {
+                            const float w = s_weight[m0 + j];
+                            float *const hs = p.hs + ((size_t)at.u * KB2 + at.ib) * NT + m0 + j;
+                            if (w == -1.f) {
+                                if (row == 0) *hs = 0.f;
+                                continue;
+                            }
+                            const float4 f = *reinterpret_cast<const float4 *>(s_top + (m0 + j) * 4);
+                            const float sc = fp8_scale_of(max_magnitude(max_magnitude(f.x, f.y), max_magnitude(f.z, f.w)));
+                            p.hq[((size_t)at.u * NT + m0 + j) * p.I + at.ib * 128 + row] = (uint8_t)e4m3x2(ga[j] * fp8_inverse(sc), 0.f);
+                            if (row == 0) *hs = sc * w;
+                        }
+                        named_sync(1, kSumThreads);
+                    }
+                    begin = t + 1;
+                }
+                at = nx;
+                sg = ng;
+                su = nu;
+            }
+        }
+        __threadfence();
+        fence_async();
+        named_sync(1, kSumThreads);
+        if (st == 0) {
+            __threadfence();
+            atomicAdd(barrier, 1);
+        }
+        {
+            float acc[H];
+            DownAt at;
+            at.set(b0, U, KB2);
+            long begin = b0;
+            const long per = (long)U * KB2;
+            const auto scale_at = [&](const DownAt &x) {
+                const bool sh = x.u < p.n_shared;
+                return __ldg((sh ? p.sdown_s : p.down_s) + ((size_t)(sh ? x.u : s_unit[x.u - p.n_shared]) * nR + x.rb) * KB2 + x.kb);
+            };
+            float sw = b0 < b1 ? scale_at(at) : 0.f;
+            for (long t = b0; t < b1; ++t, ++g, ++slot) {
+                if (t == begin) {
+#pragma unroll
+                    for (int j = 0; j < H; ++j) acc[j] = 0.f;
+                }
+                DownAt nx = at;
+                nx.next(U, KB2);
+                const float nw = t + 1 < b1 ? scale_at(nx) : 0.f;
+                const int b = (int)(g % NB), s = (int)(slot % NS);
+                if (ready(b, s)) {
+                    uint32_t v[H];
+                    tmem_ld<H>(my + b * 2 * NT, v);
+                    tmem_wait_ld();
+                    const float *const sc = sS + s * NT + m0;
+#pragma unroll
+                    for (int j = 0; j < H; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(sc + j);
+                        const float x[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (x[i] != 0.f) acc[j + i] = fmaf(__uint_as_float(v[j + i]), x[i] * sw, acc[j + i]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&acc_empty[b]);
+                        mbar_arrive(&empty[s]);
+                    }
+                }
+                if ((at.u == U - 1 && at.kb == KB2 - 1) || t + 1 == b1) {
+                    const long i0 = at.rb * per, i1 = i0 + per;
+                    bool whole = begin == i0 && t + 1 == i1;
+                    if (!whole) {
+                        float *const mine = p.part + ((size_t)c * 2 + (begin != b0)) * kPart;
+#pragma unroll
+                        for (int j = 0; j < H; ++j) __stcg(mine + (m0 + j) * 128 + row, acc[j]);
+                        const int c0 = s2.owner(i0), c1 = s2.owner(i1 - 1);
+                        if ((whole = last_part(p.count + G + c0, c1 - c0 + 1))) {
+#pragma unroll
+                            for (int j = 0; j < H; ++j) acc[j] = 0.f;
+                            for (int k = c0; k <= c1; ++k) {
+                                const float *const their = p.part + ((size_t)k * 2 + (k == c0 && s2.start(c0) != i0)) * kPart;
+#pragma unroll
+                                for (int j = 0; j < H; ++j) acc[j] += __ldcg(their + (m0 + j) * 128 + row);
+                            }
+                        }
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int j = 0; j < H; ++j) {
+                            if (m0 + j >= p.M) break;
+                            const size_t o = (size_t)(m0 + j) * p.Hd + at.rb * 128 + row;
+                            p.y[o] = float_to_bf16_bits(p.residual ? acc[j] + bf16_bits_to_float(p.residual[o]) : acc[j]);
+                        }
+                    }
+                    begin = t + 1;
+                }
+                at = nx;
+                sw = nw;
+            }
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (tid == 0 && !s_int[1])  // after a wait that gave up: the last fill of each slot may be in flight
+        for (int s = 0; s < NS; ++s) {
+            if (issued <= s) continue;
+            const long f = issued - 1 - (issued - 1 - s) % NS;
+            if (!fp8_wait(&full[s], (uint32_t)(f / NS) & 1, p.status)) fp8_wait(&full[s], (uint32_t)(f / NS) & 1, p.status, 8 * kFp8WaitNs);
+        }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_free(tmem, F::kColumns);
+}
+
+// ----------------------------------------------------------------------------- host
+
+template <int NT>
+cudaError_t launch_moe(const MoeMaps &maps, const MoeParams &p, int grid, cudaStream_t st) {
+    static bool done[64] = {};
+    const cudaError_t e = allow_smem(moe_fp8_kernel<NT>, Moe<NT>::kSmem, done);
+    if (e != cudaSuccess) return e;
+    return launch_kernel_as(moe_fp8_kernel<NT>, dim3((unsigned)grid), dim3(kMoeThreads), Moe<NT>::kSmem, st, 1, true, maps, p);
+}
+
+int check_moe(const hla_moe_fp8 *L) {
+    HLA_REQUIRE(L && L->hidden >= 1 && L->inter >= 1 && L->n_experts >= 1 && L->top_k >= 1 && L->n_shared >= 0, HLA_ERR_INVALID_ARG);
+    HLA_REQUIRE(L->top_k <= L->n_experts, HLA_ERR_INVALID_ARG);
+    HLA_REQUIRE(L->hidden % 128 == 0 && L->inter % 128 == 0 && L->top_k <= kMaxTopK, HLA_ERR_UNSUPPORTED);
+    HLA_REQUIRE((long)L->n_experts + L->n_shared <= kMaxExperts && L->n_shared <= 16, HLA_ERR_UNSUPPORTED);
+    // rows of the weight stacks and bytes of one row stay in 31 bits
+    HLA_REQUIRE(L->hidden <= 1 << 20 && L->inter <= 1 << 20, HLA_ERR_UNSUPPORTED);
+    return HLA_OK;
+}
+
+}  // namespace
+}  // namespace hla
+
+using namespace hla;
+
+extern "C" size_t moe_fp8_forward_workspace_size(const hla_moe_fp8 *L, int M) {
+    if (check_moe(L) != HLA_OK || M < 1 || M > kMaxTokens) return 0;
+    return moe_space(L, M).total;
+}
+
+extern "C" int moe_fp8_forward(const hla_moe_fp8 *L, int M, const hla_bf16 *x, const hla_bf16 *residual, hla_bf16 *y,
+                               int32_t *topk_idx, float *topk_w, void *ws, size_t ws_bytes, hla_stream stream) {
+    int e = check_moe(L);
+    if (e != HLA_OK) return e;
+    HLA_REQUIRE(M >= 1 && x && y, HLA_ERR_INVALID_ARG);
+    HLA_REQUIRE(M <= kMaxTokens, HLA_ERR_UNSUPPORTED);
+    HLA_REQUIRE(L->W_router && L->W_gate && L->W_up && L->W_down && L->S_gate && L->S_up && L->S_down, HLA_ERR_INVALID_ARG);
+    const bool sh = L->n_shared > 0;
+    HLA_REQUIRE(!sh || (L->Ws_gate && L->Ws_up && L->Ws_down && L->Ss_gate && L->Ss_up && L->Ss_down), HLA_ERR_INVALID_ARG);
+    for (const void *q : {(const void *)x, (const void *)residual, (const void *)y, (const void *)topk_idx, (const void *)topk_w,
+                          (const void *)L->W_router, (const void *)L->W_gate, (const void *)L->W_up, (const void *)L->W_down,
+                          (const void *)L->S_gate, (const void *)L->S_up, (const void *)L->S_down})
+        HLA_REQUIRE(aligned16(q), HLA_ERR_MISALIGNED);
+    if (sh)
+        for (const void *q : {(const void *)L->Ws_gate, (const void *)L->Ws_up, (const void *)L->Ws_down, (const void *)L->Ss_gate,
+                              (const void *)L->Ss_up, (const void *)L->Ss_down})
+            HLA_REQUIRE(aligned16(q), HLA_ERR_MISALIGNED);
+    const MoeSpace sp = moe_space(L, M);
+    HLA_REQUIRE(ws && ws_bytes >= sp.total, HLA_ERR_WORKSPACE);
+    HLA_REQUIRE(aligned16(ws), HLA_ERR_MISALIGNED);
+
+    const int NT = tokens_padded(M), Hd = L->hidden, I = L->inter, E = L->n_experts, U = moe_units_most(L, M), sms = sm_count();
+    uint8_t *const w = static_cast<uint8_t *>(ws);
+    // no more CTAs than the largest phase can have blocks
+    const long most1 = (long)U * (I / 128) * (Hd / 128), most = most1;
+    const int grid = (int)(most < sms ? most : sms);
+
+    MoeParams p = {};
+    p.M = M; p.Hd = Hd; p.I = I; p.E = E; p.k = L->top_k; p.n_shared = L->n_shared;
+    p.logits = reinterpret_cast<float *>(w + sp.logits);
+    p.xs = reinterpret_cast<float *>(w + sp.xs);
+    p.gate_s = L->S_gate; p.up_s = L->S_up; p.down_s = L->S_down;
+    p.sgate_s = L->Ss_gate; p.sup_s = L->Ss_up; p.sdown_s = L->Ss_down;
+    p.residual = residual; p.y = y; p.topk_idx = topk_idx; p.topk_w = topk_w;
+    p.hq = w + sp.hq;
+    p.hs = reinterpret_cast<float *>(w + sp.hs);
+    p.part = reinterpret_cast<float *>(w + sp.part);
+    p.count = reinterpret_cast<int *>(w + sp.count);
+    p.status = device_status_word();
+    HLA_REQUIRE(p.status, HLA_ERR_CUDA);
+    p.force_timeout = wait_timeout_forced();
+    MoeMaps maps;
+    bool ok = byte_tile_map(&maps.x, w + sp.xq, M, Hd, NT) && byte_tile_map(&maps.h, p.hq, (uint64_t)U * NT, I, NT) &&
+              byte_tile_map(&maps.gate, L->W_gate, (uint64_t)E * I, Hd, 128) && byte_tile_map(&maps.up, L->W_up, (uint64_t)E * I, Hd, 128) &&
+              byte_tile_map(&maps.down, L->W_down, (uint64_t)E * Hd, I, 128);
+    if (sh)
+        ok = ok && byte_tile_map(&maps.sgate, L->Ws_gate, (uint64_t)L->n_shared * I, Hd, 128) &&
+             byte_tile_map(&maps.sup, L->Ws_up, (uint64_t)L->n_shared * I, Hd, 128) &&
+             byte_tile_map(&maps.sdown, L->Ws_down, (uint64_t)L->n_shared * Hd, I, 128);
+    else
+        maps.sgate = maps.gate, maps.sup = maps.up, maps.sdown = maps.down;
+    HLA_REQUIRE(ok, HLA_ERR_CUDA);
+
+    const cudaStream_t st = (cudaStream_t)stream;
+    set_variant("moe_fp8<tokens%d,ctas%d>", NT, grid);
+    PdlChain chain(st, pdl_default(1));
+    PrepParams q = {};
+    q.M = M; q.Hd = Hd; q.E = E; q.NT = NT;
+    q.router_clusters = (E + kPrepExperts - 1) / kPrepExperts;
+    q.counters = 2 * grid + 1;
+    q.x = x; q.Wr = L->W_router; q.logits = const_cast<float *>(p.logits); q.xq = w + sp.xq; q.xs = const_cast<float *>(p.xs); q.count = p.count;
+    const int per = kPrepCluster * (kPrepThreads / 8);
+    const long convert = ((long)M * (Hd / kFp8Block) + per - 1) / per;
+    e = launched(launch_kernel(moe_prep_kernel, dim3((unsigned)((q.router_clusters + convert) * kPrepCluster)), dim3(kPrepThreads), 0, st, q));
+    if (e != HLA_OK) return e;
+    const cudaError_t ce = NT == 16 ? launch_moe<16>(maps, p, grid, st) : NT == 32 ? launch_moe<32>(maps, p, grid, st) : launch_moe<64>(maps, p, grid, st);
+    return launched(ce);
+}

@@ -53,6 +53,16 @@ class hla_kv_cache(ctypes.Structure):
 
 CACHE = ctypes.POINTER(hla_kv_cache)
 
+
+class hla_moe_fp8(ctypes.Structure):
+    _fields_ = [("hidden", c_int), ("inter", c_int), ("n_experts", c_int), ("top_k", c_int), ("n_shared", c_int),
+                ("W_router", P), ("W_gate", P), ("W_up", P), ("W_down", P), ("S_gate", P), ("S_up", P), ("S_down", P),
+                ("Ws_gate", P), ("Ws_up", P), ("Ws_down", P), ("Ss_gate", P), ("Ss_up", P), ("Ss_down", P)]
+    device = None  # of the tensors that make_moe_fp8 was given
+
+
+MOE_FP8 = ctypes.POINTER(hla_moe_fp8)
+
 SIGNATURES = {
     "hla_status_string": (c_char_p, [c_int]),
     "hla_last_variant": (c_char_p, []),
@@ -93,6 +103,8 @@ SIGNATURES = {
                                                           c_size_t, P]),
     "fp8_quantize": (c_int, [c_int, c_int, P, c_int, c_int, P, P, P]),
     "fp8_matmul": (c_int, [c_int] * 3 + [P] * 6 + [c_int, P]),
+    "moe_fp8_forward_workspace_size": (c_size_t, [MOE_FP8, c_int]),
+    "moe_fp8_forward": (c_int, [MOE_FP8, c_int] + [P] * 6 + [c_size_t, P]),
     "skinny_proj_splitk_noalloc": (c_int, [c_int] * 3 + [P] * 4 + [c_int, c_int, P]),
     "hla_launch_count": (ctypes.c_ulonglong, []),
     "hla_device_status": (c_int, []),
@@ -427,6 +439,41 @@ def fp8_matmul(M, N, K, x, x_scale, W, w_scale, residual, y, y_dtype, stream=Non
         _tensor(fn, "W", W, e4m3, N * K, dev), _tensor(fn, "w_scale", w_scale, f32, _blocks(N) * _blocks(K), dev),
         _tensor(fn, "residual", residual, torch.bfloat16, M * N, dev),
         _tensor(fn, "y", y, torch.bfloat16 if y_dtype == HLA_BF16 else f32, M * N, dev), y_dtype, _stream(stream)))
+
+
+def make_moe_fp8(hidden, inter, n_experts, top_k, n_shared, W_router, W_gate, W_up, W_down, S_gate, S_up, S_down,
+                 Ws_gate=None, Ws_up=None, Ws_down=None, Ss_gate=None, Ss_up=None, Ss_down=None):
+    """Build an hla_moe_fp8 descriptor; it keeps the tensors it was given alive."""
+    torch, dev = _torch_and_device()
+    L = hla_moe_fp8(hidden, inter, n_experts, top_k, n_shared)
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    matrix, blocks = hidden * inter, _blocks(hidden) * _blocks(inter)
+    fields = [("W_router", W_router, torch.bfloat16, n_experts * hidden)]
+    for kind, n, w, s in (("", n_experts, (W_gate, W_up, W_down), (S_gate, S_up, S_down)),
+                          ("s", n_shared, (Ws_gate, Ws_up, Ws_down), (Ss_gate, Ss_up, Ss_down))):
+        for name, wt, st in zip(("gate", "up", "down"), w, s):
+            fields += [(f"W{kind}_{name}", wt, e4m3, n * matrix), (f"S{kind}_{name}", st, f32, n * blocks)]
+    L.tensors = [t for _, t, _, _ in fields]
+    L.device = dev if any(isinstance(t, torch.Tensor) for t in L.tensors) else None
+    for name, t, dt, least in fields:
+        setattr(L, name, _tensor("make_moe_fp8", name, t, dt, least, dev))
+    return L
+
+
+def moe_fp8_forward_workspace_size(L, M):
+    return load().moe_fp8_forward_workspace_size(ctypes.byref(L), M)
+
+
+def moe_fp8_forward(L, M, x, residual, y, topk_idx, topk_w, ws, ws_bytes, stream=None):
+    torch, dev = _torch_and_device()
+    fn, bf, n = "moe_fp8_forward", torch.bfloat16, M * L.hidden
+    if L.device is not None and L.device != dev:
+        raise HlaError(fn, HLA_ERR_INVALID_ARG, f"the weights are on device {L.device}, the current device is {dev}")
+    return _check(fn, load().moe_fp8_forward(
+        ctypes.byref(L), M, _tensor(fn, "x", x, bf, n, dev), _tensor(fn, "residual", residual, bf, n, dev),
+        _tensor(fn, "y", y, bf, n, dev), _tensor(fn, "topk_idx", topk_idx, torch.int32, M * L.top_k, dev),
+        _tensor(fn, "topk_w", topk_w, torch.float32, M * L.top_k, dev), _tensor(fn, "ws", ws, torch.uint8, ws_bytes, dev),
+        ws_bytes, _stream(stream)))
 
 
 def hla_launch_count():

@@ -401,6 +401,31 @@ int fp8_quantize(int M, int K, const void *x, int x_dtype, int rows_per_scale, u
 int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_scale, const uint8_t *W, const float *w_scale,
                const hla_bf16 *residual, void *y, int y_dtype, hla_stream stream);
 
+/* The whole mixture-of-experts layer of a decode batch over such weights, in two kernels.
+ *  [VLLM-K3] Part 1 sec. 3 (router, routed and shared experts).
+ *  Router, choice and weights as moe_route_topk, from x itself.  Experts as moe_expert_forward, on the values of
+ *  xq = fp8_quantize(x, 1 row): h = SiLU(W_gate xq) * (W_up xq), hq = fp8_quantize(h, 1 row),
+ *  y[m] = sum_j topk_w[m, j] * W_down hq_j + sum_s (the same for shared expert s) (+ residual[m]), rounded once to bf16.
+ *  An expert's weights reach only the tokens that chose it: NaN weights of one do not spread to others.
+ *  x, y bf16 [M, Hd]; residual bf16 [M, Hd] or NULL (y may be the residual, or x); topk_idx int32 [M, k] and topk_w fp32
+ *  [M, k] receive the choice, or NULL.  1 <= M <= 64, Hd % 128 == 0, I % 128 == 0, 1 <= k <= 16, k <= E,
+ *  E + n_shared <= 1024, n_shared <= 16.
+ *  Each active expert's weights are read once per call.  The second kernel is a cooperative launch of at most one block
+ *  per SM with one grid barrier (bounded, as every wait: hla_device_status), so calls on different streams, with their own
+ *  workspaces, run one after another and cannot block each other.  The workspace needs no initialisation and may
+ *  serve any later call. */
+typedef struct hla_moe_fp8 {
+    int hidden, inter, n_experts, top_k, n_shared;  /* Hd, I, E, k */
+    const hla_bf16 *W_router;                       /* bf16 [E, Hd] */
+    const uint8_t *W_gate, *W_up, *W_down;          /* e4m3 [E, I, Hd], [E, I, Hd], [E, Hd, I] */
+    const float *S_gate, *S_up, *S_down;            /* fp32 [E, I/128, Hd/128] x2, [E, Hd/128, I/128] */
+    const uint8_t *Ws_gate, *Ws_up, *Ws_down;       /* the same with n_shared in place of E; NULL when n_shared = 0 */
+    const float *Ss_gate, *Ss_up, *Ss_down;
+} hla_moe_fp8;
+size_t moe_fp8_forward_workspace_size(const hla_moe_fp8 *L, int M);
+int moe_fp8_forward(const hla_moe_fp8 *L, int M, const hla_bf16 *x, const hla_bf16 *residual, hla_bf16 *y, int32_t *topk_idx,
+                    float *topk_w, void *ws, size_t ws_bytes, hla_stream stream);
+
 /* ---------------------------------------------------------------------------
  * Paged key-value cache of the softmax-attention layers that a hybrid model interleaves with its KDA
  * layers.  [KIMI-WEBINAR] names the pair: a fixed-size recurrent state next to an attention cache that

@@ -1,5 +1,7 @@
 """Refusals of the 8-bit entry points on the host, before any launch."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -25,6 +27,38 @@ def matmul(lib, **kw):
     a = dict(M=4, N=256, K=256, x=FAKE, xs=FAKE, W=FAKE, ws=FAKE, residual=None, y=FAKE, y_dtype=hla.HLA_BF16)
     a.update(kw)
     return lib.fp8_matmul(*a.values(), None)
+
+
+def moe(lib, M=4, ws=FAKE, n=1 << 40, x=FAKE, residual=None, y=FAKE, idx=None, w=None, L=None, null=False, **kw):
+    a = dict(hidden=256, inter=128, n_experts=8, top_k=2, n_shared=1)
+    a.update({k: v for k, v in kw.items() if k in a})
+    L = hla.hla_moe_fp8(*a.values())
+    for name, _ in hla.hla_moe_fp8._fields_[5:]:
+        setattr(L, name, kw.get(name, FAKE))
+    return lib.moe_fp8_forward(None if null else ctypes.byref(L), M, x, residual, y, idx, w, ws, n, None)
+
+
+def test_moe_refusals(lib):
+    assert moe(lib, null=True) == INVALID
+    for kw in (dict(hidden=0), dict(inter=0), dict(n_experts=0), dict(top_k=0), dict(n_shared=-1), dict(top_k=9), dict(M=0), dict(x=None),
+               dict(y=None), *({n: None} for n, _ in hla.hla_moe_fp8._fields_[5:])):
+        assert moe(lib, **kw) == INVALID, kw
+    for kw in (dict(hidden=192), dict(inter=64), dict(top_k=17, n_experts=64), dict(n_experts=1024), dict(n_shared=17), dict(M=65),
+               dict(hidden=1 << 21)):
+        assert moe(lib, **kw) == UNSUPPORTED, kw
+    for kw in (dict(x=FAKE + 2), dict(residual=FAKE + 8), dict(y=FAKE + 2), dict(idx=FAKE + 4), dict(w=FAKE + 4), dict(ws=FAKE + 8),
+               *({n: FAKE + 4} for n, _ in hla.hla_moe_fp8._fields_[5:])):
+        assert moe(lib, **kw) == MISALIGNED, kw
+    for kw in (dict(ws=None), dict(n=1024)):
+        assert moe(lib, **kw) == WORKSPACE, kw
+
+
+def test_moe_workspace(lib):
+    L = hla.hla_moe_fp8(256, 128, 8, 2, 1)
+    sizes = [hla.moe_fp8_forward_workspace_size(L, M) for M in (1, 2, 16, 17, 33, 64)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    assert [hla.moe_fp8_forward_workspace_size(L, M) for M in (0, -1, 65)] == [0, 0, 0]
+    assert hla.moe_fp8_forward_workspace_size(hla.hla_moe_fp8(200, 128, 8, 2, 1), 4) == 0
 
 
 def test_quantize_refusals(lib):
