@@ -54,15 +54,23 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
     return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// The issuing warp runs converged and one elected lane issues: the operands stay in uniform registers, where a lane that
+// issues alone spends 90 cycles an instruction on moving them (128x128x32 takes 64).
 __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+__device__ __forceinline__ void umma_commit_elected(uint64_t *bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+        : "memory");
+}
 
-// D = A x B^T over one block of 128 along K (four instructions of 32).
+// D = A x B^T over one block of 128 along K (four instructions of 32); the whole warp.
 __device__ __forceinline__ void umma_block(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem, uint32_t idesc) {
     const uint64_t da = sw128_desc(a_smem), db = sw128_desc(b_smem);
 #pragma unroll
@@ -81,14 +89,27 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// A bounded wait: its first polls do not read the clock (a read of %globaltimer takes longer than most waits here).
 __device__ __forceinline__ bool fp8_wait(uint64_t *bar, uint32_t parity, int *status, uint64_t limit = kFp8WaitNs) {
+    const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (done) return true;
+    }
     return mbar_wait_for(bar, parity, limit, status);
 }
 
-// COLS consecutive 32-bit tensor-memory columns of this thread's lane, without waiting for them.
+// COLS consecutive 32-bit tensor-memory columns of this thread's lane; tmem_wait(v) before v is used: the values pass
+// through the wait, so that nothing which uses them moves ahead of it.
 template <int COLS>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[COLS]) {
-    static_assert(COLS == 8 || COLS == 16 || COLS % 32 == 0, "columns per load");
+    static_assert(COLS == 8 || COLS == 16 || COLS == 32, "columns per load");
     if constexpr (COLS == 8) {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
@@ -100,9 +121,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[COLS]) {
               "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
             : "r"(taddr));
     } else {
-#pragma unroll
-        for (int c = 0; c < COLS; c += 32) tmem_ld32(taddr + c, v + c);
+        tmem_ld32(taddr, v);
     }
+}
+template <int COLS>
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[COLS]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])::"memory");
+#pragma unroll
+    for (int c = 8; c < COLS; c += 8)
+        asm volatile("" : "+r"(v[c]), "+r"(v[c + 1]), "+r"(v[c + 2]), "+r"(v[c + 3]), "+r"(v[c + 4]), "+r"(v[c + 5]), "+r"(v[c + 6]), "+r"(v[c + 7])::"memory");
 }
 
 // Allocate / free `columns` (a power of two from 32) of tensor memory; one whole warp.
@@ -122,9 +149,21 @@ __device__ __forceinline__ float peer_float(const float *p, uint32_t rank) {
     uint32_t a;
     float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
     return v;
 }
+__device__ __forceinline__ float4 peer_float4(const float *p, uint32_t rank) {
+    uint32_t a;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+// The register share of a warpgroup (all four of its warps); a block's shares add up to what it was launched with.
+template <int N>
+__device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 // A barrier among `threads` threads of the block (whole warps).
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");

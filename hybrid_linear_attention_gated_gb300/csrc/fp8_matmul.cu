@@ -28,6 +28,7 @@ struct MatmulParams {
     const uint16_t *residual;
     void *y;
     int y_bf16;
+    int direct;                // rows of y keep 32-byte stores aligned
     int *status;
     int force_timeout;
 };
@@ -36,6 +37,27 @@ __device__ __forceinline__ void store_y(const MatmulParams &p, size_t at, float 
     if (p.residual) v += bf16_bits_to_float(p.residual[at]);
     if (p.y_bf16) static_cast<uint16_t *>(p.y)[at] = float_to_bf16_bits(v);
     else static_cast<float *>(p.y)[at] = v;
+}
+
+// Four columns of token m from a column that is a multiple of 4 on: one access where y's rows keep it aligned.
+__device__ __forceinline__ void store_y4(const MatmulParams &p, int m, int col, float4 v) {
+    const size_t at = (size_t)m * p.N + col;
+    if (p.N % 4 == 0) {
+        if (col >= p.N) return;
+        if (p.residual) {
+            const uint2 r = *reinterpret_cast<const uint2 *>(p.residual + at);
+            v.x += bf16_lo(r.x), v.y += bf16_hi(r.x), v.z += bf16_lo(r.y), v.w += bf16_hi(r.y);
+        }
+        if (p.y_bf16)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.y) + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at) = v;
+        return;
+    }
+    const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (col + j < p.N) store_y(p, at + j, x[j]);
 }
 
 // ----------------------------------------------------------------------------- up to 64 tokens
@@ -116,19 +138,19 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             tma_tile(sX + s * F::kTokenBytes, &tmX, (c0 + i) * kFp8Block, 0, &full[s]);
             issued = i + 1;
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         int i = 0;
         for (; i < n; ++i) {
             const int s = i % NS, b = i % NB;
-            if (i >= NB && !fp8_wait(&acc_empty[b], (i / NB - 1) & 1, p.status)) break;
-            if (!fp8_wait(&full[s], (i / NS) & 1, p.status)) break;
+            if (!__all_sync(~0u, (i < NB || fp8_wait(&acc_empty[b], (i / NB - 1) & 1, p.status)) && fp8_wait(&full[s], (i / NS) & 1, p.status)))
+                break;
             tc_fence_after();
             umma_block(tmem + b * NT, smem_u32(sW + s * kTileBytes), smem_u32(sX + s * F::kTokenBytes), idesc_e4m3(128, NT));
-            umma_commit(&empty[s]);
-            umma_commit(&acc_full[b]);
+            umma_commit_elected(&empty[s]);
+            umma_commit_elected(&acc_full[b]);
         }
-        *consumed_slot = i;
-        umma_commit(done);
+        if (lane == 0) *consumed_slot = i;
+        umma_commit_elected(done);
         if (!fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
     } else if (warp >= 2) {
         const int t = tid - 64, row = (warp & 3) * 32 + lane;  // a warp reads the quarter of the lanes of its number mod 4
@@ -150,20 +172,26 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             ok = __all_sync(~0u, ok && fp8_wait(&acc_full[b], (i / NB) & 1, p.status));
             if (!ok) continue;
             tc_fence_after();
-            uint32_t v[NT];
-            tmem_ld<NT>(my + b * NT, v);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[b]);
             const float *const sc = sScale + (i % kScaleChunk) * NT;
+            constexpr int C = NT < 32 ? NT : 32;
 #pragma unroll
-            for (int j = 0; j < NT; j += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(sc + j);
-                acc[j] = fmaf(__uint_as_float(v[j]), f.x, acc[j]);
-                acc[j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y, acc[j + 1]);
-                acc[j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z, acc[j + 2]);
-                acc[j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w, acc[j + 3]);
+            for (int c = 0; c < NT; c += C) {
+                uint32_t v[C];
+                tmem_ld<C>(my + b * NT + c, v);
+                tmem_wait(v);
+                if (c + C == NT) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[b]);
+                }
+#pragma unroll
+                for (int j = 0; j < C; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(sc + c + j);
+                    acc[c + j] = fmaf(__uint_as_float(v[j]), f.x, acc[c + j]);
+                    acc[c + j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y, acc[c + j + 1]);
+                    acc[c + j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z, acc[c + j + 2]);
+                    acc[c + j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w, acc[c + j + 3]);
+                }
             }
         }
         if (p.split == 1 && ok) {
@@ -188,12 +216,17 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             for (int j = 0; j < NT; ++j) sums[j * 128 + row] = acc[j];
         }
         cluster_sync();
-        for (int e = rank * kFewThreads + tid; e < p.M * 128; e += p.split * kFewThreads) {
+        for (int e = (rank * kFewThreads + tid) * 4; e < p.M * 128; e += p.split * kFewThreads * 4) {
             const int m = e >> 7, col = rb * 128 + (e & 127);
-            if (col >= p.N) continue;
-            float v = 0.f;
-            for (int r = 0; r < p.split; ++r) v += peer_float(sums + e, r);
-            store_y(p, (size_t)m * p.N + col, v);
+            float4 part[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < p.split) part[r] = peer_float4(sums + e, r);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < p.split) v.x += part[r].x, v.y += part[r].y, v.z += part[r].z, v.w += part[r].w;
+            store_y4(p, m, col, v);
         }
         cluster_sync();  // no CTA leaves while another reads its sums
     }
@@ -204,20 +237,25 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
 // ----------------------------------------------------------------------------- more tokens
 
-constexpr int kManyThreads = 320;  // copies, products, eight warps of sums
+constexpr int kManyThreads = 384;  // a warpgroup of copies and products, two of sums
 
 template <int NT>
 struct Many {
-    static constexpr int kStages = NT == 256 ? 4 : 3;  // 192 KB, or 96 KB for two CTAs to an SM
-    static constexpr int kCtas = NT == 256 ? 1 : 2;
+    static constexpr int kCols = NT / 2;                   // columns of a warpgroup
+    static constexpr int kStages = NT == 256 ? 4 : 6;      // 192 KB
+    static constexpr int kAcc = 512 / NT;                  // accumulators: all of tensor memory
+    // registers a thread: 168 at launch; 128 sums and 64 values on their way take more, which the first warpgroup leaves
+    static constexpr bool kShift = NT == 256;
+    static constexpr int kFewRegs = 56, kManyRegs = 224;
     static constexpr uint32_t kWeightBytes = NT * 128;
-    static constexpr int kHalf = NT / 2;               // columns per warp: two groups of four warps
-    static constexpr int kPad = 33;
-    static constexpr size_t kSums = 128 * (NT + 1) * 4;                  // of the join
+    static constexpr int kPitch = NT + 4;                  // floats of a row of the join
     static constexpr size_t kRing = kStages * (kTileBytes + kWeightBytes);
-    static constexpr size_t kOut = 8 * 16 * kPad * 4;                    // a warp's 16 rows x 32 columns on their way out
-    static constexpr size_t kSmem = 1024 + kRing + kOut + (2 * kStages + 5) * 8 + 16;
-    static_assert(kSums <= kRing, "the sums of the join take the place of the tiles");
+    static constexpr int kOutPitch = 33;
+    static constexpr size_t kOut = 8 * 16 * kOutPitch * 4; // a warp's 16 rows x 32 columns on their way out
+    static constexpr size_t kSmem = 1024 + kRing + kOut + (2 * kStages + 2 * kAcc + 1) * 8 + 16;
+    static_assert(128 * kPitch * 4 <= kRing, "the sums of the join take the place of the tiles");
+    static_assert(kSmem <= 227 * 1024, "one CTA to an SM");
+    static_assert(kFewRegs + 2 * kManyRegs <= 3 * 168, "shares of the registers at launch");
 };
 
 // Tiles in bands of 16 row tiles, down a band's columns: the 152 or 304 tiles in flight share their operands in L2.
@@ -230,11 +268,73 @@ __device__ __forceinline__ void tile_at(const MatmulParams &p, int t, int *rt, i
     *rt = first + r - *ct * rows;
 }
 
+// A thread's row of COLS columns, straight from registers: 32 bytes a store, whole sectors.
+__device__ __forceinline__ void st32b(void *p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+template <int COLS>
+__device__ __forceinline__ void store_row(const MatmulParams &p, size_t at, int columns, const float (&acc)[COLS]) {
+    if (p.y_bf16) {
+        uint16_t *const y = static_cast<uint16_t *>(p.y) + at;
+#pragma unroll
+        for (int c = 0; c < COLS; c += 16) {
+            if (c >= columns) break;
+            uint32_t r[8], w[8] = {};
+            if (p.residual) {
+                const uint4 a = ld_act_v4(p.residual + at + c), b = ld_act_v4(p.residual + at + c + 8);
+                w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                r[j] = p.residual ? pack_bf16x2(acc[c + 2 * j] + bf16_lo(w[j]), acc[c + 2 * j + 1] + bf16_hi(w[j]))
+                                  : pack_bf16x2(acc[c + 2 * j], acc[c + 2 * j + 1]);
+            st32b(y + c, r);
+        }
+    } else {
+        float *const y = static_cast<float *>(p.y) + at;
+#pragma unroll
+        for (int c = 0; c < COLS; c += 8) {
+            if (c >= columns) break;
+            uint32_t r[8];
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (p.residual) w = ld_act_v4(p.residual + at + c);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                r[j] = __float_as_uint(p.residual ? acc[c + j] + (j & 1 ? bf16_hi(x[j >> 1]) : bf16_lo(x[j >> 1])) : acc[c + j]);
+            st32b(y + c, r);
+        }
+    }
+}
+
+// This CTA's share of the tile's rows: the sums of the cluster's CTAs, in rank order.
 template <int NT>
-__global__ void __launch_bounds__(kManyThreads, Many<NT>::kCtas)
+__device__ __forceinline__ void join_tile(const MatmulParams &p, int unit, int rank, const float *sums) {
+    using F = Many<NT>;
+    int rt, ct;
+    tile_at(p, unit, &rt, &ct);
+    for (int e = rank * kManyThreads + threadIdx.x; e < 128 * (NT / 4); e += p.split * kManyThreads) {
+        const int r = e / (NT / 4), c = e % (NT / 4) * 4, tok = rt * 128 + r;
+        if (tok >= p.M) continue;
+        float4 part[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < p.split) part[k] = peer_float4(sums + r * F::kPitch + c, k);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < p.split) v.x += part[k].x, v.y += part[k].y, v.z += part[k].z, v.w += part[k].w;
+        store_y4(p, tok, ct * NT + c, v);
+    }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kManyThreads, 1)
     many_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const MatmulParams p) {
     using F = Many<NT>;
-    constexpr int NS = F::kStages, NB = 2;
+    constexpr int NS = F::kStages, NB = F::kAcc, COLS = F::kCols;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *const sX = smem, *const sW = smem + NS * kTileBytes;
@@ -242,7 +342,7 @@ __global__ void __launch_bounds__(kManyThreads, Many<NT>::kCtas)
     uint64_t *const full = reinterpret_cast<uint64_t *>(smem + F::kRing + F::kOut);
     uint64_t *const empty = full + NS, *const acc_full = empty + NS, *const acc_empty = acc_full + NB, *const done = acc_empty + NB;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-    int *const consumed_slot = reinterpret_cast<int *>(tmem_slot + 1);
+    int *const failed_slot = reinterpret_cast<int *>(tmem_slot + 1);
 
     if (p.force_timeout) {
         forced_timeout(done, p.status);
@@ -266,143 +366,158 @@ __global__ void __launch_bounds__(kManyThreads, Many<NT>::kCtas)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 1) tmem_alloc(tmem_slot, NB * NT);
+    if (warp == 1) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait_trigger();
 
-    long issued = 0;
-    float acc[F::kHalf];
-    bool ok = true;
-    const int half = warp >= 6;                               // which half of the columns
-    const int row = (warp & 3) * 32 + lane;                   // which token of the tile
-    if (warp == 0 && lane == 0) {
-        for (int t = unit; t < tiles && ok; t += units) {
-            int rt, ct;
-            tile_at(p, t, &rt, &ct);
-            for (int i = 0; i < n; ++i, ++issued) {
-                const int s = (int)(issued % NS);
-                if (issued >= NS && !(ok = fp8_wait(&empty[s], (uint32_t)(issued / NS - 1) & 1, p.status))) break;
-                mbar_expect_tx(&full[s], kTileBytes + F::kWeightBytes);
-                tma_tile(sX + s * kTileBytes, &tmX, (c0 + i) * kFp8Block, rt * 128, &full[s]);
-                tma_tile(sW + s * F::kWeightBytes, &tmW, (c0 + i) * kFp8Block, ct * NT, &full[s]);
+    const int group = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;  // which half of the columns, and which token of the tile
+    if (group < 0) {
+        if constexpr (F::kShift) registers_down<F::kFewRegs>();
+        int issued = 0, fails = 0;  // fills so far, up to multiples of 2 NS
+        if (warp == 0 && lane == 0) {
+            bool ok = true;
+            int s = 0, turn = 0;    // the stage, and how often the ring went round
+            for (int t = unit; t < tiles && ok; t += units) {
+                int rt, ct;
+                tile_at(p, t, &rt, &ct);
+                for (int i = 0; i < n; ++i) {
+                    if (turn > 0 && !(ok = fp8_wait(&empty[s], (turn - 1) & 1, p.status))) break;
+                    mbar_expect_tx(&full[s], kTileBytes + F::kWeightBytes);
+                    tma_tile(sX + s * kTileBytes, &tmX, (c0 + i) * kFp8Block, rt * 128, &full[s]);
+                    tma_tile(sW + s * F::kWeightBytes, &tmW, (c0 + i) * kFp8Block, ct * NT, &full[s]);
+                    if (++s == NS) s = 0, ++turn;
+                }
+            }
+            issued = turn > 1 ? (turn & 1 ? NS : 2 * NS) + s : turn * NS + s;
+        } else if (warp == 1) {
+            bool ok = true;
+            int s = 0, ring = 0, b = 0, turn = 0;  // stage and its parity, accumulator and how often it was used
+            for (int t = unit; t < tiles && ok; t += units)
+                for (int i = 0; i < n; ++i) {
+                    ok = __all_sync(~0u, (turn == 0 || fp8_wait(&acc_empty[b], (turn - 1) & 1, p.status)) && fp8_wait(&full[s], ring, p.status));
+                    if (!ok) break;
+                    tc_fence_after();
+                    umma_block(tmem + b * NT, smem_u32(sX + s * kTileBytes), smem_u32(sW + s * F::kWeightBytes), idesc_e4m3(128, NT));
+                    umma_commit_elected(&empty[s]);
+                    umma_commit_elected(&acc_full[b]);
+                    if (++s == NS) s = 0, ring ^= 1;
+                    if (++b == NB) b = 0, ++turn;
+                }
+            if (lane == 0) *failed_slot = !ok;
+            umma_commit_elected(done);
+            if (!fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
+        }
+        __syncwarp();
+        named_sync(1, 128);
+        fails = *failed_slot;
+        if (tid == 0 && fails) {
+            // after a wait that gave up: the last fill of each stage may be waited for by no product
+            for (int s = 0; s < NS; ++s) {
+                if (issued <= s) continue;
+                const int f = issued - 1 - (issued - 1 - s) % NS;
+                if (!fp8_wait(&full[s], f / NS & 1, p.status)) fp8_wait(&full[s], f / NS & 1, p.status, 8 * kFp8WaitNs);
             }
         }
-    } else if (warp == 1 && lane == 0) {
-        long g = 0;
-        for (int t = unit; t < tiles && ok; t += units)
-            for (int i = 0; i < n; ++i, ++g) {
-                const int s = (int)(g % NS), b = (int)(g % NB);
-                if (g >= NB && !(ok = fp8_wait(&acc_empty[b], (uint32_t)(g / NB - 1) & 1, p.status))) break;
-                if (!(ok = fp8_wait(&full[s], (uint32_t)(g / NS) & 1, p.status))) break;
-                tc_fence_after();
-                umma_block(tmem + b * NT, smem_u32(sX + s * kTileBytes), smem_u32(sW + s * F::kWeightBytes), idesc_e4m3(128, NT));
-                umma_commit(&empty[s]);
-                umma_commit(&acc_full[b]);
-            }
-        *consumed_slot = (int)(g % (2 * NS)) | (int)(ok ? 0 : 1 << 30);
-        umma_commit(done);
-        if (!fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
-    } else if (warp >= 2) {
-        const uint32_t my = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * F::kHalf;
-        long g = 0;
+        __syncwarp();
+        __syncthreads();
+        if (p.split > 1) {
+            cluster_sync();
+            join_tile<NT>(p, unit, rank, reinterpret_cast<const float *>(smem));
+            cluster_sync();
+        }
+    } else {
+        if constexpr (F::kShift) registers_up<F::kManyRegs>();
+        const uint32_t my = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * COLS;
+        constexpr int C = 32;
+        float acc[COLS];
+        bool ok = true;
+        int b = 0, ring = 0;
         for (int t = unit; t < tiles && ok; t += units) {
             int rt, ct;
             tile_at(p, t, &rt, &ct);
-            const int m = rt * 128 + row;
-            int wb = (ct * NT + half * F::kHalf) >> 7;
-            const int last_wb = (p.N - 1) >> 7;
-            if (wb > last_wb) wb = last_wb;  // columns behind the last: their values are not stored
+            const int m = rt * 128 + row, n0 = ct * NT + group * COLS;
+            const int last_wb = (p.N - 1) >> 7, wb = (n0 >> 7) < last_wb ? n0 >> 7 : last_wb;  // columns behind the last are not stored
             const float *const xs = p.xs + (size_t)(m < p.M ? m : p.M - 1) * p.KB + c0, *const ws = p.ws + (size_t)wb * p.KB + c0;
 #pragma unroll
-            for (int j = 0; j < F::kHalf; ++j) acc[j] = 0.f;
+            for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
             float sx = xs[0], sw = ws[0];
-            for (int i = 0; i < n; ++i, ++g) {
-                const float sc = sx * sw;
-                if (i + 1 < n) {  // the next block's scales are on their way during this one
-                    sx = xs[i + 1];
-                    sw = ws[i + 1];
-                }
-                const int b = (int)(g % NB);
-                ok = __all_sync(~0u, fp8_wait(&acc_full[b], (uint32_t)(g / NB) & 1, p.status));
+            for (int i = 0; i < n; ++i) {
+                const float nx = i + 1 < n ? xs[i + 1] : 0.f, nw = i + 1 < n ? ws[i + 1] : 0.f;  // on their way during this block
+                ok = __all_sync(~0u, fp8_wait(&acc_full[b], ring, p.status));
                 if (!ok) break;
                 tc_fence_after();
+                const float sc = sx * sw;
+                uint32_t v[2][C];
+                tmem_ld<C>(my + b * NT, v[0]);
 #pragma unroll
-                for (int c = 0; c < F::kHalf; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld<32>(my + b * NT + c, v);
-                    tmem_wait_ld();
-                    if (c + 32 == F::kHalf) {
+                for (int c = 0; c < COLS / C; ++c) {
+                    tmem_wait(v[c & 1]);
+                    if (c + 1 < COLS / C) {
+                        tmem_ld<C>(my + b * NT + (c + 1) * C, v[(c + 1) & 1]);
+                    } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&acc_empty[b]);
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(v[j]), sc, acc[c + j]);
+                    for (int j = 0; j < C; ++j) acc[c * C + j] = fmaf(__uint_as_float(v[c & 1][j]), sc, acc[c * C + j]);
                 }
+                if (++b == NB) b = 0, ring ^= 1;
+                sx = nx;
+                sw = nw;
             }
             if (!ok || p.split > 1) continue;
-            // out through shared memory, 16 rows x 32 columns a warp at a time: a row's 32 columns leave together
-            float *const out = sOut + (warp - 2) * 16 * F::kPad;
-            const int n0 = ct * NT + half * F::kHalf;
+            if (p.direct) {
+                if (m < p.M && n0 < p.N) store_row(p, (size_t)m * p.N + n0, p.N - n0, acc);
+                continue;
+            }
+            // rows that keep no alignment leave through shared memory, 16 rows x 32 columns a warp at a time
+            float *const out = sOut + (warp - 4) * 16 * F::kOutPitch;
 #pragma unroll
-            for (int c = 0; c < F::kHalf; c += 32)
+            for (int c = 0; c < COLS; c += 32)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     __syncwarp();
                     if (lane >> 4 == h) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) out[(lane & 15) * F::kPad + j] = acc[c + j];
+                        for (int j = 0; j < 32; ++j) out[(lane & 15) * F::kOutPitch + j] = acc[c + j];
                     }
                     __syncwarp();
-                    const int col = n0 + c + lane;
+                    const int col = n0 + c + lane, tok = rt * 128 + (warp & 3) * 32 + h * 16;
                     if (col < p.N) {
-#pragma unroll 4
-                        for (int r = 0; r < 16; ++r) {
-                            const int tok = rt * 128 + (warp & 3) * 32 + h * 16 + r;
-                            if (tok < p.M) store_y(p, (size_t)tok * p.N + col, out[r * F::kPad + lane]);
-                        }
+                        const size_t at = (size_t)tok * p.N + col;
+                        float r[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            r[k] = p.residual && tok + k < p.M ? bf16_bits_to_float(p.residual[at + (size_t)k * p.N]) : 0.f;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (tok + k < p.M) {
+                                const float o = out[k * F::kOutPitch + lane] + r[k];
+                                if (p.y_bf16) static_cast<uint16_t *>(p.y)[at + (size_t)k * p.N] = float_to_bf16_bits(o);
+                                else static_cast<float *>(p.y)[at + (size_t)k * p.N] = o;
+                            }
                     }
                 }
         }
-    }
-    __syncwarp();
-    __syncthreads();
-    if (tid == 0 && (*consumed_slot >> 30)) {
-        // after a wait that gave up: at most one fill per stage is waited for by no product
-        for (int s = 0; s < NS; ++s) {
-            // the last fill of stage s, if any, has index (issued - 1) - ((issued - 1 - s) mod NS)
-            if (issued <= s) continue;
-            const long f = issued - 1 - (issued - 1 - s) % NS;
-            if (!fp8_wait(&full[s], (uint32_t)(f / NS) & 1, p.status)) fp8_wait(&full[s], (uint32_t)(f / NS) & 1, p.status, 8 * kFp8WaitNs);
-        }
-    }
-    __syncwarp();
-    __syncthreads();
-    if (p.split > 1) {
-        // one tile per cluster; the tiles of the ring are used up: their place takes the sums [token][NT + 1]
-        float *const sums = reinterpret_cast<float *>(smem);
-        if (warp >= 2) {
+        __syncwarp();
+        __syncthreads();
+        if (p.split > 1) {
+            // one tile per cluster; the tiles of the ring are used up: their place takes the sums, a row per token
+            float *const sums = reinterpret_cast<float *>(smem) + row * F::kPitch + group * COLS;
 #pragma unroll
-            for (int j = 0; j < F::kHalf; ++j) sums[row * (NT + 1) + half * F::kHalf + j] = acc[j];
+            for (int j = 0; j < COLS; j += 4) *reinterpret_cast<float4 *>(sums + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+            cluster_sync();
+            join_tile<NT>(p, unit, rank, reinterpret_cast<const float *>(smem));
+            cluster_sync();
         }
-        cluster_sync();
-        int rt, ct;
-        tile_at(p, unit, &rt, &ct);
-        for (int e = rank * kManyThreads + tid; e < 128 * NT; e += p.split * kManyThreads) {
-            const int r = e / NT, c = e - r * NT, tok = rt * 128 + r, col = ct * NT + c;
-            if (tok >= p.M || col >= p.N) continue;
-            float v = 0.f;
-            for (int k = 0; k < p.split; ++k) v += peer_float(sums + r * (NT + 1) + c, k);
-            store_y(p, (size_t)tok * p.N + col, v);
-        }
-        cluster_sync();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_free(tmem, NB * NT);
+    if (warp == 1) tmem_free(tmem, 512);
 }
 
 // ----------------------------------------------------------------------------- host
@@ -425,9 +540,10 @@ cudaError_t launch_many(MatmulParams p, const void *x, const void *W, cudaStream
     if (e != cudaSuccess) return e;
     CUtensorMap mw, mx;
     if (!byte_tile_map(&mw, W, p.N, p.K, NT) || !byte_tile_map(&mx, x, p.M, p.K, 128)) return cudaErrorInvalidValue;
+    p.direct = p.N % 16 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 31) == 0;
     p.row_tiles = (p.M + 127) / 128;
     p.col_tiles = (p.N + NT - 1) / NT;
-    const long tiles = (long)p.row_tiles * p.col_tiles, slots = (long)Many<NT>::kCtas * sm_count();
+    const long tiles = (long)p.row_tiles * p.col_tiles, slots = (long)1 * sm_count();
     const long grid = p.split > 1 ? tiles * p.split : tiles < slots ? tiles : slots;
     return launch_kernel_as(many_kernel<NT>, dim3((unsigned)grid), dim3(kManyThreads), Many<NT>::kSmem, st, p.split, false, mx, mw, p);
 }
@@ -469,7 +585,7 @@ extern "C" int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_
     } else {
         const long rows = (M + 127) / 128, wide = rows * ((N + 255) / 256);
         const bool use_wide = wide >= sms;
-        p.split = use_wide ? 1 : split_of(rows * ((N + 127) / 128), p.KB, 2 * sms, 4);
+        p.split = use_wide ? 1 : split_of(rows * ((N + 127) / 128), p.KB, sms, 4);
         set_variant("fp8_matmul<tile128x%d,split%d>", use_wide ? 256 : 128, p.split);
         ce = use_wide ? launch_many<256>(p, x, W, st) : launch_many<128>(p, x, W, st);
     }

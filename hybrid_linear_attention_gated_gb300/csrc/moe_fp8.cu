@@ -448,34 +448,35 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             tokens(s);
             ++issued;
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ---- products
         bool ok = true;
-        long g = 0, slot = 0;
-        for (long t = a0; t < a1; ++t, ++g, slot += 2) {
-            const int b = (int)(g % NB), s = (int)(slot % NS);
-            if (g >= NB && !(ok = fp8_wait(&acc_empty[b], (uint32_t)(g / NB - 1) & 1, p.status))) break;
-            if (!(ok = fp8_wait(&full[s], (uint32_t)(slot / NS) & 1, p.status))) break;
+        int s = 0, ring = 0, b = 0, turn = 0;  // slot and its parity, accumulator and how often it was used
+        for (long t = a0; t < a1; ++t) {
+            ok = __all_sync(~0u, (turn == 0 || fp8_wait(&acc_empty[b], (turn - 1) & 1, p.status)) && fp8_wait(&full[s], ring, p.status) &&
+                                     fp8_wait(&full[s + 1], ring, p.status));
+            if (!ok) break;
             tc_fence_after();
             umma_block(tmem + b * 2 * NT, smem_u32(sA + s * F::kTile), smem_u32(sB + s * F::kTokens), idesc_e4m3(128, NT));
-            if (!(ok = fp8_wait(&full[s + 1], (uint32_t)(slot / NS) & 1, p.status))) break;
-            tc_fence_after();
             umma_block(tmem + b * 2 * NT + NT, smem_u32(sA + (s + 1) * F::kTile), smem_u32(sB + s * F::kTokens), idesc_e4m3(128, NT));
-            umma_commit(&empty[s]);
-            umma_commit(&empty[s + 1]);
-            umma_commit(&acc_full[b]);
+            umma_commit_elected(&empty[s]);
+            umma_commit_elected(&empty[s + 1]);
+            umma_commit_elected(&acc_full[b]);
+            if ((s += 2) == NS) s = 0, ring ^= 1;
+            if (++b == NB) b = 0, ++turn;
         }
-        for (long t = b0; t < b1 && ok; ++t, ++g, ++slot) {
-            const int b = (int)(g % NB), s = (int)(slot % NS);
-            if (g >= NB && !(ok = fp8_wait(&acc_empty[b], (uint32_t)(g / NB - 1) & 1, p.status))) break;
-            if (!(ok = fp8_wait(&full[s], (uint32_t)(slot / NS) & 1, p.status))) break;
+        for (long t = b0; t < b1 && ok; ++t) {
+            ok = __all_sync(~0u, (turn == 0 || fp8_wait(&acc_empty[b], (turn - 1) & 1, p.status)) && fp8_wait(&full[s], ring, p.status));
+            if (!ok) break;
             tc_fence_after();
             umma_block(tmem + b * 2 * NT, smem_u32(sA + s * F::kTile), smem_u32(sB + s * F::kTokens), idesc_e4m3(128, NT));
-            umma_commit(&empty[s]);
-            umma_commit(&acc_full[b]);
+            umma_commit_elected(&empty[s]);
+            umma_commit_elected(&acc_full[b]);
+            if (++s == NS) s = 0, ring ^= 1;
+            if (++b == NB) b = 0, ++turn;
         }
-        s_int[1] = ok;
-        umma_commit(done);
+        if (lane == 0) s_int[1] = ok;
+        umma_commit_elected(done);
         if (!fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
     } else if (warp >= kSumWarp0) {
         // ---- sums: group `grp` of four warps has tokens [grp * H, grp * H + H) of every weight row
@@ -531,7 +532,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                     uint32_t vg[H], vu[H];
                     tmem_ld<H>(my + b * 2 * NT, vg);
                     tmem_ld<H>(my + b * 2 * NT + NT, vu);
-                    tmem_wait_ld();
+                    tmem_wait(vg);
+                    tmem_wait(vu);
                     const float *const sc = sS + s * NT + m0;
 #pragma unroll
                     for (int j = 0; j < H; j += 4) {
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                 if (ready(b, s)) {
                     uint32_t v[H];
                     tmem_ld<H>(my + b * 2 * NT, v);
-                    tmem_wait_ld();
+                    tmem_wait(v);
                     const float *const sc = sS + s * NT + m0;
 #pragma unroll
                     for (int j = 0; j < H; j += 4) {
