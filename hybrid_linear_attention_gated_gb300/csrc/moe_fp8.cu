@@ -176,9 +176,10 @@ __global__ void __launch_bounds__(kPrepThreads) __cluster_dims__(kPrepCluster, 1
 constexpr int kMoeThreads = 384;    // copies, products, two warps of the choice only, two groups of four warps of sums
 constexpr int kSumThreads = 256;
 constexpr int kSumWarp0 = 4;
+constexpr int kSparse = 0x8000;     // of a unit's entry: few tokens chose it
 
 struct MoeMaps {
-    CUtensorMap x, h, gate, up, down, sgate, sup, sdown;
+    CUtensorMap x, h, hfew, gate, up, down, sgate, sup, sdown;
 };
 
 struct MoeParams {
@@ -198,17 +199,22 @@ struct MoeParams {
 
 template <int NT>
 struct Moe {
-    static constexpr int kSlots = NT == 16 ? 12 : NT == 32 ? 10 : 8;  // even: gate and up tiles alternate
+    static constexpr int kSlots = NT == 16 ? 10 : NT == 32 ? 8 : 7;
     static constexpr int kAcc = 4;                                    // accumulators of 2 NT columns
     static constexpr uint32_t kTile = 128 * 128, kTokens = NT * 128, kScales = NT * 4;
     static constexpr uint32_t kColumns = kAcc * 2 * NT;
-    static constexpr int kHalf = NT / 2;                              // tokens of a group of four warps
-    static constexpr size_t kTables = NT * kMaxTopK * 8 + kMaxExperts * 2 + kMaxExperts / 8 + NT * 4 + NT * 16 + 64;
+    // 64 tokens: an expert that at most 8 tokens of each half of the batch chose is sparse: its sums and its rows of h
+    // are the 16 positions of those tokens, not the 64 tokens
+    static constexpr bool kLists = NT == 64;
+    static constexpr int kSums = NT == 16 ? 16 : 32;                  // of a thread, for gate and for up
+    static constexpr size_t kExchange = (NT == 16 ? 16 : 32) * 1024;  // sums on their way between the groups; y's sums of 64 tokens
+    static constexpr size_t kTables = NT * kMaxTopK * 8 + kMaxExperts * 2 + kMaxExperts * 8 + NT * 4 + NT * 16;
+    static constexpr size_t kSmem = 1024 + kSlots * (kTile + kTokens + kScales) + kExchange + (2 * kSlots + 2 * kAcc + 2) * 8 + 16 + kTables;
     static_assert((2 * kSlots + 2 * kAcc + 2) * 8 % 16 == 0 && NT % 4 == 0, "vectors of four in the tables");
-    static constexpr size_t kSmem = 1024 + kSlots * (kTile + kTokens + kScales) + (2 * kSlots + 2 * kAcc + 2) * 8 + 16 + kTables;
+    static_assert(kSmem <= 227 * 1024, "one CTA to an SM");
 };
 
-// A share of one phase: units of one block of K, [t0, t1) of T for this CTA among `ctas`.
+// A share of one phase: T units of one block of K over `ctas` CTAs, as equal as whole units can be.
 struct Share {
     long T;
     int ctas;
@@ -249,6 +255,16 @@ struct DownAt {
         }
     }
 };
+// A place in a ring and how often the ring has gone round.
+template <int N>
+struct Ring {
+    int s = 0, turn = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == N) s = 0, ++turn;
+    }
+    __device__ __forceinline__ uint32_t filled() const { return turn & 1; }            // parity of this use's completion
+    __device__ __forceinline__ uint32_t freed() const { return (turn - 1) & 1; }       // and of the one before, from the second use on
+};
 
 __device__ __forceinline__ uint32_t ordered(float v) {  // larger floats have larger keys; none is 0
     const uint32_t b = __float_as_uint(v), k = b & 0x80000000u ? ~b : b | 0x80000000u;
@@ -259,28 +275,32 @@ __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(
 // The k largest of a token's logits by one warp, ties to the lower index: lane j gets the jth index and its logit.
 template <int PER>
 __device__ __forceinline__ void choose(const float *logits, int E, int k, int lane, int *idx, float *logit) {
-    uint32_t key[PER];
+    uint32_t key[PER], top = 0;
+    int at = 0;  // the largest of this lane's own, the first of equal ones
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = i * 32 + lane;
         key[i] = e < E ? ordered(__ldcg(logits + e)) : 0u;
     }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (key[i] > top) top = key[i], at = i;
     for (int j = 0; j < k; ++j) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) top = max(top, key[i]);
         const uint32_t best = __reduce_max_sync(~0u, top);
-        uint32_t at = ~0u;
-#pragma unroll
-        for (int i = PER - 1; i >= 0; --i)
-            if (key[i] == best) at = i * 32 + lane;
-        at = __reduce_min_sync(~0u, at);
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (at == static_cast<uint32_t>(i * 32 + lane)) key[i] = 0u;
+        const uint32_t owners = __ballot_sync(~0u, top == best);
+        uint32_t e = at * 32 + lane;
+        if (owners & (owners - 1)) e = __reduce_min_sync(~0u, top == best ? e : ~0u);  // equal logits in several lanes
+        else e = __shfl_sync(~0u, e, __ffs(owners) - 1);
         if (lane == j) {
-            *idx = (int)at;
+            *idx = (int)e;
             *logit = unordered(best);
+        }
+        const bool mine = (e & 31) == lane;
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            key[i] &= mine && i == (int)(e >> 5) ? 0u : ~0u;
+            if (key[i] > top) top = key[i], at = i;
         }
     }
 }
@@ -291,23 +311,30 @@ __device__ __forceinline__ int load_acquire(const int *p) {
     return v;
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr));
+}
 
 template <int NT>
 __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_constant__ MoeMaps maps, const MoeParams p) {
     using F = Moe<NT>;
-    constexpr int NS = F::kSlots, NB = F::kAcc, H = F::kHalf;
+    constexpr int NS = F::kSlots, NB = F::kAcc, S = F::kSums, H = NT / 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *const sA = smem, *const sB = smem + NS * F::kTile;
     float *const sS = reinterpret_cast<float *>(sB + NS * F::kTokens);
-    uint64_t *const full = reinterpret_cast<uint64_t *>(sS + NS * NT);
+    float *const s_sums = sS + NS * NT;
+    uint64_t *const full = reinterpret_cast<uint64_t *>(s_sums + F::kExchange / 4);
     uint64_t *const empty = full + NS, *const acc_full = empty + NS, *const acc_empty = acc_full + NB, *const done = acc_empty + NB;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(done + 2);  // 16-byte aligned, as the tables behind it
-    int *const s_int = reinterpret_cast<int *>(tmem_slot + 1);       // units, products issued, last part?
-    float *const s_weight = reinterpret_cast<float *>(tmem_slot + 4);  // [NT] of the unit at hand, NaN where not chosen
-    float *const s_top = s_weight + NT;                               // [NT][4]
-    uint32_t *const s_active = reinterpret_cast<uint32_t *>(s_top + NT * 4);  // bit e: some token chose expert e
-    int *const s_idx = reinterpret_cast<int *>(s_active + kMaxExperts / 32);  // [NT][k]
+    int *const s_int = reinterpret_cast<int *>(tmem_slot + 1);           // active experts, products issued, last part?
+    float *const s_weight = reinterpret_cast<float *>(tmem_slot + 4);    // [NT] of the unit at hand, -1 where not chosen
+    float *const s_top = s_weight + NT;                                  // [NT][4]
+    unsigned long long *const s_mask = reinterpret_cast<unsigned long long *>(s_top + NT * 4);  // tokens that chose each expert
+    int *const s_idx = reinterpret_cast<int *>(s_mask + kMaxExperts);    // [M][k]
     float *const s_w = reinterpret_cast<float *>(s_idx + NT * kMaxTopK);
     uint16_t *const s_unit = reinterpret_cast<uint16_t *>(s_w + NT * kMaxTopK);  // routed units' experts
 
@@ -330,7 +357,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         fence_async();
     }
     if (warp == 1) tmem_alloc(tmem_slot, F::kColumns);
-    for (int i = tid; i < kMaxExperts / 32; i += kMoeThreads) s_active[i] = 0;
+    for (int i = tid; i < p.E; i += kMoeThreads) s_mask[i] = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -350,7 +377,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             const float w = score / sum;
             s_idx[m * p.k + lane] = idx;
             s_w[m * p.k + lane] = w;
-            atomicOr(&s_active[idx >> 5], 1u << (idx & 31));
+            atomicOr(&s_mask[idx], 1ull << m);
             if (blockIdx.x == 0) {
                 if (p.topk_idx) p.topk_idx[m * p.k + lane] = idx;
                 if (p.topk_w) p.topk_w[m * p.k + lane] = w;
@@ -358,19 +385,19 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         }
     }
     __syncthreads();
-    for (int e = tid; e < p.E; e += kMoeThreads) {
-        if (!(s_active[e >> 5] >> (e & 31) & 1)) continue;
-        int at = __popc(s_active[e >> 5] & ((1u << (e & 31)) - 1));
-        for (int i = 0; i < e >> 5; ++i) at += __popc(s_active[i]);
-        s_unit[at] = (uint16_t)e;
-    }
-    if (tid == 0) {
+    // units: the shared experts, then the active ones in order
+    if (warp == 0) {
         int n = 0;
-        for (int i = 0; i < (p.E + 31) / 32; ++i) n += __popc(s_active[i]);
-        s_int[0] = n;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const unsigned long long mask = e0 + lane < p.E ? s_mask[e0 + lane] : 0ull;
+            const uint32_t active = __ballot_sync(~0u, mask != 0);
+            const bool sparse = F::kLists && __popc((uint32_t)mask) <= 8 && __popc((uint32_t)(mask >> 32)) <= 8;
+            if (mask) s_unit[n + __popc(active & ((1u << lane) - 1))] = (uint16_t)(e0 + lane | (sparse ? kSparse : 0));
+            n += __popc(active);
+        }
+        if (lane == 0) s_int[0] = n;
     }
     __syncthreads();
-    // units: the shared experts, then the active ones in order
     const int U = s_int[0] + p.n_shared, G = gridDim.x, c = blockIdx.x;
     const int nI = p.I / 128, nR = p.Hd / 128, KB1 = p.Hd / kFp8Block, KB2 = p.I / kFp8Block;
     Share s1, s2;
@@ -381,53 +408,54 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     const long a0 = c < s1.ctas ? s1.start(c) : 0, a1 = c < s1.ctas ? s1.start(c + 1) : 0;
     const long b0 = c < s2.ctas ? s2.start(c) : 0, b1 = c < s2.ctas ? s2.start(c + 1) : 0;
     int *const barrier = p.count + 2 * G;
-    long issued = 0;  // slots filled
+    const auto shared_unit = [&](int u) { return u < p.n_shared; };
+    const auto expert_of = [&](int u) { return u < p.n_shared ? u : (int)s_unit[u - p.n_shared] & (kSparse - 1); };
+    const auto sparse_unit = [&](int u) { return F::kLists && u >= p.n_shared && (s_unit[u - p.n_shared] & kSparse) != 0; };
+    int issued = 0;  // slots filled, up to multiples of 2 NS
 
     if (warp == 0 && lane == 0) {
         // ---- copies
         bool ok = true;
+        Ring<NS> r;
         GateAt at;
         at.set(a0, nI, KB1);
         for (long t = a0; t < a1 && ok; ++t, at.next(nI, KB1)) {
-            const bool sh = at.u < p.n_shared;
-            const int row = (sh ? at.u : s_unit[at.u - p.n_shared]) * p.I + at.ib * 128, col = at.kb * kFp8Block;
+            const bool sh = shared_unit(at.u);
+            const int row = expert_of(at.u) * p.I + at.ib * 128, col = at.kb * kFp8Block;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int s = (int)(issued % NS);
-                if (issued >= NS && !(ok = fp8_wait(&empty[s], (uint32_t)(issued / NS - 1) & 1, p.status))) break;
-                mbar_expect_tx(&full[s], F::kTile + (half ? 0 : F::kTokens + F::kScales));
-                tma_tile(sA + s * F::kTile, half ? (sh ? &maps.sup : &maps.up) : (sh ? &maps.sgate : &maps.gate), col, row, &full[s]);
+                if (r.turn > 0 && !(ok = fp8_wait(&empty[r.s], r.freed(), p.status))) break;
+                mbar_expect_tx(&full[r.s], F::kTile + (half ? 0 : F::kTokens + F::kScales));
+                tma_tile(sA + r.s * F::kTile, half ? (sh ? &maps.sup : &maps.up) : (sh ? &maps.sgate : &maps.gate), col, row, &full[r.s]);
                 if (!half) {
-                    tma_tile(sB + s * F::kTokens, &maps.x, col, 0, &full[s]);
-                    bulk_g2s(sS + s * NT, p.xs + (size_t)at.kb * NT, F::kScales, &full[s]);
+                    tma_tile(sB + r.s * F::kTokens, &maps.x, col, 0, &full[r.s]);
+                    bulk_g2s(sS + r.s * NT, p.xs + (size_t)at.kb * NT, F::kScales, &full[r.s]);
                 }
-                ++issued;
+                r.next();
             }
         }
         // the first down tiles go out before the grid barrier, their tokens and scales after it
-        const long n2 = b1 - b0, first = issued;
+        const long n2 = b1 - b0;
         const int pre = (int)(n2 < NS ? n2 : NS);
         DownAt w, h;
         w.set(b0, U, KB2);
         h = w;
         const auto weights = [&](int s) {
-            const bool sh = w.u < p.n_shared;
-            mbar_expect_tx(&full[s], F::kTile + F::kTokens + F::kScales);
-            tma_tile(sA + s * F::kTile, sh ? &maps.sdown : &maps.down, w.kb * kFp8Block,
-                     (sh ? w.u : s_unit[w.u - p.n_shared]) * p.Hd + w.rb * 128, &full[s]);
+            mbar_expect_tx(&full[s], F::kTile + F::kScales + (sparse_unit(w.u) ? 16 * 128 : F::kTokens));
+            tma_tile(sA + s * F::kTile, shared_unit(w.u) ? &maps.sdown : &maps.down, w.kb * kFp8Block, expert_of(w.u) * p.Hd + w.rb * 128, &full[s]);
             w.next(U, KB2);
         };
         const auto tokens = [&](int s) {
-            tma_tile(sB + s * F::kTokens, &maps.h, h.kb * kFp8Block, h.u * NT, &full[s]);
+            tma_tile(sB + s * F::kTokens, sparse_unit(h.u) ? &maps.hfew : &maps.h, h.kb * kFp8Block, h.u * NT, &full[s]);
             bulk_g2s(sS + s * NT, p.hs + ((size_t)h.u * KB2 + h.kb) * NT, F::kScales, &full[s]);
             h.next(U, KB2);
         };
+        const Ring<NS> first = r;
         int sent = 0;
         for (; sent < pre && ok; ++sent) {
-            const long i = first + sent;
-            const int s = (int)(i % NS);
-            if (i >= NS && !(ok = fp8_wait(&empty[s], (uint32_t)(i / NS - 1) & 1, p.status))) break;
-            weights(s);
+            if (r.turn > 0 && !(ok = fp8_wait(&empty[r.s], r.freed(), p.status))) break;
+            weights(r.s);
+            r.next();
         }
         if (n2 > 0 && ok) {
             const uint64_t began = global_ns();
@@ -439,57 +467,66 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                 }
             fence_async();
         }
-        for (int i = 0; i < sent; ++i) tokens((int)((first + i) % NS));  // after a barrier that gave up, too: the fills complete
-        issued += sent;
+        Ring<NS> q = first;
+        for (int i = 0; i < sent; ++i, q.next()) tokens(q.s);  // after a barrier that gave up, too: the fills complete
         for (long t = sent; t < n2 && ok; ++t) {
-            const int s = (int)(issued % NS);
-            if (issued >= NS && !(ok = fp8_wait(&empty[s], (uint32_t)(issued / NS - 1) & 1, p.status))) break;
-            weights(s);
-            tokens(s);
-            ++issued;
+            if (r.turn > 0 && !(ok = fp8_wait(&empty[r.s], r.freed(), p.status))) break;
+            weights(r.s);
+            tokens(r.s);
+            r.next();
         }
+        issued = r.turn > 1 ? (r.turn & 1 ? NS : 2 * NS) + r.s : r.turn * NS + r.s;
     } else if (warp == 1) {
         // ---- products
         bool ok = true;
-        int s = 0, ring = 0, b = 0, turn = 0;  // slot and its parity, accumulator and how often it was used
+        Ring<NS> r;
+        Ring<NB> b;
         for (long t = a0; t < a1; ++t) {
-            ok = __all_sync(~0u, (turn == 0 || fp8_wait(&acc_empty[b], (turn - 1) & 1, p.status)) && fp8_wait(&full[s], ring, p.status) &&
-                                     fp8_wait(&full[s + 1], ring, p.status));
+            const int s = r.s;
+            ok = (b.turn == 0 || fp8_wait(&acc_empty[b.s], b.freed(), p.status)) && fp8_wait(&full[s], r.filled(), p.status);
+            r.next();
+            ok = __all_sync(~0u, ok && fp8_wait(&full[r.s], r.filled(), p.status));
             if (!ok) break;
             tc_fence_after();
-            umma_block(tmem + b * 2 * NT, smem_u32(sA + s * F::kTile), smem_u32(sB + s * F::kTokens), idesc_e4m3(128, NT));
-            umma_block(tmem + b * 2 * NT + NT, smem_u32(sA + (s + 1) * F::kTile), smem_u32(sB + s * F::kTokens), idesc_e4m3(128, NT));
+            umma_block(tmem + b.s * 2 * NT, smem_u32(sA + s * F::kTile), smem_u32(sB + s * F::kTokens), idesc_e4m3(128, NT));
+            umma_block(tmem + b.s * 2 * NT + NT, smem_u32(sA + r.s * F::kTile), smem_u32(sB + s * F::kTokens), idesc_e4m3(128, NT));
             umma_commit_elected(&empty[s]);
-            umma_commit_elected(&empty[s + 1]);
-            umma_commit_elected(&acc_full[b]);
-            if ((s += 2) == NS) s = 0, ring ^= 1;
-            if (++b == NB) b = 0, ++turn;
+            umma_commit_elected(&empty[r.s]);
+            umma_commit_elected(&acc_full[b.s]);
+            r.next();
+            b.next();
         }
-        for (long t = b0; t < b1 && ok; ++t) {
-            ok = __all_sync(~0u, (turn == 0 || fp8_wait(&acc_empty[b], (turn - 1) & 1, p.status)) && fp8_wait(&full[s], ring, p.status));
+        DownAt at;
+        at.set(b0, U, KB2);
+        for (long t = b0; t < b1 && ok; ++t, at.next(U, KB2)) {
+            ok = __all_sync(~0u, (b.turn == 0 || fp8_wait(&acc_empty[b.s], b.freed(), p.status)) && fp8_wait(&full[r.s], r.filled(), p.status));
             if (!ok) break;
             tc_fence_after();
-            umma_block(tmem + b * 2 * NT, smem_u32(sA + s * F::kTile), smem_u32(sB + s * F::kTokens), idesc_e4m3(128, NT));
-            umma_commit_elected(&empty[s]);
-            umma_commit_elected(&acc_full[b]);
-            if (++s == NS) s = 0, ring ^= 1;
-            if (++b == NB) b = 0, ++turn;
+            umma_block(tmem + b.s * 2 * NT, smem_u32(sA + r.s * F::kTile), smem_u32(sB + r.s * F::kTokens),
+                       sparse_unit(at.u) ? idesc_e4m3(128, 16) : idesc_e4m3(128, NT));
+            umma_commit_elected(&empty[r.s]);
+            umma_commit_elected(&acc_full[b.s]);
+            r.next();
+            b.next();
         }
         if (lane == 0) s_int[1] = ok;
         umma_commit_elected(done);
         if (!fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
     } else if (warp >= kSumWarp0) {
-        // ---- sums: group `grp` of four warps has tokens [grp * H, grp * H + H) of every weight row
-        const int grp = warp >= kSumWarp0 + 4, q4 = warp & 3, row = q4 * 32 + lane, m0 = grp * H;
+        // ---- sums, each thread of one weight row.  Up to 32 tokens, and for the gate and up products of a sparse unit, the two
+        // groups of four warps take every other block of K and all tokens (or positions), and exchange halves of
+        // their sums where a segment ends; otherwise each takes its half of the tokens of every block.
+        const int grp = warp >= kSumWarp0 + 4, q4 = warp & 3, row = q4 * 32 + lane;
         const int st = tid - kSumWarp0 * 32;
-        const uint32_t my = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + m0;
-        constexpr size_t kPart = 2 * NT * 128;  // floats of a part
+        const uint32_t my = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+        constexpr size_t kPart = 2 * NT * 128;  // floats of a part: gate and up, position, row
         bool ok = true;
-        long g = 0, slot = 0;
-        // wait for an accumulator and the scales that came with it
-        const auto ready = [&](int b, int s) {
-            ok = __all_sync(~0u, ok && fp8_wait(&acc_full[b], (uint32_t)(g / NB) & 1, p.status) &&
-                                     fp8_wait(&full[s], (uint32_t)(slot / NS) & 1, p.status));
+        Ring<NS> r;
+        Ring<NB> b;
+        int turn = 0;  // which group's block the next one is
+        // waits for an accumulator and the scales that came with it
+        const auto ready = [&]() {
+            ok = __all_sync(~0u, ok && fp8_wait(&acc_full[b.s], b.filled(), p.status) && fp8_wait(&full[r.s], r.filled(), p.status));
             tc_fence_after();
             return ok;
         };
@@ -506,63 +543,132 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             return s_int[2] != 0;
         };
         {
-            float ga[H], ua[H];
+            float ga[S], ua[S];
             GateAt at;
             at.set(a0, nI, KB1);
-            long begin = a0;  // of the segment
+            long begin = a0;           // of the segment
+            bool sparse = false, both = false;
+            uint32_t lists[2] = {0u, 0u};  // tokens of a sparse unit, by half of the batch
             const auto scales_at = [&](const GateAt &x, float *sg, float *su) {
-                const bool sh = x.u < p.n_shared;
-                const size_t i = ((size_t)(sh ? x.u : s_unit[x.u - p.n_shared]) * nI + x.ib) * KB1 + x.kb;
-                *sg = __ldg((sh ? p.sgate_s : p.gate_s) + i);
-                *su = __ldg((sh ? p.sup_s : p.up_s) + i);
+                const size_t i = ((size_t)expert_of(x.u) * nI + x.ib) * KB1 + x.kb;
+                *sg = __ldg((shared_unit(x.u) ? p.sgate_s : p.gate_s) + i);
+                *su = __ldg((shared_unit(x.u) ? p.sup_s : p.up_s) + i);
             };
             float sg = 0.f, su = 0.f;
             if (a0 < a1) scales_at(at, &sg, &su);
-            for (long t = a0; t < a1; ++t, ++g, slot += 2) {
+            for (long t = a0; t < a1; ++t, turn ^= 1) {
                 if (t == begin) {
 #pragma unroll
-                    for (int j = 0; j < H; ++j) ga[j] = ua[j] = 0.f;
+                    for (int j = 0; j < S; ++j) ga[j] = ua[j] = 0.f;
+                    sparse = sparse_unit(at.u);
+                    both = F::kLists && !sparse;
+                    if (sparse) {
+                        const unsigned long long mask = s_mask[expert_of(at.u)];
+                        lists[0] = (uint32_t)mask;
+                        lists[1] = (uint32_t)(mask >> 32);
+                    }
                 }
                 GateAt nx = at;
                 nx.next(nI, KB1);
                 float ng = 0.f, nu = 0.f;
                 if (t + 1 < a1) scales_at(nx, &ng, &nu);
-                const int b = (int)(g % NB), s = (int)(slot % NS);
-                if (ready(b, s)) {
-                    uint32_t vg[H], vu[H];
-                    tmem_ld<H>(my + b * 2 * NT, vg);
-                    tmem_ld<H>(my + b * 2 * NT + NT, vu);
-                    tmem_wait(vg);
-                    tmem_wait(vu);
-                    const float *const sc = sS + s * NT + m0;
+                if ((both || turn == grp) && ready()) {
+                    const uint32_t acc = my + b.s * 2 * NT;
+                    const float *const sc = sS + r.s * NT;
+                    if (sparse) {
+                        uint32_t vg[16], vu[16];
+                        float x[16];
 #pragma unroll
-                    for (int j = 0; j < H; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(sc + j);
-                        const float x[4] = {f.x, f.y, f.z, f.w};
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t left = lists[h];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            ga[j + i] = fmaf(__uint_as_float(vg[j + i]), x[i] * sg, ga[j + i]);
-                            ua[j + i] = fmaf(__uint_as_float(vu[j + i]), x[i] * su, ua[j + i]);
+                            for (int j = 0; j < 8; ++j) {
+                                if (left) {
+                                    const int m = h * 32 + __ffs(left) - 1;
+                                    tmem_ld1(acc + m, vg[h * 8 + j]);
+                                    tmem_ld1(acc + NT + m, vu[h * 8 + j]);
+                                    x[h * 8 + j] = sc[m];
+                                    left &= left - 1;
+                                } else {
+                                    vg[h * 8 + j] = vu[h * 8 + j] = 0u;
+                                    x[h * 8 + j] = 0.f;
+                                }
+                            }
+                        }
+                        tmem_wait(vg);
+                        tmem_wait(vu);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            ga[j] = fmaf(__uint_as_float(vg[j]), x[j] * sg, ga[j]);
+                            ua[j] = fmaf(__uint_as_float(vu[j]), x[j] * su, ua[j]);
+                        }
+                    } else {
+                        // columns of this thread: all NT, or its half of 64; C of gate and of up at a time
+                        constexpr int C = 16, N = F::kLists ? H : NT;
+                        const int m0 = F::kLists ? grp * H : 0;
+#pragma unroll
+                        for (int cc = 0; cc < N; cc += C) {
+                            uint32_t vg[C], vu[C];
+                            tmem_ld<C>(acc + m0 + cc, vg);
+                            tmem_ld<C>(acc + NT + m0 + cc, vu);
+                            tmem_wait(vg);
+                            tmem_wait(vu);
+#pragma unroll
+                            for (int j = 0; j < C; j += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(sc + m0 + cc + j);
+                                const float x[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    ga[cc + j + i] = fmaf(__uint_as_float(vg[j + i]), x[i] * sg, ga[cc + j + i]);
+                                    ua[cc + j + i] = fmaf(__uint_as_float(vu[j + i]), x[i] * su, ua[cc + j + i]);
+                                }
+                            }
                         }
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&acc_empty[b]);
-                        mbar_arrive(&empty[s]);
-                        mbar_arrive(&empty[s + 1]);
+                        const uint32_t n = both ? 1 : 2;
+                        Ring<NS> up = r;
+                        up.next();
+                        mbar_arrive_n(&acc_empty[b.s], n);
+                        mbar_arrive_n(&empty[r.s], n);
+                        mbar_arrive_n(&empty[up.s], n);
                     }
                 }
+                r.next();
+                r.next();
+                b.next();
                 if (at.kb == KB1 - 1 || t + 1 == a1) {
-                    // the segment ends: a whole item, or a part of one
+                    // the segment ends: a whole item, or a part of one.  Its positions: `half` for each group.
+                    const int half = sparse ? 8 : H;
+                    if (!both) {
+#pragma unroll
+                        for (int j = 0; j < S / 2; ++j) {
+                            if (j >= half) break;
+                            const int o = j + (S == 32 && !F::kLists ? 16 : 8);
+                            s_sums[(grp * half + j) * 128 + row] = grp ? ga[j] : ga[o];
+                            s_sums[((2 + grp) * half + j) * 128 + row] = grp ? ua[j] : ua[o];
+                        }
+                        named_sync(1, kSumThreads);
+#pragma unroll
+                        for (int j = 0; j < S / 2; ++j) {
+                            if (j >= half) break;
+                            const int o = j + (S == 32 && !F::kLists ? 16 : 8);
+                            ga[j] = (grp ? ga[o] : ga[j]) + s_sums[((grp ^ 1) * half + j) * 128 + row];
+                            ua[j] = (grp ? ua[o] : ua[j]) + s_sums[((2 + (grp ^ 1)) * half + j) * 128 + row];
+                        }
+                    }
+                    const int p0 = grp * half;
                     const long i0 = t - at.kb, i1 = i0 + KB1;
                     bool whole = begin == i0 && t + 1 == i1;
                     if (!whole) {
                         float *const mine = p.part + ((size_t)c * 2 + (begin != a0)) * kPart;
 #pragma unroll
                         for (int j = 0; j < H; ++j) {
-                            __stcg(mine + (m0 + j) * 128 + row, ga[j]);
-                            __stcg(mine + (NT + m0 + j) * 128 + row, ua[j]);
+                            if (j >= half) break;
+                            __stcg(mine + (p0 + j) * 128 + row, ga[j]);
+                            __stcg(mine + (NT + p0 + j) * 128 + row, ua[j]);
                         }
                         const int c0 = s1.owner(i0), c1 = s1.owner(i1 - 1);
                         if ((whole = last_part(p.count + c0, c1 - c0 + 1))) {
@@ -572,45 +678,54 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                                 const float *const their = p.part + ((size_t)k * 2 + (k == c0 && s1.start(c0) != i0)) * kPart;
 #pragma unroll
                                 for (int j = 0; j < H; ++j) {
-                                    ga[j] += __ldcg(their + (m0 + j) * 128 + row);
-                                    ua[j] += __ldcg(their + (NT + m0 + j) * 128 + row);
+                                    if (j >= half) break;
+                                    ga[j] += __ldcg(their + (p0 + j) * 128 + row);
+                                    ua[j] += __ldcg(their + (NT + p0 + j) * 128 + row);
                                 }
                             }
                         }
                     }
                     if (whole) {
                         // h of 128 columns: every token that chose this expert, its own scale, times its weight in the mixture
-                        const bool sh = at.u < p.n_shared;
-                        if (st < NT) {
-                            float w = sh ? 1.f : -1.f;  // -1: not chosen
-                            if (!sh && st < p.M) {
-                                const int e = s_unit[at.u - p.n_shared];
-                                for (int j = 0; j < p.k; ++j)
-                                    if (s_idx[st * p.k + j] == e) w = s_w[st * p.k + j];
+                        if (st < 2 * half) {
+                            int m = st;
+                            if (sparse) {
+                                uint32_t left = st < 8 ? lists[0] : lists[1];
+                                for (int j = 0; j < (st & 7); ++j) left &= left - 1;
+                                m = left ? (st >> 3) * 32 + __ffs(left) - 1 : p.M;
                             }
-                            s_weight[st] = st < p.M ? w : -1.f;
+                            float w = -1.f;  // not chosen
+                            if (m < p.M) {
+                                if (shared_unit(at.u)) w = 1.f;
+                                else
+                                    for (int j = 0; j < p.k; ++j)
+                                        if (s_idx[m * p.k + j] == expert_of(at.u)) w = s_w[m * p.k + j];
+                            }
+                            s_weight[st] = w;
                         }
                         named_sync(1, kSumThreads);
 #pragma unroll
                         for (int j = 0; j < H; ++j) {
-                            if (s_weight[m0 + j] == -1.f) continue;  // the same for the whole group
+                            if (j >= half) break;
+                            if (s_weight[p0 + j] == -1.f) continue;  // the same for the whole group
                             const float hv = silu_f(ga[j]) * ua[j];
                             ga[j] = hv;
                             const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(hv) & 0x7FFFFFFFu);
-                            if (lane == 0) s_top[(m0 + j) * 4 + q4] = __uint_as_float(top);
+                            if (lane == 0) s_top[(p0 + j) * 4 + q4] = __uint_as_float(top);
                         }
                         named_sync(2 + grp, 128);
 #pragma unroll
                         for (int j = 0; j < H; ++j) {
-                            const float w = s_weight[m0 + j];
-                            float *const hs = p.hs + ((size_t)at.u * KB2 + at.ib) * NT + m0 + j;
+                            if (j >= half) break;
+                            const float w = s_weight[p0 + j];
+                            float *const hs = p.hs + ((size_t)at.u * KB2 + at.ib) * NT + p0 + j;
                             if (w == -1.f) {
                                 if (row == 0) *hs = 0.f;
                                 continue;
                             }
-                            const float4 f = *reinterpret_cast<const float4 *>(s_top + (m0 + j) * 4);
+                            const float4 f = *reinterpret_cast<const float4 *>(s_top + (p0 + j) * 4);
                             const float sc = fp8_scale_of(max_magnitude(max_magnitude(f.x, f.y), max_magnitude(f.z, f.w)));
-                            p.hq[((size_t)at.u * NT + m0 + j) * p.I + at.ib * 128 + row] = (uint8_t)e4m3x2(ga[j] * fp8_inverse(sc), 0.f);
+                            p.hq[((size_t)at.u * NT + p0 + j) * p.I + at.ib * 128 + row] = (uint8_t)e4m3x2(ga[j] * fp8_inverse(sc), 0.f);
                             if (row == 0) *hs = sc * w;
                         }
                         named_sync(1, kSumThreads);
@@ -630,52 +745,108 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             atomicAdd(barrier, 1);
         }
         {
-            float acc[H];
+            float acc[S];
             DownAt at;
             at.set(b0, U, KB2);
             long begin = b0;
             const long per = (long)U * KB2;
             const auto scale_at = [&](const DownAt &x) {
-                const bool sh = x.u < p.n_shared;
-                return __ldg((sh ? p.sdown_s : p.down_s) + ((size_t)(sh ? x.u : s_unit[x.u - p.n_shared]) * nR + x.rb) * KB2 + x.kb);
+                return __ldg((shared_unit(x.u) ? p.sdown_s : p.down_s) + ((size_t)expert_of(x.u) * nR + x.rb) * KB2 + x.kb);
             };
             float sw = b0 < b1 ? scale_at(at) : 0.f;
-            for (long t = b0; t < b1; ++t, ++g, ++slot) {
+            for (long t = b0; t < b1; ++t, turn ^= 1) {
                 if (t == begin) {
 #pragma unroll
-                    for (int j = 0; j < H; ++j) acc[j] = 0.f;
+                    for (int j = 0; j < S; ++j) acc[j] = 0.f;
+                    if (F::kLists)
+                        for (int j = 0; j < H; ++j) s_sums[(grp * H + j) * 128 + row] = 0.f;
                 }
                 DownAt nx = at;
                 nx.next(U, KB2);
                 const float nw = t + 1 < b1 ? scale_at(nx) : 0.f;
-                const int b = (int)(g % NB), s = (int)(slot % NS);
-                if (ready(b, s)) {
-                    uint32_t v[H];
-                    tmem_ld<H>(my + b * 2 * NT, v);
-                    tmem_wait(v);
-                    const float *const sc = sS + s * NT + m0;
+                const bool sparse = sparse_unit(at.u);
+                if ((F::kLists || turn == grp) && ready()) {
+                    const uint32_t a = my + b.s * 2 * NT;
+                    const float *const sc = sS + r.s * NT;
+                    if (sparse) {
+                        uint32_t v[8];
+                        tmem_ld<8>(a + grp * 8, v);
+                        tmem_wait(v);
 #pragma unroll
-                    for (int j = 0; j < H; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(sc + j);
-                        const float x[4] = {f.x, f.y, f.z, f.w};
+                        for (int j = 0; j < 8; j += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(sc + grp * 8 + j);
+                            acc[j] = fmaf(__uint_as_float(v[j]), f.x * sw, acc[j]);
+                            acc[j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y * sw, acc[j + 1]);
+                            acc[j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z * sw, acc[j + 2]);
+                            acc[j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w * sw, acc[j + 3]);
+                        }
+                    } else {
+                        constexpr int C = 16, N = F::kLists ? H : NT;
+                        const int m0 = F::kLists ? grp * H : 0;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (x[i] != 0.f) acc[j + i] = fmaf(__uint_as_float(v[j + i]), x[i] * sw, acc[j + i]);
+                        for (int cc = 0; cc < N; cc += C) {
+                            uint32_t v[C];
+                            tmem_ld<C>(a + m0 + cc, v);
+                            tmem_wait(v);
+#pragma unroll
+                            for (int j = 0; j < C; j += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(sc + m0 + cc + j);
+                                const float x[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)  // 0: a token that did not choose this expert
+                                    if (x[i] != 0.f) acc[cc + j + i] = fmaf(__uint_as_float(v[j + i]), x[i] * sw, acc[cc + j + i]);
+                            }
+                        }
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&acc_empty[b]);
-                        mbar_arrive(&empty[s]);
+                        mbar_arrive_n(&acc_empty[b.s], F::kLists ? 1 : 2);
+                        mbar_arrive_n(&empty[r.s], F::kLists ? 1 : 2);
                     }
                 }
-                if ((at.u == U - 1 && at.kb == KB2 - 1) || t + 1 == b1) {
+                r.next();
+                b.next();
+                const bool ends = (at.u == U - 1 && at.kb == KB2 - 1) || t + 1 == b1;
+                if (F::kLists && (at.kb == KB2 - 1 || ends)) {
+                    // 64 tokens: a unit's sums go to their tokens' (each token belongs to one group)
+                    if (sparse) {
+                        uint32_t left = (uint32_t)(s_mask[expert_of(at.u)] >> (grp * 32));
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if (left) s_sums[(grp * H + __ffs(left) - 1) * 128 + row] += acc[j];
+                            left &= left - 1;
+                            acc[j] = 0.f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < S; ++j) {
+                            s_sums[(grp * H + j) * 128 + row] += acc[j];
+                            acc[j] = 0.f;
+                        }
+                    }
+                }
+                if (ends) {
+                    if (F::kLists) {
+#pragma unroll
+                        for (int j = 0; j < S; ++j) acc[j] = s_sums[(grp * H + j) * 128 + row];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < H; ++j) s_sums[(grp * H + j) * 128 + row] = grp ? acc[j] : acc[j + H < S ? j + H : j];
+                        named_sync(1, kSumThreads);
+#pragma unroll
+                        for (int j = 0; j < H; ++j)
+                            acc[j] = (grp ? acc[j + H < S ? j + H : j] : acc[j]) + s_sums[((grp ^ 1) * H + j) * 128 + row];
+                        named_sync(1, kSumThreads);
+                    }
+                    const int m0 = grp * H;
                     const long i0 = at.rb * per, i1 = i0 + per;
                     bool whole = begin == i0 && t + 1 == i1;
                     if (!whole) {
                         float *const mine = p.part + ((size_t)c * 2 + (begin != b0)) * kPart;
 #pragma unroll
-                        for (int j = 0; j < H; ++j) __stcg(mine + (m0 + j) * 128 + row, acc[j]);
+                        for (int j = 0; j < H; ++j)
+                            if (m0 + j < p.M) __stcg(mine + (m0 + j) * 128 + row, acc[j]);
                         const int c0 = s2.owner(i0), c1 = s2.owner(i1 - 1);
                         if ((whole = last_part(p.count + G + c0, c1 - c0 + 1))) {
 #pragma unroll
@@ -683,7 +854,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                             for (int k = c0; k <= c1; ++k) {
                                 const float *const their = p.part + ((size_t)k * 2 + (k == c0 && s2.start(c0) != i0)) * kPart;
 #pragma unroll
-                                for (int j = 0; j < H; ++j) acc[j] += __ldcg(their + (m0 + j) * 128 + row);
+                                for (int j = 0; j < H; ++j)
+                                    if (m0 + j < p.M) acc[j] += __ldcg(their + (m0 + j) * 128 + row);
                             }
                         }
                     }
@@ -707,8 +879,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     if (tid == 0 && !s_int[1])  // after a wait that gave up: the last fill of each slot may be in flight
         for (int s = 0; s < NS; ++s) {
             if (issued <= s) continue;
-            const long f = issued - 1 - (issued - 1 - s) % NS;
-            if (!fp8_wait(&full[s], (uint32_t)(f / NS) & 1, p.status)) fp8_wait(&full[s], (uint32_t)(f / NS) & 1, p.status, 8 * kFp8WaitNs);
+            const int f = issued - 1 - (issued - 1 - s) % NS;
+            if (!fp8_wait(&full[s], f / NS & 1, p.status)) fp8_wait(&full[s], f / NS & 1, p.status, 8 * kFp8WaitNs);
         }
     __syncwarp();
     tc_fence_before();
@@ -788,7 +960,7 @@ extern "C" int moe_fp8_forward(const hla_moe_fp8 *L, int M, const hla_bf16 *x, c
     HLA_REQUIRE(p.status, HLA_ERR_CUDA);
     p.force_timeout = wait_timeout_forced();
     MoeMaps maps;
-    bool ok = byte_tile_map(&maps.x, w + sp.xq, M, Hd, NT) && byte_tile_map(&maps.h, p.hq, (uint64_t)U * NT, I, NT) &&
+    bool ok = byte_tile_map(&maps.x, w + sp.xq, M, Hd, NT) && byte_tile_map(&maps.h, p.hq, (uint64_t)U * NT, I, NT) && byte_tile_map(&maps.hfew, p.hq, (uint64_t)U * NT, I, 16) &&
               byte_tile_map(&maps.gate, L->W_gate, (uint64_t)E * I, Hd, 128) && byte_tile_map(&maps.up, L->W_up, (uint64_t)E * I, Hd, 128) &&
               byte_tile_map(&maps.down, L->W_down, (uint64_t)E * Hd, I, 128);
     if (sh)
