@@ -132,6 +132,14 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&v)[COLS]) {
         asm volatile("" : "+r"(v[c]), "+r"(v[c + 1]), "+r"(v[c + 2]), "+r"(v[c + 3]), "+r"(v[c + 4]), "+r"(v[c + 5]), "+r"(v[c + 6]), "+r"(v[c + 7])::"memory");
 }
 
+// (a0, a1) += (v0, v1) * (s0, s1), each rounded once: one packed instruction.
+__device__ __forceinline__ void fma2(float &a0, float &a1, uint32_t v0, uint32_t v1, float s0, float s1) {
+    asm("{\n .reg .b64 a, v, s;\n mov.b64 a, {%0, %1};\n mov.b64 v, {%2, %3};\n mov.b64 s, {%4, %5};\n"
+        " fma.rn.f32x2 a, v, s, a;\n mov.b64 {%0, %1}, a;\n}\n"
+        : "+f"(a0), "+f"(a1)
+        : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
+}
+
 // Allocate / free `columns` (a power of two from 32) of tensor memory; one whole warp.
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t columns) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(columns) : "memory");

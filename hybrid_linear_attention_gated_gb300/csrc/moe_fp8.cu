@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kPrepThreads) __cluster_dims__(kPrepCluster, 1
 
 // ----------------------------------------------------------------------------- second kernel
 
-constexpr int kMoeThreads = 384;    // copies, products, two warps of the choice only, two groups of four warps of sums
+constexpr int kMoeThreads = 384;    // copies, products, scales, a warp of the choice only, two groups of four warps of sums
 constexpr int kSumThreads = 256;
 constexpr int kSumWarp0 = 4;
 constexpr int kSparse = 0x8000;     // of a unit's entry: few tokens chose it
@@ -201,7 +201,7 @@ template <int NT>
 struct Moe {
     static constexpr int kSlots = NT == 16 ? 10 : NT == 32 ? 8 : 7;
     static constexpr int kAcc = 4;                                    // accumulators of 2 NT columns
-    static constexpr uint32_t kTile = 128 * 128, kTokens = NT * 128, kScales = NT * 4;
+    static constexpr uint32_t kTile = 128 * 128, kTokens = NT * 128;
     static constexpr uint32_t kColumns = kAcc * 2 * NT;
     // 64 tokens: an expert that at most 8 tokens of each half of the batch chose is sparse: its sums and its rows of h
     // are the 16 positions of those tokens, not the 64 tokens
@@ -209,7 +209,7 @@ struct Moe {
     static constexpr int kSums = NT == 16 ? 16 : 32;                  // of a thread, for gate and for up
     static constexpr size_t kExchange = (NT == 16 ? 16 : 32) * 1024;  // sums on their way between the groups; y's sums of 64 tokens
     static constexpr size_t kTables = NT * kMaxTopK * 8 + kMaxExperts * 2 + kMaxExperts * 8 + NT * 4 + NT * 16;
-    static constexpr size_t kSmem = 1024 + kSlots * (kTile + kTokens + kScales) + kExchange + (2 * kSlots + 2 * kAcc + 2) * 8 + 16 + kTables;
+    static constexpr size_t kSmem = 1024 + kSlots * (kTile + kTokens) + kAcc * 2 * NT * 4 + kExchange + (2 * kSlots + 2 * kAcc + 2) * 8 + 16 + kTables;
     static_assert((2 * kSlots + 2 * kAcc + 2) * 8 % 16 == 0 && NT % 4 == 0, "vectors of four in the tables");
     static_assert(kSmem <= 227 * 1024, "one CTA to an SM");
 };
@@ -218,17 +218,22 @@ struct Moe {
 struct Share {
     long T;
     int ctas;
-    __device__ __forceinline__ long start(int c) const { return T * c / ctas; }
-    __device__ __forceinline__ int owner(long t) const { return (int)(((t + 1) * ctas - 1) / T); }
+    // 64-bit divisions take some hundred cycles each
+    __device__ __forceinline__ long start(int c) const {
+        return T < 1 << 22 ? (long)((uint32_t)T * (uint32_t)c / (uint32_t)ctas) : T * c / ctas;
+    }
+    __device__ __forceinline__ int owner(long t) const {
+        return T < 1 << 22 ? (int)(((uint32_t)(t + 1) * (uint32_t)ctas - 1) / (uint32_t)T) : (int)(((t + 1) * ctas - 1) / T);
+    }
 };
 
 // Position in the order of the gate/up items: unit, block of 128 of the inner width, block of K.
 struct GateAt {
     int u, ib, kb;
     __device__ __forceinline__ void set(long t, int nI, int KB) {
-        const long item = t / KB;
+        const long item = t < 1l << 32 ? (long)((uint32_t)t / (uint32_t)KB) : t / KB;
         kb = (int)(t - item * KB);
-        u = (int)(item / nI);
+        u = item < 1l << 32 ? (int)((uint32_t)item / (uint32_t)nI) : (int)(item / nI);
         ib = (int)(item - (long)u * nI);
     }
     __device__ __forceinline__ void next(int nI, int KB) {
@@ -243,7 +248,7 @@ struct DownAt {
     int rb, u, kb;
     __device__ __forceinline__ void set(long t, int U, int KB) {
         const long per = (long)U * KB;
-        rb = (int)(t / per);
+        rb = t < 1l << 32 && per < 1l << 32 ? (int)((uint32_t)t / (uint32_t)per) : (int)(t / per);
         const int r = (int)(t - rb * per);
         u = r / KB;
         kb = r - u * KB;
@@ -310,6 +315,25 @@ __device__ __forceinline__ int load_acquire(const int *p) {
     asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
+// The bounded wait at the grid barrier.
+__device__ __forceinline__ bool wait_grid(const int *barrier, int ctas, int *status) {
+    uint64_t began = 0;
+    for (uint32_t i = 0; load_acquire(barrier) < ctas; ++i)
+        if ((i & 63) == 63) {
+            const uint64_t now = global_ns();
+            if (!began) began = now;
+            else if (now - began > kFp8WaitNs) {
+                atomicExch(status, HLA_ERR_DEVICE_TIMEOUT);
+                return false;
+            }
+        }
+    return true;
+}
+__device__ __forceinline__ int add_acq_rel(int *p, int v) {
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
@@ -325,8 +349,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *const sA = smem, *const sB = smem + NS * F::kTile;
-    float *const sS = reinterpret_cast<float *>(sB + NS * F::kTokens);
-    float *const s_sums = sS + NS * NT;
+    float *const sS = reinterpret_cast<float *>(sB + NS * F::kTokens);  // [NB][2 NT]: what each accumulator's columns are multiplied by
+    float *const s_sums = sS + NB * 2 * NT;
     uint64_t *const full = reinterpret_cast<uint64_t *>(s_sums + F::kExchange / 4);
     uint64_t *const empty = full + NS, *const acc_full = empty + NS, *const acc_empty = acc_full + NB, *const done = acc_empty + NB;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(done + 2);  // 16-byte aligned, as the tables behind it
@@ -346,10 +370,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1 + kSumThreads / 32);
+            mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < NB; ++b) {
-            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_full[b], 2);  // the products and their scales
             mbar_init(&acc_empty[b], kSumThreads / 32);
         }
         mbar_init(done, 1);
@@ -425,29 +449,25 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 if (r.turn > 0 && !(ok = fp8_wait(&empty[r.s], r.freed(), p.status))) break;
-                mbar_expect_tx(&full[r.s], F::kTile + (half ? 0 : F::kTokens + F::kScales));
+                mbar_expect_tx(&full[r.s], F::kTile + (half ? 0 : F::kTokens));
                 tma_tile(sA + r.s * F::kTile, half ? (sh ? &maps.sup : &maps.up) : (sh ? &maps.sgate : &maps.gate), col, row, &full[r.s]);
-                if (!half) {
-                    tma_tile(sB + r.s * F::kTokens, &maps.x, col, 0, &full[r.s]);
-                    bulk_g2s(sS + r.s * NT, p.xs + (size_t)at.kb * NT, F::kScales, &full[r.s]);
-                }
+                if (!half) tma_tile(sB + r.s * F::kTokens, &maps.x, col, 0, &full[r.s]);
                 r.next();
             }
         }
-        // the first down tiles go out before the grid barrier, their tokens and scales after it
+        // the first down tiles go out before the grid barrier, their tokens after it
         const long n2 = b1 - b0;
         const int pre = (int)(n2 < NS ? n2 : NS);
         DownAt w, h;
         w.set(b0, U, KB2);
         h = w;
         const auto weights = [&](int s) {
-            mbar_expect_tx(&full[s], F::kTile + F::kScales + (sparse_unit(w.u) ? 16 * 128 : F::kTokens));
+            mbar_expect_tx(&full[s], F::kTile + (sparse_unit(w.u) ? 16 * 128 : F::kTokens));
             tma_tile(sA + s * F::kTile, shared_unit(w.u) ? &maps.sdown : &maps.down, w.kb * kFp8Block, expert_of(w.u) * p.Hd + w.rb * 128, &full[s]);
             w.next(U, KB2);
         };
         const auto tokens = [&](int s) {
             tma_tile(sB + s * F::kTokens, sparse_unit(h.u) ? &maps.hfew : &maps.h, h.kb * kFp8Block, h.u * NT, &full[s]);
-            bulk_g2s(sS + s * NT, p.hs + ((size_t)h.u * KB2 + h.kb) * NT, F::kScales, &full[s]);
             h.next(U, KB2);
         };
         const Ring<NS> first = r;
@@ -458,13 +478,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             r.next();
         }
         if (n2 > 0 && ok) {
-            const uint64_t began = global_ns();
-            while (load_acquire(barrier) < G)
-                if (global_ns() - began > kFp8WaitNs) {
-                    atomicExch(p.status, HLA_ERR_DEVICE_TIMEOUT);
-                    ok = false;
-                    break;
-                }
+            ok = wait_grid(barrier, G, p.status);
             fence_async();
         }
         Ring<NS> q = first;
@@ -512,6 +526,97 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         if (lane == 0) s_int[1] = ok;
         umma_commit_elected(done);
         if (!fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
+    } else if (warp == 2) {
+        // ---- scales: token scale times weight scale of every column of an accumulator, four blocks of K loaded ahead
+        bool ok = true;
+        Ring<NB> b;
+        constexpr int A = 4, P = NT == 64 ? 2 : 1;  // blocks ahead; tokens of a lane
+        {
+            GateAt at;
+            at.set(a0, nI, KB1);
+            float x[2][A][P], sg[2][A], su[2][A];
+            bool sp[2][A];
+            const auto load = [&](int w, long t) {
+#pragma unroll
+                for (int i = 0; i < A; ++i) {
+                    if (t + i >= a1) break;
+                    const bool sh = shared_unit(at.u);
+                    const size_t q = ((size_t)expert_of(at.u) * nI + at.ib) * KB1 + at.kb;
+                    sg[w][i] = __ldg((sh ? p.sgate_s : p.gate_s) + q);
+                    su[w][i] = __ldg((sh ? p.sup_s : p.up_s) + q);
+                    sp[w][i] = sparse_unit(at.u);
+                    const float *const xs = p.xs + (size_t)at.kb * NT;
+                    if (sp[w][i]) {  // lanes 0..15 have the positions, 8 of each half of the batch
+                        uint32_t left = lane < 16 ? (uint32_t)(s_mask[expert_of(at.u)] >> (lane >> 3) * 32) : 0u;
+                        for (int j = 0; j < (lane & 7); ++j) left &= left - 1;
+                        x[w][i][0] = left ? __ldcg(xs + (lane >> 3) * 32 + __ffs(left) - 1) : 0.f;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < P; ++j) x[w][i][j] = lane + 32 * j < NT ? __ldcg(xs + lane + 32 * j) : 0.f;
+                    }
+                    at.next(nI, KB1);
+                }
+            };
+            load(0, a0);
+            for (long t = a0; t < a1 && ok; t += 2 * A) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    load(w ^ 1, t + (w + 1) * A);
+#pragma unroll
+                    for (int i = 0; i < A; ++i) {
+                        if (t + w * A + i >= a1 || !ok) break;
+                        ok = __all_sync(~0u, b.turn == 0 || fp8_wait(&acc_empty[b.s], b.freed(), p.status));
+                        float *const sc = sS + b.s * 2 * NT;
+#pragma unroll
+                        for (int j = 0; j < P; ++j)
+                            if (lane + 32 * j < NT && !(sp[w][i] && j > 0)) {
+                                sc[lane + 32 * j] = x[w][i][j] * sg[w][i];
+                                sc[NT + lane + 32 * j] = x[w][i][j] * su[w][i];
+                            }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acc_full[b.s]);
+                        b.next();
+                    }
+                }
+            }
+        }
+        if (b0 < b1 && ok) ok = __all_sync(~0u, wait_grid(barrier, G, p.status));
+        {
+            DownAt at;
+            at.set(b0, U, KB2);
+            float x[2][A][P], sw[2][A];
+            const auto load = [&](int w, long t) {
+#pragma unroll
+                for (int i = 0; i < A; ++i) {
+                    if (t + i >= b1) break;
+                    sw[w][i] = __ldg((shared_unit(at.u) ? p.sdown_s : p.down_s) + ((size_t)expert_of(at.u) * nR + at.rb) * KB2 + at.kb);
+                    const float *const hs = p.hs + ((size_t)at.u * KB2 + at.kb) * NT;
+                    const int n = sparse_unit(at.u) ? 16 : NT;
+#pragma unroll
+                    for (int j = 0; j < P; ++j) x[w][i][j] = lane + 32 * j < n ? __ldcg(hs + lane + 32 * j) : 0.f;
+                    at.next(U, KB2);
+                }
+            };
+            if (ok) load(0, b0);
+            for (long t = b0; t < b1 && ok; t += 2 * A) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    load(w ^ 1, t + (w + 1) * A);
+#pragma unroll
+                    for (int i = 0; i < A; ++i) {
+                        if (t + w * A + i >= b1 || !ok) break;
+                        ok = __all_sync(~0u, b.turn == 0 || fp8_wait(&acc_empty[b.s], b.freed(), p.status));
+                        float *const sc = sS + b.s * 2 * NT;
+#pragma unroll
+                        for (int j = 0; j < P; ++j)
+                            if (lane + 32 * j < NT) sc[lane + 32 * j] = x[w][i][j] * sw[w][i];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acc_full[b.s]);
+                        b.next();
+                    }
+                }
+            }
+        }
     } else if (warp >= kSumWarp0) {
         // ---- sums, each thread of one weight row.  Up to 32 tokens, and for the gate and up products of a sparse unit, the two
         // groups of four warps take every other block of K and all tokens (or positions), and exchange halves of
@@ -521,24 +626,18 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         const uint32_t my = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         constexpr size_t kPart = 2 * NT * 128;  // floats of a part: gate and up, position, row
         bool ok = true;
-        Ring<NS> r;
         Ring<NB> b;
         int turn = 0;  // which group's block the next one is
-        // waits for an accumulator and the scales that came with it
+        // waits for an accumulator and its scales
         const auto ready = [&]() {
-            ok = __all_sync(~0u, ok && fp8_wait(&acc_full[b.s], b.filled(), p.status) && fp8_wait(&full[r.s], r.filled(), p.status));
+            ok = __all_sync(~0u, ok && fp8_wait(&acc_full[b.s], b.filled(), p.status));
             tc_fence_after();
             return ok;
         };
         // leaves a part behind (already stored): true in the CTA that comes last, whose parts are all there
         const auto last_part = [&](int *count, int parts) {
-            __threadfence();
             named_sync(1, kSumThreads);
-            if (st == 0) {
-                const int before = atomicAdd(count, 1);
-                __threadfence();
-                s_int[2] = before == parts - 1;
-            }
+            if (st == 0) s_int[2] = add_acq_rel(count, 1) == parts - 1;
             named_sync(1, kSumThreads);
             return s_int[2] != 0;
         };
@@ -549,13 +648,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             long begin = a0;           // of the segment
             bool sparse = false, both = false;
             uint32_t lists[2] = {0u, 0u};  // tokens of a sparse unit, by half of the batch
-            const auto scales_at = [&](const GateAt &x, float *sg, float *su) {
-                const size_t i = ((size_t)expert_of(x.u) * nI + x.ib) * KB1 + x.kb;
-                *sg = __ldg((shared_unit(x.u) ? p.sgate_s : p.gate_s) + i);
-                *su = __ldg((shared_unit(x.u) ? p.sup_s : p.up_s) + i);
-            };
-            float sg = 0.f, su = 0.f;
-            if (a0 < a1) scales_at(at, &sg, &su);
             for (long t = a0; t < a1; ++t, turn ^= 1) {
                 if (t == begin) {
 #pragma unroll
@@ -568,39 +660,34 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                         lists[1] = (uint32_t)(mask >> 32);
                     }
                 }
-                GateAt nx = at;
-                nx.next(nI, KB1);
-                float ng = 0.f, nu = 0.f;
-                if (t + 1 < a1) scales_at(nx, &ng, &nu);
                 if ((both || turn == grp) && ready()) {
                     const uint32_t acc = my + b.s * 2 * NT;
-                    const float *const sc = sS + r.s * NT;
+                    const float *const sc = sS + b.s * 2 * NT;
                     if (sparse) {
                         uint32_t vg[16], vu[16];
-                        float x[16];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             uint32_t left = lists[h];
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
+                                vg[h * 8 + j] = vu[h * 8 + j] = 0u;
                                 if (left) {
                                     const int m = h * 32 + __ffs(left) - 1;
                                     tmem_ld1(acc + m, vg[h * 8 + j]);
                                     tmem_ld1(acc + NT + m, vu[h * 8 + j]);
-                                    x[h * 8 + j] = sc[m];
                                     left &= left - 1;
-                                } else {
-                                    vg[h * 8 + j] = vu[h * 8 + j] = 0u;
-                                    x[h * 8 + j] = 0.f;
                                 }
                             }
                         }
                         tmem_wait(vg);
                         tmem_wait(vu);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            ga[j] = fmaf(__uint_as_float(vg[j]), x[j] * sg, ga[j]);
-                            ua[j] = fmaf(__uint_as_float(vu[j]), x[j] * su, ua[j]);
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(sc + j), e = *reinterpret_cast<const float4 *>(sc + NT + j);
+                            fma2(ga[j], ga[j + 1], vg[j], vg[j + 1], f.x, f.y);
+                            fma2(ga[j + 2], ga[j + 3], vg[j + 2], vg[j + 3], f.z, f.w);
+                            fma2(ua[j], ua[j + 1], vu[j], vu[j + 1], e.x, e.y);
+                            fma2(ua[j + 2], ua[j + 3], vu[j + 2], vu[j + 3], e.z, e.w);
                         }
                     } else {
                         // columns of this thread: all NT, or its half of 64; C of gate and of up at a time
@@ -615,29 +702,18 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                             tmem_wait(vu);
 #pragma unroll
                             for (int j = 0; j < C; j += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(sc + m0 + cc + j);
-                                const float x[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    ga[cc + j + i] = fmaf(__uint_as_float(vg[j + i]), x[i] * sg, ga[cc + j + i]);
-                                    ua[cc + j + i] = fmaf(__uint_as_float(vu[j + i]), x[i] * su, ua[cc + j + i]);
-                                }
+                                const float4 f = *reinterpret_cast<const float4 *>(sc + m0 + cc + j), e = *reinterpret_cast<const float4 *>(sc + NT + m0 + cc + j);
+                                fma2(ga[cc + j], ga[cc + j + 1], vg[j], vg[j + 1], f.x, f.y);
+                                fma2(ga[cc + j + 2], ga[cc + j + 3], vg[j + 2], vg[j + 3], f.z, f.w);
+                                fma2(ua[cc + j], ua[cc + j + 1], vu[j], vu[j + 1], e.x, e.y);
+                                fma2(ua[cc + j + 2], ua[cc + j + 3], vu[j + 2], vu[j + 3], e.z, e.w);
                             }
                         }
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        const uint32_t n = both ? 1 : 2;
-                        Ring<NS> up = r;
-                        up.next();
-                        mbar_arrive_n(&acc_empty[b.s], n);
-                        mbar_arrive_n(&empty[r.s], n);
-                        mbar_arrive_n(&empty[up.s], n);
-                    }
+                    if (lane == 0) mbar_arrive_n(&acc_empty[b.s], both ? 1 : 2);
                 }
-                r.next();
-                r.next();
                 b.next();
                 if (at.kb == KB1 - 1 || t + 1 == a1) {
                     // the segment ends: a whole item, or a part of one.  Its positions: `half` for each group.
@@ -732,17 +808,14 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                     }
                     begin = t + 1;
                 }
-                at = nx;
-                sg = ng;
-                su = nu;
+                at.next(nI, KB1);
             }
         }
-        __threadfence();
         fence_async();
         named_sync(1, kSumThreads);
         if (st == 0) {
-            __threadfence();
-            atomicAdd(barrier, 1);
+            fence_async();
+            add_acq_rel(barrier, 1);
         }
         {
             float acc[S];
@@ -750,10 +823,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             at.set(b0, U, KB2);
             long begin = b0;
             const long per = (long)U * KB2;
-            const auto scale_at = [&](const DownAt &x) {
-                return __ldg((shared_unit(x.u) ? p.sdown_s : p.down_s) + ((size_t)expert_of(x.u) * nR + x.rb) * KB2 + x.kb);
-            };
-            float sw = b0 < b1 ? scale_at(at) : 0.f;
             for (long t = b0; t < b1; ++t, turn ^= 1) {
                 if (t == begin) {
 #pragma unroll
@@ -761,13 +830,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                     if (F::kLists)
                         for (int j = 0; j < H; ++j) s_sums[(grp * H + j) * 128 + row] = 0.f;
                 }
-                DownAt nx = at;
-                nx.next(U, KB2);
-                const float nw = t + 1 < b1 ? scale_at(nx) : 0.f;
                 const bool sparse = sparse_unit(at.u);
                 if ((F::kLists || turn == grp) && ready()) {
                     const uint32_t a = my + b.s * 2 * NT;
-                    const float *const sc = sS + r.s * NT;
+                    const float *const sc = sS + b.s * 2 * NT;
                     if (sparse) {
                         uint32_t v[8];
                         tmem_ld<8>(a + grp * 8, v);
@@ -775,10 +841,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
 #pragma unroll
                         for (int j = 0; j < 8; j += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(sc + grp * 8 + j);
-                            acc[j] = fmaf(__uint_as_float(v[j]), f.x * sw, acc[j]);
-                            acc[j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y * sw, acc[j + 1]);
-                            acc[j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z * sw, acc[j + 2]);
-                            acc[j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w * sw, acc[j + 3]);
+                            fma2(acc[j], acc[j + 1], v[j], v[j + 1], f.x, f.y);
+                            fma2(acc[j + 2], acc[j + 3], v[j + 2], v[j + 3], f.z, f.w);
                         }
                     } else {
                         constexpr int C = 16, N = F::kLists ? H : NT;
@@ -794,18 +858,14 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                                 const float x[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)  // 0: a token that did not choose this expert
-                                    if (x[i] != 0.f) acc[cc + j + i] = fmaf(__uint_as_float(v[j + i]), x[i] * sw, acc[cc + j + i]);
+                                    if (x[i] != 0.f) acc[cc + j + i] = fmaf(__uint_as_float(v[j + i]), x[i], acc[cc + j + i]);
                             }
                         }
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive_n(&acc_empty[b.s], F::kLists ? 1 : 2);
-                        mbar_arrive_n(&empty[r.s], F::kLists ? 1 : 2);
-                    }
+                    if (lane == 0) mbar_arrive_n(&acc_empty[b.s], F::kLists ? 1 : 2);
                 }
-                r.next();
                 b.next();
                 const bool ends = (at.u == U - 1 && at.kb == KB2 - 1) || t + 1 == b1;
                 if (F::kLists && (at.kb == KB2 - 1 || ends)) {
@@ -869,8 +929,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                     }
                     begin = t + 1;
                 }
-                at = nx;
-                sw = nw;
+                at.next(U, KB2);
             }
         }
     }
