@@ -208,9 +208,9 @@ struct Moe {
     static constexpr bool kLists = NT == 64;
     static constexpr int kSums = NT == 16 ? 16 : 32;                  // of a thread, for gate and for up
     static constexpr size_t kExchange = (NT == 16 ? 16 : 32) * 1024;  // sums on their way between the groups; y's sums of 64 tokens
-    static constexpr size_t kTables = NT * kMaxTopK * 8 + kMaxExperts * 2 + kMaxExperts * 8 + NT * 4 + NT * 16;
+    static constexpr size_t kTables = NT * kMaxTopK * 8 + kMaxExperts * 2 + kMaxExperts * 8;
     static constexpr size_t kSmem = 1024 + kSlots * (kTile + kTokens) + kAcc * 2 * NT * 4 + kExchange + (2 * kSlots + 2 * kAcc + 2) * 8 + 16 + kTables;
-    static_assert((2 * kSlots + 2 * kAcc + 2) * 8 % 16 == 0 && NT % 4 == 0, "vectors of four in the tables");
+    static_assert((2 * kSlots + 2 * kAcc + 2) * 8 % 16 == 0, "the tables are aligned");
     static_assert(kSmem <= 227 * 1024, "one CTA to an SM");
 };
 
@@ -277,37 +277,45 @@ __device__ __forceinline__ uint32_t ordered(float v) {  // larger floats have la
 }
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 
-// The k largest of a token's logits by one warp, ties to the lower index: lane j gets the jth index and its logit.
-template <int PER>
-__device__ __forceinline__ void choose(const float *logits, int E, int k, int lane, int *idx, float *logit) {
-    uint32_t key[PER], top = 0;
-    int at = 0;  // the largest of this lane's own, the first of equal ones
+// The k largest logits of each of T tokens by one warp, ties to the lower index: lane j gets the jth index and its logit.  The
+// tokens' chains of dependent steps run side by side.
+template <int PER, int T>
+__device__ __forceinline__ void choose(const float *const (&logits)[T], int E, int k, int lane, int (&idx)[T], float (&logit)[T]) {
+    uint32_t key[T][PER], top[T];
+    int at[T];  // the largest of this lane's own, the first of equal ones
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = i * 32 + lane;
-        key[i] = e < E ? ordered(__ldcg(logits + e)) : 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (key[i] > top) top = key[i], at = i;
-    for (int j = 0; j < k; ++j) {
-        const uint32_t best = __reduce_max_sync(~0u, top);
-        const uint32_t owners = __ballot_sync(~0u, top == best);
-        uint32_t e = at * 32 + lane;
-        if (owners & (owners - 1)) e = __reduce_min_sync(~0u, top == best ? e : ~0u);  // equal logits in several lanes
-        else e = __shfl_sync(~0u, e, __ffs(owners) - 1);
-        if (lane == j) {
-            *idx = (int)e;
-            *logit = unordered(best);
-        }
-        const bool mine = (e & 31) == lane;
-        top = 0;
+    for (int q = 0; q < T; ++q)
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            key[i] &= mine && i == (int)(e >> 5) ? 0u : ~0u;
-            if (key[i] > top) top = key[i], at = i;
+            const int e = i * 32 + lane;
+            key[q][i] = e < E ? ordered(__ldcg(logits[q] + e)) : 0u;
         }
+#pragma unroll
+    for (int q = 0; q < T; ++q) {
+        top[q] = 0;
+        at[q] = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (key[q][i] > top[q]) top[q] = key[q][i], at[q] = i;
     }
+#pragma unroll 1
+    for (int j = 0; j < k; ++j)
+#pragma unroll
+        for (int q = 0; q < T; ++q) {
+            const uint32_t best = __reduce_max_sync(~0u, top[q]);
+            const uint32_t e = __reduce_min_sync(~0u, top[q] == best ? (uint32_t)(at[q] * 32 + lane) : ~0u);
+            if (lane == j) {
+                idx[q] = (int)e;
+                logit[q] = unordered(best);
+            }
+            const bool mine = (e & 31) == lane;
+            top[q] = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                key[q][i] &= mine && i == (int)(e >> 5) ? 0u : ~0u;
+                if (key[q][i] > top[q]) top[q] = key[q][i], at[q] = i;
+            }
+        }
 }
 
 __device__ __forceinline__ int load_acquire(const int *p) {
@@ -342,6 +350,26 @@ __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &v) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr));
 }
 
+// Adds an item's parts in order: CTA c0 left its in slot `second`, the CTAs up to c1 in their first slot.  Four are loaded at once.
+__device__ __forceinline__ void add_parts(const float *at, size_t to_up, size_t part, int c0, int c1, bool second, float4 *g, float4 *u) {
+    for (int k = c0; k <= c1; k += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (k + i <= c1) {
+                const float *const q = at + ((size_t)(k + i) * 2 + (k + i == c0 && second)) * part;
+                a[i] = __ldcg(reinterpret_cast<const float4 *>(q));
+                b[i] = __ldcg(reinterpret_cast<const float4 *>(q + to_up));
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (k + i <= c1) {
+                g->x += a[i].x, g->y += a[i].y, g->z += a[i].z, g->w += a[i].w;
+                u->x += b[i].x, u->y += b[i].y, u->z += b[i].z, u->w += b[i].w;
+            }
+    }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_constant__ MoeMaps maps, const MoeParams p) {
     using F = Moe<NT>;
@@ -355,9 +383,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     uint64_t *const empty = full + NS, *const acc_full = empty + NS, *const acc_empty = acc_full + NB, *const done = acc_empty + NB;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(done + 2);  // 16-byte aligned, as the tables behind it
     int *const s_int = reinterpret_cast<int *>(tmem_slot + 1);           // active experts, products issued, last part?
-    float *const s_weight = reinterpret_cast<float *>(tmem_slot + 4);    // [NT] of the unit at hand, -1 where not chosen
-    float *const s_top = s_weight + NT;                                  // [NT][4]
-    unsigned long long *const s_mask = reinterpret_cast<unsigned long long *>(s_top + NT * 4);  // tokens that chose each expert
+    unsigned long long *const s_mask = reinterpret_cast<unsigned long long *>(tmem_slot + 4);  // tokens that chose each expert
     int *const s_idx = reinterpret_cast<int *>(s_mask + kMaxExperts);    // [M][k]
     float *const s_w = reinterpret_cast<float *>(s_idx + NT * kMaxTopK);
     uint16_t *const s_unit = reinterpret_cast<uint16_t *>(s_w + NT * kMaxTopK);  // routed units' experts
@@ -389,22 +415,41 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     pdl_wait_trigger();
 
     // ---- the choice, by every CTA for itself; the first one writes it out
-    for (int m = warp; m < p.M; m += kMoeThreads / 32) {
-        int idx = 0;
-        float logit = 0.f;
-        if (p.E <= 256) choose<8>(p.logits + (size_t)m * p.E, p.E, p.k, lane, &idx, &logit);
-        else choose<32>(p.logits + (size_t)m * p.E, p.E, p.k, lane, &idx, &logit);
-        const float score = 1.f / (1.f + expf(-logit));
-        float sum = 0.f;
-        for (int j = 0; j < p.k; ++j) sum += __shfl_sync(~0u, score, j);
-        if (lane < p.k) {
-            const float w = score / sum;
-            s_idx[m * p.k + lane] = idx;
-            s_w[m * p.k + lane] = w;
-            atomicOr(&s_mask[idx], 1ull << m);
-            if (blockIdx.x == 0) {
-                if (p.topk_idx) p.topk_idx[m * p.k + lane] = idx;
-                if (p.topk_w) p.topk_w[m * p.k + lane] = w;
+    constexpr int T = NT == 64 ? 3 : NT == 32 ? 2 : 1, W = kMoeThreads / 32;
+    for (int m0 = warp; m0 < p.M; m0 += W * T) {
+        int idx[T] = {};
+        float logit[T] = {};
+        const float *rows[T];
+#pragma unroll
+        for (int q = 0; q < T; ++q) rows[q] = p.logits + (size_t)(m0 + q * W < p.M ? m0 + q * W : m0) * p.E;
+        if (p.E <= 256) {
+            choose<8, T>(rows, p.E, p.k, lane, idx, logit);
+        } else {
+#pragma unroll
+            for (int q = 0; q < T; ++q) {
+                int i[1] = {0};
+                float l[1] = {0.f};
+                const float *const row[1] = {rows[q]};
+                choose<32, 1>(row, p.E, p.k, lane, i, l);
+                idx[q] = i[0];
+                logit[q] = l[0];
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < T; ++q) {
+            const int m = m0 + q * W;
+            const float score = 1.f / (1.f + expf(-logit[q]));
+            float sum = 0.f;
+            for (int j = 0; j < p.k; ++j) sum += __shfl_sync(~0u, score, j);
+            if (lane < p.k && m < p.M) {
+                const float w = score / sum;
+                s_idx[m * p.k + lane] = idx[q];
+                s_w[m * p.k + lane] = w;
+                atomicOr(&s_mask[idx[q]], 1ull << m);
+                if (blockIdx.x == 0) {
+                    if (p.topk_idx) p.topk_idx[m * p.k + lane] = idx[q];
+                    if (p.topk_w) p.topk_w[m * p.k + lane] = w;
+                }
             }
         }
     }
@@ -665,30 +710,30 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                     const float *const sc = sS + b.s * 2 * NT;
                     if (sparse) {
                         uint32_t vg[16], vu[16];
+                        const int n[2] = {__popc(lists[0]), __popc(lists[1])};
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             uint32_t left = lists[h];
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
-                                vg[h * 8 + j] = vu[h * 8 + j] = 0u;
-                                if (left) {
-                                    const int m = h * 32 + __ffs(left) - 1;
-                                    tmem_ld1(acc + m, vg[h * 8 + j]);
-                                    tmem_ld1(acc + NT + m, vu[h * 8 + j]);
-                                    left &= left - 1;
-                                }
+                                if (j >= n[h]) break;
+                                const int m = h * 32 + __ffs(left) - 1;
+                                tmem_ld1(acc + m, vg[h * 8 + j]);
+                                tmem_ld1(acc + NT + m, vu[h * 8 + j]);
+                                left &= left - 1;
                             }
                         }
                         tmem_wait(vg);
                         tmem_wait(vu);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(sc + j), e = *reinterpret_cast<const float4 *>(sc + NT + j);
-                            fma2(ga[j], ga[j + 1], vg[j], vg[j + 1], f.x, f.y);
-                            fma2(ga[j + 2], ga[j + 3], vg[j + 2], vg[j + 3], f.z, f.w);
-                            fma2(ua[j], ua[j + 1], vu[j], vu[j + 1], e.x, e.y);
-                            fma2(ua[j + 2], ua[j + 3], vu[j + 2], vu[j + 3], e.z, e.w);
-                        }
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int j = h * 8; j < h * 8 + 8; j += 2) {  // a pair's second value may be none: its sum is not used
+                                if (j - h * 8 >= n[h]) break;
+                                const float2 f = *reinterpret_cast<const float2 *>(sc + j), e = *reinterpret_cast<const float2 *>(sc + NT + j);
+                                fma2(ga[j], ga[j + 1], vg[j], vg[j + 1], f.x, f.y);
+                                fma2(ua[j], ua[j + 1], vu[j], vu[j + 1], e.x, e.y);
+                            }
                     } else {
                         // columns of this thread: all NT, or its half of 64; C of gate and of up at a time
                         constexpr int C = 16, N = F::kLists ? H : NT;
@@ -716,95 +761,96 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                 }
                 b.next();
                 if (at.kb == KB1 - 1 || t + 1 == a1) {
-                    // the segment ends: a whole item, or a part of one.  Its positions: `half` for each group.
-                    const int half = sparse ? 8 : H;
-                    if (!both) {
-#pragma unroll
-                        for (int j = 0; j < S / 2; ++j) {
-                            if (j >= half) break;
-                            const int o = j + (S == 32 && !F::kLists ? 16 : 8);
-                            s_sums[(grp * half + j) * 128 + row] = grp ? ga[j] : ga[o];
-                            s_sums[((2 + grp) * half + j) * 128 + row] = grp ? ua[j] : ua[o];
-                        }
-                        named_sync(1, kSumThreads);
-#pragma unroll
-                        for (int j = 0; j < S / 2; ++j) {
-                            if (j >= half) break;
-                            const int o = j + (S == 32 && !F::kLists ? 16 : 8);
-                            ga[j] = (grp ? ga[o] : ga[j]) + s_sums[((grp ^ 1) * half + j) * 128 + row];
-                            ua[j] = (grp ? ua[o] : ua[j]) + s_sums[((2 + (grp ^ 1)) * half + j) * 128 + row];
-                        }
-                    }
-                    const int p0 = grp * half;
+                    // The segment ends: a whole item, or a part of one.  The sums meet in shared memory, [gate, up][position]
+                    // [row], and each warp takes every eighth position: its token's h of 128 columns, their scale, times the
+                    // token's weight in the mixture.
+                    const int e = expert_of(at.u), n = sparse ? 16 : both ? 32 : NT;  // positions at a time
                     const long i0 = t - at.kb, i1 = i0 + KB1;
-                    bool whole = begin == i0 && t + 1 == i1;
-                    if (!whole) {
-                        float *const mine = p.part + ((size_t)c * 2 + (begin != a0)) * kPart;
-#pragma unroll
-                        for (int j = 0; j < H; ++j) {
-                            if (j >= half) break;
-                            __stcg(mine + (p0 + j) * 128 + row, ga[j]);
-                            __stcg(mine + (NT + p0 + j) * 128 + row, ua[j]);
+                    const bool whole = begin == i0 && t + 1 == i1;
+                    float *const mine = p.part + ((size_t)c * 2 + (begin != a0)) * kPart;
+                    // the token at a position, p.M if there is none
+                    const auto token_at = [&](int at_pos) {
+                        if (!sparse) return at_pos;
+                        uint32_t left = at_pos < 8 ? lists[0] : lists[1];
+                        for (int j = 0; j < (at_pos & 7); ++j) left &= left - 1;
+                        return left ? (at_pos >> 3) * 32 + __ffs(left) - 1 : p.M;
+                    };
+                    const auto finish = [&](int pos, float4 g, float4 u) {
+                        const int m = token_at(pos);
+                        float *const hs = p.hs + ((size_t)at.u * KB2 + at.ib) * NT + pos;
+                        const bool hit = m < p.M && (shared_unit(at.u) ? lane == 0 : lane < p.k && s_idx[m * p.k + lane] == e);
+                        const uint32_t hits = __ballot_sync(~0u, hit);
+                        if (!hits) {  // this token did not choose the expert
+                            if (lane == 0) *hs = 0.f;
+                            return;
                         }
-                        const int c0 = s1.owner(i0), c1 = s1.owner(i1 - 1);
-                        if ((whole = last_part(p.count + c0, c1 - c0 + 1))) {
+                        const float h0 = silu_f(g.x) * u.x, h1 = silu_f(g.y) * u.y, h2 = silu_f(g.z) * u.z, h3 = silu_f(g.w) * u.w;
+                        const float own = max_magnitude(max_magnitude(h0, h1), max_magnitude(h2, h3));
+                        const float sc = fp8_scale_of(__uint_as_float(__reduce_max_sync(~0u, __float_as_uint(own)))), inv = fp8_inverse(sc);
+                        *reinterpret_cast<uint32_t *>(p.hq + ((size_t)at.u * NT + pos) * p.I + at.ib * 128 + lane * 4) =
+                            e4m3x4(h0 * inv, h1 * inv, h2 * inv, h3 * inv);
+                        if (hit) *hs = shared_unit(at.u) ? sc : sc * s_w[m * p.k + lane];
+                    };
+                    // sums of the positions [first, first + n) into shared memory
+                    if (!both) {
+                        if (grp) {
 #pragma unroll
-                            for (int j = 0; j < H; ++j) ga[j] = ua[j] = 0.f;
-                            for (int k = c0; k <= c1; ++k) {
-                                const float *const their = p.part + ((size_t)k * 2 + (k == c0 && s1.start(c0) != i0)) * kPart;
-#pragma unroll
-                                for (int j = 0; j < H; ++j) {
-                                    if (j >= half) break;
-                                    ga[j] += __ldcg(their + (p0 + j) * 128 + row);
-                                    ua[j] += __ldcg(their + (NT + p0 + j) * 128 + row);
+                            for (int j = 0; j < S; ++j)
+                                if (j < n) {
+                                    s_sums[j * 128 + row] = ga[j];
+                                    s_sums[(n + j) * 128 + row] = ua[j];
                                 }
-                            }
-                        }
-                    }
-                    if (whole) {
-                        // h of 128 columns: every token that chose this expert, its own scale, times its weight in the mixture
-                        if (st < 2 * half) {
-                            int m = st;
-                            if (sparse) {
-                                uint32_t left = st < 8 ? lists[0] : lists[1];
-                                for (int j = 0; j < (st & 7); ++j) left &= left - 1;
-                                m = left ? (st >> 3) * 32 + __ffs(left) - 1 : p.M;
-                            }
-                            float w = -1.f;  // not chosen
-                            if (m < p.M) {
-                                if (shared_unit(at.u)) w = 1.f;
-                                else
-                                    for (int j = 0; j < p.k; ++j)
-                                        if (s_idx[m * p.k + j] == expert_of(at.u)) w = s_w[m * p.k + j];
-                            }
-                            s_weight[st] = w;
                         }
                         named_sync(1, kSumThreads);
+                        if (!grp) {
 #pragma unroll
-                        for (int j = 0; j < H; ++j) {
-                            if (j >= half) break;
-                            if (s_weight[p0 + j] == -1.f) continue;  // the same for the whole group
-                            const float hv = silu_f(ga[j]) * ua[j];
-                            ga[j] = hv;
-                            const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(hv) & 0x7FFFFFFFu);
-                            if (lane == 0) s_top[(p0 + j) * 4 + q4] = __uint_as_float(top);
+                            for (int j = 0; j < S; ++j)
+                                if (j < n) {
+                                    s_sums[j * 128 + row] += ga[j];
+                                    s_sums[(n + j) * 128 + row] += ua[j];
+                                }
                         }
-                        named_sync(2 + grp, 128);
+                    }
 #pragma unroll
-                        for (int j = 0; j < H; ++j) {
-                            if (j >= half) break;
-                            const float w = s_weight[p0 + j];
-                            float *const hs = p.hs + ((size_t)at.u * KB2 + at.ib) * NT + p0 + j;
-                            if (w == -1.f) {
-                                if (row == 0) *hs = 0.f;
+                    for (int round = 0; round < (F::kLists ? 2 : 1); ++round) {
+                        if (round > 0 && !both) break;
+                        if (both) {  // 16 tokens of each half at a time
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                s_sums[(grp * 16 + j) * 128 + row] = ga[(round * 16 + j) % S];
+                                s_sums[(32 + grp * 16 + j) * 128 + row] = ua[(round * 16 + j) % S];
+                            }
+                        }
+                        named_sync(1, kSumThreads);
+#pragma unroll 1
+                        for (int j = st >> 5; j < n; j += kSumThreads / 32) {
+                            const int pos = both ? (j >> 4) * 32 + round * 16 + (j & 15) : j;
+                            if (!sparse && pos >= p.M) {
+                                if (whole && lane == 0) p.hs[((size_t)at.u * KB2 + at.ib) * NT + pos] = 0.f;
                                 continue;
                             }
-                            const float4 f = *reinterpret_cast<const float4 *>(s_top + (p0 + j) * 4);
-                            const float sc = fp8_scale_of(max_magnitude(max_magnitude(f.x, f.y), max_magnitude(f.z, f.w)));
-                            p.hq[((size_t)at.u * NT + p0 + j) * p.I + at.ib * 128 + row] = (uint8_t)e4m3x2(ga[j] * fp8_inverse(sc), 0.f);
-                            if (row == 0) *hs = sc * w;
+                            const float4 g = *reinterpret_cast<const float4 *>(s_sums + j * 128 + lane * 4),
+                                         u = *reinterpret_cast<const float4 *>(s_sums + (n + j) * 128 + lane * 4);
+                            if (whole) {
+                                finish(pos, g, u);
+                            } else {
+                                __stcg(reinterpret_cast<float4 *>(mine + pos * 128 + lane * 4), g);
+                                __stcg(reinterpret_cast<float4 *>(mine + (NT + pos) * 128 + lane * 4), u);
+                            }
                         }
                         named_sync(1, kSumThreads);
+                    }
+                    if (!whole) {
+                        const int c0 = s1.owner(i0), c1 = s1.owner(i1 - 1);
+                        if (last_part(p.count + c0, c1 - c0 + 1)) {
+#pragma unroll 1
+                            for (int pos = st >> 5; pos < (both ? 2 : 1) * n; pos += kSumThreads / 32) {
+                                float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+                                if (sparse || pos < p.M)
+                                    add_parts(p.part + pos * 128 + lane * 4, NT * 128, kPart, c0, c1, s1.start(c0) != i0, &g, &u);
+                                finish(pos, g, u);
+                            }
+                        }
                     }
                     begin = t + 1;
                 }
@@ -887,44 +933,46 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                     }
                 }
                 if (ends) {
-                    if (F::kLists) {
+                    // [token][row] in shared memory; each warp takes every eighth token
+                    if (!F::kLists) {
+                        if (grp) {
 #pragma unroll
-                        for (int j = 0; j < S; ++j) acc[j] = s_sums[(grp * H + j) * 128 + row];
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < H; ++j) s_sums[(grp * H + j) * 128 + row] = grp ? acc[j] : acc[j + H < S ? j + H : j];
+                            for (int j = 0; j < NT; ++j) s_sums[j * 128 + row] = acc[j % S];
+                        }
                         named_sync(1, kSumThreads);
+                        if (!grp) {
 #pragma unroll
-                        for (int j = 0; j < H; ++j)
-                            acc[j] = (grp ? acc[j + H < S ? j + H : j] : acc[j]) + s_sums[((grp ^ 1) * H + j) * 128 + row];
-                        named_sync(1, kSumThreads);
-                    }
-                    const int m0 = grp * H;
-                    const long i0 = at.rb * per, i1 = i0 + per;
-                    bool whole = begin == i0 && t + 1 == i1;
-                    if (!whole) {
-                        float *const mine = p.part + ((size_t)c * 2 + (begin != b0)) * kPart;
-#pragma unroll
-                        for (int j = 0; j < H; ++j)
-                            if (m0 + j < p.M) __stcg(mine + (m0 + j) * 128 + row, acc[j]);
-                        const int c0 = s2.owner(i0), c1 = s2.owner(i1 - 1);
-                        if ((whole = last_part(p.count + G + c0, c1 - c0 + 1))) {
-#pragma unroll
-                            for (int j = 0; j < H; ++j) acc[j] = 0.f;
-                            for (int k = c0; k <= c1; ++k) {
-                                const float *const their = p.part + ((size_t)k * 2 + (k == c0 && s2.start(c0) != i0)) * kPart;
-#pragma unroll
-                                for (int j = 0; j < H; ++j)
-                                    if (m0 + j < p.M) acc[j] += __ldcg(their + (m0 + j) * 128 + row);
-                            }
+                            for (int j = 0; j < NT; ++j) s_sums[j * 128 + row] += acc[j % S];
                         }
                     }
-                    if (whole) {
-#pragma unroll
-                        for (int j = 0; j < H; ++j) {
-                            if (m0 + j >= p.M) break;
-                            const size_t o = (size_t)(m0 + j) * p.Hd + at.rb * 128 + row;
-                            p.y[o] = float_to_bf16_bits(p.residual ? acc[j] + bf16_bits_to_float(p.residual[o]) : acc[j]);
+                    named_sync(1, kSumThreads);
+                    const long i0 = at.rb * per, i1 = i0 + per;
+                    const bool whole = begin == i0 && t + 1 == i1;
+                    float *const mine = p.part + ((size_t)c * 2 + (begin != b0)) * kPart;
+                    const auto finish = [&](int m, float4 v) {
+                        const size_t o = (size_t)m * p.Hd + at.rb * 128 + lane * 4;
+                        if (p.residual) {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(p.residual + o);
+                            v.x += bf16_lo(w.x), v.y += bf16_hi(w.x), v.z += bf16_lo(w.y), v.w += bf16_hi(w.y);
+                        }
+                        *reinterpret_cast<uint2 *>(p.y + o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                    };
+#pragma unroll 1
+                    for (int m = st >> 5; m < p.M; m += kSumThreads / 32) {
+                        const float4 v = *reinterpret_cast<const float4 *>(s_sums + m * 128 + lane * 4);
+                        if (whole) finish(m, v);
+                        else __stcg(reinterpret_cast<float4 *>(mine + m * 128 + lane * 4), v);
+                    }
+                    named_sync(1, kSumThreads);
+                    if (!whole) {
+                        const int c0 = s2.owner(i0), c1 = s2.owner(i1 - 1);
+                        if (last_part(p.count + G + c0, c1 - c0 + 1)) {
+#pragma unroll 1
+                            for (int m = st >> 5; m < p.M; m += kSumThreads / 32) {
+                                float4 v = make_float4(0.f, 0.f, 0.f, 0.f), none = v;
+                                add_parts(p.part + m * 128 + lane * 4, 0, kPart, c0, c1, s2.start(c0) != i0, &v, &none);
+                                finish(m, v);
+                            }
                         }
                     }
                     begin = t + 1;
