@@ -89,11 +89,13 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// A bounded wait: its first polls do not read the clock (a read of %globaltimer takes longer than most waits here).
+// A bounded wait for the phase with the given parity; false (and the status word set) after `limit` ns of %globaltimer, which
+// is read every 256 polls only: a read takes longer than most waits here, and the loop is small because every role has several.
 __device__ __forceinline__ bool fp8_wait(uint64_t *bar, uint32_t parity, int *status, uint64_t limit = kFp8WaitNs) {
     const uint32_t a = smem_u32(bar);
+    uint64_t began = 0;
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i) {
+    for (uint32_t i = 1;; ++i) {
         uint32_t done;
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
@@ -101,8 +103,14 @@ __device__ __forceinline__ bool fp8_wait(uint64_t *bar, uint32_t parity, int *st
             : "r"(a), "r"(parity)
             : "memory");
         if (done) return true;
+        if ((i & 255) == 0) {
+            const uint64_t now = global_ns();
+            if (began == 0) began = now;
+            else if (now - began > limit) break;
+        }
     }
-    return mbar_wait_for(bar, parity, limit, status);
+    atomicExch(status, HLA_ERR_DEVICE_TIMEOUT);
+    return false;
 }
 
 // COLS consecutive 32-bit tensor-memory columns of this thread's lane; tmem_wait(v) before v is used: the values pass

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         umma_commit_elected(done);
         if (!fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
     } else if (warp >= 2) {
-        const int t = tid - 64, row = (warp & 3) * 32 + lane;  // a warp reads the quarter of the lanes of its number mod 4
+        const int t = tid - 64;
         const uint32_t my = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[j] = 0.f;
@@ -194,12 +194,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 }
             }
         }
-        if (p.split == 1 && ok) {
-            const int col = rb * 128 + row;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if (j < p.M && col < p.N) store_y(p, (size_t)j * p.N + col, acc[j]);
-        }
     }
     __syncwarp();
     __syncthreads();
@@ -208,28 +202,29 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             if (!fp8_wait(&full[i % NS], (i / NS) & 1, p.status)) fp8_wait(&full[i % NS], (i / NS) & 1, p.status, 8 * kFp8WaitNs);
     __syncwarp();
     __syncthreads();
-    if (p.split > 1) {  // the tiles are used up: their place takes the sums [token][weight row]
-        float *const sums = reinterpret_cast<float *>(smem);
-        if (warp >= 2) {
-            const int row = (warp & 3) * 32 + lane;
+    // the tiles are used up: their place takes the sums [token][weight row]
+    float *const sums = reinterpret_cast<float *>(smem);
+    if (warp >= 2) {
+        const int row = (warp & 3) * 32 + lane;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) sums[j * 128 + row] = acc[j];
-        }
-        cluster_sync();
-        for (int e = (rank * kFewThreads + tid) * 4; e < p.M * 128; e += p.split * kFewThreads * 4) {
-            const int m = e >> 7, col = rb * 128 + (e & 127);
-            float4 part[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < p.split) part[r] = peer_float4(sums + e, r);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < p.split) v.x += part[r].x, v.y += part[r].y, v.z += part[r].z, v.w += part[r].w;
-            store_y4(p, m, col, v);
-        }
-        cluster_sync();  // no CTA leaves while another reads its sums
+        for (int j = 0; j < NT; ++j) sums[j * 128 + row] = acc[j];
     }
+    if (p.split > 1) cluster_sync();
+    else __syncthreads();
+#pragma unroll 1
+    for (int e = (rank * kFewThreads + tid) * 4; e < p.M * 128; e += p.split * kFewThreads * 4) {
+        const int m = e >> 7, col = rb * 128 + (e & 127);
+        float4 part[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < p.split) part[r] = peer_float4(sums + e, r);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < p.split) v.x += part[r].x, v.y += part[r].y, v.z += part[r].z, v.w += part[r].w;
+        store_y4(p, m, col, v);
+    }
+    if (p.split > 1) cluster_sync();  // no CTA leaves while another reads its sums
     tc_fence_before();
     __syncthreads();
     if (warp == 1) tmem_free(tmem, F::kColumns);
@@ -251,7 +246,7 @@ struct Many {
     static constexpr int kPitch = NT + 4;                  // floats of a row of the join
     static constexpr size_t kRing = kStages * (kTileBytes + kWeightBytes);
     static constexpr int kOutPitch = 33;
-    static constexpr size_t kOut = 8 * 16 * kOutPitch * 4; // a warp's 16 rows x 32 columns on their way out
+    static constexpr size_t kOut = 8 * 32 * kOutPitch * 4; // a warp's 32 rows x 32 columns on their way out
     static constexpr size_t kSmem = 1024 + kRing + kOut + (2 * kStages + 2 * kAcc + 1) * 8 + 16;
     static_assert(128 * kPitch * 4 <= kRing, "the sums of the join take the place of the tiles");
     static_assert(kSmem <= 227 * 1024, "one CTA to an SM");
@@ -443,6 +438,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             const float *const xs = p.xs + (size_t)(m < p.M ? m : p.M - 1) * p.KB + c0, *const ws = p.ws + (size_t)wb * p.KB + c0;
 #pragma unroll
             for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+            if (p.residual && !p.direct && p.split == 1 && m < p.M)  // the rows that are added come to L2 while the products run
+#pragma unroll
+                for (int c = 0; c < COLS; c += 32)
+                    if (n0 + c < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.residual + (size_t)m * p.N + n0 + c));
             float sx = xs[0], sw = ws[0];
             for (int i = 0; i < n; ++i) {
                 const float nx = i + 1 < n ? xs[i + 1] : 0.f, nw = i + 1 < n ? ws[i + 1] : 0.f;  // on their way during this block
@@ -474,34 +473,35 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                 if (m < p.M && n0 < p.N) store_row(p, (size_t)m * p.N + n0, p.N - n0, acc);
                 continue;
             }
-            // rows that keep no alignment leave through shared memory, 16 rows x 32 columns a warp at a time
-            float *const out = sOut + (warp - 4) * 16 * F::kOutPitch;
+            // rows that keep no alignment leave through shared memory, 32 rows x 32 columns a warp at a time
+            float *const out = sOut + (warp - 4) * 32 * F::kOutPitch;
+            const int tok = rt * 128 + (warp & 3) * 32, rows = p.M - tok < 32 ? p.M - tok : 32;
 #pragma unroll
-            for (int c = 0; c < COLS; c += 32)
+            for (int c = 0; c < COLS; c += 32) {
+                __syncwarp();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    __syncwarp();
-                    if (lane >> 4 == h) {
+                for (int j = 0; j < 32; ++j) out[lane * F::kOutPitch + j] = acc[c + j];
+                __syncwarp();
+                const int col = n0 + c + lane;
+                if (col >= p.N) continue;
+                const size_t at = (size_t)tok * p.N + col;
+#pragma unroll 1
+                for (int k0 = 0; k0 < rows; k0 += 8) {
+                    float o[8];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) out[(lane & 15) * F::kOutPitch + j] = acc[c + j];
+                    for (int k = 0; k < 8; ++k) {
+                        o[k] = 0.f;
+                        if (p.residual && k0 + k < rows) o[k] = bf16_bits_to_float(p.residual[at + (size_t)(k0 + k) * p.N]);
                     }
-                    __syncwarp();
-                    const int col = n0 + c + lane, tok = rt * 128 + (warp & 3) * 32 + h * 16;
-                    if (col < p.N) {
-                        const size_t at = (size_t)tok * p.N + col;
-                        float r[16];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            r[k] = p.residual && tok + k < p.M ? bf16_bits_to_float(p.residual[at + (size_t)k * p.N]) : 0.f;
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (tok + k < p.M) {
-                                const float o = out[k * F::kOutPitch + lane] + r[k];
-                                if (p.y_bf16) static_cast<uint16_t *>(p.y)[at + (size_t)k * p.N] = float_to_bf16_bits(o);
-                                else static_cast<float *>(p.y)[at + (size_t)k * p.N] = o;
-                            }
+                    for (int k = 0; k < 8; ++k) {
+                        if (k0 + k >= rows) break;
+                        const float v = out[(k0 + k) * F::kOutPitch + lane] + o[k];
+                        if (p.y_bf16) static_cast<uint16_t *>(p.y)[at + (size_t)(k0 + k) * p.N] = float_to_bf16_bits(v);
+                        else static_cast<float *>(p.y)[at + (size_t)(k0 + k) * p.N] = v;
                     }
                 }
+            }
         }
         __syncwarp();
         __syncthreads();

@@ -201,7 +201,7 @@ template <int NT>
 struct Moe {
     static constexpr int kSlots = NT == 16 ? 10 : NT == 32 ? 8 : 7;
     static constexpr int kAcc = 4;                                    // accumulators of 2 NT columns
-    static constexpr uint32_t kTile = 128 * 128, kTokens = NT * 128;
+    static constexpr uint32_t kTile = 128 * 128, kTokens = NT * 128, kScales = NT * 4;
     static constexpr uint32_t kColumns = kAcc * 2 * NT;
     // 64 tokens: an expert that at most 8 tokens of each half of the batch chose is sparse: its sums and its rows of h
     // are the 16 positions of those tokens, not the 64 tokens
@@ -209,49 +209,49 @@ struct Moe {
     static constexpr int kSums = NT == 16 ? 16 : 32;                  // of a thread, for gate and for up
     static constexpr size_t kExchange = (NT == 16 ? 16 : 32) * 1024;  // sums on their way between the groups; y's sums of 64 tokens
     static constexpr size_t kTables = NT * kMaxTopK * 8 + kMaxExperts * 2 + kMaxExperts * 8;
-    static constexpr size_t kSmem = 1024 + kSlots * (kTile + kTokens) + kAcc * 2 * NT * 4 + kExchange + (2 * kSlots + 2 * kAcc + 2) * 8 + 16 + kTables;
+    static constexpr size_t kSmem = 1024 + kSlots * (kTile + kTokens + kScales) + kAcc * 2 * NT * 4 + kExchange + (2 * kSlots + 2 * kAcc + 2) * 8 + 16 + kTables;
     static_assert((2 * kSlots + 2 * kAcc + 2) * 8 % 16 == 0, "the tables are aligned");
     static_assert(kSmem <= 227 * 1024, "one CTA to an SM");
 };
 
-// A share of one phase: T units of one block of K over `ctas` CTAs, as equal as whole units can be.
+// The shares of one phase: T steps of `step` blocks of K over `ctas` CTAs, as equal as whole steps can be.  All in 32 bits: 2^24
+// blocks are 256 GB of weights.
 struct Share {
-    long T;
-    int ctas;
-    // 64-bit divisions take some hundred cycles each
-    __device__ __forceinline__ long start(int c) const {
-        return T < 1 << 22 ? (long)((uint32_t)T * (uint32_t)c / (uint32_t)ctas) : T * c / ctas;
+    uint32_t T, ctas, step;
+    __device__ __forceinline__ void set(uint32_t blocks, uint32_t per_step, uint32_t G) {
+        step = per_step;
+        T = blocks / per_step;
+        ctas = T < G ? T : G;
     }
-    __device__ __forceinline__ int owner(long t) const {
-        return T < 1 << 22 ? (int)(((uint32_t)(t + 1) * (uint32_t)ctas - 1) / (uint32_t)T) : (int)(((t + 1) * ctas - 1) / T);
-    }
+    __device__ __forceinline__ int start(uint32_t c) const { return c < ctas ? (int)(step * (T * c / ctas)) : (int)(step * T); }
+    __device__ __forceinline__ int owner(uint32_t t) const { return (int)(((t + 1) * ctas - 1) / T); }  // of block t, at step 1
 };
 
-// Position in the order of the gate/up items: unit, block of 128 of the inner width, block of K.
+// Position in the order of the gate/up items: block of 128 of the inner width, unit, block of K.  The units run inside, so that
+// those that many tokens chose, whose sums cost more, are spread over the CTAs.
 struct GateAt {
     int u, ib, kb;
-    __device__ __forceinline__ void set(long t, int nI, int KB) {
-        const long item = t < 1l << 32 ? (long)((uint32_t)t / (uint32_t)KB) : t / KB;
+    __device__ __forceinline__ void set(uint32_t t, uint32_t U, uint32_t KB) {
+        const uint32_t item = t / KB;
         kb = (int)(t - item * KB);
-        u = item < 1l << 32 ? (int)((uint32_t)item / (uint32_t)nI) : (int)(item / nI);
-        ib = (int)(item - (long)u * nI);
+        ib = (int)(item / U);
+        u = (int)(item - ib * U);
     }
-    __device__ __forceinline__ void next(int nI, int KB) {
+    __device__ __forceinline__ void next(int U, int KB) {
         if (++kb == KB) {
             kb = 0;
-            if (++ib == nI) ib = 0, ++u;
+            if (++u == U) u = 0, ++ib;
         }
     }
 };
 // Position in the order of the down items: block of output rows, unit, block of K.
 struct DownAt {
     int rb, u, kb;
-    __device__ __forceinline__ void set(long t, int U, int KB) {
-        const long per = (long)U * KB;
-        rb = t < 1l << 32 && per < 1l << 32 ? (int)((uint32_t)t / (uint32_t)per) : (int)(t / per);
-        const int r = (int)(t - rb * per);
-        u = r / KB;
-        kb = r - u * KB;
+    __device__ __forceinline__ void set(uint32_t t, uint32_t U, uint32_t KB) {
+        rb = (int)(t / (U * KB));
+        const uint32_t r = t - rb * U * KB;
+        u = (int)(r / KB);
+        kb = (int)(r - u * KB);
     }
     __device__ __forceinline__ void next(int U, int KB) {
         if (++kb == KB) {
@@ -377,7 +377,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *const sA = smem, *const sB = smem + NS * F::kTile;
-    float *const sS = reinterpret_cast<float *>(sB + NS * F::kTokens);  // [NB][2 NT]: what each accumulator's columns are multiplied by
+    float *const sX = reinterpret_cast<float *>(sB + NS * F::kTokens);  // [NS][NT]: the tokens' scales
+    float *const sS = sX + NS * NT;  // [NB][2 NT]: what each accumulator's columns are multiplied by
     float *const s_sums = sS + NB * 2 * NT;
     uint64_t *const full = reinterpret_cast<uint64_t *>(s_sums + F::kExchange / 4);
     uint64_t *const empty = full + NS, *const acc_full = empty + NS, *const acc_empty = acc_full + NB, *const done = acc_empty + NB;
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);  // the products, and the warp that reads the scales
         }
         for (int b = 0; b < NB; ++b) {
             mbar_init(&acc_full[b], 2);  // the products and their scales
@@ -406,6 +407,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
     }
+    if (warp == 3 && lane < 9) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.x + lane)) : "memory");
     if (warp == 1) tmem_alloc(tmem_slot, F::kColumns);
     for (int i = tid; i < p.E; i += kMoeThreads) s_mask[i] = 0;
     tc_fence_before();
@@ -415,42 +417,42 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     pdl_wait_trigger();
 
     // ---- the choice, by every CTA for itself; the first one writes it out
-    constexpr int T = NT == 64 ? 3 : NT == 32 ? 2 : 1, W = kMoeThreads / 32;
-    for (int m0 = warp; m0 < p.M; m0 += W * T) {
-        int idx[T] = {};
-        float logit[T] = {};
-        const float *rows[T];
-#pragma unroll
-        for (int q = 0; q < T; ++q) rows[q] = p.logits + (size_t)(m0 + q * W < p.M ? m0 + q * W : m0) * p.E;
-        if (p.E <= 256) {
-            choose<8, T>(rows, p.E, p.k, lane, idx, logit);
-        } else {
-#pragma unroll
-            for (int q = 0; q < T; ++q) {
-                int i[1] = {0};
-                float l[1] = {0.f};
-                const float *const row[1] = {rows[q]};
-                choose<32, 1>(row, p.E, p.k, lane, i, l);
-                idx[q] = i[0];
-                logit[q] = l[0];
+    constexpr int T = NT == 16 ? 1 : 2, W = kMoeThreads / 32;
+    const auto record = [&](int m, int idx, float logit) {
+        const float score = 1.f / (1.f + expf(-logit));
+        float sum = 0.f;
+        for (int j = 0; j < p.k; ++j) sum += __shfl_sync(~0u, score, j);
+        if (lane < p.k && m < p.M) {
+            const float w = score / sum;
+            s_idx[m * p.k + lane] = idx;
+            s_w[m * p.k + lane] = w;
+            atomicOr(&s_mask[idx], 1ull << m);
+            if (blockIdx.x == 0) {
+                if (p.topk_idx) p.topk_idx[m * p.k + lane] = idx;
+                if (p.topk_w) p.topk_w[m * p.k + lane] = w;
             }
         }
+    };
+    if (p.E <= 256) {
+#pragma unroll 1
+        for (int m0 = warp; m0 < p.M; m0 += W * T) {
+            int idx[T] = {};
+            float logit[T] = {};
+            const float *rows[T];
 #pragma unroll
-        for (int q = 0; q < T; ++q) {
-            const int m = m0 + q * W;
-            const float score = 1.f / (1.f + expf(-logit[q]));
-            float sum = 0.f;
-            for (int j = 0; j < p.k; ++j) sum += __shfl_sync(~0u, score, j);
-            if (lane < p.k && m < p.M) {
-                const float w = score / sum;
-                s_idx[m * p.k + lane] = idx[q];
-                s_w[m * p.k + lane] = w;
-                atomicOr(&s_mask[idx[q]], 1ull << m);
-                if (blockIdx.x == 0) {
-                    if (p.topk_idx) p.topk_idx[m * p.k + lane] = idx[q];
-                    if (p.topk_w) p.topk_w[m * p.k + lane] = w;
-                }
-            }
+            for (int q = 0; q < T; ++q) rows[q] = p.logits + (size_t)(m0 + q * W < p.M ? m0 + q * W : m0) * p.E;
+            choose<8, T>(rows, p.E, p.k, lane, idx, logit);
+            record(m0, idx[0], logit[0]);
+            if (T > 1) record(m0 + W, idx[T - 1], logit[T - 1]);
+        }
+    } else {
+#pragma unroll 1
+        for (int m = warp; m < p.M; m += W) {
+            int idx[1] = {0};
+            float logit[1] = {0.f};
+            const float *const row[1] = {p.logits + (size_t)m * p.E};
+            choose<32, 1>(row, p.E, p.k, lane, idx, logit);
+            record(m, idx[0], logit[0]);
         }
     }
     __syncthreads();
@@ -470,12 +472,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     const int U = s_int[0] + p.n_shared, G = gridDim.x, c = blockIdx.x;
     const int nI = p.I / 128, nR = p.Hd / 128, KB1 = p.Hd / kFp8Block, KB2 = p.I / kFp8Block;
     Share s1, s2;
-    s1.T = (long)U * nI * KB1;
-    s2.T = (long)nR * U * KB2;
-    s1.ctas = s1.T < G ? (int)s1.T : G;
-    s2.ctas = s2.T < G ? (int)s2.T : G;
-    const long a0 = c < s1.ctas ? s1.start(c) : 0, a1 = c < s1.ctas ? s1.start(c + 1) : 0;
-    const long b0 = c < s2.ctas ? s2.start(c) : 0, b1 = c < s2.ctas ? s2.start(c + 1) : 0;
+    // Gate/up items for three quarters of the CTAs or more, but no more than one each (one token of 8 + 1 experts of 2048: 144 on
+    // 152), stay whole: what is idle costs nothing while the rest fills the memory, and no parts are joined.
+    const int items = U * nI;
+    s1.set(items * KB1, items <= G && items * 4 >= G * 3 ? KB1 : 1, G);
+    s2.set(nR * U * KB2, 1, G);
+    const int a0 = s1.start(c), a1 = s1.start(c + 1), b0 = s2.start(c), b1 = s2.start(c + 1);
     int *const barrier = p.count + 2 * G;
     const auto shared_unit = [&](int u) { return u < p.n_shared; };
     const auto expert_of = [&](int u) { return u < p.n_shared ? u : (int)s_unit[u - p.n_shared] & (kSparse - 1); };
@@ -487,32 +489,36 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         bool ok = true;
         Ring<NS> r;
         GateAt at;
-        at.set(a0, nI, KB1);
-        for (long t = a0; t < a1 && ok; ++t, at.next(nI, KB1)) {
+        at.set(a0, U, KB1);
+        for (int t = a0; t < a1 && ok; ++t, at.next(U, KB1)) {
             const bool sh = shared_unit(at.u);
             const int row = expert_of(at.u) * p.I + at.ib * 128, col = at.kb * kFp8Block;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 if (r.turn > 0 && !(ok = fp8_wait(&empty[r.s], r.freed(), p.status))) break;
-                mbar_expect_tx(&full[r.s], F::kTile + (half ? 0 : F::kTokens));
+                mbar_expect_tx(&full[r.s], F::kTile + (half ? 0 : F::kTokens + F::kScales));
                 tma_tile(sA + r.s * F::kTile, half ? (sh ? &maps.sup : &maps.up) : (sh ? &maps.sgate : &maps.gate), col, row, &full[r.s]);
-                if (!half) tma_tile(sB + r.s * F::kTokens, &maps.x, col, 0, &full[r.s]);
+                if (!half) {
+                    tma_tile(sB + r.s * F::kTokens, &maps.x, col, 0, &full[r.s]);
+                    bulk_g2s(sX + r.s * NT, p.xs + (size_t)at.kb * NT, F::kScales, &full[r.s]);
+                }
                 r.next();
             }
         }
         // the first down tiles go out before the grid barrier, their tokens after it
-        const long n2 = b1 - b0;
-        const int pre = (int)(n2 < NS ? n2 : NS);
+        const int n2 = b1 - b0;
+        const int pre = n2 < NS ? n2 : NS;
         DownAt w, h;
         w.set(b0, U, KB2);
         h = w;
         const auto weights = [&](int s) {
-            mbar_expect_tx(&full[s], F::kTile + (sparse_unit(w.u) ? 16 * 128 : F::kTokens));
+            mbar_expect_tx(&full[s], F::kTile + F::kScales + (sparse_unit(w.u) ? 16 * 128 : F::kTokens));
             tma_tile(sA + s * F::kTile, shared_unit(w.u) ? &maps.sdown : &maps.down, w.kb * kFp8Block, expert_of(w.u) * p.Hd + w.rb * 128, &full[s]);
             w.next(U, KB2);
         };
         const auto tokens = [&](int s) {
             tma_tile(sB + s * F::kTokens, sparse_unit(h.u) ? &maps.hfew : &maps.h, h.kb * kFp8Block, h.u * NT, &full[s]);
+            bulk_g2s(sX + s * NT, p.hs + ((size_t)h.u * KB2 + h.kb) * NT, F::kScales, &full[s]);
             h.next(U, KB2);
         };
         const Ring<NS> first = r;
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         }
         Ring<NS> q = first;
         for (int i = 0; i < sent; ++i, q.next()) tokens(q.s);  // after a barrier that gave up, too: the fills complete
-        for (long t = sent; t < n2 && ok; ++t) {
+        for (int t = sent; t < n2 && ok; ++t) {
             if (r.turn > 0 && !(ok = fp8_wait(&empty[r.s], r.freed(), p.status))) break;
             weights(r.s);
             tokens(r.s);
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         bool ok = true;
         Ring<NS> r;
         Ring<NB> b;
-        for (long t = a0; t < a1; ++t) {
+        for (int t = a0; t < a1; ++t) {
             const int s = r.s;
             ok = (b.turn == 0 || fp8_wait(&acc_empty[b.s], b.freed(), p.status)) && fp8_wait(&full[s], r.filled(), p.status);
             r.next();
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         }
         DownAt at;
         at.set(b0, U, KB2);
-        for (long t = b0; t < b1 && ok; ++t, at.next(U, KB2)) {
+        for (int t = b0; t < b1 && ok; ++t, at.next(U, KB2)) {
             ok = __all_sync(~0u, (b.turn == 0 || fp8_wait(&acc_empty[b.s], b.freed(), p.status)) && fp8_wait(&full[r.s], r.filled(), p.status));
             if (!ok) break;
             tc_fence_after();
@@ -572,95 +578,89 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         umma_commit_elected(done);
         if (!fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
     } else if (warp == 2) {
-        // ---- scales: token scale times weight scale of every column of an accumulator, four blocks of K loaded ahead
+        // ---- scales: token scale (copied with the tiles) times weight scale of every column of an accumulator.  Lane i loads the
+        // weight scales of the ith of 32 blocks, 32 blocks ahead: under full memory traffic a load takes microseconds.
         bool ok = true;
+        Ring<NS> r;
         Ring<NB> b;
-        constexpr int A = 4, P = NT == 64 ? 2 : 1;  // blocks ahead; tokens of a lane
-        {
+        float sg = 0.f, su = 0.f, next_g = 0.f, next_u = 0.f;
+        const auto gate_scales = [&](int t) {
+            if (t + lane >= a1) return;
             GateAt at;
-            at.set(a0, nI, KB1);
-            float x[2][A][P], sg[2][A], su[2][A];
-            bool sp[2][A];
-            const auto load = [&](int w, long t) {
-#pragma unroll
-                for (int i = 0; i < A; ++i) {
-                    if (t + i >= a1) break;
-                    const bool sh = shared_unit(at.u);
-                    const size_t q = ((size_t)expert_of(at.u) * nI + at.ib) * KB1 + at.kb;
-                    sg[w][i] = __ldg((sh ? p.sgate_s : p.gate_s) + q);
-                    su[w][i] = __ldg((sh ? p.sup_s : p.up_s) + q);
-                    sp[w][i] = sparse_unit(at.u);
-                    const float *const xs = p.xs + (size_t)at.kb * NT;
-                    if (sp[w][i]) {  // lanes 0..15 have the positions, 8 of each half of the batch
-                        uint32_t left = lane < 16 ? (uint32_t)(s_mask[expert_of(at.u)] >> (lane >> 3) * 32) : 0u;
-                        for (int j = 0; j < (lane & 7); ++j) left &= left - 1;
-                        x[w][i][0] = left ? __ldcg(xs + (lane >> 3) * 32 + __ffs(left) - 1) : 0.f;
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < P; ++j) x[w][i][j] = lane + 32 * j < NT ? __ldcg(xs + lane + 32 * j) : 0.f;
-                    }
-                    at.next(nI, KB1);
-                }
-            };
-            load(0, a0);
-            for (long t = a0; t < a1 && ok; t += 2 * A) {
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    load(w ^ 1, t + (w + 1) * A);
-#pragma unroll
-                    for (int i = 0; i < A; ++i) {
-                        if (t + w * A + i >= a1 || !ok) break;
-                        ok = __all_sync(~0u, b.turn == 0 || fp8_wait(&acc_empty[b.s], b.freed(), p.status));
-                        float *const sc = sS + b.s * 2 * NT;
-#pragma unroll
-                        for (int j = 0; j < P; ++j)
-                            if (lane + 32 * j < NT && !(sp[w][i] && j > 0)) {
-                                sc[lane + 32 * j] = x[w][i][j] * sg[w][i];
-                                sc[NT + lane + 32 * j] = x[w][i][j] * su[w][i];
-                            }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&acc_full[b.s]);
-                        b.next();
-                    }
-                }
-            }
-        }
-        if (b0 < b1 && ok) ok = __all_sync(~0u, wait_grid(barrier, G, p.status));
-        {
+            at.set(t + lane, U, KB1);
+            const size_t q = ((size_t)expert_of(at.u) * nI + at.ib) * KB1 + at.kb;
+            next_g = __ldg((shared_unit(at.u) ? p.sgate_s : p.gate_s) + q);
+            next_u = __ldg((shared_unit(at.u) ? p.sup_s : p.up_s) + q);
+        };
+        const auto down_scales = [&](int t) {
+            if (t + lane >= b1) return;
             DownAt at;
-            at.set(b0, U, KB2);
-            float x[2][A][P], sw[2][A];
-            const auto load = [&](int w, long t) {
-#pragma unroll
-                for (int i = 0; i < A; ++i) {
-                    if (t + i >= b1) break;
-                    sw[w][i] = __ldg((shared_unit(at.u) ? p.sdown_s : p.down_s) + ((size_t)expert_of(at.u) * nR + at.rb) * KB2 + at.kb);
-                    const float *const hs = p.hs + ((size_t)at.u * KB2 + at.kb) * NT;
-                    const int n = sparse_unit(at.u) ? 16 : NT;
-#pragma unroll
-                    for (int j = 0; j < P; ++j) x[w][i][j] = lane + 32 * j < n ? __ldcg(hs + lane + 32 * j) : 0.f;
-                    at.next(U, KB2);
-                }
-            };
-            if (ok) load(0, b0);
-            for (long t = b0; t < b1 && ok; t += 2 * A) {
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    load(w ^ 1, t + (w + 1) * A);
-#pragma unroll
-                    for (int i = 0; i < A; ++i) {
-                        if (t + w * A + i >= b1 || !ok) break;
-                        ok = __all_sync(~0u, b.turn == 0 || fp8_wait(&acc_empty[b.s], b.freed(), p.status));
-                        float *const sc = sS + b.s * 2 * NT;
-#pragma unroll
-                        for (int j = 0; j < P; ++j)
-                            if (lane + 32 * j < NT) sc[lane + 32 * j] = x[w][i][j] * sw[w][i];
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&acc_full[b.s]);
-                        b.next();
-                    }
-                }
+            at.set(t + lane, U, KB2);
+            next_g = __ldg((shared_unit(at.u) ? p.sdown_s : p.down_s) + ((size_t)expert_of(at.u) * nR + at.rb) * KB2 + at.kb);
+        };
+        const auto ready = [&]() {
+            ok = __all_sync(~0u, (b.turn == 0 || fp8_wait(&acc_empty[b.s], b.freed(), p.status)) && fp8_wait(&full[r.s], r.filled(), p.status));
+        };
+        GateAt at;
+        at.set(a0, U, KB1);
+        gate_scales(a0);
+        int from = -1;  // the token of lanes 0..15 in a sparse unit
+        for (int t = a0; t < a1 && ok; ++t, at.next(U, KB1)) {
+            const int i = (t - a0) & 31;
+            if (i == 0) {
+                sg = next_g;
+                su = next_u;
+                gate_scales(t + 32);
             }
+            const bool sparse = sparse_unit(at.u);
+            if (sparse && (at.kb == 0 || t == a0)) {
+                uint32_t left = lane < 16 ? (uint32_t)(s_mask[expert_of(at.u)] >> (lane >> 3) * 32) : 0u;
+                for (int j = 0; j < (lane & 7); ++j) left &= left - 1;
+                from = left ? (lane >> 3) * 32 + __ffs(left) - 1 : -1;
+            }
+            ready();
+            if (!ok) break;
+            const float g = __shfl_sync(~0u, sg, i), u = __shfl_sync(~0u, su, i);
+            const float *const x = sX + r.s * NT;
+            float *const sc = sS + b.s * 2 * NT;
+#pragma unroll
+            for (int m = lane; m < NT; m += 32) {
+                if (sparse && m >= 16) break;
+                const float v = !sparse ? x[m] : from >= 0 ? x[from] : 0.f;
+                sc[m] = v * g;
+                sc[NT + m] = v * u;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&acc_full[b.s]);
+                mbar_arrive(&empty[r.s]);
+            }
+            r.next();
+            if (lane == 0) mbar_arrive(&empty[r.s]);
+            r.next();
+            b.next();
+        }
+        if (ok) down_scales(b0);
+        for (int t = b0; t < b1 && ok; ++t) {
+            const int i = (t - b0) & 31;
+            if (i == 0) {
+                sg = next_g;
+                down_scales(t + 32);
+            }
+            ready();
+            if (!ok) break;
+            const float g = __shfl_sync(~0u, sg, i);
+            const float *const x = sX + r.s * NT;
+            float *const sc = sS + b.s * 2 * NT;
+#pragma unroll
+            for (int m = lane; m < NT; m += 32) sc[m] = x[m] * g;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&acc_full[b.s]);
+                mbar_arrive(&empty[r.s]);
+            }
+            r.next();
+            b.next();
         }
     } else if (warp >= kSumWarp0) {
         // ---- sums, each thread of one weight row.  Up to 32 tokens, and for the gate and up products of a sparse unit, the two
@@ -689,11 +689,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         {
             float ga[S], ua[S];
             GateAt at;
-            at.set(a0, nI, KB1);
-            long begin = a0;           // of the segment
+            at.set(a0, U, KB1);
+            int begin = a0;            // of the segment
             bool sparse = false, both = false;
             uint32_t lists[2] = {0u, 0u};  // tokens of a sparse unit, by half of the batch
-            for (long t = a0; t < a1; ++t, turn ^= 1) {
+            for (int t = a0; t < a1; ++t, turn ^= 1) {
                 if (t == begin) {
 #pragma unroll
                     for (int j = 0; j < S; ++j) ga[j] = ua[j] = 0.f;
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                             }
                     } else {
                         // columns of this thread: all NT, or its half of 64; C of gate and of up at a time
-                        constexpr int C = 16, N = F::kLists ? H : NT;
+                        constexpr int C = F::kLists ? 8 : 16, N = F::kLists ? H : NT;
                         const int m0 = F::kLists ? grp * H : 0;
 #pragma unroll
                         for (int cc = 0; cc < N; cc += C) {
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                     // [row], and each warp takes every eighth position: its token's h of 128 columns, their scale, times the
                     // token's weight in the mixture.
                     const int e = expert_of(at.u), n = sparse ? 16 : both ? 32 : NT;  // positions at a time
-                    const long i0 = t - at.kb, i1 = i0 + KB1;
+                    const int i0 = t - at.kb, i1 = i0 + KB1;
                     const bool whole = begin == i0 && t + 1 == i1;
                     float *const mine = p.part + ((size_t)c * 2 + (begin != a0)) * kPart;
                     // the token at a position, p.M if there is none
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                     }
                     begin = t + 1;
                 }
-                at.next(nI, KB1);
+                at.next(U, KB1);
             }
         }
         fence_async();
@@ -867,9 +867,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             float acc[S];
             DownAt at;
             at.set(b0, U, KB2);
-            long begin = b0;
-            const long per = (long)U * KB2;
-            for (long t = b0; t < b1; ++t, turn ^= 1) {
+            int begin = b0;
+            const int per = U * KB2;
+            for (int t = b0; t < b1; ++t, turn ^= 1) {
                 if (t == begin) {
 #pragma unroll
                     for (int j = 0; j < S; ++j) acc[j] = 0.f;
@@ -920,8 +920,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                         uint32_t left = (uint32_t)(s_mask[expert_of(at.u)] >> (grp * 32));
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            if (left) s_sums[(grp * H + __ffs(left) - 1) * 128 + row] += acc[j];
-                            left &= left - 1;
+                            if (left) {
+                                s_sums[(grp * H + __ffs(left) - 1) * 128 + row] += acc[j];
+                                left &= left - 1;
+                            }
                             acc[j] = 0.f;
                         }
                     } else {
@@ -946,7 +948,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                         }
                     }
                     named_sync(1, kSumThreads);
-                    const long i0 = at.rb * per, i1 = i0 + per;
+                    const int i0 = at.rb * per, i1 = i0 + per;
                     const bool whole = begin == i0 && t + 1 == i1;
                     float *const mine = p.part + ((size_t)c * 2 + (begin != b0)) * kPart;
                     const auto finish = [&](int m, float4 v) {
@@ -1010,8 +1012,9 @@ int check_moe(const hla_moe_fp8 *L) {
     HLA_REQUIRE(L->top_k <= L->n_experts, HLA_ERR_INVALID_ARG);
     HLA_REQUIRE(L->hidden % 128 == 0 && L->inter % 128 == 0 && L->top_k <= kMaxTopK, HLA_ERR_UNSUPPORTED);
     HLA_REQUIRE((long)L->n_experts + L->n_shared <= kMaxExperts && L->n_shared <= 16, HLA_ERR_UNSUPPORTED);
-    // rows of the weight stacks and bytes of one row stay in 31 bits
+    // rows of the weight stacks and bytes of one row stay in 31 bits, and blocks (256 GB of a matrix) in 24
     HLA_REQUIRE(L->hidden <= 1 << 20 && L->inter <= 1 << 20, HLA_ERR_UNSUPPORTED);
+    HLA_REQUIRE(((long)L->n_experts + L->n_shared) * (L->hidden / 128) * (L->inter / 128) < 1L << 24, HLA_ERR_UNSUPPORTED);
     return HLA_OK;
 }
 
