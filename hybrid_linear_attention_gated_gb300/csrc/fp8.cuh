@@ -113,6 +113,17 @@ __device__ __forceinline__ bool fp8_wait(uint64_t *bar, uint32_t parity, int *st
     return false;
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // COLS consecutive 32-bit tensor-memory columns of this thread's lane; tmem_wait(v) before v is used: the values pass
 // through the wait, so that nothing which uses them moves ahead of it.
 template <int COLS>
@@ -155,6 +166,52 @@ __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t columns) {
 }
 __device__ __forceinline__ void tmem_free(uint32_t taddr, uint32_t columns) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(columns) : "memory");
+}
+
+// ---- pairs of CTAs (cta_group::2): the even CTA of a cluster issues products of 256 rows, whose operands and accumulator lie
+// half in each CTA's shared and tensor memory, at the same places
+__host__ __device__ constexpr uint32_t idesc_e4m3_pair(int n) { return idesc_e4m3(256, n); }
+__device__ __forceinline__ void umma_block_pair(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem, uint32_t idesc) {
+    const uint64_t da = sw128_desc(a_smem), db = sw128_desc(b_smem);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+        asm volatile(
+            "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+            " @q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+            "l"(da + 2 * kk), "l"(db + 2 * kk), "r"(idesc), "r"(static_cast<uint32_t>(kk > 0))
+            : "memory");
+}
+// Arrives at the barrier at this place in both CTAs once the products issued so far are done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+__device__ __forceinline__ uint32_t peer_address(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+// A copy into this CTA's shared memory that completes on a barrier of the pair's even CTA.
+__device__ __forceinline__ void tma_tile_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *slot, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t taddr, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(columns) : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync() {

@@ -15,6 +15,7 @@
 //
 // Every wait is bounded (see tc_gemm.cu for the drain order): a wait that gives up sets the device status word, the roles
 // leave their loops, issued products and copies are waited for, and tensor memory is freed.
+#include <cstdlib>
 #include "fp8.cuh"
 
 namespace hla {
@@ -233,27 +234,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 // ----------------------------------------------------------------------------- more tokens
 
 constexpr int kManyThreads = 384;  // a warpgroup of copies and products, two of sums
+constexpr int kOutPitch = 33;
+constexpr size_t kOutBytes = 8 * 32 * kOutPitch * 4;  // a warp's 32 rows x 32 columns on their way out
 
-template <int NT>
-struct Many {
-    static constexpr int kCols = NT / 2;                   // columns of a warpgroup
-    static constexpr int kStages = NT == 256 ? 4 : 6;      // 192 KB
-    static constexpr int kAcc = 512 / NT;                  // accumulators: all of tensor memory
-    // registers a thread: 168 at launch; 128 sums and 64 values on their way take more, which the first warpgroup leaves
-    static constexpr bool kShift = NT == 256;
-    static constexpr int kFewRegs = 56, kManyRegs = 224;
-    static constexpr uint32_t kWeightBytes = NT * 128;
-    static constexpr int kPitch = NT + 4;                  // floats of a row of the join
-    static constexpr size_t kRing = kStages * (kTileBytes + kWeightBytes);
-    static constexpr int kOutPitch = 33;
-    static constexpr size_t kOut = 8 * 32 * kOutPitch * 4; // a warp's 32 rows x 32 columns on their way out
-    static constexpr size_t kSmem = 1024 + kRing + kOut + (2 * kStages + 2 * kAcc + 1) * 8 + 16;
-    static_assert(128 * kPitch * 4 <= kRing, "the sums of the join take the place of the tiles");
-    static_assert(kSmem <= 227 * 1024, "one CTA to an SM");
-    static_assert(kFewRegs + 2 * kManyRegs <= 3 * 168, "shares of the registers at launch");
-};
-
-// Tiles in bands of 16 row tiles, down a band's columns: the 152 or 304 tiles in flight share their operands in L2.
+// Tiles in bands of `kBand` row tiles, down a band's columns: the tiles in flight share their operands in L2.
 __device__ __forceinline__ void tile_at(const MatmulParams &p, int t, int *rt, int *ct) {
     constexpr int kBand = 16;
     const int band = t / (kBand * p.col_tiles), first = band * kBand;
@@ -263,12 +247,71 @@ __device__ __forceinline__ void tile_at(const MatmulParams &p, int t, int *rt, i
     *rt = first + r - *ct * rows;
 }
 
-// A thread's row of COLS columns, straight from registers: 32 bytes a store, whole sectors.
+// Scales in shared memory, kScaleRing blocks of K ahead: a warp copies the 128 tokens' and, for `blocks` blocks of weight rows
+// from `wb` on, one each.  An entry is 128 + 4 floats; its `full` barrier counts every lane's copies, its `empty` the eight
+// warps of sums.
+constexpr int kScaleRing = 8, kScaleEntry = 132;
+constexpr size_t kScaleBytes = kScaleRing * kScaleEntry * 4;
+
+struct ScaleRing {
+    float *entries;
+    uint64_t *full, *empty;
+    int e = 0, turn = 0;
+    __device__ __forceinline__ void init() const {
+        for (int i = 0; i < kScaleRing; ++i) {
+            mbar_init(&full[i], 32);
+            mbar_init(&empty[i], 8);
+        }
+    }
+    __device__ __forceinline__ void next() {
+        if (++e == kScaleRing) e = 0, ++turn;
+    }
+    // one tile's blocks [c0, c0 + n), tokens from `tok` on; false if a wait gave up
+    __device__ __forceinline__ bool copy_tile(const MatmulParams &p, int tok, int wb, int c0, int n, int lane) {
+        const int last = (p.N - 1) >> 7;  // columns behind the last are not stored, whatever their scale
+        const float *x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = p.xs + (size_t)(tok + j * 32 + lane < p.M ? tok + j * 32 + lane : p.M - 1) * p.KB + c0;
+        const float *const w = p.ws + (size_t)(wb + lane < last ? wb + lane : last) * p.KB + c0;
+        for (int i = 0; i < n; ++i) {
+            if (!__all_sync(~0u, turn == 0 || fp8_wait(&empty[e], (turn - 1) & 1, p.status))) return false;
+            float *const to = entries + e * kScaleEntry;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cp_async4(to + j * 32 + lane, x[j] + i);
+            if (lane < 2) cp_async4(to + 128 + lane, w + i);
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[e])) : "memory");
+            next();
+        }
+        return true;
+    }
+};
+
+// acc += the accumulator's COLS columns at `at`, times the scales: `s0` up to column `cut` * 32, `s1` from there on.  `early` is
+// called while the first columns are on their way, `release` once the last have been read.  16 columns at a time: 128 at
+// 357 cycles beside the products; with 32 the registers spill (575).
+template <int COLS, typename Early, typename Release>
+__device__ __forceinline__ void add_block(float (&acc)[COLS], uint32_t at, float s0, float s1, int cut, Early early, Release release) {
+    constexpr int C = 16;
+    uint32_t v[2][C];
+    tmem_ld<C>(at, v[0]);
+    early();
+#pragma unroll
+    for (int c = 0; c < COLS / C; ++c) {
+        tmem_wait(v[c & 1]);
+        if (c + 1 < COLS / C) tmem_ld<C>(at + (c + 1) * C, v[(c + 1) & 1]);
+        else release();
+        const float sc = c * C < cut * 32 ? s0 : s1;
+#pragma unroll
+        for (int j = 0; j < C; j += 2) fma2(acc[c * C + j], acc[c * C + j + 1], v[c & 1][j], v[c & 1][j + 1], sc, sc);
+    }
+}
+
 __device__ __forceinline__ void st32b(void *p, const uint32_t (&r)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
                  "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+// A thread's row of COLS columns, straight from registers: 32 bytes a store, whole sectors.
 template <int COLS>
 __device__ __forceinline__ void store_row(const MatmulParams &p, size_t at, int columns, const float (&acc)[COLS]) {
     if (p.y_bf16) {
@@ -282,9 +325,7 @@ __device__ __forceinline__ void store_row(const MatmulParams &p, size_t at, int 
                 w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                r[j] = p.residual ? pack_bf16x2(acc[c + 2 * j] + bf16_lo(w[j]), acc[c + 2 * j + 1] + bf16_hi(w[j]))
-                                  : pack_bf16x2(acc[c + 2 * j], acc[c + 2 * j + 1]);
+            for (int j = 0; j < 8; ++j) r[j] = pack_bf16x2(acc[c + 2 * j] + bf16_lo(w[j]), acc[c + 2 * j + 1] + bf16_hi(w[j]));
             st32b(y + c, r);
         }
     } else {
@@ -297,46 +338,106 @@ __device__ __forceinline__ void store_row(const MatmulParams &p, size_t at, int 
             if (p.residual) w = ld_act_v4(p.residual + at + c);
             const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                r[j] = __float_as_uint(p.residual ? acc[c + j] + (j & 1 ? bf16_hi(x[j >> 1]) : bf16_lo(x[j >> 1])) : acc[c + j]);
+            for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(acc[c + j] + (j & 1 ? bf16_hi(x[j >> 1]) : bf16_lo(x[j >> 1])));
             st32b(y + c, r);
         }
     }
 }
 
+// A warp's 32 tokens from `tok` on (lane = token), COLS columns from n0 on.
+template <int COLS>
+__device__ __forceinline__ void store_tile(const MatmulParams &p, int tok, int n0, int lane, const float (&acc)[COLS], float *out) {
+    const int rows = p.M - tok < 32 ? p.M - tok : 32;
+    if (p.direct) {
+        if (lane < rows && n0 < p.N) store_row(p, (size_t)(tok + lane) * p.N + n0, p.N - n0, acc);
+        return;
+    }
+    // rows that keep no alignment leave through shared memory, 32 rows x 32 columns at a time
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) out[lane * kOutPitch + j] = acc[c + j];
+        __syncwarp();
+        const int col = n0 + c + lane;
+        if (col >= p.N) continue;
+        const size_t at = (size_t)tok * p.N + col;
+#pragma unroll 1
+        for (int k0 = 0; k0 < rows; k0 += 16) {
+            float o[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                o[k] = 0.f;
+                if (p.residual && k0 + k < rows) o[k] = bf16_bits_to_float(p.residual[at + (size_t)(k0 + k) * p.N]);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                if (k0 + k >= rows) break;
+                const float v = out[(k0 + k) * kOutPitch + lane] + o[k];
+                if (p.y_bf16) static_cast<uint16_t *>(p.y)[at + (size_t)(k0 + k) * p.N] = float_to_bf16_bits(v);
+                else static_cast<float *>(p.y)[at + (size_t)(k0 + k) * p.N] = v;
+            }
+        }
+    }
+}
+
+// The rows that store_tile adds come to L2 while the products run.
+template <int COLS>
+__device__ __forceinline__ void prefetch_residual(const MatmulParams &p, int m, int n0) {
+    if (!p.residual || m >= p.M) return;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32)
+        if (n0 + c < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.residual + (size_t)m * p.N + n0 + c));
+}
+
+// ---- one CTA a tile of 128 tokens x 128 weight rows; K cut among the CTAs of a cluster
+
+struct Many {
+    static constexpr int kCols = 64;      // columns of a warpgroup
+    static constexpr int kStages = 5;     // 160 KB
+    static constexpr int kAcc = 4;        // accumulators: all of tensor memory
+    static constexpr int kPitch = 132;    // floats of a row of the join
+    static constexpr size_t kRing = kStages * 2 * kTileBytes;
+    static constexpr size_t kSmem = 1024 + kRing + kOutBytes + kScaleBytes + (2 * kStages + 2 * kAcc + 2 * kScaleRing + 1) * 8 + 16;
+    static_assert(128 * kPitch * 4 <= kRing, "the sums of the join take the place of the tiles");
+    static_assert(kSmem <= 227 * 1024, "one CTA to an SM");
+};
+
 // This CTA's share of the tile's rows: the sums of the cluster's CTAs, in rank order.
-template <int NT>
 __device__ __forceinline__ void join_tile(const MatmulParams &p, int unit, int rank, const float *sums) {
-    using F = Many<NT>;
     int rt, ct;
     tile_at(p, unit, &rt, &ct);
-    for (int e = rank * kManyThreads + threadIdx.x; e < 128 * (NT / 4); e += p.split * kManyThreads) {
-        const int r = e / (NT / 4), c = e % (NT / 4) * 4, tok = rt * 128 + r;
+#pragma unroll 1
+    for (int e = rank * kManyThreads + threadIdx.x; e < 128 * 32; e += p.split * kManyThreads) {
+        const int r = e >> 5, c = (e & 31) * 4, tok = rt * 128 + r;
         if (tok >= p.M) continue;
         float4 part[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (k < p.split) part[k] = peer_float4(sums + r * F::kPitch + c, k);
+            if (k < p.split) part[k] = peer_float4(sums + r * Many::kPitch + c, k);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (k < p.split) v.x += part[k].x, v.y += part[k].y, v.z += part[k].z, v.w += part[k].w;
-        store_y4(p, tok, ct * NT + c, v);
+        store_y4(p, tok, ct * 128 + c, v);
     }
 }
 
-template <int NT>
 __global__ void __launch_bounds__(kManyThreads, 1)
     many_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const MatmulParams p) {
-    using F = Many<NT>;
+    using F = Many;
     constexpr int NS = F::kStages, NB = F::kAcc, COLS = F::kCols;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *const sX = smem, *const sW = smem + NS * kTileBytes;
     float *const sOut = reinterpret_cast<float *>(smem + F::kRing);
-    uint64_t *const full = reinterpret_cast<uint64_t *>(smem + F::kRing + F::kOut);
+    uint64_t *const full = reinterpret_cast<uint64_t *>(smem + F::kRing + kOutBytes + kScaleBytes);
     uint64_t *const empty = full + NS, *const acc_full = empty + NS, *const acc_empty = acc_full + NB, *const done = acc_empty + NB;
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    ScaleRing scales;
+    scales.entries = reinterpret_cast<float *>(smem + F::kRing + kOutBytes);
+    scales.full = done + 1;
+    scales.empty = scales.full + kScaleRing;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(scales.empty + kScaleRing);
     int *const failed_slot = reinterpret_cast<int *>(tmem_slot + 1);
 
     if (p.force_timeout) {
@@ -357,6 +458,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 8);
         }
+        scales.init();
         mbar_init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -369,155 +471,278 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     pdl_wait_trigger();
 
     const int group = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;  // which half of the columns, and which token of the tile
-    if (group < 0) {
-        if constexpr (F::kShift) registers_down<F::kFewRegs>();
-        int issued = 0, fails = 0;  // fills so far, up to multiples of 2 NS
-        if (warp == 0 && lane == 0) {
-            bool ok = true;
-            int s = 0, turn = 0;    // the stage, and how often the ring went round
-            for (int t = unit; t < tiles && ok; t += units) {
-                int rt, ct;
-                tile_at(p, t, &rt, &ct);
-                for (int i = 0; i < n; ++i) {
-                    if (turn > 0 && !(ok = fp8_wait(&empty[s], (turn - 1) & 1, p.status))) break;
-                    mbar_expect_tx(&full[s], kTileBytes + F::kWeightBytes);
-                    tma_tile(sX + s * kTileBytes, &tmX, (c0 + i) * kFp8Block, rt * 128, &full[s]);
-                    tma_tile(sW + s * F::kWeightBytes, &tmW, (c0 + i) * kFp8Block, ct * NT, &full[s]);
-                    if (++s == NS) s = 0, ++turn;
-                }
-            }
-            issued = turn > 1 ? (turn & 1 ? NS : 2 * NS) + s : turn * NS + s;
-        } else if (warp == 1) {
-            bool ok = true;
-            int s = 0, ring = 0, b = 0, turn = 0;  // stage and its parity, accumulator and how often it was used
-            for (int t = unit; t < tiles && ok; t += units)
-                for (int i = 0; i < n; ++i) {
-                    ok = __all_sync(~0u, (turn == 0 || fp8_wait(&acc_empty[b], (turn - 1) & 1, p.status)) && fp8_wait(&full[s], ring, p.status));
-                    if (!ok) break;
-                    tc_fence_after();
-                    umma_block(tmem + b * NT, smem_u32(sX + s * kTileBytes), smem_u32(sW + s * F::kWeightBytes), idesc_e4m3(128, NT));
-                    umma_commit_elected(&empty[s]);
-                    umma_commit_elected(&acc_full[b]);
-                    if (++s == NS) s = 0, ring ^= 1;
-                    if (++b == NB) b = 0, ++turn;
-                }
-            if (lane == 0) *failed_slot = !ok;
-            umma_commit_elected(done);
-            if (!fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
-        }
-        __syncwarp();
-        named_sync(1, 128);
-        fails = *failed_slot;
-        if (tid == 0 && fails) {
-            // after a wait that gave up: the last fill of each stage may be waited for by no product
-            for (int s = 0; s < NS; ++s) {
-                if (issued <= s) continue;
-                const int f = issued - 1 - (issued - 1 - s) % NS;
-                if (!fp8_wait(&full[s], f / NS & 1, p.status)) fp8_wait(&full[s], f / NS & 1, p.status, 8 * kFp8WaitNs);
-            }
-        }
-        __syncwarp();
-        __syncthreads();
-        if (p.split > 1) {
-            cluster_sync();
-            join_tile<NT>(p, unit, rank, reinterpret_cast<const float *>(smem));
-            cluster_sync();
-        }
-    } else {
-        if constexpr (F::kShift) registers_up<F::kManyRegs>();
-        const uint32_t my = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * COLS;
-        constexpr int C = 32;
-        float acc[COLS];
+    float acc[COLS];
+    int issued = 0;  // fills so far, up to multiples of 2 NS
+    if (warp == 0 && lane == 0) {
         bool ok = true;
+        int s = 0, turn = 0;    // the stage, and how often the ring went round
+        for (int t = unit; t < tiles && ok; t += units) {
+            int rt, ct;
+            tile_at(p, t, &rt, &ct);
+            for (int i = 0; i < n; ++i) {
+                if (turn > 0 && !(ok = fp8_wait(&empty[s], (turn - 1) & 1, p.status))) break;
+                mbar_expect_tx(&full[s], 2 * kTileBytes);
+                tma_tile(sX + s * kTileBytes, &tmX, (c0 + i) * kFp8Block, rt * 128, &full[s]);
+                tma_tile(sW + s * kTileBytes, &tmW, (c0 + i) * kFp8Block, ct * 128, &full[s]);
+                if (++s == NS) s = 0, ++turn;
+            }
+        }
+        issued = turn > 1 ? (turn & 1 ? NS : 2 * NS) + s : turn * NS + s;
+    } else if (warp == 1) {
+        bool ok = true;
+        int s = 0, ring = 0, b = 0, turn = 0;  // stage and its parity, accumulator and how often it was used
+        for (int t = unit; t < tiles && ok; t += units)
+            for (int i = 0; i < n; ++i) {
+                ok = __all_sync(~0u, (turn == 0 || fp8_wait(&acc_empty[b], (turn - 1) & 1, p.status)) && fp8_wait(&full[s], ring, p.status));
+                if (!ok) break;
+                tc_fence_after();
+                umma_block(tmem + b * 128, smem_u32(sX + s * kTileBytes), smem_u32(sW + s * kTileBytes), idesc_e4m3(128, 128));
+                umma_commit_elected(&empty[s]);
+                umma_commit_elected(&acc_full[b]);
+                if (++s == NS) s = 0, ring ^= 1;
+                if (++b == NB) b = 0, ++turn;
+            }
+        if (lane == 0) *failed_slot = !ok;
+        umma_commit_elected(done);
+        if (!fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
+    } else if (warp == 2) {
+        bool ok = true;
+        for (int t = unit; t < tiles && ok; t += units) {
+            int rt, ct;
+            tile_at(p, t, &rt, &ct);
+            ok = scales.copy_tile(p, rt * 128, ct, c0, n, lane);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp >= 4) {
+        const uint32_t my = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * COLS;
+        bool ok = true, early = false;  // early: the next block was seen to be ready
         int b = 0, ring = 0;
         for (int t = unit; t < tiles && ok; t += units) {
             int rt, ct;
             tile_at(p, t, &rt, &ct);
-            const int m = rt * 128 + row, n0 = ct * NT + group * COLS;
-            const int last_wb = (p.N - 1) >> 7, wb = (n0 >> 7) < last_wb ? n0 >> 7 : last_wb;  // columns behind the last are not stored
-            const float *const xs = p.xs + (size_t)(m < p.M ? m : p.M - 1) * p.KB + c0, *const ws = p.ws + (size_t)wb * p.KB + c0;
+            const int m = rt * 128 + row, n0 = ct * 128 + group * COLS;
 #pragma unroll
             for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
-            if (p.residual && !p.direct && p.split == 1 && m < p.M)  // the rows that are added come to L2 while the products run
-#pragma unroll
-                for (int c = 0; c < COLS; c += 32)
-                    if (n0 + c < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.residual + (size_t)m * p.N + n0 + c));
-            float sx = xs[0], sw = ws[0];
+            if (p.split == 1) prefetch_residual<COLS>(p, m, n0);
             for (int i = 0; i < n; ++i) {
-                const float nx = i + 1 < n ? xs[i + 1] : 0.f, nw = i + 1 < n ? ws[i + 1] : 0.f;  // on their way during this block
-                ok = __all_sync(~0u, fp8_wait(&acc_full[b], ring, p.status));
+                ok = early || __all_sync(~0u, fp8_wait(&scales.full[scales.e], scales.turn & 1, p.status) && fp8_wait(&acc_full[b], ring, p.status));
                 if (!ok) break;
                 tc_fence_after();
-                const float sc = sx * sw;
-                uint32_t v[2][C];
-                tmem_ld<C>(my + b * NT, v[0]);
-#pragma unroll
-                for (int c = 0; c < COLS / C; ++c) {
-                    tmem_wait(v[c & 1]);
-                    if (c + 1 < COLS / C) {
-                        tmem_ld<C>(my + b * NT + (c + 1) * C, v[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&acc_empty[b]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < C; ++j) acc[c * C + j] = fmaf(__uint_as_float(v[c & 1][j]), sc, acc[c * C + j]);
-                }
+                const float *const sc = scales.entries + scales.e * kScaleEntry;
+                const float s0 = sc[row] * sc[128];
+                const int this_b = b, this_e = scales.e;
+                scales.next();
                 if (++b == NB) b = 0, ring ^= 1;
-                sx = nx;
-                sw = nw;
+                bool next = false;
+                add_block<COLS>(acc, my + this_b * 128, s0, s0, COLS,
+                                [&] { next = mbar_test(&scales.full[scales.e], scales.turn & 1) && mbar_test(&acc_full[b], ring); },
+                                [&] {
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) {
+                                        mbar_arrive(&acc_empty[this_b]);
+                                        mbar_arrive(&scales.empty[this_e]);
+                                    }
+                                });
+                early = __all_sync(~0u, next);
             }
-            if (!ok || p.split > 1) continue;
-            if (p.direct) {
-                if (m < p.M && n0 < p.N) store_row(p, (size_t)m * p.N + n0, p.N - n0, acc);
-                continue;
-            }
-            // rows that keep no alignment leave through shared memory, 32 rows x 32 columns a warp at a time
-            float *const out = sOut + (warp - 4) * 32 * F::kOutPitch;
-            const int tok = rt * 128 + (warp & 3) * 32, rows = p.M - tok < 32 ? p.M - tok : 32;
-#pragma unroll
-            for (int c = 0; c < COLS; c += 32) {
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) out[lane * F::kOutPitch + j] = acc[c + j];
-                __syncwarp();
-                const int col = n0 + c + lane;
-                if (col >= p.N) continue;
-                const size_t at = (size_t)tok * p.N + col;
-#pragma unroll 1
-                for (int k0 = 0; k0 < rows; k0 += 8) {
-                    float o[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        o[k] = 0.f;
-                        if (p.residual && k0 + k < rows) o[k] = bf16_bits_to_float(p.residual[at + (size_t)(k0 + k) * p.N]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if (k0 + k >= rows) break;
-                        const float v = out[(k0 + k) * F::kOutPitch + lane] + o[k];
-                        if (p.y_bf16) static_cast<uint16_t *>(p.y)[at + (size_t)(k0 + k) * p.N] = float_to_bf16_bits(v);
-                        else static_cast<float *>(p.y)[at + (size_t)(k0 + k) * p.N] = v;
-                    }
-                }
-            }
+            if (ok && p.split == 1) store_tile<COLS>(p, rt * 128 + (warp & 3) * 32, n0, lane, acc, sOut + (warp - 4) * 32 * kOutPitch);
         }
-        __syncwarp();
-        __syncthreads();
-        if (p.split > 1) {
-            // one tile per cluster; the tiles of the ring are used up: their place takes the sums, a row per token
-            float *const sums = reinterpret_cast<float *>(smem) + row * F::kPitch + group * COLS;
-#pragma unroll
-            for (int j = 0; j < COLS; j += 4) *reinterpret_cast<float4 *>(sums + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-            cluster_sync();
-            join_tile<NT>(p, unit, rank, reinterpret_cast<const float *>(smem));
-            cluster_sync();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (tid == 0 && *failed_slot)  // after a wait that gave up: the last fill of each stage may be waited for by no product
+        for (int s = 0; s < NS; ++s) {
+            if (issued <= s) continue;
+            const int f = issued - 1 - (issued - 1 - s) % NS;
+            if (!fp8_wait(&full[s], f / NS & 1, p.status)) fp8_wait(&full[s], f / NS & 1, p.status, 8 * kFp8WaitNs);
         }
+    __syncwarp();
+    __syncthreads();
+    if (p.split > 1) {
+        // one tile per cluster; the tiles of the ring are used up: their place takes the sums, a row per token
+        float *const sums = reinterpret_cast<float *>(smem);
+        if (warp >= 4) {
+#pragma unroll
+            for (int j = 0; j < COLS; j += 4)
+                *reinterpret_cast<float4 *>(sums + row * F::kPitch + group * COLS + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+        }
+        cluster_sync();
+        join_tile(p, unit, rank, sums);
+        cluster_sync();
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) tmem_free(tmem, 512);
+}
+
+// ---- a pair of CTAs a tile of 256 tokens x NT weight rows: each CTA copies 128 tokens and half of the weight rows, the even one
+// issues the products of both (cta_group::2), and each adds up its own tokens.  A CTA reads (128 + NT / 2) x 128 bytes per
+// 128 x NT of output, where one that is alone reads (128 + NT) x 128: the 48 bytes a cycle that reach an SM bound both.
+
+template <int NT>
+struct Pair {
+    static constexpr int kCols = NT / 2;                    // columns of a warpgroup
+    static constexpr uint32_t kWeightBytes = NT / 2 * 128;  // of a CTA
+    static constexpr int kStages = 5;
+    static constexpr int kPlace = NT == 128 ? 128 : 256;    // columns between accumulators
+    static constexpr int kAcc = 512 / kPlace;
+    // registers a thread: 168 at launch; the sums and 64 values on their way take more, which the first warpgroup leaves
+    static constexpr bool kShift = NT > 128;
+    static constexpr int kFewRegs = 56, kManyRegs = 224;
+    static constexpr size_t kRing = kStages * (kTileBytes + kWeightBytes);
+    static constexpr size_t kSmem = 1024 + kRing + kOutBytes + kScaleBytes + (2 * kStages + 2 * kAcc + 2 * kScaleRing + 1) * 8 + 16;
+    static_assert(kSmem <= 227 * 1024, "one CTA to an SM");
+    static_assert(kFewRegs + 2 * kManyRegs <= 3 * 168, "shares of the registers at launch");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const MatmulParams p) {
+    using F = Pair<NT>;
+    constexpr int NS = F::kStages, NB = F::kAcc, COLS = F::kCols;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *const sX = smem, *const sW = smem + NS * kTileBytes;
+    float *const sOut = reinterpret_cast<float *>(smem + F::kRing);
+    uint64_t *const full = reinterpret_cast<uint64_t *>(smem + F::kRing + kOutBytes + kScaleBytes);  // the even CTA's serve both
+    uint64_t *const empty = full + NS, *const acc_full = empty + NS, *const acc_empty = acc_full + NB, *const done = acc_empty + NB;
+    ScaleRing scales;
+    scales.entries = reinterpret_cast<float *>(smem + F::kRing + kOutBytes);
+    scales.full = done + 1;
+    scales.empty = scales.full + kScaleRing;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(scales.empty + kScaleRing);
+    int *const failed_slot = reinterpret_cast<int *>(tmem_slot + 1);
+
+    if (p.force_timeout) {
+        forced_timeout(done, p.status);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, rank = blockIdx.x & 1, n = p.KB;
+    const int tiles = p.row_tiles * p.col_tiles;
+
+    if (tid == 0) {
+        *failed_slot = 0;
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 16);
+        }
+        scales.init();
+        mbar_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+    tc_fence_before();
+    cluster_sync();  // the other CTA's barriers are set up too
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait_trigger();
+
+    const int group = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
+    if (group < 0) {
+        if constexpr (F::kShift) registers_down<F::kFewRegs>();
+        if (warp == 0 && lane == 0) {
+            bool ok = true;
+            int s = 0, turn = 0;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int rt, ct;
+                tile_at(p, t, &rt, &ct);
+                for (int i = 0; i < n; ++i) {
+                    if (turn > 0 && !(ok = fp8_wait(&empty[s], (turn - 1) & 1, p.status))) break;
+                    if (rank == 0) mbar_expect_tx(&full[s], 2 * (kTileBytes + F::kWeightBytes));
+                    const uint32_t bar = peer_address(&full[s], 0);
+                    tma_tile_pair(sX + s * kTileBytes, &tmX, i * kFp8Block, rt * 256 + rank * 128, bar);
+                    tma_tile_pair(sW + s * F::kWeightBytes, &tmW, i * kFp8Block, ct * NT + rank * (NT / 2), bar);
+                    if (++s == NS) s = 0, ++turn;
+                }
+            }
+            if (!ok) *failed_slot = 1;
+        } else if (warp == 1 && rank == 0) {
+            bool ok = true;
+            int s = 0, ring = 0, b = 0, turn = 0;
+            for (int t = pair; t < tiles && ok; t += pairs)
+                for (int i = 0; i < n; ++i) {
+                    ok = __all_sync(~0u, (turn == 0 || fp8_wait(&acc_empty[b], (turn - 1) & 1, p.status)) && fp8_wait(&full[s], ring, p.status));
+                    if (!ok) break;
+                    tc_fence_after();
+                    umma_block_pair(tmem + b * F::kPlace, smem_u32(sX + s * kTileBytes), smem_u32(sW + s * F::kWeightBytes), idesc_e4m3_pair(NT));
+                    umma_commit_pair(&empty[s]);
+                    umma_commit_pair(&acc_full[b]);
+                    if (++s == NS) s = 0, ring ^= 1;
+                    if (++b == NB) b = 0, ++turn;
+                }
+            if (!ok && lane == 0) *failed_slot = 1;
+            umma_commit_pair(done);
+        }
+        if (warp == 2) {
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int rt, ct;
+                tile_at(p, t, &rt, &ct);
+                ok = scales.copy_tile(p, rt * 256 + rank * 128, (ct * NT) >> 7, 0, n, lane);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+        // in both CTAs: the products are done, and what they signal has arrived
+        if (warp == 1 && !fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
+    } else {
+        if constexpr (F::kShift) registers_up<F::kManyRegs>();
+        const uint32_t my = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * COLS;
+        float acc[COLS];
+        bool ok = true, early = false;
+        int b = 0, ring = 0;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            int rt, ct;
+            tile_at(p, t, &rt, &ct);
+            const int tok = rt * 256 + rank * 128, m = tok + row, n0 = ct * NT + group * COLS, cut = (128 - (n0 & 127)) / 32;
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+            prefetch_residual<COLS>(p, m, n0);
+            // this warpgroup's first block of weight rows among the tile's two, and its second, if it has one
+            const int w0 = (n0 >> 7) - ((ct * NT) >> 7), w1 = NT == 192 && w0 == 0 ? 1 : w0;
+            for (int i = 0; i < n; ++i) {
+                ok = early || __all_sync(~0u, fp8_wait(&scales.full[scales.e], scales.turn & 1, p.status) && fp8_wait(&acc_full[b], ring, p.status));
+                if (!ok) break;
+                tc_fence_after();
+                const float *const sc = scales.entries + scales.e * kScaleEntry;
+                const float x = sc[row], s0 = x * sc[128 + w0], s1 = NT == 192 ? x * sc[128 + w1] : s0;
+                const int this_b = b, this_e = scales.e;
+                scales.next();
+                if (++b == NB) b = 0, ring ^= 1;
+                bool next = false;
+                add_block<COLS>(acc, my + this_b * F::kPlace, s0, s1, NT == 192 ? cut : COLS,
+                                [&] { next = mbar_test(&scales.full[scales.e], scales.turn & 1) && mbar_test(&acc_full[b], ring); },
+                                [&] {
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) {
+                                        mbar_arrive_peer(peer_address(&acc_empty[this_b], 0));
+                                        mbar_arrive(&scales.empty[this_e]);
+                                    }
+                                });
+                early = __all_sync(~0u, next);
+            }
+            if (ok) store_tile<COLS>(p, tok + (warp & 3) * 32, n0, lane, acc, sOut + (warp - 4) * 32 * kOutPitch);
+        }
+        if (!ok && lane == 0) *failed_slot = 1;
+    }
+    __syncwarp();
+    __syncthreads();
+    if (*failed_slot && tid == 0) {
+        // After a wait that gave up, copies may be on their way that no barrier of this CTA counts: give them time to land.
+        const uint64_t began = global_ns();
+        while (global_ns() - began < 20000000ull) {
+        }
+    }
+    tc_fence_before();
+    cluster_sync();  // no CTA leaves while the other's products, commits or arrivals may reach it
+    if (warp == 1) tmem_free_pair(tmem, 512);
 }
 
 // ----------------------------------------------------------------------------- host
@@ -533,19 +758,30 @@ cudaError_t launch_few(const MatmulParams &p, const void *x, const void *W, cuda
                             p.split, false, mw, mx, p);
 }
 
-template <int NT>
 cudaError_t launch_many(MatmulParams p, const void *x, const void *W, cudaStream_t st) {
     static bool done[64] = {};
-    const cudaError_t e = allow_smem(many_kernel<NT>, Many<NT>::kSmem, done);
+    const cudaError_t e = allow_smem(many_kernel, Many::kSmem, done);
     if (e != cudaSuccess) return e;
     CUtensorMap mw, mx;
-    if (!byte_tile_map(&mw, W, p.N, p.K, NT) || !byte_tile_map(&mx, x, p.M, p.K, 128)) return cudaErrorInvalidValue;
-    p.direct = p.N % 16 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 31) == 0;
+    if (!byte_tile_map(&mw, W, p.N, p.K, 128) || !byte_tile_map(&mx, x, p.M, p.K, 128)) return cudaErrorInvalidValue;
     p.row_tiles = (p.M + 127) / 128;
-    p.col_tiles = (p.N + NT - 1) / NT;
-    const long tiles = (long)p.row_tiles * p.col_tiles, slots = (long)1 * sm_count();
+    p.col_tiles = (p.N + 127) / 128;
+    const long tiles = (long)p.row_tiles * p.col_tiles, slots = sm_count();
     const long grid = p.split > 1 ? tiles * p.split : tiles < slots ? tiles : slots;
-    return launch_kernel_as(many_kernel<NT>, dim3((unsigned)grid), dim3(kManyThreads), Many<NT>::kSmem, st, p.split, false, mx, mw, p);
+    return launch_kernel_as(many_kernel, dim3((unsigned)grid), dim3(kManyThreads), Many::kSmem, st, p.split, false, mx, mw, p);
+}
+
+template <int NT>
+cudaError_t launch_pair(MatmulParams p, const void *x, const void *W, cudaStream_t st) {
+    static bool done[64] = {};
+    const cudaError_t e = allow_smem(pair_kernel<NT>, Pair<NT>::kSmem, done);
+    if (e != cudaSuccess) return e;
+    CUtensorMap mw, mx;
+    if (!byte_tile_map(&mw, W, p.N, p.K, NT / 2) || !byte_tile_map(&mx, x, p.M, p.K, 128)) return cudaErrorInvalidValue;
+    p.row_tiles = (p.M + 255) / 256;
+    p.col_tiles = (p.N + NT - 1) / NT;
+    const long tiles = (long)p.row_tiles * p.col_tiles, slots = sm_count() / 2;
+    return launch_kernel(pair_kernel<NT>, dim3((unsigned)(2 * (tiles < slots ? tiles : slots))), dim3(kManyThreads), Pair<NT>::kSmem, st, mx, mw, p);
 }
 
 // CTAs per cluster: as many as keep at least `least` blocks each and do not pass the CTAs that run at once.
@@ -583,11 +819,18 @@ extern "C" int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_
         set_variant("fp8_matmul<tokens%d,split%d>", nt, p.split);
         ce = nt == 16 ? launch_few<16>(p, x, W, st) : nt == 32 ? launch_few<32>(p, x, W, st) : launch_few<64>(p, x, W, st);
     } else {
-        const long rows = (M + 127) / 128, wide = rows * ((N + 255) / 256);
-        const bool use_wide = wide >= sms;
-        p.split = use_wide ? 1 : split_of(rows * ((N + 127) / 128), p.KB, sms, 4);
-        set_variant("fp8_matmul<tile128x%d,split%d>", use_wide ? 256 : 128, p.split);
-        ce = use_wide ? launch_many<256>(p, x, W, st) : launch_many<128>(p, x, W, st);
+        p.direct = N % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 31) == 0;
+        const char *ev = getenv("PAIR"); const int w = ev ? atoi(ev) : 256;
+        if (w) {
+            p.split = 1;
+            set_variant("fp8_matmul<pair256x%d>", w);
+            ce = w == 256 ? launch_pair<256>(p, x, W, st) : w == 192 ? launch_pair<192>(p, x, W, st) : launch_pair<128>(p, x, W, st);
+        } else {
+        const long rows = (M + 127) / 128;
+        p.split = split_of(rows * ((N + 127) / 128), p.KB, sms, 4);
+        set_variant("fp8_matmul<tile128x128,split%d>", p.split);
+        ce = launch_many(p, x, W, st);
+        }
     }
     return launched(ce);
 }
