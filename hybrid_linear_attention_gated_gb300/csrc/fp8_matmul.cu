@@ -9,13 +9,12 @@
 //    16 to 64 tokens on the columns, so that a product of few tokens still fills the tensor core's rows.  K is cut among the
 //    1 to 8 CTAs of a cluster, which add their sums through distributed shared memory in rank order: one launch, no
 //    workspace, no atomics.
-//  * More tokens (`many_kernel`): 128 tokens on the lanes, 128 or 256 weight rows on the columns.  A thread's row has one
-//    token scale and its columns one weight scale per block, so scaling is one multiplication per block and one FMA per
-//    value.
+//  * More tokens (`many_kernel`, `pair_kernel`): 128 tokens on the lanes of a CTA, 128 weight rows (192 or 256 of a pair of CTAs) on the
+//    columns.  A thread's row has one token scale and its columns one or two weight scales per block, so scaling is one
+//    multiplication per block and one FMA per value; a warp copies the scales eight blocks ahead.
 //
 // Every wait is bounded (see tc_gemm.cu for the drain order): a wait that gives up sets the device status word, the roles
 // leave their loops, issued products and copies are waited for, and tensor memory is freed.
-#include <cstdlib>
 #include "fp8.cuh"
 
 namespace hla {
@@ -234,6 +233,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 // ----------------------------------------------------------------------------- more tokens
 
 constexpr int kManyThreads = 384;  // a warpgroup of copies and products, two of sums
+// registers a thread: 168 at launch; the sums and what is on its way take more, which the first warpgroup leaves
+constexpr int kFewRegs = 56, kManyRegs = 224;
+static_assert(kFewRegs + 2 * kManyRegs <= 3 * 168, "shares of the registers at launch");
 constexpr int kOutPitch = 33;
 constexpr size_t kOutBytes = 8 * 32 * kOutPitch * 4;  // a warp's 32 rows x 32 columns on their way out
 
@@ -352,30 +354,44 @@ __device__ __forceinline__ void store_tile(const MatmulParams &p, int tok, int n
         if (lane < rows && n0 < p.N) store_row(p, (size_t)(tok + lane) * p.N + n0, p.N - n0, acc);
         return;
     }
-    // rows that keep no alignment leave through shared memory, 32 rows x 32 columns at a time
+    // Rows that keep no alignment leave through shared memory, 32 rows x 32 columns at a time, so that a warp's stores are 64
+    // bytes of one row.  What is added is loaded in as large groups as the registers hold beside the sums: 333 x 7001 tokens
+    // and rows of 4112, 16 rows x 32 columns at once 39 us, 32 x 64 27 us.
+    constexpr int B = COLS == 96 ? 2 : 1, R = COLS == 64 ? 16 : 32;  // blocks of 32 columns, and rows, of a group
 #pragma unroll
-    for (int c = 0; c < COLS; c += 32) {
-        __syncwarp();
+    for (int c0 = 0; c0 < COLS; c0 += 32 * B) {
+        uint16_t o[B][R];
+        const auto load = [&](int h, int k0) {
+            const int col = n0 + c0 + h * 32 + lane;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) out[lane * kOutPitch + j] = acc[c + j];
-        __syncwarp();
-        const int col = n0 + c + lane;
-        if (col >= p.N) continue;
-        const size_t at = (size_t)tok * p.N + col;
+            for (int k = 0; k < R; ++k)
+                o[h][k] = c0 + h * 32 < COLS && col < p.N && k0 + k < rows ? p.residual[(size_t)(tok + k0 + k) * p.N + col] : (uint16_t)0;
+        };
+        if (p.residual && R == 32) {
+#pragma unroll
+            for (int h = 0; h < B; ++h) load(h, 0);
+        }
+#pragma unroll
+        for (int h = 0; h < B; ++h) {
+            if (c0 + h * 32 >= COLS) break;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) out[lane * kOutPitch + j] = acc[(c0 + h * 32 + j) % COLS];
+            __syncwarp();
+            const int col = n0 + c0 + h * 32 + lane;
 #pragma unroll 1
-        for (int k0 = 0; k0 < rows; k0 += 16) {
-            float o[16];
+            for (int k0 = 0; k0 < rows; k0 += R) {
+                if (p.residual && R < 32) load(h, k0);
+                if (col >= p.N) break;
+                const size_t at = (size_t)(tok + k0) * p.N + col;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                o[k] = 0.f;
-                if (p.residual && k0 + k < rows) o[k] = bf16_bits_to_float(p.residual[at + (size_t)(k0 + k) * p.N]);
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                if (k0 + k >= rows) break;
-                const float v = out[(k0 + k) * kOutPitch + lane] + o[k];
-                if (p.y_bf16) static_cast<uint16_t *>(p.y)[at + (size_t)(k0 + k) * p.N] = float_to_bf16_bits(v);
-                else static_cast<float *>(p.y)[at + (size_t)(k0 + k) * p.N] = v;
+                for (int k = 0; k < R; ++k) {
+                    if (k0 + k >= rows) break;
+                    float v = out[(k0 + k) * kOutPitch + lane];
+                    if (p.residual) v += bf16_bits_to_float(o[h][k]);
+                    if (p.y_bf16) static_cast<uint16_t *>(p.y)[at + (size_t)k * p.N] = float_to_bf16_bits(v);
+                    else static_cast<float *>(p.y)[at + (size_t)k * p.N] = v;
+                }
             }
         }
     }
@@ -585,15 +601,10 @@ struct Pair {
     static constexpr int kCols = NT / 2;                    // columns of a warpgroup
     static constexpr uint32_t kWeightBytes = NT / 2 * 128;  // of a CTA
     static constexpr int kStages = 5;
-    static constexpr int kPlace = NT == 128 ? 128 : 256;    // columns between accumulators
-    static constexpr int kAcc = 512 / kPlace;
-    // registers a thread: 168 at launch; the sums and 64 values on their way take more, which the first warpgroup leaves
-    static constexpr bool kShift = NT > 128;
-    static constexpr int kFewRegs = 56, kManyRegs = 224;
+    static constexpr int kAcc = 2, kPlace = 256;            // accumulators, and columns between them
     static constexpr size_t kRing = kStages * (kTileBytes + kWeightBytes);
     static constexpr size_t kSmem = 1024 + kRing + kOutBytes + kScaleBytes + (2 * kStages + 2 * kAcc + 2 * kScaleRing + 1) * 8 + 16;
     static_assert(kSmem <= 227 * 1024, "one CTA to an SM");
-    static_assert(kFewRegs + 2 * kManyRegs <= 3 * 168, "shares of the registers at launch");
 };
 
 template <int NT>
@@ -646,7 +657,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
 
     const int group = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
     if (group < 0) {
-        if constexpr (F::kShift) registers_down<F::kFewRegs>();
+        registers_down<kFewRegs>();
         if (warp == 0 && lane == 0) {
             bool ok = true;
             int s = 0, turn = 0;
@@ -692,7 +703,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
         // in both CTAs: the products are done, and what they signal has arrived
         if (warp == 1 && !fp8_wait(done, 0, p.status)) fp8_wait(done, 0, p.status, 8 * kFp8WaitNs);
     } else {
-        if constexpr (F::kShift) registers_up<F::kManyRegs>();
+        registers_up<kManyRegs>();
         const uint32_t my = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * COLS;
         float acc[COLS];
         bool ok = true, early = false;
@@ -820,16 +831,22 @@ extern "C" int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_
         ce = nt == 16 ? launch_few<16>(p, x, W, st) : nt == 32 ? launch_few<32>(p, x, W, st) : launch_few<64>(p, x, W, st);
     } else {
         p.direct = N % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 31) == 0;
-        const char *ev = getenv("PAIR"); const int w = ev ? atoi(ev) : 256;
-        if (w) {
-            p.split = 1;
-            set_variant("fp8_matmul<pair256x%d>", w);
-            ce = w == 256 ? launch_pair<256>(p, x, W, st) : w == 192 ? launch_pair<192>(p, x, W, st) : launch_pair<128>(p, x, W, st);
+        // The variant whose waves of tiles take the fewest cycles a block of K, measured at 512 to 8192 tokens: 600 for a CTA's
+        // 128 x 128, 900 and 970 for a pair's 256 x 192 and 256 x 256 (512 tokens to 7168 of 4096: 24.4, 20.6, 21.4 us; 256 to 16416
+        // of 7168: 38, 54, 33 us; 256 to 7168 of 4096: 14, 20, 21 us).
+        const auto waves = [](long tiles, long slots) { return (tiles + slots - 1) / slots; };
+        const long rows = (M + 127) / 128L, pairs = (M + 255) / 256L, one = rows * ((N + 127) / 128L);
+        const long cost1 = 600 * waves(one, sms), cost192 = 900 * waves(pairs * ((N + 191) / 192L), sms / 2),
+                   cost256 = 970 * waves(pairs * ((N + 255) / 256L), sms / 2);
+        HLA_REQUIRE(one < 1L << 30, HLA_ERR_UNSUPPORTED);
+        if (cost1 <= cost192 && cost1 <= cost256) {
+            p.split = split_of(one, p.KB, sms, 4);
+            set_variant("fp8_matmul<tile128x128,split%d>", p.split);
+            ce = launch_many(p, x, W, st);
         } else {
-        const long rows = (M + 127) / 128;
-        p.split = split_of(rows * ((N + 127) / 128), p.KB, sms, 4);
-        set_variant("fp8_matmul<tile128x128,split%d>", p.split);
-        ce = launch_many(p, x, W, st);
+            p.split = 1;
+            set_variant("fp8_matmul<pair256x%d>", cost192 < cost256 ? 192 : 256);
+            ce = cost192 < cost256 ? launch_pair<192>(p, x, W, st) : launch_pair<256>(p, x, W, st);
         }
     }
     return launched(ce);
