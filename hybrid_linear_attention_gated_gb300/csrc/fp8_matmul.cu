@@ -5,8 +5,8 @@
 // warps of their own read it back and add it, scaled, to sums in registers, while the next block's product runs into another
 // accumulator.  One warp copies tiles by TMA into a ring, one issues the products.
 //
-//  * Up to 64 tokens (`few_kernel`): bound by HBM, every weight byte is read once.  128 weight rows lie on the lanes and
-//    16 to 64 tokens on the columns, so that a product of few tokens still fills the tensor core's rows.  K is cut among the
+//  * Up to 32 tokens (`few_kernel`): bound by HBM, every weight byte is read once.  128 weight rows lie on the lanes and
+//    16 or 32 tokens on the columns, so that a product of few tokens still fills the tensor core's rows.  K is cut among the
 //    1 to 8 CTAs of a cluster, which add their sums through distributed shared memory in rank order: one launch, no
 //    workspace, no atomics.
 //  * More tokens (`many_kernel`, `pair_kernel`): 128 tokens on the lanes of a CTA, 128 weight rows (192 or 256 of a pair of CTAs) on the
@@ -60,7 +60,7 @@ __device__ __forceinline__ void store_y4(const MatmulParams &p, int m, int col, 
         if (col + j < p.N) store_y(p, at + j, x[j]);
 }
 
-// ----------------------------------------------------------------------------- up to 64 tokens
+// ----------------------------------------------------------------------------- up to 32 tokens
 
 constexpr int kFewThreads = 192;       // copies, products, four warps of sums
 constexpr int kScaleChunk = 32;        // blocks whose scales are in shared memory at once
@@ -68,7 +68,7 @@ constexpr uint32_t kTileBytes = 128 * 128;
 
 template <int NT>
 struct Few {
-    static constexpr int kStages = NT == 16 ? 6 : NT == 32 ? 5 : 4;  // about 100 KB: two CTAs to an SM
+    static constexpr int kStages = NT == 16 ? 6 : 5;                 // about 100 KB: two CTAs to an SM
     static constexpr int kAcc = 4;                                   // accumulators in tensor memory
     static constexpr uint32_t kTokenBytes = NT * 128;
     static constexpr uint32_t kColumns = kAcc * NT;
@@ -116,27 +116,33 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (tid != 0) pdl_wait_trigger();  // the copying thread waits after its first weight tiles
+    if (warp != 0) pdl_wait_trigger();  // the copying thread waits after its first weight tiles
 
     int issued = 0;
     float acc[NT];
     bool ok = true;
-    if (warp == 0 && lane == 0) {
-        const int pre = n < NS ? n : NS;
-        for (int i = 0; i < pre; ++i) {
-            mbar_expect_tx(&full[i], kTileBytes + F::kTokenBytes);
-            tma_tile(sW + i * kTileBytes, &tmW, (c0 + i) * kFp8Block, rb * 128, &full[i]);
-        }
+    if (warp == 0) {
+        // two weight tiles go out before the kernel that writes the tokens is done, the rest once the first scales are on their
+        // way: behind a whole ring of tiles they would arrive microseconds later
+        const int pre = n < 2 ? n : 2;
+        if (lane == 0)
+            for (int i = 0; i < pre; ++i) {
+                mbar_expect_tx(&full[i], kTileBytes + F::kTokenBytes);
+                tma_tile(sW + i * kTileBytes, &tmW, (c0 + i) * kFp8Block, rb * 128, &full[i]);
+            }
         pdl_wait_trigger();
-        for (int i = 0; i < pre; ++i) tma_tile(sX + i * F::kTokenBytes, &tmX, (c0 + i) * kFp8Block, 0, &full[i]);
-        issued = pre;
-        for (int i = pre; i < n; ++i) {
-            const int s = i % NS;
-            if (!fp8_wait(&empty[s], (i / NS - 1) & 1, p.status)) break;
-            mbar_expect_tx(&full[s], kTileBytes + F::kTokenBytes);
-            tma_tile(sW + s * kTileBytes, &tmW, (c0 + i) * kFp8Block, rb * 128, &full[s]);
-            tma_tile(sX + s * F::kTokenBytes, &tmX, (c0 + i) * kFp8Block, 0, &full[s]);
-            issued = i + 1;
+        named_sync(2, 160);
+        if (lane == 0) {
+            for (int i = 0; i < pre; ++i) tma_tile(sX + i * F::kTokenBytes, &tmX, (c0 + i) * kFp8Block, 0, &full[i]);
+            issued = pre;
+            for (int i = pre; i < n; ++i) {
+                const int s = i % NS;
+                if (i >= NS && !fp8_wait(&empty[s], (i / NS - 1) & 1, p.status)) break;
+                mbar_expect_tx(&full[s], kTileBytes + F::kTokenBytes);
+                tma_tile(sW + s * kTileBytes, &tmW, (c0 + i) * kFp8Block, rb * 128, &full[s]);
+                tma_tile(sX + s * F::kTokenBytes, &tmX, (c0 + i) * kFp8Block, 0, &full[s]);
+                issued = i + 1;
+            }
         }
     } else if (warp == 1) {
         int i = 0;
@@ -155,17 +161,27 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     } else if (warp >= 2) {
         const int t = tid - 64;
         const uint32_t my = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        constexpr int kPer = NT * kScaleChunk / 128;
+        float sx[kPer], sw = 0.f;  // this thread's block of a chunk, and every fourth token's scale
+        const auto load_scales = [&](int i0) {
+            const int k = i0 + t % kScaleChunk;
+            if (k < n) sw = p.ws[(size_t)rb * p.KB + c0 + k];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int tok = t / kScaleChunk + j * (128 / kScaleChunk);
+                sx[j] = k < n && tok < p.M ? p.xs[(size_t)tok * p.KB + c0 + k] : 0.f;
+            }
+        };
+        load_scales(0);
+        named_sync(2, 160);
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[j] = 0.f;
         for (int i = 0; i < n; ++i) {  // to the end even after a wait that gave up: the four warps meet at each chunk
-            if (i % kScaleChunk == 0) {  // x_scale * w_scale of the next blocks, a row of tokens per block
-                named_sync(1, 128);
-                const int m = n - i < kScaleChunk ? n - i : kScaleChunk;
-                for (int e = t; e < NT * kScaleChunk; e += 128) {
-                    const int tok = e / kScaleChunk, k = e % kScaleChunk;
-                    if (tok < p.M && k < m)
-                        sScale[k * NT + tok] = p.xs[(size_t)tok * p.KB + c0 + i + k] * p.ws[(size_t)rb * p.KB + c0 + i + k];
-                }
+            if (i % kScaleChunk == 0) {  // x_scale * w_scale of the next blocks, a row of tokens per block; those behind them are loaded
+                if (i > 0) named_sync(1, 128);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) sScale[(t % kScaleChunk) * NT + t / kScaleChunk + j * (128 / kScaleChunk)] = sx[j] * sw;
+                load_scales(i + kScaleChunk);
                 named_sync(1, 128);
             }
             const int b = i % NB;
@@ -811,7 +827,7 @@ extern "C" int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_
                           const hla_bf16 *residual, void *y, int y_dtype, hla_stream stream) {
     HLA_REQUIRE(M >= 1 && N >= 1 && K >= 1 && x && x_scale && W && w_scale && y, HLA_ERR_INVALID_ARG);
     HLA_REQUIRE(y_dtype == HLA_F32 || y_dtype == HLA_BF16, HLA_ERR_INVALID_ARG);
-    HLA_REQUIRE(K % 16 == 0, HLA_ERR_UNSUPPORTED);
+    HLA_REQUIRE(K % 16 == 0 && M <= 1 << 30 && N <= 1 << 30 && K <= 1 << 30, HLA_ERR_UNSUPPORTED);
     HLA_REQUIRE(aligned16(x) && aligned16(x_scale) && aligned16(W) && aligned16(w_scale) && aligned16(residual) && aligned16(y),
                 HLA_ERR_MISALIGNED);
     MatmulParams p = {};
@@ -824,11 +840,11 @@ extern "C" int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_
     const cudaStream_t st = (cudaStream_t)stream;
     const int sms = sm_count();
     cudaError_t ce;
-    if (M <= 64) {
-        const int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    if (M <= 32) {
+        const int nt = M <= 16 ? 16 : 32;
         p.split = split_of((N + 127) / 128, p.KB, 2 * sms, 2);
         set_variant("fp8_matmul<tokens%d,split%d>", nt, p.split);
-        ce = nt == 16 ? launch_few<16>(p, x, W, st) : nt == 32 ? launch_few<32>(p, x, W, st) : launch_few<64>(p, x, W, st);
+        ce = nt == 16 ? launch_few<16>(p, x, W, st) : launch_few<32>(p, x, W, st);
     } else {
         p.direct = N % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 31) == 0;
         // The variant whose waves of tiles take the fewest cycles a block of K, measured at 512 to 8192 tokens: 600 for a CTA's

@@ -636,7 +636,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                 mbar_arrive(&empty[r.s]);
             }
             r.next();
-            if (lane == 0) mbar_arrive(&empty[r.s]);
+            // The up tile's slot is given back once this use of it has begun: earlier, the arrival could count for the use before,
+            // whose products may still be reading (with seven slots it was a gate tile's).
+            ok = __all_sync(~0u, fp8_wait(&full[r.s], r.filled(), p.status));
+            if (ok && lane == 0) mbar_arrive(&empty[r.s]);
             r.next();
             b.next();
         }

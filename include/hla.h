@@ -51,7 +51,7 @@
  *    (skinny_proj_splitk, skinny_proj_splitk_noalloc, skinny_proj_residual_rmsnorm,
  *    kda_qkvg_proj, moe_route_topk, moe_expert_forward, hla_decode_layer; and
  *    attn_paged_decode and attn_paged_sparse with more than 64 query rows per kv head, a bf16 cache
- *    and a bf16 output) can therefore return HLA_OK with invalid outputs; a caller that must know
+ *    and a bf16 output; and fp8_matmul and moe_fp8_forward at any size) can therefore return HLA_OK with invalid outputs; a caller that must know
  *    checks hla_device_status() after synchronising.
  *  - Results are deterministic: every reduction runs in a fixed order, so the
  *    same inputs give bit-identical outputs run to run.
@@ -112,7 +112,7 @@ int hla_version(void);
  * kda_qkvg_proj, skinny_proj_splitk and its no-allocation form, skinny_proj_residual_rmsnorm,
  * moe_route_topk, moe_expert_forward) chains its own kernels at up to 32 tokens, and attn_paged_decode,
  * attn_paged_sparse and attn_select_blocks theirs at any size (the environment variable HLA_PDL=0 / 1
- * turns that off / on at any size) and, inside a caller's chain on the same
+ * turns that off / on at any size), moe_fp8_forward its own two kernels at any size, and, inside a caller's chain on the same
  * stream, continues it.  Its first kernel follows whatever the caller queued before it.
  * -------------------------------------------------------------------------*/
 int hla_chain_begin(hla_stream stream);
@@ -396,7 +396,7 @@ int fp8_quantize(int M, int K, const void *x, int x_dtype, int rows_per_scale, u
  *  x e4m3 [M, K], x_scale fp32 [M, ceil(K / 128)]; W e4m3 [N, K], w_scale fp32 [ceil(N / 128), ceil(K / 128)]; any
  *  scales, not only powers of two (their product is formed in fp32); residual bf16 [M, N] or NULL; y [M, N] fp32 or bf16
  *  (y_dtype), which may be the residual itself when it is bf16.  Products and sums fp32, one rounding to y's type.
- *  M, N, K >= 1, K % 16 == 0.  No workspace: K is cut inside a thread-block cluster.  Runs on tcgen05 with bounded waits
+ *  1 <= M, N, K <= 2^30, K % 16 == 0.  No workspace: K is cut inside a thread-block cluster.  Runs on tcgen05 with bounded waits
  *  at any size (hla_device_status). */
 int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_scale, const uint8_t *W, const float *w_scale,
                const hla_bf16 *residual, void *y, int y_dtype, hla_stream stream);
@@ -577,8 +577,8 @@ unsigned long long hla_launch_count(void);
  * last read.  Synchronous (copies 4 bytes from the device); HLA_ERR_CUDA if that copy fails. */
 int hla_device_status(void);
 /* Test hook for the failure path, with no counterpart on the source pages.  While on != 0,
- * every launch that has bounded device waits (the tensor-core projections, and the attention of more
- * than 64 query rows per kv head with a bf16 cache and output) makes one of them give up (block
+ * every launch that has bounded device waits (the tensor-core projections, fp8_matmul, the second kernel of
+ * moe_fp8_forward, and the attention of more than 64 query rows per kv head with a bf16 cache and output) makes one of them give up (block
  * 0 waits 1 ms on a barrier that nothing arrives at) and records HLA_ERR_DEVICE_TIMEOUT, and
  * every block returns before it allocates tensor memory or issues a copy or an MMA; the
  * launch writes no output.  Other launches are not affected.  This lets a test check the status

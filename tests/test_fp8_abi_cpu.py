@@ -74,7 +74,7 @@ def test_matmul_refusals(lib):
     for kw in (dict(M=0), dict(N=0), dict(K=0), dict(x=None), dict(xs=None), dict(W=None), dict(ws=None), dict(y=None),
                dict(y_dtype=hla.HLA_E4M3), dict(K=-16)):
         assert matmul(lib, **kw) == INVALID, kw
-    for kw in (dict(K=40), dict(K=8)):
+    for kw in (dict(K=40), dict(K=8), dict(M=2**31 - 1), dict(N=2**31 - 1), dict(K=2**31 - 16)):
         assert matmul(lib, **kw) == UNSUPPORTED, kw
     for kw in (dict(x=FAKE + 8), dict(xs=FAKE + 4), dict(W=FAKE + 1), dict(ws=FAKE + 8), dict(residual=FAKE + 2), dict(y=FAKE + 2)):
         assert matmul(lib, **kw) == MISALIGNED, kw
