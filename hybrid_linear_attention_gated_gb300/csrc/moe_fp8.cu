@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     uint64_t *const empty = full + NS, *const acc_full = empty + NS, *const acc_empty = acc_full + NB, *const done = acc_empty + NB;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(done + 2);  // 16-byte aligned, as the tables behind it
     int *const s_int = reinterpret_cast<int *>(tmem_slot + 1);           // active experts, products issued, last part?
-    unsigned long long *const s_mask = reinterpret_cast<unsigned long long *>(tmem_slot + 4);  // tokens that chose each expert
+    uint2 *const s_mask = reinterpret_cast<uint2 *>(tmem_slot + 4);      // tokens that chose each expert, by half of the batch
     int *const s_idx = reinterpret_cast<int *>(s_mask + kMaxExperts);    // [M][k]
     float *const s_w = reinterpret_cast<float *>(s_idx + NT * kMaxTopK);
     uint16_t *const s_unit = reinterpret_cast<uint16_t *>(s_w + NT * kMaxTopK);  // routed units' experts
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     }
     if (warp == 3 && lane < 9) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.x + lane)) : "memory");
     if (warp == 1) tmem_alloc(tmem_slot, F::kColumns);
-    for (int i = tid; i < p.E; i += kMoeThreads) s_mask[i] = 0;
+    for (int i = tid; i < p.E; i += kMoeThreads) s_mask[i] = make_uint2(0u, 0u);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -422,11 +422,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         const float score = 1.f / (1.f + expf(-logit));
         float sum = 0.f;
         for (int j = 0; j < p.k; ++j) sum += __shfl_sync(~0u, score, j);
-        if (lane < p.k && m < p.M) {
+        if (lane < p.k) {
             const float w = score / sum;
             s_idx[m * p.k + lane] = idx;
             s_w[m * p.k + lane] = w;
-            atomicOr(&s_mask[idx], 1ull << m);
+            atomicOr(m < 32 ? &s_mask[idx].x : &s_mask[idx].y, 1u << (m & 31));
             if (blockIdx.x == 0) {
                 if (p.topk_idx) p.topk_idx[m * p.k + lane] = idx;
                 if (p.topk_w) p.topk_w[m * p.k + lane] = w;
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             for (int q = 0; q < T; ++q) rows[q] = p.logits + (size_t)(m0 + q * W < p.M ? m0 + q * W : m0) * p.E;
             choose<8, T>(rows, p.E, p.k, lane, idx, logit);
             record(m0, idx[0], logit[0]);
-            if (T > 1) record(m0 + W, idx[T - 1], logit[T - 1]);
+            if (T > 1 && m0 + W < p.M) record(m0 + W, idx[T - 1], logit[T - 1]);
         }
     } else {
 #pragma unroll 1
@@ -460,10 +460,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     if (warp == 0) {
         int n = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const unsigned long long mask = e0 + lane < p.E ? s_mask[e0 + lane] : 0ull;
-            const uint32_t active = __ballot_sync(~0u, mask != 0);
-            const bool sparse = F::kLists && __popc((uint32_t)mask) <= 8 && __popc((uint32_t)(mask >> 32)) <= 8;
-            if (mask) s_unit[n + __popc(active & ((1u << lane) - 1))] = (uint16_t)(e0 + lane | (sparse ? kSparse : 0));
+            const uint2 mask = e0 + lane < p.E ? s_mask[e0 + lane] : make_uint2(0u, 0u);
+            const bool any = (mask.x | mask.y) != 0;
+            const uint32_t active = __ballot_sync(~0u, any);
+            const bool sparse = F::kLists && __popc(mask.x) <= 8 && __popc(mask.y) <= 8;
+            if (any) s_unit[n + __popc(active & ((1u << lane) - 1))] = (uint16_t)(e0 + lane | (sparse ? kSparse : 0));
             n += __popc(active);
         }
         if (lane == 0) s_int[0] = n;
@@ -614,7 +615,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             }
             const bool sparse = sparse_unit(at.u);
             if (sparse && (at.kb == 0 || t == a0)) {
-                uint32_t left = lane < 16 ? (uint32_t)(s_mask[expert_of(at.u)] >> (lane >> 3) * 32) : 0u;
+                const uint2 mask = s_mask[expert_of(at.u)];
+                uint32_t left = lane < 8 ? mask.x : lane < 16 ? mask.y : 0u;
                 for (int j = 0; j < (lane & 7); ++j) left &= left - 1;
                 from = left ? (lane >> 3) * 32 + __ffs(left) - 1 : -1;
             }
@@ -703,9 +705,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                     sparse = sparse_unit(at.u);
                     both = F::kLists && !sparse;
                     if (sparse) {
-                        const unsigned long long mask = s_mask[expert_of(at.u)];
-                        lists[0] = (uint32_t)mask;
-                        lists[1] = (uint32_t)(mask >> 32);
+                        const uint2 mask = s_mask[expert_of(at.u)];
+                        lists[0] = mask.x;
+                        lists[1] = mask.y;
                     }
                 }
                 if ((both || turn == grp) && ready()) {
@@ -920,7 +922,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                 if (F::kLists && (at.kb == KB2 - 1 || ends)) {
                     // 64 tokens: a unit's sums go to their tokens' (each token belongs to one group)
                     if (sparse) {
-                        uint32_t left = (uint32_t)(s_mask[expert_of(at.u)] >> (grp * 32));
+                        const uint2 mask = s_mask[expert_of(at.u)];
+                        uint32_t left = grp ? mask.y : mask.x;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             if (left) {
