@@ -564,22 +564,16 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         }
         DownAt at;
         at.set(b0, U, KB2);
-        bool early = false;  // the block was seen to be ready during the one before
-        for (int t = b0; t < b1 && ok; ++t) {
-            const uint32_t idesc = sparse_unit(at.u) ? idesc_e4m3(128, 16) : idesc_e4m3(128, NT);
-            ok = early || __all_sync(~0u, (b.turn == 0 || fp8_wait(&acc_empty[b.s], b.freed(), p.status)) && fp8_wait(&full[r.s], r.filled(), p.status));
+        for (int t = b0; t < b1 && ok; ++t, at.next(U, KB2)) {
+            ok = __all_sync(~0u, (b.turn == 0 || fp8_wait(&acc_empty[b.s], b.freed(), p.status)) && fp8_wait(&full[r.s], r.filled(), p.status));
             if (!ok) break;
             tc_fence_after();
-            const Ring<NS> this_r = r;
-            const Ring<NB> this_b = b;
+            umma_block(tmem + b.s * 2 * NT, smem_u32(sA + r.s * F::kTile), smem_u32(sB + r.s * F::kTokens),
+                       sparse_unit(at.u) ? idesc_e4m3(128, 16) : idesc_e4m3(128, NT));
+            umma_commit_elected(&empty[r.s]);
+            umma_commit_elected(&acc_full[b.s]);
             r.next();
             b.next();
-            at.next(U, KB2);
-            const bool next = (b.turn == 0 || mbar_test(&acc_empty[b.s], b.freed())) && mbar_test(&full[r.s], r.filled());
-            umma_block(tmem + this_b.s * 2 * NT, smem_u32(sA + this_r.s * F::kTile), smem_u32(sB + this_r.s * F::kTokens), idesc);
-            umma_commit_elected(&empty[this_r.s]);
-            umma_commit_elected(&acc_full[this_b.s]);
-            early = __all_sync(~0u, next);
         }
         if (lane == 0) s_int[1] = ok;
         umma_commit_elected(done);
