@@ -207,7 +207,7 @@ struct Moe {
     // are the 16 positions of those tokens, not the 64 tokens
     static constexpr bool kLists = NT == 64;
     static constexpr int kSums = NT == 16 ? 16 : 32;                  // of a thread, for gate and for up
-    static constexpr size_t kExchange = (NT == 16 ? 16 : 32) * 1024;  // sums on their way between the groups; y's sums of 64 tokens
+    static constexpr size_t kExchange = (NT == 16 ? 16 : 32) * 1024;  // where the groups' sums meet; y's sums of 64 tokens
     static constexpr size_t kTables = NT * kMaxTopK * 8 + kMaxExperts * 2 + kMaxExperts * 8;
     static constexpr size_t kSmem = 1024 + kSlots * (kTile + kTokens + kScales) + kAcc * 2 * NT * 4 + kExchange + (2 * kSlots + 2 * kAcc + 2) * 8 + 16 + kTables;
     static_assert((2 * kSlots + 2 * kAcc + 2) * 8 % 16 == 0, "the tables are aligned");
@@ -419,7 +419,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     // ---- the choice, by every CTA for itself; the first one writes it out
     constexpr int T = NT == 16 ? 1 : 2, W = kMoeThreads / 32;
     const auto record = [&](int m, int idx, float logit) {
-        const float score = 1.f / (1.f + expf(-logit));
+        // sigmoid, relative to the largest one's exponential where all logits are negative: their scores may all be below fp32
+        const float top = fminf(__shfl_sync(~0u, logit, 0), 0.f);
+        const float score = logit >= 0.f ? 1.f / (1.f + expf(-logit)) : expf(logit - top) / (1.f + expf(logit));
         float sum = 0.f;
         for (int j = 0; j < p.k; ++j) sum += __shfl_sync(~0u, score, j);
         if (lane < p.k) {
@@ -669,8 +671,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
         }
     } else if (warp >= kSumWarp0) {
         // ---- sums, each thread of one weight row.  Up to 32 tokens, and for the gate and up products of a sparse unit, the two
-        // groups of four warps take every other block of K and all tokens (or positions), and exchange halves of
-        // their sums where a segment ends; otherwise each takes its half of the tokens of every block.
+        // groups of four warps take every other block of K and all tokens (or positions), and their sums meet in shared
+        // memory where a segment ends; otherwise each takes its half of the tokens of every block.
         const int grp = warp >= kSumWarp0 + 4, q4 = warp & 3, row = q4 * 32 + lane;
         const int st = tid - kSumWarp0 * 32;
         const uint32_t my = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
@@ -796,7 +798,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                             e4m3x4(h0 * inv, h1 * inv, h2 * inv, h3 * inv);
                         if (hit) *hs = shared_unit(at.u) ? sc : sc * s_w[m * p.k + lane];
                     };
-                    // sums of the positions [first, first + n) into shared memory
                     if (!both) {
                         if (grp) {
 #pragma unroll

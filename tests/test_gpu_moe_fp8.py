@@ -54,6 +54,10 @@ def test_full_size():
         x = layer.tokens(M, M)
         # one of 18432 values of h on another side of a rounding border moves y by 2^-4 / 136 of itself: bf16 rounding dominates
         check(layer, x, torch.randn(M, 7168, device=dev, generator=torch.Generator(dev).manual_seed(M)).to(BF), rel_limit=2.0 ** -8)
+        ws = layer.workspace(M)
+        first = layer.run(x, ws=ws)[0]
+        for _ in range(3):  # the same bits, however the CTAs' work falls
+            assert torch.equal(layer.run(x, ws=ws)[0], first)
 
 
 @pytest.mark.parametrize("M", [16, 24, 40, 64])
@@ -127,6 +131,24 @@ def test_nan_reaches_only_its_tokens(M):
         z, idx, _ = layer.run(xx)
         assert torch.all(z[1].isnan()) and torch.equal(z[0], y[0]) and torch.equal(z[2:], y[2:])
         assert torch.all((idx >= 0) & (idx < 12))
+
+
+def test_scores_below_fp32_keep_their_weights():
+    """Logits near -150: every sigmoid is below the smallest fp32 number, their shares are not."""
+    dev = require_gpu()
+    layer = Moe(hla, dev, 256, 128, 20, 4, 1, seed=13)
+    layer.W_r = (layer.W_r.float() - 150.0 / 256).to(BF)
+    layer.L = layer.descriptor()
+    x = torch.ones(5, 256, device=dev).to(BF) + layer.tokens(5, 1) * 0.05
+    y, idx, w = layer.run(x.contiguous())
+    logits = (x.double() @ layer.W_r.double().T).sort(-1, descending=True).values[:, :5]
+    assert logits.max() < -104 and logits.diff(dim=-1).abs().min() > 1e-3
+    want, bound, want_idx, want_w = layer.reference(x)
+    assert torch.equal(idx.long(), want_idx)
+    # fp32 sums of 256 products of size 0.6 move a logit by 256 * 2^-24 * 150 at most, and a share by as much of itself
+    assert torch.all((w.double() - want_w).abs() <= 3e-3 * want_w) and torch.all(y.isfinite())
+    check_rel = float((y.double() - want).norm() / want.norm())
+    assert check_rel < MOE_FROB_REL
 
 
 def test_graphs_share_a_workspace_and_see_new_inputs():
