@@ -370,6 +370,15 @@ __device__ __forceinline__ void add_parts(const float *at, size_t to_up, size_t 
     }
 }
 
+// The most CTAs that share an item of `blocks` blocks.  n of them stream it in about 600 blocks / n cycles, and the last adds n
+// parts at 400 + 8 M cycles each: least at the root of the quotient.  It counts for layers of few items: 64 tokens, hidden 256, inner
+// 1024, 64 + 1 experts 120 us with all CTAs, 81 with so many (86 with 600 / 3 M, 90 with 600 / 44 M); 23 tokens, hidden 384, inner
+// 768, 8 + 1 experts 35, 22 (29, 23); one token, hidden 256, inner 128, 16 experts 13.9, 12.1.
+__device__ __forceinline__ uint32_t sharers(int blocks, int M) {
+    const float p = sqrtf(600.f * blocks / (400.f + 8.f * M));
+    return p < 1.f ? 1u : p > 1024.f ? 1024u : (uint32_t)p;
+}
+
 template <int NT>
 __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_constant__ MoeMaps maps, const MoeParams p) {
     using F = Moe<NT>;
@@ -478,8 +487,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     // Gate/up items for three quarters of the CTAs or more, but no more than one each (one token of 8 + 1 experts of 2048: 144 on
     // 152), stay whole: what is idle costs nothing while the rest fills the memory, and no parts are joined.
     const int items = U * nI;
-    s1.set(items * KB1, items <= G && items * 4 >= G * 3 ? KB1 : 1, G);
-    s2.set(nR * U * KB2, 1, G);
+    s1.set(items * KB1, items <= G && items * 4 >= G * 3 ? KB1 : 1, min((uint32_t)G, items * sharers(KB1, p.M)));
+    s2.set(nR * U * KB2, 1, min((uint32_t)G, nR * sharers(U * KB2, p.M)));
     const int a0 = s1.start(c), a1 = s1.start(c + 1), b0 = s2.start(c), b1 = s2.start(c + 1);
     int *const barrier = p.count + 2 * G;
     const auto shared_unit = [&](int u) { return u < p.n_shared; };
