@@ -1,15 +1,17 @@
-// The whole mixture-of-experts layer for up to 64 tokens over 8-bit weights with block scales, in two kernels.
+// The whole mixture-of-experts layer for up to 64 tokens over 8-bit weights with block scales.
 //
 //   logits = x W_r^T, the k largest, w = sigmoid / sum; xq = e4m3 blocks of x;
 //   h = SiLU(xq Wg^T) * (xq Wu^T) per chosen and shared expert, hq = e4m3 blocks of h;  y = residual + sum w (hq Wd^T).
 //
 // Bound by HBM: the weights of the distinct chosen experts, 3 Hd I bytes each, are read once; everything else is small.
 //
-//  1. `moe_prep_kernel`: the router's logits (mma.sync, clusters of four CTAs cut K) beside the conversion of x, and the second
+//  1. `moe_prep_kernel`: the router's logits (mma.sync, clusters of four CTAs cut K) beside the conversion of x, and the last
 //     kernel's counters set to zero.
-//  2. `moe_fp8_kernel`, one CTA per SM, a cooperative launch: every CTA derives the choice and the list of active experts from
-//     the logits, and streams an equal, contiguous share of all gate and up tiles, then, after one grid barrier, of all down
-//     tiles.  A tile is 128 weight rows x 128 of K.  The weight rows lie on the lanes of tcgen05 and all tokens of the
+//  2. `moe_choose_kernel`, more than 8 tokens only: the choice, a warp per token.  Fewer are chosen by every CTA of the next kernel for
+//     itself, a launch less.  The whole layer without and with this kernel, 256 experts, top 8: 64 tokens of hidden 1024 124, 113 us;
+//     of hidden 512 16 tokens 33.3, 31.4, 12 tokens 29.0, 28.5, 6 tokens 23.7, 24.0; one token of hidden 256, 16 experts 10.7, 12.0.
+//  3. `moe_fp8_kernel`, one CTA per SM, a cooperative launch: every CTA derives the list of active experts from the choice, and
+//     streams an equal, contiguous share of all gate and up tiles, then, after one grid barrier, of all down tiles.  A tile is 128 weight rows x 128 of K.  The weight rows lie on the lanes of tcgen05 and all tokens of the
 //     batch on the columns (16, 32 or 64): tokens that did not choose the expert cost nothing that the memory does not hide, and
 //     nothing has to be gathered.  Products of one block of K are read back and added, scaled, to sums in registers.
 //     Items cut between CTAs leave their parts in the workspace, and the CTA that comes last adds them in order: no CTA waits
@@ -27,11 +29,12 @@ namespace {
 constexpr int kMaxExperts = 1024;   // routed and shared together
 constexpr int kMaxTopK = 16;
 constexpr int kMaxTokens = 64;
+constexpr int kChooseInside = 8;    // the most tokens that moe_fp8_kernel chooses for itself
 
 // ----------------------------------------------------------------------------- workspace
 
 struct MoeSpace {
-    size_t logits, xq, xs, hq, hs, part, count, total;
+    size_t logits, idx, w, xq, xs, hq, hs, part, count, total;
 };
 
 inline int tokens_padded(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
@@ -50,6 +53,8 @@ MoeSpace moe_space(const hla_moe_fp8 *L, int M) {
         return r;
     };
     s.logits = take((size_t)M * L->n_experts * 4);
+    s.idx = take(M > kChooseInside ? (size_t)M * L->top_k * 4 : 0);
+    s.w = take(M > kChooseInside ? (size_t)M * L->top_k * 4 : 0);
     s.xq = take((size_t)M * L->hidden);
     s.xs = take(NT * (L->hidden / kFp8Block) * 4);
     s.hq = take(U * NT * L->inter);
@@ -60,7 +65,7 @@ MoeSpace moe_space(const hla_moe_fp8 *L, int M) {
     return s;
 }
 
-// ----------------------------------------------------------------------------- first kernel
+// ----------------------------------------------------------------------------- logits and conversion
 
 constexpr int kPrepThreads = 256;
 constexpr int kPrepCluster = 4;
@@ -171,7 +176,82 @@ __global__ void __launch_bounds__(kPrepThreads) __cluster_dims__(kPrepCluster, 1
     cluster_sync();
 }
 
-// ----------------------------------------------------------------------------- second kernel
+// ----------------------------------------------------------------------------- the choice
+
+__device__ __forceinline__ uint32_t ordered(float v) {  // larger floats have larger keys; none is 0
+    const uint32_t b = __float_as_uint(v), k = b & 0x80000000u ? ~b : b | 0x80000000u;
+    return k ? k : 1u;
+}
+__device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
+
+// The k largest of a token's E <= 32 PER logits by one warp, ties to the lower index: lane j gets the jth index and its logit.
+template <int PER>
+__device__ __forceinline__ void choose(const float *logits, int E, int k, int lane, int *idx, float *logit) {
+    uint32_t key[PER], top = 0;
+    int at = 0;  // the largest of this lane's own, the first of equal ones
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = i * 32 + lane;
+        key[i] = e < E ? ordered(__ldcg(logits + e)) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (key[i] > top) top = key[i], at = i;
+#pragma unroll 1
+    for (int j = 0; j < k; ++j) {
+        const uint32_t best = __reduce_max_sync(~0u, top);
+        const uint32_t e = __reduce_min_sync(~0u, top == best ? (uint32_t)(at * 32 + lane) : ~0u);
+        if (lane == j) {
+            *idx = (int)e;
+            *logit = unordered(best);
+        }
+        const bool mine = (e & 31) == lane;
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            key[i] &= mine && i == (int)(e >> 5) ? 0u : ~0u;
+            if (key[i] > top) top = key[i], at = i;
+        }
+    }
+}
+
+// Lane j's jth choice of a token and its weight in the mixture: its sigmoid over the sum of the k.  Relative to the largest one's
+// exponential where all logits are negative: their scores may all be below fp32.
+__device__ __forceinline__ void choose_token(const float *logits, int E, int k, int lane, int *idx, float *w) {
+    float logit = 0.f;
+    *idx = 0;
+    if (E <= 256) choose<8>(logits, E, k, lane, idx, &logit);
+    else choose<32>(logits, E, k, lane, idx, &logit);
+    const float top = fminf(__shfl_sync(~0u, logit, 0), 0.f);
+    const float score = logit >= 0.f ? 1.f / (1.f + expf(-logit)) : expf(logit - top) / (1.f + expf(logit));
+    float sum = 0.f;
+    for (int j = 0; j < k; ++j) sum += __shfl_sync(~0u, score, j);
+    *w = score / sum;
+}
+
+// The choice of many tokens, a warp each.
+struct ChooseParams {
+    int E, k;
+    const float *logits;
+    int32_t *idx, *topk_idx;
+    float *w, *topk_w;
+};
+__global__ void __launch_bounds__(32) moe_choose_kernel(const ChooseParams p) {
+    pdl_wait_trigger();
+    const int lane = threadIdx.x, m = blockIdx.x;
+    int idx;
+    float w;
+    choose_token(p.logits + (size_t)m * p.E, p.E, p.k, lane, &idx, &w);
+    if (lane < p.k) {
+        const int at = m * p.k + lane;
+        p.idx[at] = idx;
+        p.w[at] = w;
+        if (p.topk_idx) p.topk_idx[at] = idx;
+        if (p.topk_w) p.topk_w[at] = w;
+    }
+}
+
+// ----------------------------------------------------------------------------- the experts
 
 constexpr int kMoeThreads = 384;    // copies, products, scales, a warp of the choice only, two groups of four warps of sums
 constexpr int kSumThreads = 256;
@@ -190,6 +270,8 @@ struct MoeParams {
     uint16_t *y;
     int32_t *topk_idx;
     float *topk_w;
+    const int32_t *idx;        // the choice [M, k] of more than kChooseInside tokens, or NULL
+    const float *w;
     uint8_t *hq;
     float *hs, *part;
     int *count;                // [G] parts of cut gate/up items, [G] parts of cut output blocks, [1] grid barrier
@@ -270,53 +352,6 @@ struct Ring {
     __device__ __forceinline__ uint32_t filled() const { return turn & 1; }            // parity of this use's completion
     __device__ __forceinline__ uint32_t freed() const { return (turn - 1) & 1; }       // and of the one before, from the second use on
 };
-
-__device__ __forceinline__ uint32_t ordered(float v) {  // larger floats have larger keys; none is 0
-    const uint32_t b = __float_as_uint(v), k = b & 0x80000000u ? ~b : b | 0x80000000u;
-    return k ? k : 1u;
-}
-__device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
-
-// The k largest logits of each of T tokens by one warp, ties to the lower index: lane j gets the jth index and its logit.  The
-// tokens' chains of dependent steps run side by side.
-template <int PER, int T>
-__device__ __forceinline__ void choose(const float *const (&logits)[T], int E, int k, int lane, int (&idx)[T], float (&logit)[T]) {
-    uint32_t key[T][PER], top[T];
-    int at[T];  // the largest of this lane's own, the first of equal ones
-#pragma unroll
-    for (int q = 0; q < T; ++q)
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = i * 32 + lane;
-            key[q][i] = e < E ? ordered(__ldcg(logits[q] + e)) : 0u;
-        }
-#pragma unroll
-    for (int q = 0; q < T; ++q) {
-        top[q] = 0;
-        at[q] = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[q][i] > top[q]) top[q] = key[q][i], at[q] = i;
-    }
-#pragma unroll 1
-    for (int j = 0; j < k; ++j)
-#pragma unroll
-        for (int q = 0; q < T; ++q) {
-            const uint32_t best = __reduce_max_sync(~0u, top[q]);
-            const uint32_t e = __reduce_min_sync(~0u, top[q] == best ? (uint32_t)(at[q] * 32 + lane) : ~0u);
-            if (lane == j) {
-                idx[q] = (int)e;
-                logit[q] = unordered(best);
-            }
-            const bool mine = (e & 31) == lane;
-            top[q] = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                key[q][i] &= mine && i == (int)(e >> 5) ? 0u : ~0u;
-                if (key[q][i] > top[q]) top[q] = key[q][i], at[q] = i;
-            }
-        }
-}
 
 __device__ __forceinline__ int load_acquire(const int *p) {
     int v;
@@ -425,46 +460,28 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     const uint32_t tmem = *tmem_slot;
     pdl_wait_trigger();
 
-    // ---- the choice, by every CTA for itself; the first one writes it out
-    constexpr int T = NT == 16 ? 1 : 2, W = kMoeThreads / 32;
-    const auto record = [&](int m, int idx, float logit) {
-        // sigmoid, relative to the largest one's exponential where all logits are negative: their scores may all be below fp32
-        const float top = fminf(__shfl_sync(~0u, logit, 0), 0.f);
-        const float score = logit >= 0.f ? 1.f / (1.f + expf(-logit)) : expf(logit - top) / (1.f + expf(logit));
-        float sum = 0.f;
-        for (int j = 0; j < p.k; ++j) sum += __shfl_sync(~0u, score, j);
-        if (lane < p.k) {
-            const float w = score / sum;
-            s_idx[m * p.k + lane] = idx;
-            s_w[m * p.k + lane] = w;
-            atomicOr(m < 32 ? &s_mask[idx].x : &s_mask[idx].y, 1u << (m & 31));
-            if (blockIdx.x == 0) {
-                if (p.topk_idx) p.topk_idx[m * p.k + lane] = idx;
-                if (p.topk_w) p.topk_w[m * p.k + lane] = w;
+    // ---- the choice: of few tokens by every CTA for itself, and the first one writes it out
+    const auto record = [&](int m, int lane, int idx, float w) {
+        s_idx[m * p.k + lane] = idx;
+        s_w[m * p.k + lane] = w;
+        atomicOr(m < 32 ? &s_mask[idx].x : &s_mask[idx].y, 1u << (m & 31));
+    };
+    if (NT == 16 && !p.idx) {
+#pragma unroll 1
+        for (int m = warp; m < p.M; m += kMoeThreads / 32) {
+            int idx;
+            float w;
+            choose_token(p.logits + (size_t)m * p.E, p.E, p.k, lane, &idx, &w);
+            if (lane < p.k) {
+                record(m, lane, idx, w);
+                if (blockIdx.x == 0) {
+                    if (p.topk_idx) p.topk_idx[m * p.k + lane] = idx;
+                    if (p.topk_w) p.topk_w[m * p.k + lane] = w;
+                }
             }
         }
-    };
-    if (p.E <= 256) {
-#pragma unroll 1
-        for (int m0 = warp; m0 < p.M; m0 += W * T) {
-            int idx[T] = {};
-            float logit[T] = {};
-            const float *rows[T];
-#pragma unroll
-            for (int q = 0; q < T; ++q) rows[q] = p.logits + (size_t)(m0 + q * W < p.M ? m0 + q * W : m0) * p.E;
-            choose<8, T>(rows, p.E, p.k, lane, idx, logit);
-            record(m0, idx[0], logit[0]);
-            if (T > 1 && m0 + W < p.M) record(m0 + W, idx[T - 1], logit[T - 1]);
-        }
     } else {
-#pragma unroll 1
-        for (int m = warp; m < p.M; m += W) {
-            int idx[1] = {0};
-            float logit[1] = {0.f};
-            const float *const row[1] = {p.logits + (size_t)m * p.E};
-            choose<32, 1>(row, p.E, p.k, lane, idx, logit);
-            record(m, idx[0], logit[0]);
-        }
+        for (int i = tid; i < p.M * p.k; i += kMoeThreads) record(i / p.k, i % p.k, __ldcg(p.idx + i), __ldcg(p.w + i));
     }
     __syncthreads();
     // units: the shared experts, then the active ones in order
@@ -1109,6 +1126,13 @@ extern "C" int moe_fp8_forward(const hla_moe_fp8 *L, int M, const hla_bf16 *x, c
     const long convert = ((long)M * (Hd / kFp8Block) + per - 1) / per;
     e = launched(launch_kernel(moe_prep_kernel, dim3((unsigned)((q.router_clusters + convert) * kPrepCluster)), dim3(kPrepThreads), 0, st, q));
     if (e != HLA_OK) return e;
+    if (M > kChooseInside) {
+        const ChooseParams r = {E, L->top_k, p.logits, reinterpret_cast<int32_t *>(w + sp.idx), topk_idx, reinterpret_cast<float *>(w + sp.w), topk_w};
+        p.idx = r.idx;
+        p.w = r.w;
+        e = launched(launch_kernel(moe_choose_kernel, dim3((unsigned)M), dim3(32), 0, st, r));
+        if (e != HLA_OK) return e;
+    }
     const cudaError_t ce = NT == 16 ? launch_moe<16>(maps, p, grid, st) : NT == 32 ? launch_moe<32>(maps, p, grid, st) : launch_moe<64>(maps, p, grid, st);
     return launched(ce);
 }

@@ -112,7 +112,7 @@ int hla_version(void);
  * kda_qkvg_proj, skinny_proj_splitk and its no-allocation form, skinny_proj_residual_rmsnorm,
  * moe_route_topk, moe_expert_forward) chains its own kernels at up to 32 tokens, and attn_paged_decode,
  * attn_paged_sparse and attn_select_blocks theirs at any size (the environment variable HLA_PDL=0 / 1
- * turns that off / on at any size), moe_fp8_forward its own two kernels at any size, and, inside a caller's chain on the same
+ * turns that off / on at any size), moe_fp8_forward its own kernels at any size, and, inside a caller's chain on the same
  * stream, continues it.  Its first kernel follows whatever the caller queued before it.
  * -------------------------------------------------------------------------*/
 int hla_chain_begin(hla_stream stream);
@@ -401,7 +401,7 @@ int fp8_quantize(int M, int K, const void *x, int x_dtype, int rows_per_scale, u
 int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_scale, const uint8_t *W, const float *w_scale,
                const hla_bf16 *residual, void *y, int y_dtype, hla_stream stream);
 
-/* The whole mixture-of-experts layer of a decode batch over such weights, in two kernels.
+/* The whole mixture-of-experts layer of a decode batch over such weights, in two kernels, three past 8 tokens.
  *  [VLLM-K3] Part 1 sec. 3 (router, routed and shared experts).
  *  Router, choice and weights as moe_route_topk, from x itself.  Experts as moe_expert_forward, on the values of
  *  xq = fp8_quantize(x, 1 row): h = SiLU(W_gate xq) * (W_up xq), hq = fp8_quantize(h, 1 row),
@@ -410,7 +410,7 @@ int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_scale, cons
  *  x, y bf16 [M, Hd]; residual bf16 [M, Hd] or NULL (y may be the residual, or x); topk_idx int32 [M, k] and topk_w fp32
  *  [M, k] receive the choice, or NULL.  1 <= M <= 64, Hd % 128 == 0, I % 128 == 0, 1 <= k <= 16, k <= E,
  *  E + n_shared <= 1024, n_shared <= 16.
- *  Each active expert's weights are read once per call.  The second kernel is a cooperative launch of at most one block
+ *  Each active expert's weights are read once per call.  The last kernel is a cooperative launch of at most one block
  *  per SM with one grid barrier (bounded, as every wait: hla_device_status), so calls on different streams, with their own
  *  workspaces, run one after another and cannot block each other.  The workspace needs no initialisation and may
  *  serve any later call. */
@@ -577,7 +577,7 @@ unsigned long long hla_launch_count(void);
  * last read.  Synchronous (copies 4 bytes from the device); HLA_ERR_CUDA if that copy fails. */
 int hla_device_status(void);
 /* Test hook for the failure path, with no counterpart on the source pages.  While on != 0,
- * every launch that has bounded device waits (the tensor-core projections, fp8_matmul, the second kernel of
+ * every launch that has bounded device waits (the tensor-core projections, fp8_matmul, the last kernel of
  * moe_fp8_forward, and the attention of more than 64 query rows per kv head with a bf16 cache and output) makes one of them give up (block
  * 0 waits 1 ms on a barrier that nothing arrives at) and records HLA_ERR_DEVICE_TIMEOUT, and
  * every block returns before it allocates tensor memory or issues a copy or an MMA; the

@@ -47,6 +47,20 @@ def test_many_experts(E, k, shared):
         check(layer, layer.tokens(M, M))
 
 
+@pytest.mark.parametrize("M,Hd,I,E,k,shared", [
+    (8, 128, 256, 40, 8, 1), (9, 128, 256, 40, 8, 1), (8, 256, 128, 300, 3, 0), (9, 256, 128, 300, 16, 0),  # either place of the choice
+    (1, 256, 2048, 16, 4, 1), (23, 384, 768, 8, 2, 1), (53, 512, 256, 60, 4, 2), (64, 128, 1024, 64, 8, 1), (2, 2048, 128, 4, 1, 0)])
+def test_few_items_and_either_choice(M, Hd, I, E, k, shared):
+    """Layers of so few output blocks that not all CTAs share them, the choice in the last kernel and in its own."""
+    dev = require_gpu()
+    layer = Moe(hla, dev, Hd, I, E, k, shared, seed=M + Hd)
+    x = layer.tokens(M, M)
+    first = layer.run(x)
+    check(layer, x, got=first)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(layer.run(x), first))
+
+
 def test_full_size():
     dev = require_gpu()
     layer = Moe(hla, dev, 7168, 2048, 256, 8, 1, seed=1)
