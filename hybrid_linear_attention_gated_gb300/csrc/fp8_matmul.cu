@@ -329,35 +329,43 @@ __device__ __forceinline__ void st32b(void *p, const uint32_t (&r)[8]) {
                  "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
-// A thread's row of COLS columns, straight from registers: 32 bytes a store, whole sectors.
+// A thread's row of COLS columns, straight from registers: 32 bytes a store, whole sectors.  What is added is loaded 64 columns
+// at once.
 template <int COLS>
 __device__ __forceinline__ void store_row(const MatmulParams &p, size_t at, int columns, const float (&acc)[COLS]) {
-    if (p.y_bf16) {
-        uint16_t *const y = static_cast<uint16_t *>(p.y) + at;
+    constexpr int B = COLS == 128 ? 64 : 32;
 #pragma unroll
-        for (int c = 0; c < COLS; c += 16) {
-            if (c >= columns) break;
-            uint32_t r[8], w[8] = {};
-            if (p.residual) {
-                const uint4 a = ld_act_v4(p.residual + at + c), b = ld_act_v4(p.residual + at + c + 8);
-                w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-            }
+    for (int c0 = 0; c0 < COLS; c0 += B) {
+        uint4 w[B / 8] = {};
+        if (p.residual) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] = pack_bf16x2(acc[c + 2 * j] + bf16_lo(w[j]), acc[c + 2 * j + 1] + bf16_hi(w[j]));
-            st32b(y + c, r);
+            for (int c = 0; c < B; c += 8)
+                if (c0 + c < COLS && c0 + c < columns) w[c / 8] = ld_act_v4(p.residual + at + c0 + c);
         }
-    } else {
-        float *const y = static_cast<float *>(p.y) + at;
 #pragma unroll
-        for (int c = 0; c < COLS; c += 8) {
-            if (c >= columns) break;
+        for (int c = 0; c < B; c += 16) {
+            if (c0 + c >= COLS || c0 + c >= columns) break;
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                const uint4 &q = w[(c + j) / 8];
+                const uint32_t r = j % 8 == 0 ? q.x : j % 8 == 2 ? q.y : j % 8 == 4 ? q.z : q.w;
+                v[j] = acc[(c0 + c + j) % COLS] + bf16_lo(r);
+                v[j + 1] = acc[(c0 + c + j + 1) % COLS] + bf16_hi(r);
+            }
             uint32_t r[8];
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (p.residual) w = ld_act_v4(p.residual + at + c);
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            if (p.y_bf16) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(acc[c + j] + (j & 1 ? bf16_hi(x[j >> 1]) : bf16_lo(x[j >> 1])));
-            st32b(y + c, r);
+                for (int j = 0; j < 8; ++j) r[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                st32b(static_cast<uint16_t *>(p.y) + at + c0 + c, r);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(v[8 * h + j]);
+                    st32b(static_cast<float *>(p.y) + at + c0 + c + 8 * h, r);
+                }
+            }
         }
     }
 }
@@ -371,43 +379,36 @@ __device__ __forceinline__ void store_tile(const MatmulParams &p, int tok, int n
         return;
     }
     // Rows that keep no alignment leave through shared memory, 32 rows x 32 columns at a time, so that a warp's stores are 64
-    // bytes of one row.  What is added is loaded in as large groups as the registers hold beside the sums: 333 x 7001 tokens
-    // and rows of 4112, 16 rows x 32 columns at once 39 us, 32 x 64 27 us.
-    constexpr int B = COLS == 96 ? 2 : 1, R = COLS == 64 ? 16 : 32;  // blocks of 32 columns, and rows, of a group
+    // bytes of one row.  What is added is loaded as many rows at once as the registers hold beside the sums.  Behind the last row
+    // and column those themselves are loaded: with a condition at each load they wait for one another (280 tokens to rows of 5115 of
+    // K 224: 13.2 us, 8.8 without; 333 to rows of 7001 of 4112: 27.3, 24.8).
+    constexpr int R = COLS == 64 ? 16 : 32;
 #pragma unroll
-    for (int c0 = 0; c0 < COLS; c0 += 32 * B) {
-        uint16_t o[B][R];
-        const auto load = [&](int h, int k0) {
-            const int col = n0 + c0 + h * 32 + lane;
+    for (int c0 = 0; c0 < COLS; c0 += 32) {
+        const int col = n0 + c0 + lane;
+        uint16_t o[R];
+        const auto load = [&](int k0) {
+            const uint16_t *const at = p.residual + (size_t)tok * p.N + (col < p.N ? col : p.N - 1);
 #pragma unroll
-            for (int k = 0; k < R; ++k)
-                o[h][k] = c0 + h * 32 < COLS && col < p.N && k0 + k < rows ? p.residual[(size_t)(tok + k0 + k) * p.N + col] : (uint16_t)0;
+            for (int k = 0; k < R; ++k) o[k] = at[(size_t)(k0 + k < rows ? k0 + k : rows - 1) * p.N];
         };
-        if (p.residual && R == 32) {
+        if (p.residual && R == 32 && rows > 0) load(0);
+        __syncwarp();
 #pragma unroll
-            for (int h = 0; h < B; ++h) load(h, 0);
-        }
-#pragma unroll
-        for (int h = 0; h < B; ++h) {
-            if (c0 + h * 32 >= COLS) break;
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) out[lane * kOutPitch + j] = acc[(c0 + h * 32 + j) % COLS];
-            __syncwarp();
-            const int col = n0 + c0 + h * 32 + lane;
+        for (int j = 0; j < 32; ++j) out[lane * kOutPitch + j] = acc[c0 + j];
+        __syncwarp();
 #pragma unroll 1
-            for (int k0 = 0; k0 < rows; k0 += R) {
-                if (p.residual && R < 32) load(h, k0);
-                if (col >= p.N) break;
-                const size_t at = (size_t)(tok + k0) * p.N + col;
+        for (int k0 = 0; k0 < rows; k0 += R) {
+            if (p.residual && R < 32) load(k0);
+            if (col >= p.N) break;
+            const size_t at = (size_t)(tok + k0) * p.N + col;
 #pragma unroll
-                for (int k = 0; k < R; ++k) {
-                    if (k0 + k >= rows) break;
-                    float v = out[(k0 + k) * kOutPitch + lane];
-                    if (p.residual) v += bf16_bits_to_float(o[h][k]);
-                    if (p.y_bf16) static_cast<uint16_t *>(p.y)[at + (size_t)k * p.N] = float_to_bf16_bits(v);
-                    else static_cast<float *>(p.y)[at + (size_t)k * p.N] = v;
-                }
+            for (int k = 0; k < R; ++k) {
+                if (k0 + k >= rows) break;
+                float v = out[(k0 + k) * kOutPitch + lane];
+                if (p.residual) v += bf16_bits_to_float(o[k]);
+                if (p.y_bf16) static_cast<uint16_t *>(p.y)[at + (size_t)k * p.N] = float_to_bf16_bits(v);
+                else static_cast<float *>(p.y)[at + (size_t)k * p.N] = v;
             }
         }
     }
@@ -610,7 +611,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 
 // ---- a pair of CTAs a tile of 256 tokens x NT weight rows: each CTA copies 128 tokens and half of the weight rows, the even one
 // issues the products of both (cta_group::2), and each adds up its own tokens.  A CTA reads (128 + NT / 2) x 128 bytes per
-// 128 x NT of output, where one that is alone reads (128 + NT) x 128: the 48 bytes a cycle that reach an SM bound both.
+// 128 x NT of output, where one that is alone reads (128 + NT) x 128.  What bounds both is the sums: reading
+// 128 x 256 accumulators back and the barriers take about 900 cycles a block, the products 512.
 
 template <int NT>
 struct Pair {
