@@ -125,9 +125,12 @@ __global__ void __launch_bounds__(kQuantThreads) quant_tiles_kernel(const QuantP
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const long row = rb * 128 + i * 32 + (threadIdx.x >> 3);
-        if (row < p.M && col < p.K) v[i].load(p.x, (size_t)row * p.K + col);
-        else v[i].zero();
+        // the last row again behind it: without conditions the four are loaded together (16416 x 7168 fp32: 85.5 us, 83.3)
+        v[i].load(p.x, (size_t)(row < p.M ? row : p.M - 1) * p.K + (col < p.K ? col : 0));
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (col >= p.K) v[i].zero();
 #pragma unroll
     for (int i = 0; i < 4; ++i) top = max_magnitude(top, v[i].top());
 #pragma unroll
