@@ -11,7 +11,8 @@
 //     itself, a launch less.  The whole layer without and with this kernel, 256 experts, top 8: 64 tokens of hidden 1024 124, 113 us;
 //     of hidden 512 16 tokens 33.3, 31.4, 12 tokens 29.0, 28.5, 6 tokens 23.7, 24.0; one token of hidden 256, 16 experts 10.7, 12.0.
 //  3. `moe_fp8_kernel`, one CTA per SM, a cooperative launch: every CTA derives the list of active experts from the choice, and
-//     streams an equal, contiguous share of all gate and up tiles, then, after one grid barrier, of all down tiles.  A tile is 128 weight rows x 128 of K.  The weight rows lie on the lanes of tcgen05 and all tokens of the
+//     streams an equal, contiguous share of all gate and up tiles, then, after one grid barrier, of all down tiles (small
+//     layers: some of the CTAs).  A tile is 128 weight rows x 128 of K.  The weight rows lie on the lanes of tcgen05 and all tokens of the
 //     batch on the columns (16, 32 or 64): tokens that did not choose the expert cost nothing that the memory does not hide, and
 //     nothing has to be gathered.  Products of one block of K are read back and added, scaled, to sums in registers.
 //     Items cut between CTAs leave their parts in the workspace, and the CTA that comes last adds them in order: no CTA waits
@@ -1005,10 +1006,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                         const int c0 = s2.owner(i0), c1 = s2.owner(i1 - 1);
                         if (last_part(p.count + G + c0, c1 - c0 + 1)) {
 #pragma unroll 1
-                            for (int m = st >> 5; m < p.M; m += kSumThreads / 32) {
-                                float4 v = make_float4(0.f, 0.f, 0.f, 0.f), none = v;
-                                add_parts(p.part + m * 128 + lane * 4, 0, kPart, c0, c1, s2.start(c0) != i0, &v, &none);
+                            for (int m = st >> 5; m < p.M; m += 2 * (kSumThreads / 32)) {  // a second token beside it: 64 of hidden 1024 104 us, 96
+                                const int m2 = m + kSumThreads / 32 < p.M ? m + kSumThreads / 32 : m;
+                                float4 v = make_float4(0.f, 0.f, 0.f, 0.f), v2 = v;
+                                add_parts(p.part + m * 128 + lane * 4, (m2 - m) * 128, kPart, c0, c1, s2.start(c0) != i0, &v, &v2);
                                 finish(m, v);
+                                if (m2 != m) finish(m2, v2);
                             }
                         }
                     }
