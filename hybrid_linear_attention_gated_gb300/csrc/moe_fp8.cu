@@ -409,9 +409,10 @@ __device__ __forceinline__ void add_parts(const float *at, size_t to_up, size_t 
 }
 
 // The most CTAs that share an item of `blocks` blocks.  n of them stream it in about 600 blocks / n cycles, and the last adds n
-// parts at 400 + 8 M cycles each: least at the root of the quotient.  It counts for layers of few items: 64 tokens, hidden 256, inner
-// 1024, 64 + 1 experts 120 us with all CTAs, 81 with so many (86 with 600 / 3 M, 90 with 600 / 44 M); 23 tokens, hidden 384, inner
-// 768, 8 + 1 experts 35, 22 (29, 23); one token, hidden 256, inner 128, 16 experts 13.9, 12.1.
+// parts at 400 + 8 M cycles each: least at the root of the quotient.  It counts for layers of few items.  With all CTAs, when this
+// came in: 64 tokens, hidden 256, inner 1024, 64 + 1 experts 120 us, 81 so; one token, hidden 256, inner 128, 16 experts 13.9,
+// 12.1.  Now, and with 250 + 5 M and 600 + 8 M: 61 tokens, hidden 3200, inner 512, 8 + 1 experts 44.3, 49.9, 45.1 us; 23 tokens,
+// hidden 384, inner 768, 8 + 1 experts 20.9, 24.0, 21.5; the one token 12.2, 14.3, 12.3.
 __device__ __forceinline__ uint32_t sharers(int blocks, int M) {
     const float p = sqrtf(600.f * blocks / (400.f + 8.f * M));
     return p < 1.f ? 1u : p > 1024.f ? 1024u : (uint32_t)p;
