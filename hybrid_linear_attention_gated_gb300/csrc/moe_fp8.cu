@@ -690,7 +690,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             const float *const x = sX + r.s * NT;
             float *const sc = sS + b.s * 2 * NT;
 #pragma unroll
-            for (int m = lane; m < NT; m += 32) sc[m] = x[m] * g;
+            for (int m = lane; m < NT; m += 32)  // 0, whatever the weights' scale (NaN, infinity), where the token did not choose this expert
+                sc[m] = x[m] != 0.f ? x[m] * g : 0.f;
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&acc_full[b.s]);

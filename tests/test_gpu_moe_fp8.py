@@ -272,3 +272,29 @@ def test_a_decode_step_of_the_8_bit_operators():
                                                   [tuple(val(n, shared) for n in names)], f(r))
     assert np.array_equal(idx.cpu().numpy(), want_idx) and np.allclose(f(w), want_w, rtol=2e-6)
     assert np.linalg.norm(f(y) - want) / np.linalg.norm(want) < MOE_FROB_REL
+
+
+@pytest.mark.parametrize("M", [3, 20, 64])
+@pytest.mark.parametrize("name", ["gate", "up", "down"])
+def test_nan_and_infinite_scales_reach_only_tokens_of_their_expert(M, name):
+    """A block of weights that holds a NaN or an infinity is converted to a NaN scale; scales may be infinite, too."""
+    dev = require_gpu()
+    for v in (float("nan"), float("inf"), -float("inf")):
+        layer = Moe(hla, dev, 256, 256, 12, 2, 0, seed=4)
+        x = layer.tokens(M, M)
+        x[M // 2:] = x[M // 2]
+        y, idx, _ = layer.run(x)
+        count = torch.bincount(idx.flatten().long(), minlength=12).cpu()
+        scale = layer.s[name]
+        for bad in {int(count.argmax()), int(count.masked_fill(count == 0, M + 1).argmin()), int(idx[0, 1])}:  # crowded, and few tokens'
+            keep = scale[bad, 0, 1].clone()
+            scale[bad, 0, 1] = v
+            z, idx2, _ = layer.run(x)
+            scale[bad, 0, 1] = keep
+            hit = (idx == bad).any(-1)
+            assert torch.equal(idx, idx2) and bool(hit.any())
+            assert torch.equal(z[~hit], y[~hit])
+            if name == "down":  # 128 of the output's rows
+                assert not torch.any(z[hit][:, :128].isfinite()) and torch.equal(z[:, 128:], y[:, 128:])
+            else:               # 128 of h, whose scale is then NaN: all of the output
+                assert not torch.any(z[hit].isfinite())
