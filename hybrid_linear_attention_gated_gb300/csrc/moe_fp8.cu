@@ -355,6 +355,11 @@ struct Ring {
     __device__ __forceinline__ uint32_t freed() const { return (turn - 1) & 1; }       // and of the one before, from the second use on
 };
 
+// Scales of the down products: +0 stands for a token that did not choose the expert, and for nothing else.  A chosen one's that
+// is 0 (weights' scale 0, underflow) is -0: its products are added, so that NaN weights reach it all the same.
+__device__ __forceinline__ float chosen(float scale) { return scale == 0.f ? -0.f : scale; }
+__device__ __forceinline__ bool is_chosen(float scale) { return __float_as_uint(scale) != 0u; }
+
 __device__ __forceinline__ int load_acquire(const int *p) {
     int v;
     asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -690,8 +695,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
             const float *const x = sX + r.s * NT;
             float *const sc = sS + b.s * 2 * NT;
 #pragma unroll
-            for (int m = lane; m < NT; m += 32)  // 0, whatever the weights' scale (NaN, infinity), where the token did not choose this expert
-                sc[m] = x[m] != 0.f ? x[m] * g : 0.f;
+            for (int m = lane; m < NT; m += 32) sc[m] = is_chosen(x[m]) ? chosen(x[m] * g) : 0.f;  // whatever the weights' scale (NaN, infinity)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&acc_full[b.s]);
@@ -827,7 +831,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                         const float sc = fp8_scale_of(__uint_as_float(__reduce_max_sync(~0u, __float_as_uint(own)))), inv = fp8_inverse(sc);
                         *reinterpret_cast<uint32_t *>(p.hq + ((size_t)at.u * NT + pos) * p.I + at.ib * 128 + lane * 4) =
                             e4m3x4(h0 * inv, h1 * inv, h2 * inv, h3 * inv);
-                        if (hit) *hs = shared_unit(at.u) ? sc : sc * s_w[m * p.k + lane];
+                        if (hit) *hs = shared_unit(at.u) ? sc : chosen(sc * s_w[m * p.k + lane]);
                     };
                     if (!both) {
                         if (grp) {
@@ -940,8 +944,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
                                 const float4 f = *reinterpret_cast<const float4 *>(sc + m0 + cc + j);
                                 const float x[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)  // 0: a token that did not choose this expert
-                                    if (x[i] != 0.f) acc[cc + j + i] = fmaf(__uint_as_float(v[j + i]), x[i], acc[cc + j + i]);
+                                for (int i = 0; i < 4; ++i)
+                                    if (is_chosen(x[i])) acc[cc + j + i] = fmaf(__uint_as_float(v[j + i]), x[i], acc[cc + j + i]);
                             }
                         }
                     }

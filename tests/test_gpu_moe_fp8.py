@@ -298,3 +298,27 @@ def test_nan_and_infinite_scales_reach_only_tokens_of_their_expert(M, name):
                 assert not torch.any(z[hit][:, :128].isfinite()) and torch.equal(z[:, 128:], y[:, 128:])
             else:               # 128 of h, whose scale is then NaN: all of the output
                 assert not torch.any(z[hit].isfinite())
+
+
+@pytest.mark.parametrize("M", [3, 20, 64])
+def test_a_scale_of_zero_hides_no_nan(M):
+    """NaN times a scale of 0 is NaN for the tokens of the expert, however many they are, and nothing for the others."""
+    dev = require_gpu()
+    layer = Moe(hla, dev, 256, 256, 12, 2, 0, seed=4)
+    x = layer.tokens(M, M)
+    x[M // 2:] = x[M // 2]
+    y, idx, _ = layer.run(x)
+    count = torch.bincount(idx.flatten().long(), minlength=12).cpu()
+    for bad in (int(count.argmax()), int(count.masked_fill(count == 0, M + 1).argmin())):
+        w, scale = layer.w["down"].view(torch.uint8), layer.s["down"]
+        keep, byte = scale[bad, 0, 1].clone(), w[bad, 3, 200].clone()
+        hit = (idx == bad).any(-1)
+        scale[bad, 0, 1] = 0.0
+        z, _, _ = layer.run(x)                      # zeros alone: finite
+        assert torch.all(z.isfinite()) and torch.equal(z[~hit], y[~hit]) and torch.equal(z[:, 128:], y[:, 128:])
+        w[bad, 3, 200] = 0x7F
+        again, _, _ = layer.run(x)
+        scale[bad, 0, 1], w[bad, 3, 200] = keep, byte
+        assert torch.all(again[hit][:, 3].isnan())
+        again[hit, 3] = z[hit, 3]
+        assert torch.equal(again, z)
