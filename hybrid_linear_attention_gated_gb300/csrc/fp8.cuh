@@ -85,6 +85,11 @@ __device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *map, int 
         : "memory");
 }
 
+// Counts `bytes` as copied that were expected and will not come.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -217,6 +222,9 @@ __device__ __forceinline__ void tmem_free_pair(uint32_t taddr, uint32_t columns)
 __device__ __forceinline__ void cluster_sync() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void peer_store(int *p, uint32_t rank, int v) {
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_address(p, rank)), "r"(v) : "memory");
 }
 __device__ __forceinline__ float peer_float(const float *p, uint32_t rank) {
     uint32_t a;

@@ -625,6 +625,21 @@ struct Pair {
     static_assert(kSmem <= 227 * 1024, "one CTA to an SM");
 };
 
+// After a wait that gave up in the even CTA, and once neither copies any more: waits for the last fill of each stage.  Both CTAs'
+// copies, `bytes` each, complete on the even one's barriers, which expect them together.  A stage that one of them filled once more
+// than the other (no more than once: the fill behind it waits for a product of both halves) gets what is missing: the arrival and the
+// bytes of the other's, or the other's bytes as if they had come.  Where the even CTA did not give up, its products waited for all.
+template <int NS>
+__device__ __forceinline__ void drain_pair(uint64_t *full, int even, int odd, uint32_t bytes, int *status) {
+    for (int s = 0; s < NS; ++s) {
+        const int a = (even + NS - 1 - s) / NS, b = (odd + NS - 1 - s) / NS, last = (a > b ? a : b) - 1;
+        if (last < 0) continue;
+        if (a < b) mbar_expect_tx(&full[s], bytes);
+        if (a > b) mbar_complete_tx(&full[s], bytes);
+        if (!fp8_wait(&full[s], last & 1, status)) fp8_wait(&full[s], last & 1, status, 8 * kFp8WaitNs);
+    }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const MatmulParams p) {
@@ -641,7 +656,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
     scales.full = done + 1;
     scales.empty = scales.full + kScaleRing;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(scales.empty + kScaleRing);
-    int *const failed_slot = reinterpret_cast<int *>(tmem_slot + 1);
+    int *const failed_slot = reinterpret_cast<int *>(tmem_slot + 1), *const fills_slot = failed_slot + 1, *const drain_slot = failed_slot + 2;
 
     if (p.force_timeout) {
         forced_timeout(done, p.status);
@@ -652,7 +667,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
     const int tiles = p.row_tiles * p.col_tiles;
 
     if (tid == 0) {
-        *failed_slot = 0;
+        *failed_slot = *drain_slot = 0;
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -691,6 +706,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
                     if (++s == NS) s = 0, ++turn;
                 }
             }
+            *fills_slot = turn * NS + s;
             if (!ok) *failed_slot = 1;
         } else if (warp == 1 && rank == 0) {
             bool ok = true;
@@ -763,14 +779,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) __cluster_dims__(2, 1, 1)
     }
     __syncwarp();
     __syncthreads();
-    if (*failed_slot && tid == 0) {
-        // After a wait that gave up, copies may be on their way that no barrier of this CTA counts: give them time to land.
-        const uint64_t began = global_ns();
-        while (global_ns() - began < 20000000ull) {
-        }
-    }
+    if (rank == 0 && tid < 2 && *failed_slot) peer_store(drain_slot, tid, 1);
     tc_fence_before();
     cluster_sync();  // no CTA leaves while the other's products, commits or arrivals may reach it
+    if (*drain_slot) {  // in both: copies may be on their way into either
+        if (rank == 0 && tid == 0)
+            drain_pair<NS>(full, *fills_slot, __float_as_int(peer_float(reinterpret_cast<const float *>(fills_slot), 1)), kTileBytes + F::kWeightBytes, p.status);
+        cluster_sync();
+    }
     if (warp == 1) tmem_free_pair(tmem, 512);
 }
 
