@@ -118,6 +118,17 @@ __device__ __forceinline__ bool fp8_wait(uint64_t *bar, uint32_t parity, int *st
     return false;
 }
 
+// After a wait that gave up: waits for the last fill of each stage of a ring of NS, which no product may have waited for.  `issued`
+// counts the fills, up to multiples of 2 NS.
+template <int NS>
+__device__ __forceinline__ void drain_fills(uint64_t *full, int issued, int *status) {
+    for (int s = 0; s < NS; ++s) {
+        if (issued <= s) continue;
+        const int f = issued - 1 - (issued - 1 - s) % NS;
+        if (!fp8_wait(&full[s], f / NS & 1, status)) fp8_wait(&full[s], f / NS & 1, status, 8 * kFp8WaitNs);
+    }
+}
+
 // Whether the phase has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t done;

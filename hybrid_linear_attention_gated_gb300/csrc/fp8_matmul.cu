@@ -189,33 +189,25 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             if (!ok) continue;
             tc_fence_after();
             const float *const sc = sScale + (i % kScaleChunk) * NT;
-            constexpr int C = NT < 32 ? NT : 32;
+            uint32_t v[NT];
+            tmem_ld<NT>(my + b * NT, v);
+            tmem_wait(v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[b]);
 #pragma unroll
-            for (int c = 0; c < NT; c += C) {
-                uint32_t v[C];
-                tmem_ld<C>(my + b * NT + c, v);
-                tmem_wait(v);
-                if (c + C == NT) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_empty[b]);
-                }
-#pragma unroll
-                for (int j = 0; j < C; j += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(sc + c + j);
-                    acc[c + j] = fmaf(__uint_as_float(v[j]), f.x, acc[c + j]);
-                    acc[c + j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y, acc[c + j + 1]);
-                    acc[c + j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z, acc[c + j + 2]);
-                    acc[c + j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w, acc[c + j + 3]);
-                }
+            for (int j = 0; j < NT; j += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(sc + j);
+                acc[j] = fmaf(__uint_as_float(v[j]), f.x, acc[j]);
+                acc[j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y, acc[j + 1]);
+                acc[j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z, acc[j + 2]);
+                acc[j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w, acc[j + 3]);
             }
         }
     }
     __syncwarp();
     __syncthreads();
-    if (tid == 0)  // fills that no product waited for (after a wait that gave up)
-        for (int i = *consumed_slot; i < issued; ++i)
-            if (!fp8_wait(&full[i % NS], (i / NS) & 1, p.status)) fp8_wait(&full[i % NS], (i / NS) & 1, p.status, 8 * kFp8WaitNs);
+    if (tid == 0 && *consumed_slot < issued) drain_fills<NS>(full, issued, p.status);
     __syncwarp();
     __syncthreads();
     // the tiles are used up: their place takes the sums [token][weight row]
@@ -584,12 +576,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
     __syncwarp();
     __syncthreads();
-    if (tid == 0 && *failed_slot)  // after a wait that gave up: the last fill of each stage may be waited for by no product
-        for (int s = 0; s < NS; ++s) {
-            if (issued <= s) continue;
-            const int f = issued - 1 - (issued - 1 - s) % NS;
-            if (!fp8_wait(&full[s], f / NS & 1, p.status)) fp8_wait(&full[s], f / NS & 1, p.status, 8 * kFp8WaitNs);
-        }
+    if (tid == 0 && *failed_slot) drain_fills<NS>(full, issued, p.status);
     __syncwarp();
     __syncthreads();
     if (p.split > 1) {

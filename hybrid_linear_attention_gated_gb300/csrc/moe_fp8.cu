@@ -1029,12 +1029,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     }
     __syncwarp();
     __syncthreads();
-    if (tid == 0 && !s_int[1])  // after a wait that gave up: the last fill of each slot may be in flight
-        for (int s = 0; s < NS; ++s) {
-            if (issued <= s) continue;
-            const int f = issued - 1 - (issued - 1 - s) % NS;
-            if (!fp8_wait(&full[s], f / NS & 1, p.status)) fp8_wait(&full[s], f / NS & 1, p.status, 8 * kFp8WaitNs);
-        }
+    if (tid == 0 && !s_int[1]) drain_fills<NS>(full, issued, p.status);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -1096,7 +1091,7 @@ extern "C" int moe_fp8_forward(const hla_moe_fp8 *L, int M, const hla_bf16 *x, c
     const int NT = tokens_padded(M), Hd = L->hidden, I = L->inter, E = L->n_experts, U = moe_units_most(L, M), sms = sm_count();
     uint8_t *const w = static_cast<uint8_t *>(ws);
     // no more CTAs than the largest phase can have blocks
-    const long most1 = (long)U * (I / 128) * (Hd / 128), most = most1;
+    const long most = (long)U * (I / 128) * (Hd / 128);
     const int grid = (int)(most < sms ? most : sms);
 
     MoeParams p = {};

@@ -322,3 +322,30 @@ def test_a_scale_of_zero_hides_no_nan(M):
         assert torch.all(again[hit][:, 3].isnan())
         again[hit, 3] = z[hit, 3]
         assert torch.equal(again, z)
+
+
+def test_views_aligned_to_16_bytes():
+    dev = require_gpu()
+
+    def off(t):  # t at an address that is 16 bytes past a multiple of 512
+        raw = torch.zeros(t.numel() * t.element_size() + 512, dtype=torch.uint8, device=dev)
+        v = raw[16:16 + t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+        v.view(torch.uint8).copy_(t.view(torch.uint8))
+        assert v.data_ptr() % 512 == 16
+        return v
+
+    layer = Moe(hla, dev, 384, 256, 20, 3, 1, seed=2)
+    for M in (3, 20, 64):
+        x = layer.tokens(M, M)
+        residual = torch.randn(M, 384, device=dev).to(BF)
+        y, idx, w = layer.run(x, residual)
+        keep = layer.W_r, dict(layer.w), dict(layer.s)
+        layer.W_r = off(layer.W_r)
+        layer.w = {n: off(t) for n, t in layer.w.items()}
+        layer.s = {n: off(t) for n, t in layer.s.items()}
+        L = layer.descriptor()
+        layer.W_r, layer.w, layer.s = keep
+        ws = off(layer.workspace(M))
+        y2, idx2, w2 = off(torch.full_like(y, 7.0)), off(torch.full_like(idx, -7)), off(torch.full_like(w, 7.0))
+        hla.moe_fp8_forward(L, M, off(x), off(residual), y2, idx2, w2, ws, ws.numel())
+        assert torch.equal(y2, y) and torch.equal(idx2, idx) and torch.equal(w2, w)
