@@ -854,7 +854,10 @@ extern "C" int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_
         p.direct = N % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 31) == 0;
         // The variant whose waves of tiles take the fewest cycles a block of K, measured at 512 to 8192 tokens: 600 for a CTA's
         // 128 x 128, 900 and 970 for a pair's 256 x 192 and 256 x 256 (512 tokens to 7168 of 4096: 24.2, 20.0, 22.3 us; 256 to 16416
-        // of 7168: 38, 53, 34 us; 256 to 7168 of 4096: 14, 19, 21 us; 8192 to 16416 of 7168: 920, 877, 801 us).
+        // of 7168: 38, 53, 34 us; 256 to 7168 of 4096: 14, 19, 21 us; 8192 to 16416 of 7168: 920, 877, 801 us).  Neither the tile's end nor
+        // the cutting of K is counted.  Where stores decide, that costs up to 9%: 8192 to 16416 of K 128 84.7, 77.8, 84.7 us (the last is
+        // taken), 256 to 16416 of K 256 7.0, 8.5, 7.4 (the last).  Few tiles of long K are cut by the 128 x 128 variant alone, which the
+        // waves prefer there anyway: 256 to 2048 of 7168 11.2, 27.7, 31.2, 1000 to 2048 of 7168 20.4, 28.7, 32.5.
         const auto waves = [](long tiles, long slots) { return (tiles + slots - 1) / slots; };
         const long rows = (M + 127) / 128L, pairs = (M + 255) / 256L, one = rows * ((N + 127) / 128L);
         const long cost1 = 600 * waves(one, sms), cost192 = 900 * waves(pairs * ((N + 191) / 192L), sms / 2),

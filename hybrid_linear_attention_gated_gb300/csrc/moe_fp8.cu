@@ -71,7 +71,10 @@ MoeSpace moe_space(const hla_moe_fp8 *L, int M) {
 constexpr int kPrepThreads = 256;
 constexpr int kPrepCluster = 4;
 constexpr int kPrepExperts = 8;     // experts per cluster: the columns of one mma.sync
-constexpr int kPrepAhead = 7;       // K steps of 32 whose weights are loaded at once
+// K steps of 32 whose weights are loaded at once.  A warp has hidden / 1024 steps, so that 7168 takes one round trip; it matters
+// little: 64 tokens, inner 256, 256 + 1 experts of hidden 7168 with 4, 7, 8, 12 at once 247.6, 246.1, 247.0, 247.3 us; hidden 2048, 64 + 1
+// experts 49.4, 49.9, 49.9, 51.2; hidden 3200, 8 + 1 experts 44.3, 44.5, 44.9, 45.5.
+constexpr int kPrepAhead = 7;
 
 struct PrepParams {
     int M, Hd, E, NT, router_clusters, counters;
@@ -510,8 +513,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_fp8_kernel(const __grid_co
     const int U = s_int[0] + p.n_shared, G = gridDim.x, c = blockIdx.x;
     const int nI = p.I / 128, nR = p.Hd / 128, KB1 = p.Hd / kFp8Block, KB2 = p.I / kFp8Block;
     Share s1, s2;
-    // Gate/up items for three quarters of the CTAs or more, but no more than one each (one token of 8 + 1 experts of 2048: 144 on
-    // 152), stay whole: what is idle costs nothing while the rest fills the memory, and no parts are joined.
+    // Gate/up items for three quarters of the CTAs or more, but no more than one each, stay whole: what is idle costs nothing while the
+    // rest fills the memory, and no parts are joined.  One token of 8 + 1 experts, whole and cut: 144 items on 152 CTAs 75.9, 78.4 us
+    // of hidden 7168 and 20.5, 23.4 of 512; 117 items 65.4, 67.3 and 19.9, 22.3.  The border is a careful one: 108 items gain so, too
+    // (62.0, 63.6 and 19.5, 22.3), 81 of hidden 7168 lose (54.3, 52.3).
     const int items = U * nI;
     s1.set(items * KB1, items <= G && items * 4 >= G * 3 ? KB1 : 1, min((uint32_t)G, items * sharers(KB1, p.M)));
     s2.set(nR * U * KB2, 1, min((uint32_t)G, nR * sharers(U * KB2, p.M)));

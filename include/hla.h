@@ -406,7 +406,7 @@ int fp8_matmul(int M, int N, int K, const uint8_t *x, const float *x_scale, cons
  *  Router, choice and weights as moe_route_topk, from x itself.  Experts as moe_expert_forward, on the values of
  *  xq = fp8_quantize(x, 1 row): h = SiLU(W_gate xq) * (W_up xq), hq = fp8_quantize(h, 1 row),
  *  y[m] = sum_j topk_w[m, j] * W_down hq_j + sum_s (the same for shared expert s) (+ residual[m]), rounded once to bf16.
- *  An expert's weights reach only the tokens that chose it: NaN weights of one do not spread to others.
+ *  An expert's weights reach only the tokens that chose it: NaN weights, and NaN or infinite scales, of one do not spread to others.
  *  x, y bf16 [M, Hd]; residual bf16 [M, Hd] or NULL (y may be the residual, or x); topk_idx int32 [M, k] and topk_w fp32
  *  [M, k] receive the choice, or NULL.  1 <= M <= 64, Hd % 128 == 0, I % 128 == 0, 1 <= k <= 16, k <= E,
  *  E + n_shared <= 1024, n_shared <= 16.
