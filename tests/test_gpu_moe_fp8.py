@@ -349,3 +349,39 @@ def test_views_aligned_to_16_bytes():
         y2, idx2, w2 = off(torch.full_like(y, 7.0)), off(torch.full_like(idx, -7)), off(torch.full_like(w, 7.0))
         hla.moe_fp8_forward(L, M, off(x), off(residual), y2, idx2, w2, ws, ws.numel())
         assert torch.equal(y2, y) and torch.equal(idx2, idx) and torch.equal(w2, w)
+
+
+def test_parallel_branches_of_a_graph():
+    """Two layers, and products beside them, on branches of one graph that nothing orders: each with its own workspace."""
+    dev = require_gpu()
+    a, b = Moe(hla, dev, 1024, 512, 32, 4, 1, seed=7), Moe(hla, dev, 2048, 256, 16, 4, 0, seed=8)
+    xa, xb = a.tokens(64, 1), b.tokens(5, 2)
+    want_a, want_b = a.run(xa)[0], b.run(xb)[0]
+    M, N, K = 600, 4000, 1024
+    q, W = (torch.randn(n, K, device=dev).to(torch.float8_e4m3fn) for n in (M, N))
+    s, ws = torch.ones(M, up(K, 128), device=dev), torch.ones(up(N, 128), up(K, 128), device=dev)
+    y = torch.empty(M, N, dtype=BF, device=dev)
+    hla.fp8_matmul(M, N, K, q, s, W, ws, None, y, hla.HLA_BF16)
+    want_y = y.clone()
+    ya, yb = torch.empty_like(xa), torch.empty_like(xb)
+    spaces = a.workspace(64), b.workspace(5)
+    torch.cuda.synchronize()
+    graph, side, third = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        third.wait_stream(main)
+        for _ in range(4):
+            hla.moe_fp8_forward(a.L, 64, xa, None, ya, None, None, spaces[0], spaces[0].numel())
+            with torch.cuda.stream(side):
+                hla.moe_fp8_forward(b.L, 5, xb, None, yb, None, None, spaces[1], spaces[1].numel())
+            with torch.cuda.stream(third):
+                hla.fp8_matmul(M, N, K, q, s, W, ws, None, y, hla.HLA_BF16)
+        main.wait_stream(side)
+        main.wait_stream(third)
+    for _ in range(10):
+        ya.zero_(), yb.zero_(), y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert hla.hla_device_status() == 0
+        assert torch.equal(ya, want_a) and torch.equal(yb, want_b) and torch.equal(y, want_y)
